@@ -319,11 +319,12 @@ def _quantize(x, c):
     """Codes (packed), scales (as bytes) and zero points of float32 x [..., d]; the stored scale gives the codes."""
     g = c["group"]
     y = x.unflatten(-1, (c["d"] // g, g))
+    steps = torch.tensor(7.0 if c["sym"] else 15.0, device=DEV).expand(y.shape[:-1])  # a tensor: a true division
     if c["sym"]:
-        s = y.abs().amax(-1) / 7.0
+        s = y.abs().amax(-1) / steps
     else:
         lo, hi = y.amin(-1).clamp(max=0.0), y.amax(-1).clamp(min=0.0)
-        s = (hi - lo) / 15.0
+        s = (hi - lo) / steps
     s = torch.where(s == 0, torch.ones_like(s), s)
     stored = s if c["sdt"] == "f32" else s.to(torch.bfloat16)
     s = stored.float()[..., None]
