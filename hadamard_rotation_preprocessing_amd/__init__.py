@@ -16,6 +16,9 @@ Entry points (same names as the C ABI):
 With ``mix=dict(perm=..., in_signs=..., out_signs=...)`` (device tensors,
 int32 / int8 / int8, any subset) the first three call the ``*_mixed`` entry
 points (randomised rotations, hr_mix in the header).
+
+The paged 4-bit key/value cache that takes the rotated keys (CacheSpec,
+cache_append, cache_attention, cache_update, cache_compact) is in ``cache.py``.
 """
 from __future__ import annotations
 
@@ -269,3 +272,10 @@ def kron_order(n: int, with_matrix: bool = False):
         h = np.frombuffer(bytes(buf), dtype=np.int8).reshape(K.value, K.value).copy()
         return K.value, M.value, h
     return K.value, M.value
+
+
+from .cache import (CacheSpec, cache_append, cache_attention, cache_attention_work, cache_compact,  # noqa: E402,F401
+                    cache_pool, cache_sections, cache_update)
+
+__all__ += ["CacheSpec", "cache_append", "cache_attention", "cache_attention_work", "cache_compact", "cache_pool",
+            "cache_sections", "cache_update"]

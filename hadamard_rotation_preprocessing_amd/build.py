@@ -54,7 +54,9 @@ def build(verbose: bool = True) -> str:
     hipcc = _hipcc()
     obj_dir = os.path.join(LIBDIR, "obj")
     os.makedirs(obj_dir, exist_ok=True)
-    sources = [("kernels.hip", True), ("fast.hip", True), ("colrot.hip", True), ("api.cpp", False), ("paley.cpp", False)]
+    sources = [("kernels.hip", True), ("fast.hip", True), ("colrot.hip", True), ("cache_attn_256.hip", True),
+               ("cache_attn_128.hip", True), ("cache_attn_64.hip", True), ("cache_pages.hip", True), ("api.cpp", False),
+               ("paley.cpp", False), ("cache_api.cpp", False), ("cache_attn.cpp", False)]
     cmds, objs = [], []
     for src, device in sources:
         out = os.path.join(obj_dir, src + ".o")

@@ -671,6 +671,14 @@ int dequant_impl(const void* codes, const void* scales, const void* zeros, const
 
 }  // namespace
 
+namespace hr {
+// for the cache's host layer, which reports through the same hr_last_error
+int set_error(int status, const char* text) {
+    g_err = text;
+    return status;
+}
+}  // namespace hr
+
 extern "C" {
 
 const char* hr_last_error(void) { return g_err.c_str(); }

@@ -1,0 +1,568 @@
+// Writing the paged 4-bit cache (hr_cache_append) and moving its pages
+// (hr_cache_update, hr_cache_compact).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "cache.h"
+#include "codes.h"
+
+namespace hr {
+namespace {
+
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
+
+// ---------------------------------------------------------------------------
+// append
+//
+// A wave takes the K and V vectors of one kv head at 1024 / D consecutive
+// positions of a sequence, aligned to that number, so that it owns every byte
+// of zero points it writes.  D / 16 lanes share a vector, 16 consecutive
+// elements each: four bits of the Hadamard transform are inside the lane, the
+// other two to four are lane bits, and a group of 32 to 256 elements is 2 to
+// 16 consecutive lanes.  The stages go in the order of the index bits.
+
+template <int CTRL, int BANKS = 0xF>
+__device__ __forceinline__ float dpp(float old, float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, 0xF, BANKS, false));
+}
+
+// the value of lane ^ X (X = 1, 2, 4, 8, inside 16 lanes)
+template <int X>
+__device__ __forceinline__ float lane_xor(float v) {
+    if constexpr (X == 1) return dpp<0xB1>(v, v);         // quad_perm [1,0,3,2]
+    if constexpr (X == 2) return dpp<0x4E>(v, v);         // quad_perm [2,3,0,1]
+    if constexpr (X == 4) return dpp<0x114, 0xA>(dpp<0x104, 0x5>(v, v), v);  // banks of four: shl 4 into even, shr 4 into odd
+    return dpp<0x128>(v, v);                               // row_ror 8
+}
+
+template <int LANES, class F>
+__device__ __forceinline__ float over_lanes(float v, F f) {
+    if constexpr (LANES >= 2) v = f(v, lane_xor<1>(v));
+    if constexpr (LANES >= 4) v = f(v, lane_xor<2>(v));
+    if constexpr (LANES >= 8) v = f(v, lane_xor<4>(v));
+    if constexpr (LANES >= 16) v = f(v, lane_xor<8>(v));
+    return v;
+}
+
+template <int X>
+__device__ __forceinline__ void lane_stage(float (&v)[16], int lane) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float y = lane_xor<X>(v[i]);
+        v[i] = (lane & X) ? y - v[i] : v[i] + y;
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void hadamard(float (&v)[16], int lane, float norm) {
+#pragma unroll
+    for (int s = 1; s < 16; s *= 2)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (!(i & s)) {
+                const float x = v[i], y = v[i + s];
+                v[i] = x + y;
+                v[i + s] = x - y;
+            }
+    lane_stage<1>(v, lane);
+    lane_stage<2>(v, lane);
+    if constexpr (D >= 128) lane_stage<4>(v, lane);
+    if constexpr (D >= 256) lane_stage<8>(v, lane);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= norm;
+}
+
+template <class T>
+__device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4v x = reinterpret_cast<const uint4v*>(p)[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[8 * i + 2 * j] = __uint_as_float(x[j] << 16);
+                v[8 * i + 2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4v x = reinterpret_cast<const uint4v*>(p)[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[4 * i + j] = __uint_as_float(x[j]);
+        }
+    }
+}
+
+// Quantizes the lane's 16 elements: scale s = range / steps of the group,
+// stored (f32 or nearest-even bf16), codes from the stored scale.  y / s is
+// the correctly rounded quotient: one division gives r = 1 / s, and with
+// t = y r the remainder fma(-t, s, y) is exact, so fma(remainder, r, t) rounds
+// to y / s (P. Markstein, IBM J. Res. Dev. 34, 1990).  That keeps every code
+// equal to the definition's, ties included, at two more instructions than a
+// product with the reciprocal.
+template <int LANES, bool SYM>
+__device__ __forceinline__ uint2v quantize(const float (&v)[16], bool sf32, uint32_t* scale, uint32_t* zero) {
+#pragma clang fp contract(off)
+    float s, z = 0.0f;
+    if constexpr (SYM) {
+        float top = fabsf(v[0]);
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, fabsf(v[i]));
+        top = over_lanes<LANES>(top, [](float a, float b) { return fmaxf(a, b); });
+        s = top / 7.0f;
+    } else {
+        float lo = fminf(v[0], 0.0f), hi = fmaxf(v[0], 0.0f);
+#pragma unroll
+        for (int i = 1; i < 16; ++i) {
+            lo = fminf(lo, v[i]);
+            hi = fmaxf(hi, v[i]);
+        }
+        lo = over_lanes<LANES>(lo, [](float a, float b) { return fminf(a, b); });
+        hi = over_lanes<LANES>(hi, [](float a, float b) { return fmaxf(a, b); });
+        s = (hi - lo) / 15.0f;
+        z = lo;
+    }
+    if (s == 0.0f) s = 1.0f;
+    if (sf32) {
+        *scale = __float_as_uint(s);
+    } else {
+        *scale = f2bf(s);
+        s = bf2f(*scale);
+    }
+    const float r = 1.0f / s;
+    float least = -8.0f, most = 7.0f;
+    if constexpr (!SYM) {
+        z = fminf(fmaxf(rintf(-z / s), 0.0f), 15.0f);
+        *zero = static_cast<uint32_t>(static_cast<int>(z));
+        least = 0.0f;
+        most = 15.0f;
+    }
+    uint2v w = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float t = v[i] * r;
+        const float q = rintf(__builtin_fmaf(__builtin_fmaf(-t, s, v[i]), r, t));
+        const int c = static_cast<int>(fminf(fmaxf(q + z, least), most));
+        w[i / 8] |= (static_cast<uint32_t>(c) & 15u) << (4 * (i & 7));
+    }
+    return w;
+}
+
+template <int D, int G, bool SYM, class T>
+__global__ void __launch_bounds__(256) cache_append(const CacheAppendArgs a) {
+    constexpr int LPV = D / 16, POS = 64 / LPV, LANES = G / 16, NG = D / G;
+    const int lane = threadIdx.x & 63;
+    // four heads of a block of positions to a workgroup
+    const int groups = (a.pg.hkv + 3) / 4;
+    const int h = static_cast<int>(blockIdx.x % groups) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int u = blockIdx.x / groups;
+    if (h >= a.pg.hkv) return;
+    // the block's sequence: the last b with floor(cu(b) / POS) + 2 b <= u, a
+    // bound that leaves every sequence at least the blocks it touches
+    auto cu = [&](int b) { return min(max(a.sq.cu ? a.sq.cu[b] : b * a.sq.per, 0), a.sq.tokens); };
+    int b = 0, hi = a.sq.rows - 1;
+    while (b < hi) {
+        const int mid = (b + hi + 1) / 2;
+        if (cu(mid) / POS + 2 * mid <= u) b = mid;
+        else hi = mid - 1;
+    }
+    const int start = cu(b), n = max(cu(b + 1) - start, 0);
+    const int len = min(max(a.sq.lens[b], 0), a.sq.max_pages << a.pg.logp);
+    const int first = len - n;  // position of the first new token; may lie before 0
+    const int nth = u - (start / POS + 2 * b);
+    const int p0 = (max(first, 0) / POS + nth) * POS;
+    if (nth < 0 || p0 >= len) return;
+    const int page = a.sq.table[static_cast<int64_t>(b) * a.sq.max_pages + (p0 >> a.pg.logp)];
+    if (static_cast<uint32_t>(page) >= static_cast<uint64_t>(a.sq.n_pages)) return;
+    uint8_t* base = a.pool + page * a.pg.page_bytes + h * a.pg.head_bytes;
+    const int pos = p0 + lane / LPV, off = pos & (a.pg.page - 1), e = lane % LPV;
+    const bool mine = pos >= max(first, 0) && pos < len;
+    const int64_t tok = start + min(max(pos - first, 0), n - 1);
+    float k[16], v[16];
+    load16(static_cast<const T*>(a.k) + tok * a.k_st + h * a.k_sh + 16 * e, k);
+    load16(static_cast<const T*>(a.v) + tok * a.v_st + h * a.v_sh + 16 * e, v);
+    if (a.rotate) hadamard<D>(k, lane, a.norm);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        uint32_t scale, zero = 0;
+        const uint2v w = quantize<LANES, SYM>(x ? v : k, a.pg.sf32, &scale, &zero);
+        const int g = e / LANES, at = off * NG + g;
+        if (mine) {
+            *reinterpret_cast<uint2v*>(base + (x ? a.pg.vc : a.pg.kc) + off * (D / 2) + 8 * e) = w;
+            if (e % LANES == 0) {
+                uint8_t* sp = base + (x ? a.pg.vs : a.pg.ks);
+                if (a.pg.sf32) reinterpret_cast<uint32_t*>(sp)[at] = scale;
+                else reinterpret_cast<uint16_t*>(sp)[at] = static_cast<uint16_t>(scale);
+            }
+        }
+        if constexpr (!SYM) {
+            // two zero points to a byte: the other one belongs to the next
+            // group, or with one group to the next position, G / 16 lanes on
+            const uint32_t other = __shfl_xor(zero, LANES);
+            const bool others = __shfl_xor(static_cast<int>(mine), LANES) != 0;
+            uint8_t* zp = base + (x ? a.pg.vz : a.pg.kz) + at / 2;
+            if (e % LANES == 0) {
+                if (mine && others) {
+                    if (!(at & 1)) *zp = static_cast<uint8_t>(zero | (other << 4));
+                } else if (mine) {
+                    const uint32_t old = *zp;
+                    *zp = static_cast<uint8_t>((at & 1) ? (old & 15u) | (zero << 4) : (old & 0xF0u) | zero);
+                }
+            }
+        }
+    }
+}
+
+template <int D, int G, class T>
+int append_launch(const CacheAppendArgs& a, hipStream_t s) {
+    const dim3 grid(static_cast<uint32_t>(a.units) * ((a.pg.hkv + 3) / 4));
+    if (a.pg.sym) hipLaunchKernelGGL((cache_append<D, G, true, T>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((cache_append<D, G, false, T>), grid, dim3(256), 0, s, a);
+    return static_cast<int>(hipGetLastError());
+}
+
+template <int D, class T>
+int append_group(const CacheAppendArgs& a, hipStream_t s) {
+    const int g = D / a.pg.ng;
+    if (g == 32) return append_launch<D, 32, T>(a, s);
+    if (g == 64) return append_launch<D, 64, T>(a, s);
+    if constexpr (D >= 128)
+        if (g == 128) return append_launch<D, 128, T>(a, s);
+    if constexpr (D >= 256)
+        if (g == 256) return append_launch<D, 256, T>(a, s);
+    return static_cast<int>(hipErrorInvalidValue);
+}
+
+template <class T>
+int append_dim(const CacheAppendArgs& a, hipStream_t s) {
+    if (a.pg.d == 64) return append_group<64, T>(a, s);
+    if (a.pg.d == 128) return append_group<128, T>(a, s);
+    return append_group<256, T>(a, s);
+}
+
+// ---------------------------------------------------------------------------
+// update and compact
+//
+// Both count the holders of every page from the table itself (integer
+// additions, so the order of the atomics does not matter), number the free or
+// live pages by a scan in ascending order in one workgroup, and then write the
+// new table and copy the pages in one launch.
+
+constexpr int kScan = 1024;  // threads of a scanning workgroup
+
+__global__ void __launch_bounds__(256) fill_words(int32_t* p, int64_t n, int32_t v) {
+    for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) p[i] = v;
+}
+
+// exclusive sum of v over the workgroup's kScan threads, and the total
+__device__ __forceinline__ int scan_wg(int v, int* total, int* lds) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int inc = v;
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) {
+        const int y = __shfl_up(inc, x);
+        if (lane >= x) inc += y;
+    }
+    __syncthreads();
+    if (lane == 63) lds[wave] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int x = 0; x < kScan / 64; ++x) {
+        const int y = lds[x];
+        if (x < wave) before += y;
+        all += y;
+    }
+    *total = all;
+    return before + inc - v;
+}
+
+// What row i of the new table takes from the old one.
+struct Kept {
+    const int32_t* row;   // the parent's entries
+    int before, after;    // lengths
+    int kept, held;       // pages inherited, pages of the new length
+    int last;             // slot of the page that it goes on in, or -1
+};
+__device__ __forceinline__ Kept kept_of(const CacheUpdateArgs& a, int i) {
+    Kept k;
+    const int p = a.parents[i];
+    const bool has = p >= 0 && p < a.rows;
+    k.row = a.table + static_cast<int64_t>(has ? p : 0) * a.max_pages;
+    const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page;
+    k.before = has ? static_cast<int>(min(static_cast<int64_t>(max(a.lens[p], 0)), cap)) : 0;
+    k.after = static_cast<int>(min(max(static_cast<int64_t>(k.before) + a.grow[i], int64_t{0}), cap));
+    k.held = (k.after + a.page - 1) / a.page;
+    k.kept = min((k.before + a.page - 1) / a.page, k.held);
+    k.last = k.after > k.before && k.before % a.page > 0 ? k.before / a.page : -1;
+    return k;
+}
+__device__ __forceinline__ int page_in(int32_t page, int64_t n) {
+    return page >= 0 && page < n ? page : -1;
+}
+
+// refs: entries of the new rows that inherit a page; writers, lowest: how many
+// rows go on in it, and the lowest of them.  A workgroup a row.
+__global__ void __launch_bounds__(256) update_count(const CacheUpdateArgs a, int32_t* writers, int32_t* lowest) {
+    for (int i = blockIdx.x; i < a.new_rows; i += gridDim.x) {
+        const Kept k = kept_of(a, i);
+        for (int j = threadIdx.x; j < k.kept; j += 256) {
+            const int p = page_in(k.row[j], a.n_pages);
+            if (p < 0) continue;
+            atomicAdd(a.refs + p, 1);
+            if (j == k.last) {
+                atomicAdd(writers + p, 1);
+                atomicMin(lowest + p, i);
+            }
+        }
+    }
+}
+
+// Which row copies its last page, how many pages each row needs before it,
+// and the free pages in ascending order (as many as are needed).
+__global__ void __launch_bounds__(kScan) update_plan(const CacheUpdateArgs a, const int32_t* writers, const int32_t* lowest,
+                                                     int32_t* base, int32_t* copies, int32_t* free_list, int32_t* counts) {
+    __shared__ int lds[kScan / 64];
+    int need = 0;
+    for (int c = 0; c < a.new_rows; c += kScan) {
+        const int i = c + threadIdx.x;
+        int mine = 0, copy = 0;
+        if (i < a.new_rows) {
+            const Kept k = kept_of(a, i);
+            if (k.last >= 0) {
+                const int p = page_in(k.row[k.last], a.n_pages);
+                copy = p >= 0 && !(lowest[p] == i && a.refs[p] == writers[p]);
+            }
+            mine = copy + k.held - k.kept;
+            copies[i] = copy;
+        }
+        int total;
+        const int before = scan_wg(mine, &total, lds);
+        if (i < a.new_rows) base[i] = need + before;
+        need += total;
+    }
+    int found = 0;
+    for (int64_t c = 0; c < a.n_pages; c += kScan) {
+        const int64_t p = c + threadIdx.x;
+        const int is = p < a.n_pages && a.refs[p] == 0;
+        int total;
+        const int before = scan_wg(is, &total, lds);
+        if (is && found + before < need) free_list[found + before] = static_cast<int32_t>(p);
+        found += total;
+    }
+    if (threadIdx.x == 0) {
+        counts[0] = need;
+        counts[1] = found;
+    }
+}
+
+// Copies n 16-byte words with the workgroup.
+__device__ __forceinline__ void copy_words(const uint4v* from, uint4v* to, int64_t n) {
+    for (int64_t i = threadIdx.x; i < n; i += 256) to[i] = from[i];
+}
+
+// blockIdx.y = 0: row i of the new table; above: the row's copy, one layer each.
+__global__ void __launch_bounds__(256) update_write(const CacheUpdateArgs a, const int32_t* base, const int32_t* copies,
+                                                    const int32_t* free_list, const int32_t* counts) {
+    const int found = counts[1];
+    for (int i = blockIdx.x; i < a.new_rows; i += gridDim.x) {
+        const Kept k = kept_of(a, i);
+        const int at = base[i], copy = copies[i];
+        const int own = copy ? (at < found ? free_list[at] : -1) : -1;
+        if (blockIdx.y > 0) {
+            const int src = copy ? page_in(k.row[k.last], a.n_pages) : -1;
+            if (own < 0 || src < 0) continue;
+            for (int64_t l = blockIdx.y - 1; l < a.layers; l += gridDim.y - 1) {
+                uint8_t* layer = a.pool + l * a.n_pages * a.page_bytes;
+                copy_words(reinterpret_cast<const uint4v*>(layer + src * a.page_bytes),
+                           reinterpret_cast<uint4v*>(layer + own * a.page_bytes), a.page_bytes / 16);
+            }
+            continue;
+        }
+        int32_t* row = a.new_table + static_cast<int64_t>(i) * a.max_pages;
+        for (int j = threadIdx.x; j < a.max_pages; j += 256) {
+            int p = -1;
+            if (j < k.kept) {
+                p = page_in(k.row[j], a.n_pages);
+                if (copy && j == k.last) {
+                    atomicAdd(a.refs + p, -1);   // copy: p is a page
+                    p = own;
+                    if (p >= 0) a.refs[p] = 1;
+                }
+            } else if (j < k.held) {
+                const int64_t f = static_cast<int64_t>(at) + copy + j - k.kept;
+                p = f < found ? free_list[f] : -1;
+                if (p >= 0) a.refs[p] = 1;
+            }
+            row[j] = p;
+        }
+        if (threadIdx.x == 0) a.new_lens[i] = k.after;
+    }
+}
+
+// status: in use = inherited pages (all but the free ones) + those handed out
+__global__ void __launch_bounds__(kScan) update_status(const CacheUpdateArgs a, const int32_t* base, const int32_t* copies,
+                                                       const int32_t* counts) {
+    __shared__ int lds[kScan / 64];
+    const int need = counts[0], found = counts[1];
+    int done = 0;
+    for (int i = threadIdx.x; i < a.new_rows; i += kScan) done += copies[i] && base[i] < found;
+    int total;
+    scan_wg(done, &total, lds);
+    if (threadIdx.x == 0) {
+        const int given = min(need, found);
+        const int used = static_cast<int>(a.n_pages) - found + given;
+        a.status[0] = used;
+        a.status[1] = need - given;
+        a.status[2] = total;
+        a.status[3] = static_cast<int>(a.n_pages) - used;
+    }
+}
+
+__device__ __forceinline__ int held_pages(const CacheCompactArgs& a, int i) {
+    const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page;
+    const int64_t len = min(static_cast<int64_t>(max(a.lens[i], 0)), cap);
+    return static_cast<int>((len + a.page - 1) / a.page);
+}
+
+// counts[p]: entries of the table that hold page p
+__global__ void __launch_bounds__(256) compact_count(const CacheCompactArgs a, int32_t* counts) {
+    for (int i = blockIdx.x; i < a.rows; i += gridDim.x) {
+        const int held = held_pages(a, i);
+        const int32_t* row = a.table + static_cast<int64_t>(i) * a.max_pages;
+        for (int j = threadIdx.x; j < held; j += 256) {
+            const int p = page_in(row[j], a.n_pages);
+            if (p >= 0) atomicAdd(counts + p, 1);
+        }
+    }
+}
+
+// to[p]: the new place of page p, or -1.  Within the pool also the list of
+// holes (places below the number of live pages that are free), ascending.
+__global__ void __launch_bounds__(kScan) compact_plan(const CacheCompactArgs a, const int32_t* counts, int32_t* to,
+                                                      int32_t* holes) {
+    __shared__ int lds[kScan / 64];
+    int live = 0;
+    for (int64_t p = threadIdx.x; p < a.n_pages; p += kScan) live += counts[p] > 0;
+    int total;
+    scan_wg(live, &total, lds);
+    live = total;
+    int rank = 0, moved = 0, free = 0;
+    if (!a.into) {
+        for (int64_t c = 0; c < live; c += kScan) {
+            const int64_t p = c + threadIdx.x;
+            const int is = p < live && counts[p] == 0;
+            const int before = scan_wg(is, &total, lds);
+            if (is) holes[free + before] = static_cast<int32_t>(p);
+            free += total;
+        }
+        __threadfence_block();
+        __syncthreads();
+    }
+    for (int64_t c = 0; c < a.n_pages; c += kScan) {
+        const int64_t p = c + threadIdx.x;
+        const bool is = p < a.n_pages && counts[p] > 0;
+        const bool counted = is && (a.into || p >= live);
+        const int before = scan_wg(counted, &total, lds);
+        if (p < a.n_pages) {
+            int t = -1;
+            if (is && a.into) t = rank + before < a.into_pages ? rank + before : -1;
+            else if (is) t = p < live ? static_cast<int>(p) : holes[rank + before];
+            to[p] = t;
+        }
+        rank += total;
+    }
+    moved = a.into ? static_cast<int>(min(static_cast<int64_t>(rank), a.into_pages)) : rank;
+    if (threadIdx.x == 0) {
+        const int placed = a.into ? moved : live;
+        a.status[0] = live;
+        a.status[1] = live - placed;
+        a.status[2] = moved;
+        a.status[3] = static_cast<int>(a.into_pages) - placed;
+    }
+}
+
+// The new table (blockIdx.y = 0), the counts in the new places (1) and the pages
+// themselves (2 and above: a layer each).
+__global__ void __launch_bounds__(256) compact_write(const CacheCompactArgs a, const int32_t* counts, const int32_t* to) {
+    if (blockIdx.y == 0) {
+        for (int i = blockIdx.x; i < a.rows; i += gridDim.x) {
+            const int held = held_pages(a, i);
+            const int64_t at = static_cast<int64_t>(i) * a.max_pages;
+            for (int j = threadIdx.x; j < a.max_pages; j += 256) {
+                const int p = j < held ? page_in(a.table[at + j], a.n_pages) : -1;
+                a.new_table[at + j] = p < 0 ? -1 : to[p];
+            }
+        }
+        return;
+    }
+    if (blockIdx.y == 1) {
+        for (int64_t p = blockIdx.x * 256 + threadIdx.x; p < a.n_pages; p += static_cast<int64_t>(gridDim.x) * 256)
+            if (to[p] >= 0) a.refs[to[p]] = counts[p];
+        return;
+    }
+    for (int64_t p = blockIdx.x; p < a.n_pages; p += gridDim.x) {
+        const int t = to[p];
+        if (t < 0 || (!a.into && t == p)) continue;
+        for (int64_t l = blockIdx.y - 2; l < a.layers; l += gridDim.y - 2) {
+            const uint8_t* from = a.pool + (l * a.n_pages + p) * a.page_bytes;
+            uint8_t* dst = (a.into ? a.into + l * a.into_pages * a.page_bytes : a.pool + l * a.n_pages * a.page_bytes) +
+                           t * a.page_bytes;
+            copy_words(reinterpret_cast<const uint4v*>(from), reinterpret_cast<uint4v*>(dst), a.page_bytes / 16);
+        }
+    }
+}
+
+int fill(int32_t* p, int64_t n, int32_t v, hipStream_t s) {
+    const int64_t grid = (n + 255) / 256;
+    hipLaunchKernelGGL(fill_words, dim3(static_cast<uint32_t>(grid < 1024 ? grid : 1024)), dim3(256), 0, s, p, n, v);
+    return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace
+
+int launch_cache_append(const CacheAppendArgs& a, int bf16, void* stream) {
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return bf16 ? append_dim<uint16_t>(a, s) : append_dim<float>(a, s);
+}
+
+int launch_cache_update(const CacheUpdateArgs& a, void* stream) {
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    int32_t* writers = a.work;
+    int32_t* lowest = writers + a.n_pages;
+    int32_t* free_list = lowest + a.n_pages;
+    int32_t* base = free_list + a.n_pages;
+    int32_t* copies = base + a.new_rows;
+    int32_t* counts = copies + a.new_rows;
+    int e;
+    if ((e = fill(a.refs, a.n_pages, 0, s)) || (e = fill(writers, a.n_pages, 0, s)) ||
+        (e = fill(lowest, a.n_pages, 0x7FFFFFFF, s)))
+        return e;
+    const uint32_t rows = static_cast<uint32_t>(a.new_rows < 65536 ? (a.new_rows > 0 ? a.new_rows : 1) : 65536);
+    hipLaunchKernelGGL(update_count, dim3(rows), dim3(256), 0, s, a, writers, lowest);
+    hipLaunchKernelGGL(update_plan, dim3(1), dim3(kScan), 0, s, a, writers, lowest, base, copies, free_list, counts);
+    hipLaunchKernelGGL(update_write, dim3(rows, static_cast<uint32_t>(a.layers < 1024 ? a.layers : 1024) + 1), dim3(256), 0, s, a,
+                       base, copies, free_list, counts);
+    hipLaunchKernelGGL(update_status, dim3(1), dim3(kScan), 0, s, a, base, copies, counts);
+    return static_cast<int>(hipGetLastError());
+}
+
+int launch_cache_compact(const CacheCompactArgs& a, void* stream) {
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    int32_t* counts = a.work;
+    int32_t* to = counts + a.n_pages;
+    int32_t* holes = to + a.n_pages;
+    int e;
+    if ((e = fill(counts, a.n_pages, 0, s)) || (e = fill(a.refs, a.into_pages, 0, s))) return e;
+    const uint32_t rows = static_cast<uint32_t>(a.rows < 65536 ? (a.rows > 0 ? a.rows : 1) : 65536);
+    hipLaunchKernelGGL(compact_count, dim3(rows), dim3(256), 0, s, a, counts);
+    hipLaunchKernelGGL(compact_plan, dim3(1), dim3(kScan), 0, s, a, counts, to, holes);
+    const uint32_t pages = static_cast<uint32_t>(a.n_pages < 4096 ? a.n_pages : 4096);
+    hipLaunchKernelGGL(compact_write, dim3(pages, static_cast<uint32_t>(a.layers < 1024 ? a.layers : 1024) + 2), dim3(256), 0, s, a,
+                       counts, to);
+    return static_cast<int>(hipGetLastError());
+}
+
+}  // namespace hr
