@@ -103,8 +103,8 @@ int check_spec(const hr_cache_spec* s, hr::CachePage* p) {
     p->vc = static_cast<int32_t>(codes);
     p->ks = static_cast<int32_t>(2 * codes);
     p->vs = static_cast<int32_t>(2 * codes + scales);
-    p->kz = static_cast<int32_t>(2 * codes + 2 * scales);
-    p->vz = static_cast<int32_t>(2 * codes + 2 * scales + zeros);
+    p->kz = p->sym ? 0 : static_cast<int32_t>(2 * codes + 2 * scales);
+    p->vz = p->sym ? 0 : static_cast<int32_t>(2 * codes + 2 * scales + zeros);
     p->head_bytes = up(2 * (codes + scales + zeros), 128);
     p->page_bytes = p->head_bytes * p->hkv;
     return HR_OK;
@@ -248,8 +248,8 @@ int hr_cache_page_layout(const hr_cache_spec* spec, hr_cache_page* out) {
     out->v_codes = p.vc;
     out->k_scales = p.ks;
     out->v_scales = p.vs;
-    out->k_zeros = p.sym ? 0 : p.kz;
-    out->v_zeros = p.sym ? 0 : p.vz;
+    out->k_zeros = p.kz;
+    out->v_zeros = p.vz;
     return ok();
 }
 

@@ -3,12 +3,14 @@
 //
 // Mathematics.  With a key k = s (c - z) (codes c, zero point z, scale s of
 // its group) a score is q . k = sum over groups of s (q . c - z sum(q)): the
-// matrix product runs over the integer codes, and scale and zero point are
-// applied to its 16 x 16 results.  The softmax is taken in one pass: a running
-// maximum m, l = sum exp(w - m) and o = sum exp(w - m) v, rescaled when m
-// grows.  With one group per vector the value's scale multiplies the
-// probability, so that o is a matrix product over the integers c - z too;
-// with several groups it multiplies the values.
+// matrix product runs over the integer codes, with one more step for
+// z . -sum(q), and s is applied to its 16 x 16 results.  The softmax is taken
+// in one pass: a running maximum m, l = sum exp(w - m) and o = sum exp(w - m) v.
+// m only has to keep the exponentials in range, so it moves when one passes
+// 2^kSlack, and everything is rescaled then: the test is on the exponentials
+// themselves, and scores are not formed otherwise.  With one group per vector
+// the value's scale multiplies the probability, so that o is a matrix product
+// over the integers c - z too; with several groups it multiplies the values.
 //
 // Layout.  No tile is staged: a wave turns the packed codes it has loaded into
 // operands of v_mfma_f32_16x16x32_f16 in its registers.
@@ -79,14 +81,44 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 __device__ __forceinline__ float lo_f32(uint32_t h) { return static_cast<float>(__builtin_bit_cast(half2v, h).x); }
 __device__ __forceinline__ float hi_f32(uint32_t h) { return static_cast<float>(__builtin_bit_cast(half2v, h).y); }
 
-// sum and maximum over the four lane groups of a query (lanes l, l + 16, ...)
-__device__ __forceinline__ float sum_groups(float v) {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+// The value of lane ^ X inside 32 lanes: a swizzle, whose pattern is in the
+// instruction (a general shuffle would hold its addresses in registers).
+template <int X>
+__device__ __forceinline__ uint32_t swizzle_xor(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_ds_swizzle(static_cast<int>(v), (X << 10) | 0x1F));
 }
-__device__ __forceinline__ float max_groups(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
+template <int X>
+__device__ __forceinline__ float swizzle_xor(float v) {
+    return __uint_as_float(swizzle_xor<X>(__float_as_uint(v)));
+}
+// f over the values of lanes l and l + 32, and over those of rows of 16 lanes
+// 2 i and 2 i + 1: one register exchange each
+template <class F>
+__device__ __forceinline__ float over_halves(float v, F f) {
+    const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return f(__uint_as_float(x[0]), __uint_as_float(x[1]));
+}
+template <class F>
+__device__ __forceinline__ float over_rows(float v, F f) {
+    const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return f(__uint_as_float(x[0]), __uint_as_float(x[1]));
+}
+struct Sum {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct Max {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+// over the four lane groups of a query (lanes l, l + 16, ...)
+__device__ __forceinline__ float sum_groups(float v) { return over_halves(over_rows(v, Sum()), Sum()); }
+__device__ __forceinline__ float max_groups(float v) { return over_halves(over_rows(v, Max()), Max()); }
+// over the wave
+__device__ __forceinline__ float max_wave(float v) {
+    v = fmaxf(v, swizzle_xor<1>(v));
+    v = fmaxf(v, swizzle_xor<2>(v));
+    v = fmaxf(v, swizzle_xor<4>(v));
+    v = fmaxf(v, swizzle_xor<8>(v));
+    return max_groups(v);
 }
 
 // bf16 (finite or not) from float32, nearest even, NaN kept
@@ -96,25 +128,41 @@ __device__ __forceinline__ uint32_t to_bf16(float f) {
     return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
 
+// The phases of a step stay in order: left alone, the scheduler forms all
+// operands of a step at once, and spills.
+#define HR_PHASE() __builtin_amdgcn_sched_barrier(0)
+
 constexpr float kLow = -3.0e38f;      // running maximum of nothing
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPExp = 9;              // probabilities are at most 2^kSlack and carry 2^kPExp in float16
-constexpr float kSlack = 6.0f;        // how far (log2) a score may pass the running maximum before it moves
+constexpr int kSlack = 6;             // how far (log2) a score may pass the running maximum before it moves
 constexpr int kSExp = 8;              // value scales (several groups) carry 2^kSExp
 
-// A sequence of the call, clamped so that nothing leaves its buffer.
+// Integers read at an address that is the same in all lanes: through the scalar
+// cache, into scalar registers.
+typedef const int32_t __attribute__((address_space(4)))* ConstInts;
+
+// A sequence of the call, clamped so that nothing leaves its buffer.  UNI: b is
+// the same in all lanes.
 struct Seq {
     int start, n, len;
 };
+template <bool UNI>
+__device__ __forceinline__ int int_at(const int32_t* p, int64_t i) {
+    if constexpr (UNI) return ((ConstInts)(p))[i];
+    return p[i];
+}
+template <bool UNI>
 __device__ __forceinline__ int cu_at(const CacheSeqs& s, int b) {
-    const int c = s.cu ? s.cu[b] : b * s.per;
+    const int c = s.cu ? int_at<UNI>(s.cu, b) : b * s.per;
     return min(max(c, 0), s.tokens);
 }
+template <bool UNI>
 __device__ __forceinline__ Seq seq_at(const CacheSeqs& s, int logp, int b) {
     Seq r;
-    r.start = cu_at(s, b);
-    r.n = max(cu_at(s, b + 1) - r.start, 0);
-    r.len = min(max(s.lens[b], 0), s.max_pages << logp);
+    r.start = cu_at<UNI>(s, b);
+    r.n = max(cu_at<UNI>(s, b + 1) - r.start, 0);
+    r.len = min(max(int_at<UNI>(s.lens, b), 0), s.max_pages << logp);
     return r;
 }
 
@@ -145,8 +193,7 @@ struct Cfg {
     static constexpr int KEYS = 32 * WT;           // keys of an item
     static constexpr int ES = SF32 ? 4 : 2;
     static constexpr int KSW = NG * ES;            // 32-bit words of four positions' scales
-    static constexpr int ZW = (NG + 1) / 2;        // 32-bit words of four positions' zero points (one group: 16 bits)
-    static constexpr int VSN = NG == 1 ? KSW : 8;  // words of value scales per 16 (one group) or 32 keys
+    static constexpr int WAVES = RT == 1 && !WIDE && D <= 128 ? 3 : 2;  // waves per SIMD
     static constexpr int P = WIDE ? 2 : 1;         // float16 terms of an operand
     static constexpr bool SUBK = !WIDE;            // subnormal codes of K
     static constexpr bool SUBV = !WIDE && NG == 1; // and of V
@@ -157,11 +204,10 @@ template <class C>
 struct Raw {
     uint32_t k[2][C::KS];
     uint32_t ks[2][C::KSW];
-    uint32_t kz[2][C::ZW];
+    uint32_t kz[2];          // zero points of key m, a nibble for each group
     uint32_t v[8][C::VW];
     uint32_t vs[C::NG == 1 ? 2 : 8][C::NG == 1 ? C::KSW : 1];
     uint32_t vz[C::NG == 1 ? 2 : 8];
-    int here;   // bit a: subtile a's page is present
 };
 
 template <int N>
@@ -184,55 +230,107 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
     }
 }
 
-// Loads 32 keys from t0 (a multiple of 16).  Pages outside the pool are
-// read as page 0 and marked absent; t0 is below the table's last position.
+// The pages of the 16-key subtiles at t0 and t0 + 16 (uniform over the wave; t0
+// a multiple of 16), out of range where absent.  A constant-address load, so
+// that it goes through the scalar cache and leaves the vector loads' count.
+struct Pages {
+    int p[2];
+};
+__device__ __forceinline__ Pages pages_at(const CacheAttnArgs& a, const int32_t* table, int t0) {
+    const ConstInts tab = (ConstInts)(table);
+    Pages r;
+    const int last = a.sq.max_pages - 1;
+    r.p[0] = tab[min(t0 >> a.pg.logp, last)];
+    r.p[1] = tab[min((t0 + 16) >> a.pg.logp, last)];
+    return r;
+}
+__device__ __forceinline__ bool present(const CacheAttnArgs& a, int page) {
+    return static_cast<uint32_t>(page) < static_cast<uint64_t>(a.sq.n_pages);
+}
+
+// The value of a lane offset as it stands here: sums with constants formed from
+// it stay beside their load, as its immediate offset, instead of each holding
+// a register throughout the loop.
+#define HR_KEEP(v) asm volatile("" : "+v"(v))
+
+// N words (or 1 or 2 bytes) from a buffer: a descriptor and an offset that are
+// the same in all lanes, plus the lane's offset.
+template <int N>
+__device__ __forceinline__ void buffer_words(__amdgpu_buffer_rsrc_t r, int lane_at, int at, uint32_t* w) {
+    if constexpr (N == 1) {
+        w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, lane_at, at, 0);
+    } else if constexpr (N == 2) {
+        const uint2v x = __builtin_bit_cast(uint2v, __builtin_amdgcn_raw_buffer_load_b64(r, lane_at, at, 0));
+        w[0] = x.x;
+        w[1] = x.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4v x = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(r, lane_at + 4 * i, at, 0));
+            w[i] = x.x;
+            w[i + 1] = x.y;
+            w[i + 2] = x.z;
+            w[i + 3] = x.w;
+        }
+    }
+}
+__device__ __forceinline__ uint32_t buffer_u16(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
+    return static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, lane_at, at, 0));
+}
+__device__ __forceinline__ uint32_t buffer_u8(__amdgpu_buffer_rsrc_t r, int lane_at, int at) {
+    return static_cast<uint8_t>(__builtin_amdgcn_raw_buffer_load_b8(r, lane_at, at, 0));
+}
+
+// Loads 32 keys from t0.  The buffer is a head's part of a page; an absent
+// page's has no bytes, so that its loads give zeros.
 template <class C>
-__device__ __forceinline__ void load_keys(const CacheAttnArgs& a, const int32_t* table, int h, int t0, Raw<C>& w) {
+__device__ __forceinline__ void load_keys(const CacheAttnArgs& a, const Pages& pages, int h, int t0, Raw<C>& w) {
     constexpr int D = C::D, NG = C::NG;
     const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
-    w.here = 0;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const int t = t0 + 16 * s;
-        const int slot = min(t >> a.pg.logp, a.sq.max_pages - 1);
-        int page = table[slot];
-        if (static_cast<uint32_t>(page) < static_cast<uint64_t>(a.sq.n_pages)) w.here |= 1 << s;
-        else page = 0;
-        const uint8_t* base = a.pool + page * a.pg.page_bytes + h * a.pg.head_bytes;
-        const int off = t & (a.pg.page - 1);
+        const bool here = present(a, pages.p[s]);
+        const int off = (t0 + 16 * s) & (a.pg.page - 1);
+        const uint8_t* base = a.pool + (here ? pages.p[s] : 0) * a.pg.page_bytes + h * a.pg.head_bytes;
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t*>(base), 0, here ? static_cast<int>(a.pg.head_bytes) : 0, 0x00020000);
+        const int kc = a.pg.kc + off * (D / 2), vc = a.pg.vc + off * (D / 2);
+        const int ks = a.pg.ks + off * (NG * C::ES), vs = a.pg.vs + off * (NG * C::ES);
+        const int kz = a.pg.kz + off * NG / 2, vz = a.pg.vz + off * NG / 2;
         // keys: a lane holds D/4 dimensions of key m, one run with one group,
         // eight of every 32 with several (a matrix step is then one group's)
-        const uint8_t* kp = base + a.pg.kc + (off + m) * (D / 2);
+        int kl = m * (D / 2) + g * (NG == 1 ? D / 8 : 4);
+        HR_KEEP(kl);
         if constexpr (NG == 1) {
-            load_words<C::KS>(kp + g * (D / 8), w.k[s]);
+            buffer_words<C::KS>(r, kl, kc, w.k[s]);
         } else {
 #pragma unroll
-            for (int i = 0; i < C::KS; ++i) load_words<1>(kp + i * 16 + g * 4, &w.k[s][i]);
+            for (int i = 0; i < C::KS; ++i) buffer_words<1>(r, kl + i * 16, kc, &w.k[s][i]);
         }
-        load_words<C::KSW>(base + a.pg.ks + (off + 4 * g) * (NG * C::ES), w.ks[s]);
-        if (!a.pg.sym) {
-            const uint8_t* zp = base + a.pg.kz + (off + 4 * g) * NG / 2;
-            if constexpr (NG == 1) w.kz[s][0] = *reinterpret_cast<const uint16_t*>(zp);
-            else load_words<C::ZW>(zp, w.kz[s]);
-        }
+        buffer_words<C::KSW>(r, 4 * g * NG * C::ES, ks, w.ks[s]);
+        if constexpr (NG == 1) w.kz[s] = buffer_u8(r, m / 2, kz);
+        else if constexpr (NG == 2) w.kz[s] = buffer_u8(r, m, kz);
+        else if constexpr (NG == 4) w.kz[s] = buffer_u16(r, 2 * m, kz);
+        else buffer_words<1>(r, 4 * m, kz, &w.kz[s]);
         // values: D/16 dimensions of keys 4g + r
-        const uint8_t* vp = base + a.pg.vc + (off + 4 * g) * (D / 2) + m * (D / 32);
+        int vl = 4 * g * (D / 2) + m * (D / 32);
+        HR_KEEP(vl);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            if constexpr (D == 64) w.v[4 * s + r][0] = *reinterpret_cast<const uint16_t*>(vp + r * (D / 2));
-            else load_words<C::VW>(vp + r * (D / 2), w.v[4 * s + r]);
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (D == 64) w.v[4 * s + i][0] = buffer_u16(r, vl + i * (D / 2), vc);
+            else buffer_words<C::VW>(r, vl + i * (D / 2), vc, w.v[4 * s + i]);
         }
         if constexpr (NG == 1) {
-            load_words<C::KSW>(base + a.pg.vs + (off + 4 * g) * C::ES, w.vs[s]);
-            if (!a.pg.sym) w.vz[s] = *reinterpret_cast<const uint16_t*>(base + a.pg.vz + (off + 4 * g) / 2);
+            buffer_words<C::KSW>(r, 4 * g * C::ES, vs, w.vs[s]);
+            w.vz[s] = buffer_u16(r, 2 * g, vz);
         } else {
-            const int gi = m / (16 / NG);  // the lane's group
+            int at = 4 * g * NG + m / (16 / NG);  // the lane's group of key 4g
+            HR_KEEP(at);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int at = (off + 4 * g + r) * NG + gi;
-                if constexpr (C::SF32) w.vs[4 * s + r][0] = *reinterpret_cast<const uint32_t*>(base + a.pg.vs + 4 * at);
-                else w.vs[4 * s + r][0] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(base + a.pg.vs + 2 * at)) << 16;
-                if (!a.pg.sym) w.vz[4 * s + r] = (base[a.pg.vz + at / 2] >> (4 * (at & 1))) & 15u;
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (C::SF32) buffer_words<1>(r, 4 * at + 4 * i * NG, vs, w.vs[4 * s + i]);
+                else w.vs[4 * s + i][0] = buffer_u16(r, 2 * at + 2 * i * NG, vs);
+                w.vz[4 * s + i] = buffer_u8(r, at / 2 + i * (NG / 2), vz);
             }
         }
     }
@@ -245,24 +343,39 @@ __device__ __forceinline__ float scale_at(const uint32_t* w, int i) {
     return __uint_as_float((i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
 }
 
+// Symmetric codes are two's complement nibbles: flipping the top bit gives
+// c + 8 with zero point 8.  Where there is no section of zero points the loads
+// above read codes instead (offset 0), and are masked away here.
+struct Zeros {
+    uint32_t flip;         // 8 in both halves, or 0
+    uint32_t mask, fixed;  // zero point = (what was read & mask) | fixed, in both halves
+};
+__device__ __forceinline__ Zeros zeros_of(const CacheAttnArgs& a) {
+    Zeros z;
+    z.flip = a.pg.sym ? 0x00080008u : 0u;
+    z.mask = a.pg.sym ? 0u : 0x000F000Fu;
+    z.fixed = z.flip;
+    return z;
+}
+
 // Four operand words of eight codes: (0,4) (1,5) (2,6) (3,7).  Subnormal: in
-// units of 2^-24, the second and fourth word with a factor of 16.
+// units of 2^-24, the second and fourth word with a factor of 16.  Ordinary
+// numbers: less the zero point, z0 = its float16 1024 + z twice, z1 = 64 + z.
 template <bool SUB>
-__device__ __forceinline__ uint4v code_operand(uint32_t w) {
+__device__ __forceinline__ uint4v code_operand(uint32_t w, uint32_t flip, uint32_t z0, uint32_t z1) {
+    const uint32_t f0 = SUB ? flip : flip | 0x64006400u, f1 = SUB ? flip << 4 : flip << 4 | 0x54005400u;
     uint4v f;
-    if constexpr (!SUB) {
-        f.x = pk_sub((w & 0x000F000Fu) | 0x64006400u, 0x64006400u);
-        f.y = pk_sub((w & 0x00F000F0u) | 0x54005400u, 0x54005400u);
-        w >>= 8;
-        f.z = pk_sub((w & 0x000F000Fu) | 0x64006400u, 0x64006400u);
-        f.w = pk_sub((w & 0x00F000F0u) | 0x54005400u, 0x54005400u);
-        return f;
-    }
-    f.x = w & 0x000F000Fu;
-    f.y = w & 0x00F000F0u;
+    f.x = (w & 0x000F000Fu) ^ f0;
+    f.y = (w & 0x00F000F0u) ^ f1;
     w >>= 8;
-    f.z = w & 0x000F000Fu;
-    f.w = w & 0x00F000F0u;
+    f.z = (w & 0x000F000Fu) ^ f0;
+    f.w = (w & 0x00F000F0u) ^ f1;
+    if constexpr (!SUB) {
+        f.x = pk_sub(f.x, z0);
+        f.y = pk_sub(f.y, z1);
+        f.z = pk_sub(f.z, z0);
+        f.w = pk_sub(f.w, z1);
+    }
     return f;
 }
 
@@ -270,11 +383,10 @@ __device__ __forceinline__ uint4v code_operand(uint32_t w) {
 template <class C>
 struct Rows {
     uint4v q[C::RT][C::P][C::KS];
-    float qsum[C::RT][C::NG];   // sum of a group's queries (as float16), over the whole vector, in raw units
-    float c[C::RT];             // log2 units of one unit of a raw score
-    float slack[C::RT];         // kSlack in raw units
+    uint4v qz[C::RT][C::SUBK ? C::NG : 1];  // -sum(q) of a group as an operand (subnormal codes)
+    float c;                    // log2 units of one raw score unit
     int lim[C::RT], lo[C::RT];  // keys [lo, lim) are seen
-    float m[C::RT], mc[C::RT];  // running maximum, raw and in log2 units
+    float mc[C::RT];            // running maximum, log2 units
     float l[C::RT];             // sum of exponentials (this lane's keys)
     float4v o[C::RT][C::DT];
     int e;                      // exponent of the value scales in o
@@ -283,9 +395,11 @@ struct Rows {
 // Loads rows r0 + 16 rt + (lane & 15) of kv head h, rotates them and makes
 // them operands.  Rows past the sequence's repeat its last one.
 template <class C, class T>
-__device__ void load_rows(const CacheAttnArgs& a, const Seq& s, int h, int r0, Rows<C>& w) {
+__device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, int h, int r0, Rows<C>& w) {
     constexpr int D = C::D, N = D / 4;
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    float v[C::RT][N];
+    float top = 0.0f;
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt) {
         const int row = min(r0 + 16 * rt + n, s.n * a.rep - 1);
@@ -295,7 +409,6 @@ __device__ void load_rows(const CacheAttnArgs& a, const Seq& s, int h, int r0, R
         const int pos = s.len - s.n + tok;
         w.lim[rt] = a.causal ? min(pos + 1, s.len) : s.len;
         w.lo[rt] = a.window ? pos - a.window + 1 : 0;
-        float v[N];
 #pragma unroll
         for (int i = 0; i < N / 8; ++i) {
             const int at = C::NG == 1 ? g * N + i * 8 : i * 32 + g * 8;
@@ -304,14 +417,14 @@ __device__ void load_rows(const CacheAttnArgs& a, const Seq& s, int h, int r0, R
                 load_words<4>(reinterpret_cast<const uint8_t*>(p + at), x);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    v[8 * i + 2 * j] = __uint_as_float(x[j] << 16);
-                    v[8 * i + 2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+                    v[rt][8 * i + 2 * j] = __uint_as_float(x[j] << 16);
+                    v[rt][8 * i + 2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
                 }
             } else {
                 uint32_t x[8];
                 load_words<8>(reinterpret_cast<const uint8_t*>(p + at), x);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[8 * i + j] = __uint_as_float(x[j]);
+                for (int j = 0; j < 8; ++j) v[rt][8 * i + j] = __uint_as_float(x[j]);
             }
         }
         if (a.rotate) {
@@ -322,31 +435,34 @@ __device__ void load_rows(const CacheAttnArgs& a, const Seq& s, int h, int r0, R
 #pragma unroll
                 for (int j = 0; j < N; ++j)
                     if (!(j & st)) {
-                        const float x = v[j], y = v[j + st];
-                        v[j] = x + y;
-                        v[j + st] = x - y;
+                        const float x = v[rt][j], y = v[rt][j + st];
+                        v[rt][j] = x + y;
+                        v[rt][j + st] = x - y;
                     }
+            // (+ in the lower of two lanes, lower - upper in the other)
+            const uint32_t s0 = (lane & 16) << 27, s1 = (lane & 32) << 26;
+            const auto diff0 = [s0](float x, float y) { return x + __uint_as_float(__float_as_uint(y) ^ s0); };
+            const auto diff1 = [s1](float x, float y) { return x + __uint_as_float(__float_as_uint(y) ^ s1); };
 #pragma unroll
-            for (int st = 16; st < 64; st *= 2)
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const float y = __shfl_xor(v[j], st);
-                    v[j] = (lane & st) ? y - v[j] : v[j] + y;
-                }
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[j] *= a.norm;
+            for (int j = 0; j < N; ++j) v[rt][j] = over_halves(over_rows(v[rt][j], diff0), diff1) * a.norm;
         }
-        float top = 0.0f;
+        // (a row of infinities or NaN scales nothing: it gives NaN all the same)
+        float own = 0.0f;
 #pragma unroll
-        for (int j = 0; j < N; ++j) top = fmaxf(top, fabsf(v[j]));
-        top = max_groups(top);
-        // the largest element at 2^10 .. 2^11 of float16; rows of infinities
-        // keep their exponent (they give NaN all the same)
-        int e = 0;
-        if (top > 0.0f && top < __builtin_inff()) e = min(max(11 - (static_cast<int>(__float_as_uint(top) >> 23) - 126), -100), 100);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        w.c[rt] = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + (C::SUBK ? 24 : 0) - e) << 23);
-        w.slack[rt] = kSlack / w.c[rt];
+        for (int j = 0; j < N; ++j) own = fmaxf(own, fabsf(v[rt][j]));
+        if (own < __builtin_inff()) top = fmaxf(top, own);
+    }
+    // one power of two for all rows of the wave puts the largest element at
+    // 2^5 .. 2^6 (a group's sum then stays in float16's range); an element
+    // 2^-20 of it still has all eleven bits, one of 2^-30 still one
+    top = max_wave(top);
+    int e = 0;
+    if (top > 0.0f) e = min(max(6 - (static_cast<int>(__float_as_uint(top) >> 23) - 126), -100), 100);
+    e = __builtin_amdgcn_readfirstlane(e);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    w.c = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + (C::SUBK ? 24 : 0) - e) << 23);
+#pragma unroll
+    for (int rt = 0; rt < C::RT; ++rt) {
         float sum[C::NG];
 #pragma unroll
         for (int i = 0; i < C::NG; ++i) sum[i] = 0.0f;
@@ -360,21 +476,27 @@ __device__ void load_rows(const CacheAttnArgs& a, const Seq& s, int h, int r0, R
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float f = C::SUBK && (j & 1) ? up * 0.0625f : up;
-                const float x = v[8 * i + j] * f, y = v[8 * i + j + 4] * f;
+                const float x = v[rt][8 * i + j] * f, y = v[rt][8 * i + j + 4] * f;
                 hi[j] = pack_f16(x, y);
-                float back = lo_f32(hi[j]) + hi_f32(hi[j]);
-                if constexpr (C::WIDE) {
-                    lo[j] = pack_f16(x - lo_f32(hi[j]), y - hi_f32(hi[j]));
-                    back += lo_f32(lo[j]) + hi_f32(lo[j]);
+                if constexpr (C::WIDE) lo[j] = pack_f16(x - lo_f32(hi[j]), y - hi_f32(hi[j]));
+                if constexpr (C::SUBK) {
+                    const float back = lo_f32(hi[j]) + hi_f32(hi[j]);
+                    sum[C::NG == 1 ? 0 : i / C::KG] += (j & 1) ? back * 16.0f : back;
                 }
-                sum[C::NG == 1 ? 0 : i / C::KG] += C::SUBK && (j & 1) ? back * 16.0f : back;
             }
             w.q[rt][0][i] = uint4v{hi[0], hi[1], hi[2], hi[3]};
             if constexpr (C::WIDE) w.q[rt][1][i] = uint4v{lo[0], lo[1], lo[2], lo[3]};
         }
+        if constexpr (C::SUBK) {
+            // the zero point's operand has z in k slots 0 and 1 of lane group
+            // 0: -sum(q) there as two float16
 #pragma unroll
-        for (int i = 0; i < C::NG; ++i) w.qsum[rt][i] = sum_groups(sum[i]) * (C::SUBK ? 0x1p-24f : 1.0f);
-        w.m[rt] = kLow;
+            for (int i = 0; i < C::NG; ++i) {
+                const float t = -sum_groups(sum[i]);
+                const uint32_t hi = pack_f16(t, 0.0f);
+                w.qz[rt][i] = uint4v{g == 0 ? (hi & 0xFFFFu) | (pack_f16(t - lo_f32(hi), 0.0f) << 16) : 0u, 0u, 0u, 0u};
+            }
+        }
         w.mc[rt] = kLow;
         w.l[rt] = 0.0f;
 #pragma unroll
@@ -383,34 +505,35 @@ __device__ void load_rows(const CacheAttnArgs& a, const Seq& s, int h, int r0, R
     w.e = -100;
 }
 
-// One step over 32 keys.  MASK: some of them are not seen by every row.
-template <class C, bool MASK>
-__device__ __forceinline__ void step(const CacheAttnArgs& a, Raw<C>& w, int t0, Rows<C>& st) {
+// Raw scores of 32 keys, in log2 units once multiplied by mul:
+// x[rt][4 s + r] is key 16 s + 4 g + r.
+template <class C>
+__device__ __forceinline__ void scores(const Zeros& zs, const Raw<C>& w, const Rows<C>& st, float (&x)[C::RT][8],
+                                       float (&mul)[8]) {
     constexpr int NG = C::NG, RT = C::RT;
-    const int lane = threadIdx.x & 63, g = lane >> 4;
-    const bool sym = a.pg.sym;
-    if (sym) {  // two's complement nibbles: c + 8, zero point 8
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int i = 0; i < C::KS; ++i) w.k[s][i] ^= 0x88888888u;
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int i = 0; i < C::VW; ++i) w.v[t][i] ^= 0x88888888u;
-    }
-    // raw scores: sc[rt][4 s + r] of key t0 + 16 s + 4 g + r
-    float sc[RT][8];
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
         for (int gi = 0; gi < NG; ++gi) {
+            HR_PHASE();
+            // zero point of key m, in the low and in the second nibble
+            const uint32_t z = NG == 1 ? w.kz[s] >> (4 * (lane & 1)) : w.kz[s] >> (4 * gi);
             float4v acc[RT];
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) acc[rt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+            uint32_t z0 = (((z << 16) | (z & 0xFFFFu)) & zs.mask) | zs.fixed, z1 = 0;
+            if constexpr (C::SUBK) {
+                const uint4v za = {lane < 16 ? z0 : 0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) acc[rt] = mfma(za, st.qz[rt][gi], acc[rt]);
+            } else {
+                z1 = (z0 << 4) | 0x54005400u;
+                z0 |= 0x64006400u;
+            }
 #pragma unroll
             for (int i = gi * C::KG; i < (gi + 1) * C::KG; ++i) {
-                const uint4v f = code_operand<C::SUBK>(w.k[s][i]);
+                const uint4v f = code_operand<C::SUBK>(w.k[s][i], zs.flip, z0, z1);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     acc[rt] = mfma(f, st.q[rt][0][i], acc[rt]);
@@ -419,132 +542,149 @@ __device__ __forceinline__ void step(const CacheAttnArgs& a, Raw<C>& w, int t0, 
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const float ks = scale_at<C::SF32>(w.ks[s], r * NG + gi);
-                const int nib = r * NG + gi;
-                const float kz = sym ? 8.0f : static_cast<float>((w.kz[s][nib / 8] >> (4 * (nib & 7))) & 15u);
+                const float ks = scale_at<C::SF32>(w.ks[s], r * NG + gi) * st.c;
+                if constexpr (NG == 1) mul[4 * s + r] = ks;
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    const float x = fmaf(-kz, st.qsum[rt][gi], acc[rt][r]);
-                    if constexpr (NG == 1) sc[rt][4 * s + r] = x * ks;
-                    else sc[rt][4 * s + r] = gi == 0 ? x * ks : fmaf(x, ks, sc[rt][4 * s + r]);
+                    if constexpr (NG == 1) x[rt][4 * s + r] = acc[rt][r];
+                    else x[rt][4 * s + r] = gi == 0 ? acc[rt][r] * ks : fmaf(acc[rt][r], ks, x[rt][4 * s + r]);
                 }
             }
         }
     }
-    bool seen[RT][8];
-    if constexpr (MASK) {
+    if constexpr (NG > 1) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = t0 + 16 * s + 4 * g + r;
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    seen[rt][4 * s + r] = ((w.here >> s) & 1) && t < st.lim[rt] && t >= st.lo[rt];
-                    if (!seen[rt][4 * s + r]) sc[rt][4 * s + r] = -__builtin_inff();
-                }
-            }
+        for (int t = 0; t < 8; ++t) mul[t] = 1.0f;
     }
-    // value scales of the lane's keys; those that no row of the wave may see
-    // (past the sequence or on an absent page) are not looked at
+}
+
+// One step of the softmax: x becomes exp2(x mul - mc), moving the running
+// maximum first if one of them would pass 2^kSlack.  (Unseen keys have -inf
+// and a finite mul.)
+template <class C>
+__device__ __forceinline__ void exponentials(Rows<C>& st, int rt, float (&x)[8], const float (&mul)[8]) {
+    float p[8], top = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) p[t] = __builtin_amdgcn_exp2f(fmaf(x[t], mul[t], -st.mc[rt]));
+#pragma unroll
+    for (int t = 0; t < 8; ++t) top = fmaxf(top, p[t]);
+    if (__any(top > static_cast<float>(1 << kSlack))) {
+        top = kLow;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) top = fmaxf(top, x[t] * mul[t]);
+        const float mc = fmaxf(max_groups(top), st.mc[rt]);
+        const float f = exp2f(st.mc[rt] - mc);
+        st.mc[rt] = mc;
+        st.l[rt] *= f;
+#pragma unroll
+        for (int j = 0; j < C::DT; ++j) st.o[rt][j] *= f;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) p[t] = __builtin_amdgcn_exp2f(fmaf(x[t], mul[t], -mc));
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+        st.l[rt] += p[t];
+        x[t] = p[t];
+    }
+}
+
+// Makes the exponent of the value scales in o cover |vs| < 2^e and returns
+// 2^(shift - e), the factor that the scales are taken with.
+template <class C>
+__device__ __forceinline__ float cover_scales(Rows<C>& st, const float (&vs)[8], int shift) {
+    float big = fabsf(vs[0]);
+#pragma unroll
+    for (int t = 1; t < 8; ++t) big = fmaxf(big, fabsf(vs[t]));
+    if (__any(big > __uint_as_float(static_cast<uint32_t>(127 + st.e) << 23))) {
+        // (scales that are not finite say nothing about the range)
+        big = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) big = fmaxf(big, fabsf(vs[t]) < __builtin_inff() ? fabsf(vs[t]) : 0.0f);
+        big = max_wave(big);
+        const int e = __builtin_amdgcn_readfirstlane(max(static_cast<int>(__float_as_uint(big) >> 23) - 126, st.e));
+        const float f = ldexpf(1.0f, st.e - e);
+#pragma unroll
+        for (int rt = 0; rt < C::RT; ++rt)
+#pragma unroll
+            for (int j = 0; j < C::DT; ++j) st.o[rt][j] *= f;
+        st.e = e;
+    }
+    return ldexpf(1.0f, shift - st.e);
+}
+
+// One step over 32 keys; mask: some of them are not seen by every row.
+template <class C>
+__device__ __forceinline__ void step(const CacheAttnArgs& a, const Raw<C>& w, const Pages& pages, bool mask, int t0, Rows<C>& st) {
+    constexpr int NG = C::NG, RT = C::RT;
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    const Zeros zs = zeros_of(a);
+    float x[RT][8], mul[8];
+    scores<C>(zs, w, st, x, mul);
+    HR_PHASE();
     float vs[8];
-    uint32_t nz[8];   // several groups: zero points
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
         if constexpr (NG == 1) vs[t] = scale_at<C::SF32>(w.vs[t / 4], t & 3);
-        else vs[t] = __uint_as_float(w.vs[t][0]);
-        if constexpr (MASK) {
+        else vs[t] = __uint_as_float(C::SF32 ? w.vs[t][0] : w.vs[t][0] << 16);
+    }
+    if (mask) {
+        // unseen scores become -inf, whatever they are; the scales of keys
+        // that no row may see (past the sequence or on an absent page) are
+        // not looked at
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const int key = t0 + 16 * (t / 4) + 4 * g + t % 4;
             bool any = false;
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) any |= seen[rt][t];
+            for (int rt = 0; rt < RT; ++rt) {
+                const bool seen = present(a, pages.p[t / 4]) && key < st.lim[rt] && key >= st.lo[rt];
+                any |= seen;
+                x[rt][t] = seen ? x[rt][t] * mul[t] : -__builtin_inff();
+            }
+            mul[t] = 1.0f;
             // (several groups: the scale goes into the operand that all 16
             // queries share, so it must be dropped only if none sees the key)
-            if constexpr (NG == 1) {
-                if (!any) vs[t] = 0.0f;
-            } else if (__ballot(any) == 0) {
-                vs[t] = 0.0f;
-            }
+            if constexpr (NG > 1) any = (__ballot(any) >> (16 * g)) & 0xFFFFu;
+            if (!any) vs[t] = 0.0f;
         }
     }
-    // the exponent of the value scales: grows to cover the largest
-    float big = 0.0f;
+    const float down = cover_scales<C>(st, vs, NG == 1 ? kPExp : kSExp);
+    bool odd = false;
 #pragma unroll
-    for (int t = 0; t < 8; ++t) big = fmaxf(big, fabsf(vs[t]) < __builtin_inff() ? fabsf(vs[t]) : 0.0f);
-    const float cover = __uint_as_float(static_cast<uint32_t>(127 + st.e) << 23);
-    if (__any(big > cover)) {
-        big = max_groups(big);
-#pragma unroll
-        for (int x = 1; x < 16; x *= 2) big = fmaxf(big, __shfl_xor(big, x));
-        const int e = min(max(static_cast<int>(__float_as_uint(big) >> 23) - 126, -100), 127);
-        const int eu = __builtin_amdgcn_readfirstlane(e);
-        const float f = ldexpf(1.0f, st.e - eu);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int j = 0; j < C::DT; ++j) st.o[rt][j] *= f;
-        st.e = eu;
+    for (int t = 0; t < 8; ++t) {
+        vs[t] *= down;
+        odd |= !(fabsf(vs[t]) < __builtin_inff());
     }
-    const float down = ldexpf(1.0f, (NG == 1 ? kPExp : kSExp) - st.e);
+    if (__any(odd)) {
+        // a value scale that is not finite must reach the queries that see its
+        // key and no others: it leaves the step, and their scores become NaN
 #pragma unroll
-    for (int t = 0; t < 8; ++t) vs[t] *= down;
-    if constexpr (NG > 1) {
+        for (int t = 0; t < 8; ++t) {
+            const bool bad = !(fabsf(vs[t]) < __builtin_inff());
+            if (bad) vs[t] = 0.0f;
+            if ((__ballot(bad) >> (16 * g)) & 0xFFFFu) {
 #pragma unroll
-        for (int t = 0; t < 8; ++t) nz[t] = sym ? 8u : w.vz[t];
-        // a scale that is not finite must reach the queries that see its key
-        // and no others: it leaves the shared operand, and their probability
-        // becomes NaN instead
-        bool odd = false;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) odd |= !(fabsf(vs[t]) < __builtin_inff());
-        if (__any(odd)) {
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                int bad = !(fabsf(vs[t]) < __builtin_inff());
-                if (bad) vs[t] = 0.0f;
-#pragma unroll
-                for (int x = 1; x < 16; x *= 2) bad |= __shfl_xor(bad, x);
-                if (bad) {
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-                        if (sc[rt][t] > -__builtin_inff()) sc[rt][t] = __builtin_nanf("");
+                for (int rt = 0; rt < RT; ++rt) {
+                    const int key = t0 + 16 * (t / 4) + 4 * g + t % 4;
+                    if (key < st.lim[rt] && key >= st.lo[rt]) x[rt][t] = __builtin_nanf("");
                 }
             }
         }
     }
-    // softmax: probabilities as operands
+    // probabilities as operands
     uint4v ph[RT], pl[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        float top = sc[rt][0];
-#pragma unroll
-        for (int t = 1; t < 8; ++t) top = fmaxf(top, sc[rt][t]);
-        if (__any(top > st.m[rt] + st.slack[rt])) {
-            top = fmaxf(max_groups(top), st.m[rt]);
-            const float mc = top > kLow ? top * st.c[rt] : kLow;
-            const float f = exp2f(st.mc[rt] - mc);
-            st.m[rt] = top;
-            st.mc[rt] = mc;
-            st.l[rt] *= f;
-#pragma unroll
-            for (int j = 0; j < C::DT; ++j) st.o[rt][j] *= f;
-        }
-        float p[8];
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            float x = __builtin_amdgcn_exp2f(fmaf(sc[rt][t], st.c[rt], -st.mc[rt]));
-            if constexpr (MASK)
-                if (!seen[rt][t]) x = 0.0f;   // (a row that has seen nothing yet has no usable m)
-            st.l[rt] += x;
-            if constexpr (NG == 1) p[t] = x * vs[t];
-            else p[t] = x * static_cast<float>(1 << kPExp);
-            if constexpr (MASK && NG == 1)
-                if (!seen[rt][t]) p[t] = 0.0f;   // (nor may another row's infinite scale reach this one)
-        }
+        HR_PHASE();
+        exponentials<C>(st, rt, x[rt], mul);
         uint32_t hw[4], lw[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            hw[i] = pack_f16(p[2 * i], p[2 * i + 1]);
-            if constexpr (C::WIDE) lw[i] = pack_f16(p[2 * i] - lo_f32(hw[i]), p[2 * i + 1] - hi_f32(hw[i]));
+            float p[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) p[j] = x[rt][2 * i + j] * (NG == 1 ? vs[2 * i + j] : static_cast<float>(1 << kPExp));
+            hw[i] = pack_f16(p[0], p[1]);
+            if constexpr (C::WIDE) lw[i] = pack_f16(p[0] - lo_f32(hw[i]), p[1] - hi_f32(hw[i]));
         }
         ph[rt] = uint4v{hw[0], hw[1], hw[2], hw[3]};
         if constexpr (C::WIDE) pl[rt] = uint4v{lw[0], lw[1], lw[2], lw[3]};
@@ -553,16 +693,15 @@ __device__ __forceinline__ void step(const CacheAttnArgs& a, Raw<C>& w, int t0, 
     uint32_t z0[4], z1[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        uint32_t u;
         if constexpr (NG == 1) {
-            if (sym) {
-                z0[i] = 0x00080008u;
-            } else {
-                const uint32_t u = w.vz[i / 2] >> (8 * (i & 1));
-                z0[i] = ((u << 12) | u) & 0x000F000Fu;
-            }
+            u = w.vz[i / 2] >> (8 * (i & 1));
+            u |= u << 12;
         } else {
-            z0[i] = nz[2 * i] | (nz[2 * i + 1] << 16);
+            const int gi = (lane & 15) / (16 / NG);
+            u = (w.vz[2 * i] | (w.vz[2 * i + 1] << 16)) >> (4 * (gi & 1));
         }
+        z0[i] = (u & zs.mask) | zs.fixed;
         z1[i] = z0[i] << 4;
         if constexpr (!C::SUBV) {
             z0[i] |= 0x64006400u;
@@ -578,19 +717,20 @@ __device__ __forceinline__ void step(const CacheAttnArgs& a, Raw<C>& w, int t0, 
         }
     }
     // O^T += V^T P^T, two dimensions a byte
+    const uint32_t f0 = C::SUBV ? zs.flip : zs.flip | 0x64006400u, f1 = C::SUBV ? zs.flip << 4 : zs.flip << 4 | 0x54005400u;
 #pragma unroll
     for (int b = 0; b < (C::D == 64 ? 2 : 4 * C::VW); ++b) {
+        HR_PHASE();
         const uint32_t sel = 0x0C040C00u + 0x00010001u * (b & 3);
-        uint32_t x[4];
+        uint32_t y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = __builtin_amdgcn_perm(w.v[2 * i + 1][b / 4], w.v[2 * i][b / 4], sel);
+        for (int i = 0; i < 4; ++i) y[i] = __builtin_amdgcn_perm(w.v[2 * i + 1][b / 4], w.v[2 * i][b / 4], sel);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             uint32_t f[4], fl[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                f[i] = x[i] & (half ? 0x00F000F0u : 0x000F000Fu);
-                if constexpr (!C::SUBV) f[i] |= half ? 0x54005400u : 0x64006400u;
+                f[i] = half ? (y[i] & 0x00F000F0u) ^ f1 : (y[i] & 0x000F000Fu) ^ f0;
                 f[i] = pk_sub(f[i], half ? z1[i] : z0[i]);
                 if constexpr (NG > 1) {
                     const uint32_t d = f[i];
@@ -616,17 +756,31 @@ __device__ __forceinline__ void step(const CacheAttnArgs& a, Raw<C>& w, int t0, 
 }
 
 // A wave's share of keys [k0, k1) (k0 a multiple of 32) of a unit: every WT-th
-// 32 of them.
+// 32 of them.  The next step's keys are loaded before a step is computed, and
+// the pages of the one after it are looked up.
 template <class C>
 __device__ __forceinline__ void walk(const CacheAttnArgs& a, const int32_t* table, int h, const Span& sp, int k0, int k1,
                                      int wt, Rows<C>& st) {
+    constexpr int S = 32 * C::WT;
     k0 = max(k0, sp.lo & ~31);
     k1 = min(k1, sp.hi);
-    for (int t = k0 + 32 * wt; t < k1; t += 32 * C::WT) {
-        Raw<C> w;
-        load_keys<C>(a, table, h, t, w);
-        if (t >= sp.flo && t + 32 <= sp.fhi && w.here == 3) step<C, false>(a, w, t, st);
-        else step<C, true>(a, w, t, st);
+    int t = k0 + 32 * wt;
+    if (t >= k1) return;
+    Raw<C> w;
+    Pages now = pages_at(a, table, t), next = pages_at(a, table, t + S);
+    load_keys<C>(a, now, h, t, w);
+    while (true) {
+        Raw<C> n;
+        const bool more = t + S < k1;
+        if (more) load_keys<C>(a, next, h, t + S, n);
+        const Pages after = pages_at(a, table, t + 2 * S);
+        const bool all = t >= sp.flo && t + 32 <= sp.fhi && present(a, now.p[0]) && present(a, now.p[1]);
+        step<C>(a, w, now, !all, t, st);
+        if (!more) return;
+        t += S;
+        w = n;
+        now = next;
+        next = after;
     }
 }
 
@@ -801,7 +955,7 @@ template <class C, class F>
 __device__ __forceinline__ Place place(const CacheAttnArgs& a, int64_t* lds, F want_of) {
     const int tid = threadIdx.x;
     int64_t sum = 0;
-    for (int b = tid; b < a.sq.rows; b += 256) sum += items_of<C>(a, seq_at(a.sq, a.pg.logp, b)).total;
+    for (int b = tid; b < a.sq.rows; b += 256) sum += items_of<C>(a, seq_at<false>(a.sq, a.pg.logp, b)).total;
     // total over the workgroup
     for (int x = 1; x < 64; x *= 2) sum += __shfl_xor(sum, x);
     __syncthreads();
@@ -815,7 +969,7 @@ __device__ __forceinline__ Place place(const CacheAttnArgs& a, int64_t* lds, F w
     p.before = p.total;
     for (int c = 0; c < a.sq.rows; c += 256) {
         const int b = c + tid;
-        const int64_t own = b < a.sq.rows ? items_of<C>(a, seq_at(a.sq, a.pg.logp, b)).total : 0;
+        const int64_t own = b < a.sq.rows ? items_of<C>(a, seq_at<false>(a.sq, a.pg.logp, b)).total : 0;
         int64_t inc = own;
         for (int x = 1; x < 64; x *= 2) {
             const int64_t y = __shfl_up(inc, x);
@@ -868,7 +1022,7 @@ __device__ __forceinline__ int64_t holder(int64_t u, int64_t nw, int64_t total) 
 // unit that it does not hold whole goes to scratch slot 2 w + 1 if it begins
 // here, else 2 w.
 template <class C, class T>
-__global__ void __launch_bounds__(256) cache_attn_split(const CacheAttnArgs a) {
+__global__ void __launch_bounds__(256, C::WAVES) cache_attn_split(const CacheAttnArgs a) {
     __shared__ float lds[join_floats<C>() > 16 ? join_floats<C>() : 16];
     int64_t i0 = 0, i1 = 0;
     const Place p = place<C>(a, reinterpret_cast<int64_t*>(lds), [&](int64_t total) {
@@ -882,7 +1036,7 @@ __global__ void __launch_bounds__(256) cache_attn_split(const CacheAttnArgs a) {
     i1 = uniform64(i1);
     int64_t before = uniform64(p.before);
     for (int b = __builtin_amdgcn_readfirstlane(p.b); b < a.sq.rows && i0 < i1; ++b) {
-        const Seq s = seq_at(a.sq, a.pg.logp, b);
+        const Seq s = seq_at<true>(a.sq, a.pg.logp, b);
         const Items it = items_of<C>(a, s);
         while (i0 < i1 && i0 < before + it.total) {
             const int64_t at = i0 - before;
@@ -917,19 +1071,19 @@ __global__ void __launch_bounds__(256) cache_attn_join(const CacheAttnArgs a) {
             int hi = a.sq.rows - 1;
             while (b < hi) {
                 const int mid = (b + hi + 1) / 2;
-                if (cu_at(a.sq, mid) <= token) b = mid;
+                if (cu_at<true>(a.sq, mid) <= token) b = mid;
                 else hi = mid - 1;
             }
         } else {
             b = static_cast<int>(min(token / a.sq.per, static_cast<int64_t>(a.sq.rows - 1)));
         }
-        const Seq s = seq_at(a.sq, a.pg.logp, b);
+        const Seq s = seq_at<true>(a.sq, a.pg.logp, b);
         if (token < s.start || token >= s.start + s.n) continue;
         const Items it = items_of<C>(a, s);
         // items before the sequence, and of the call
         int64_t sum = 0, pre = 0;
         for (int x = tid; x < a.sq.rows; x += 256) {
-            const int64_t t = items_of<C>(a, seq_at(a.sq, a.pg.logp, x)).total;
+            const int64_t t = items_of<C>(a, seq_at<false>(a.sq, a.pg.logp, x)).total;
             sum += t;
             if (x < b) pre += t;
         }
@@ -993,16 +1147,16 @@ __global__ void __launch_bounds__(256) cache_attn_join(const CacheAttnArgs a) {
 // sequence b with floor(cu(b) rep / ROWS) + b <= u; a sequence has at most
 // as many units as that bound leaves it.
 template <class C, class T>
-__global__ void __launch_bounds__(256) cache_attn_whole(const CacheAttnArgs a) {
+__global__ void __launch_bounds__(256, C::WAVES) cache_attn_whole(const CacheAttnArgs a) {
     const int u = blockIdx.x % a.units, h = blockIdx.x / a.units;
-    auto first = [&](int b) { return static_cast<int64_t>(cu_at(a.sq, b)) * a.rep / C::ROWS + b; };
+    auto first = [&](int b) { return static_cast<int64_t>(cu_at<true>(a.sq, b)) * a.rep / C::ROWS + b; };
     int b = 0, hi = a.sq.rows - 1;
     while (b < hi) {
         const int mid = (b + hi + 1) / 2;
         if (first(mid) <= u) b = mid;
         else hi = mid - 1;
     }
-    const Seq s = seq_at(a.sq, a.pg.logp, b);
+    const Seq s = seq_at<true>(a.sq, a.pg.logp, b);
     const int64_t rbs = (static_cast<int64_t>(s.n) * a.rep + C::ROWS - 1) / C::ROWS;
     // the last row blocks see the most keys: they go first
     const int64_t rb = rbs - 1 - (u - first(b));
