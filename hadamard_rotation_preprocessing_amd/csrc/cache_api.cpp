@@ -228,8 +228,9 @@ int attn_work_bytes(const hr::CacheAttnKey& k, int* workers, int64_t* bytes) {
     if (!k.split) return HR_OK;
     const int e = hr::cache_attn_workers(k, workers);
     if (e != 0) return fail(HR_EDEVICE, "occupancy query failed: %s", hipGetErrorString(static_cast<hipError_t>(e)));
-    // two partial results per workgroup: rows of d sums, a maximum and a sum of exponentials
-    *bytes = int64_t{*workers} * 2 * (16 * k.rt * k.wr) * (k.d + 2) * 4;
+    // two partial results per workgroup, rows of d sums, a maximum and a sum of
+    // exponentials each, and a record of the unit that it leaves unfinished
+    *bytes = int64_t{*workers} * (2 * (16 * k.rt * k.wr) * (k.d + 4) * 4 + 32);
     return HR_OK;
 }
 

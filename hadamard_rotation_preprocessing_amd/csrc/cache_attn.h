@@ -193,7 +193,7 @@ struct Cfg {
     static constexpr int KEYS = 32 * WT;           // keys of an item
     static constexpr int ES = SF32 ? 4 : 2;
     static constexpr int KSW = NG * ES;            // 32-bit words of four positions' scales
-    static constexpr int WAVES = RT == 1 && !WIDE && D <= 128 ? 3 : 2;  // waves per SIMD
+    static constexpr int WAVES = 2;  // waves per SIMD
     static constexpr int P = WIDE ? 2 : 1;         // float16 terms of an operand
     static constexpr bool SUBK = !WIDE;            // subnormal codes of K
     static constexpr bool SUBV = !WIDE && NG == 1; // and of V
@@ -757,35 +757,60 @@ __device__ __forceinline__ void step(const CacheAttnArgs& a, const Raw<C>& w, co
 
 // A wave's share of keys [k0, k1) (k0 a multiple of 32) of a unit: every WT-th
 // 32 of them.  The next step's keys are loaded before a step is computed, and
-// the pages of the one after it are looked up.
+// the pages of the one after it are looked up; start() is called before the
+// rows are loaded, so that the first keys are on their way meanwhile.
 template <class C>
-__device__ __forceinline__ void walk(const CacheAttnArgs& a, const int32_t* table, int h, const Span& sp, int k0, int k1,
-                                     int wt, Rows<C>& st) {
-    constexpr int S = 32 * C::WT;
-    k0 = max(k0, sp.lo & ~31);
-    k1 = min(k1, sp.hi);
-    int t = k0 + 32 * wt;
-    if (t >= k1) return;
+struct Walk {
+    static constexpr int S = 32 * C::WT;
+    const int32_t* table;
+    int h, t, end;
+    Pages now, next;
     Raw<C> w;
-    Pages now = pages_at(a, table, t), next = pages_at(a, table, t + S);
-    load_keys<C>(a, now, h, t, w);
-    while (true) {
-        Raw<C> n;
-        const bool more = t + S < k1;
-        if (more) load_keys<C>(a, next, h, t + S, n);
-        const Pages after = pages_at(a, table, t + 2 * S);
-        const bool all = t >= sp.flo && t + 32 <= sp.fhi && present(a, now.p[0]) && present(a, now.p[1]);
-        step<C>(a, w, now, !all, t, st);
-        if (!more) return;
-        t += S;
-        w = n;
-        now = next;
-        next = after;
+
+    __device__ __forceinline__ void start(const CacheAttnArgs& a, const Span& sp, int k0, int k1, int wt) {
+        t = max(k0, sp.lo & ~31) + 32 * wt;
+        end = min(k1, sp.hi);
+        if (t >= end) return;
+        now = pages_at(a, table, t);
+        next = pages_at(a, table, t + S);
+        load_keys<C>(a, now, h, t, w);
     }
+    __device__ __forceinline__ void run(const CacheAttnArgs& a, const Span& sp, Rows<C>& st) {
+        if (t >= end) return;
+        while (true) {
+            Raw<C> n;
+            const bool more = t + S < end;
+            if (more) load_keys<C>(a, next, h, t + S, n);
+            const Pages after = pages_at(a, table, t + 2 * S);
+            const bool all = t >= sp.flo && t + 32 <= sp.fhi && present(a, now.p[0]) && present(a, now.p[1]);
+            step<C>(a, w, now, !all, t, st);
+            if (!more) return;
+            t += S;
+            w = n;
+            now = next;
+            next = after;
+        }
+    }
+};
+
+// Four neighbouring elements of an output row.
+template <class T>
+__device__ __forceinline__ void store4(T* to, float4v x) {
+    if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint2v*>(to) = uint2v{to_bf16(x[0]) | (to_bf16(x[1]) << 16), to_bf16(x[2]) | (to_bf16(x[3]) << 16)};
+    else *reinterpret_cast<float4v*>(to) = x;
+}
+__device__ __forceinline__ float log_sum(float m2, float l) {
+    return l == 0.0f ? -__builtin_inff() : (m2 + __log2f(l)) * 0.6931471805599453f;
+}
+// A part of a row in the scratch: d sums, the maximum (log2 units), the sum of
+// exponentials, padded to 16 bytes.
+template <class C>
+constexpr int part_stride() {
+    return C::D + 4;
 }
 
 // Writes a wave's finished rows, or its part of them to the scratch.
-// o: sums in value units relative to m (raw scores times c = log2 units).
 template <class C, class T>
 __device__ __forceinline__ void put_rows(const CacheAttnArgs& a, const Seq& s, int h, int r0, const Rows<C>& st, float* part,
                                          int part_row) {
@@ -794,18 +819,19 @@ __device__ __forceinline__ void put_rows(const CacheAttnArgs& a, const Seq& s, i
     for (int rt = 0; rt < C::RT; ++rt) {
         const int row = r0 + 16 * rt + n;
         if (row >= s.n * a.rep) continue;
-        const float m2 = st.mc[rt], l = st.l[rt];
+        const float l = st.l[rt];
         if (part) {
-            float* p = part + static_cast<int64_t>(part_row + 16 * rt + n) * (C::D + 2);
+            float* p = part + (part_row + 16 * rt + n) * part_stride<C>();
             if (g == 0) {
-                p[0] = l > 0.0f || l != l ? m2 : kLow;
-                p[1] = l;
+                p[C::D] = l > 0.0f || l != l ? st.mc[rt] : kLow;
+                p[C::D + 1] = l;
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int j = 0; j < C::DT; j += 2)
-                    *reinterpret_cast<float2*>(p + 2 + (4 * g + r) * C::DT + j) = make_float2(st.o[rt][j][r], st.o[rt][j + 1][r]);
+                for (int j = 0; j < C::DT; j += 4)
+                    *reinterpret_cast<float4v*>(p + (4 * g + r) * C::DT + j) =
+                        float4v{st.o[rt][j][r], st.o[rt][j + 1][r], st.o[rt][j + 2][r], st.o[rt][j + 3][r]};
             continue;
         }
         const int tok = row / a.rep, hh = row - tok * a.rep;
@@ -817,16 +843,12 @@ __device__ __forceinline__ void put_rows(const CacheAttnArgs& a, const Seq& s, i
         for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int j = 0; j < C::DT; j += 4) {
-                float x[4];
+                float4v x;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[i] = st.o[rt][j + i][r] * inv;
-                T* to = p + (4 * g + r) * C::DT + j;
-                if constexpr (sizeof(T) == 2)
-                    *reinterpret_cast<uint2v*>(to) =
-                        uint2v{to_bf16(x[0]) | (to_bf16(x[1]) << 16), to_bf16(x[2]) | (to_bf16(x[3]) << 16)};
-                else *reinterpret_cast<float4v*>(to) = float4v{x[0], x[1], x[2], x[3]};
+                store4<T>(p + (4 * g + r) * C::DT + j, x);
             }
-        if (a.lse && g == 0) a.lse[t * a.hq + head] = l == 0.0f ? -__builtin_inff() : (m2 + __log2f(l)) * 0.6931471805599453f;
+        if (a.lse && g == 0) a.lse[t * a.hq + head] = log_sum(st.mc[rt], l);
     }
 }
 
@@ -844,61 +866,74 @@ __device__ __forceinline__ void settle(Rows<C>& st) {
     }
 }
 
-// Joins the waves that took different keys of the same rows: all get the
-// common maximum, then halves add up through LDS.  The result is wave 0's.
-template <class C>
-__device__ __forceinline__ void join_waves(Rows<C>& st, float* lds) {
-    static_assert(C::WT == 4 && C::WR == 1, "four waves along the keys");
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    float* ml = lds;                                       // [4][RT * 16]
-    float* buf = lds + 4 * C::RT * 16;                     // [2][RT][DT][64] float4
-    __syncthreads();
-#pragma unroll
-    for (int rt = 0; rt < C::RT; ++rt)
-        if (g == 0) ml[wave * C::RT * 16 + rt * 16 + n] = st.mc[rt];
-    __syncthreads();
-#pragma unroll
-    for (int rt = 0; rt < C::RT; ++rt) {
-        float top = kLow;
-        for (int x = 0; x < 4; ++x) top = fmaxf(top, ml[x * C::RT * 16 + rt * 16 + n]);
-        const float f = exp2f(st.mc[rt] - top);
-        st.mc[rt] = top;
-        st.l[rt] *= f;
-#pragma unroll
-        for (int j = 0; j < C::DT; ++j) st.o[rt][j] *= f;
-    }
-    constexpr int W = C::RT * (C::DT * 4 + 1) * 64;        // floats of one wave's rows
-    for (int half = 2; half >= 1; half /= 2) {
-        if (wave >= half && wave < 2 * half) {
-            float* p = buf + (wave - half) * W + lane;
-#pragma unroll
-            for (int rt = 0; rt < C::RT; ++rt) {
-#pragma unroll
-                for (int j = 0; j < C::DT; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) p[((rt * C::DT + j) * 4 + r) * 64] = st.o[rt][j][r];
-                p[(C::RT * C::DT * 4 + rt) * 64] = st.l[rt];
-            }
-        }
-        __syncthreads();
-        if (wave < half) {
-            const float* p = buf + wave * W + lane;
-#pragma unroll
-            for (int rt = 0; rt < C::RT; ++rt) {
-#pragma unroll
-                for (int j = 0; j < C::DT; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) st.o[rt][j][r] += p[((rt * C::DT + j) * 4 + r) * 64];
-                st.l[rt] += p[(C::RT * C::DT * 4 + rt) * 64];
-            }
-        }
-        __syncthreads();
-    }
-}
-
+// Joins the four waves that took different keys of the same rows and writes
+// the rows, or their part to the scratch: maxima first, then every wave's sums
+// through LDS in a few rows at a time, 16 threads to a row.
 template <class C>
 constexpr int join_floats() {
-    return C::WT == 1 ? 1 : 4 * C::RT * 16 + 2 * C::RT * (C::DT * 4 + 1) * 64;
+    return C::WT == 1 ? 16 : 2 * 4 * 16 + 4 * 16 * (C::D + 4);
+}
+template <class C, class T>
+__device__ __forceinline__ void join_waves(const CacheAttnArgs& a, const Seq& s, int h, int r0, Rows<C>& st, float* part,
+                                           float* lds) {
+    static_assert(C::WT == 4 && C::WR == 1, "four waves along the keys");
+    constexpr int D = C::D, LD = D + 4;                    // (rows 16 bytes apart in the banks)
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, g = lane >> 4;
+    float* ml = lds;                                       // [2][4][16]: maxima, sums
+    float* so = lds + 128;                                 // [4][16][LD]
+#pragma unroll
+    for (int rt = 0; rt < C::RT; ++rt) {
+        const int rows = min(s.n * a.rep - r0 - 16 * rt, 16);
+        if (rows <= 0) break;
+        __syncthreads();
+        if (g == 0) {
+            ml[wave * 16 + n] = st.mc[rt];
+            ml[64 + wave * 16 + n] = st.l[rt];
+        }
+        if (n < rows) {
+            float* p = so + (wave * 16 + n) * LD + 4 * g * C::DT;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < C::DT; j += 4)
+                    *reinterpret_cast<float4v*>(p + r * C::DT + j) =
+                        float4v{st.o[rt][j][r], st.o[rt][j + 1][r], st.o[rt][j + 2][r], st.o[rt][j + 3][r]};
+        }
+        __syncthreads();
+        const int row = tid >> 4, i = tid & 15;            // 16 threads to a row
+        if (row < rows) {
+            float top = kLow, l = 0.0f, f[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) top = fmaxf(top, ml[x * 16 + row]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                f[x] = exp2f(ml[x * 16 + row] - top);
+                l += f[x] * ml[64 + x * 16 + row];
+            }
+            const int at = r0 + 16 * rt + row, tok = at / a.rep;
+            const int64_t t = s.start + tok, head = h * a.rep + at - tok * a.rep;
+            const float inv = part ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+            float* pp = part + (16 * rt + row) * part_stride<C>();
+            T* po = static_cast<T*>(a.out) + t * a.o_st + head * a.o_sh;
+#pragma unroll
+            for (int j = 0; j < D; j += 64) {
+                float4v v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) v += *reinterpret_cast<const float4v*>(so + (x * 16 + row) * LD + j + 4 * i) * f[x];
+                v *= inv;
+                if (part) *reinterpret_cast<float4v*>(pp + j + 4 * i) = v;
+                else store4<T>(po + j + 4 * i, v);
+            }
+            if (i == 0) {
+                if (part) {
+                    pp[D] = l > 0.0f || l != l ? top : kLow;
+                    pp[D + 1] = l;
+                } else if (a.lse) {
+                    a.lse[t * a.hq + head] = log_sum(top, l);
+                }
+            }
+        }
+    }
 }
 
 // Rows [r0, r0 + ROWS) of kv head h of a sequence over the keys [k0, k1);
@@ -911,21 +946,23 @@ __device__ __forceinline__ void segment(const CacheAttnArgs& a, const Seq& s, in
     const int row = r0 + wr * 16 * C::RT;
     const int rows = min(row + 16 * C::RT, s.n * a.rep);
     if (C::WT == 1 && row >= rows) return;   // (no barriers along the rows)
+    const Span sp = span_of(a, s, row, rows);
+    Walk<C> keys;
+    keys.table = a.sq.table + static_cast<int64_t>(b) * a.sq.max_pages;
+    keys.h = h;
+    keys.start(a, sp, k0, k1, wt);
     Rows<C> st;
     load_rows<C, T>(a, s, h, row, st);
-    const Span sp = span_of(a, s, row, rows);
-    walk<C>(a, a.sq.table + static_cast<int64_t>(b) * a.sq.max_pages, h, sp, k0, k1, wt, st);
+    keys.run(a, sp, st);
     settle<C>(st);
-    if constexpr (C::WT > 1) {
-        join_waves<C>(st, lds);
-        if (wave == 0) put_rows<C, T>(a, s, h, row, st, part, row - r0);
-    } else {
-        put_rows<C, T>(a, s, h, row, st, part, row - r0);
-    }
+    if constexpr (C::WT > 1) join_waves<C, T>(a, s, h, row, st, part, lds);
+    else put_rows<C, T>(a, s, h, row, st, part, row - r0);
 }
 
-// The items of a sequence: heads x row blocks x blocks of keys, at least one
-// block of keys so that rows that see nothing are written too.
+// The items of a sequence: for each kv head and row block a unit of kSetup items
+// that stand for its start and end, then one for each block of keys, at least
+// one so that rows that see nothing are written too.
+constexpr int kSetup = 4;  // a unit's start and end cost about four blocks of keys (7 against 1.7 us)
 struct Items {
     int first, blocks, rbs;   // first key (a multiple of 32), key blocks, row blocks
     int64_t total;
@@ -941,58 +978,79 @@ __device__ __forceinline__ Items items_of(const CacheAttnArgs& a, const Seq& s) 
         it.first = min(sp.lo, sp.hi) & ~31;
         it.blocks = max((sp.hi - it.first + C::KEYS - 1) / C::KEYS, 1);
     }
-    it.total = static_cast<int64_t>(a.pg.hkv) * it.rbs * it.blocks;
+    it.total = static_cast<int64_t>(a.pg.hkv) * it.rbs * (it.blocks + kSetup);
     return it;
 }
 
-// All items of the call, and the sequence that holds item `want` with the
-// items before it.  Every thread of the workgroup takes part.
+// sum of v over the workgroup's threads before this one, and over all
+__device__ __forceinline__ int64_t scan_items(int64_t v, int64_t* all, int64_t* lds) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int64_t inc = v;
+#pragma unroll
+    for (int x = 1; x < 64; x *= 2) {
+        const int64_t y = __shfl_up(inc, x);
+        if (lane >= x) inc += y;
+    }
+    __syncthreads();
+    if (lane == 63) lds[wave] = inc;
+    __syncthreads();
+    int64_t before = 0, sum = 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int64_t y = lds[x];
+        if (x < wave) before += y;
+        sum += y;
+    }
+    *all = sum;
+    return before + inc - v;
+}
+
+// Workgroup w of the split form: its items [i0, i1), the sequence b that holds
+// the first and the items before that sequence.  Every thread takes part.
 struct Place {
-    int64_t total, before;
+    int64_t total, nw;    // items of the call, workgroups that share them
+    int64_t i0, i1, before;
     int b;
 };
-template <class C, class F>
-__device__ __forceinline__ Place place(const CacheAttnArgs& a, int64_t* lds, F want_of) {
+template <class C>
+__device__ __forceinline__ Place place(const CacheAttnArgs& a, int64_t* lds) {
     const int tid = threadIdx.x;
-    int64_t sum = 0;
-    for (int b = tid; b < a.sq.rows; b += 256) sum += items_of<C>(a, seq_at<false>(a.sq, a.pg.logp, b)).total;
-    // total over the workgroup
-    for (int x = 1; x < 64; x *= 2) sum += __shfl_xor(sum, x);
-    __syncthreads();
-    if ((tid & 63) == 0) lds[tid >> 6] = sum;
-    __syncthreads();
     Place p;
-    p.total = lds[0] + lds[1] + lds[2] + lds[3];
-    const int64_t want = want_of(p.total);
-    int64_t base = 0;
-    p.b = a.sq.rows;
-    p.before = p.total;
+    int64_t total = 0, own = 0, pre = 0;
+    // (a call of up to 256 sequences is scanned once)
     for (int c = 0; c < a.sq.rows; c += 256) {
         const int b = c + tid;
-        const int64_t own = b < a.sq.rows ? items_of<C>(a, seq_at<false>(a.sq, a.pg.logp, b)).total : 0;
-        int64_t inc = own;
-        for (int x = 1; x < 64; x *= 2) {
-            const int64_t y = __shfl_up(inc, x);
-            if ((tid & 63) >= x) inc += y;
-        }
-        __syncthreads();
-        if ((tid & 63) == 63) lds[tid >> 6] = inc;
-        if (tid == 0) lds[4] = -1;
-        __syncthreads();
-        for (int x = 0; x < (tid >> 6); ++x) inc += lds[x];
-        const int64_t chunk = lds[0] + lds[1] + lds[2] + lds[3];
-        if (want >= base + inc - own && want < base + inc) {
-            lds[4] = b;
-            lds[5] = base + inc - own;
-        }
-        __syncthreads();
-        if (lds[4] >= 0) {
-            p.b = static_cast<int>(lds[4]);
-            p.before = lds[5];
-            break;
-        }
-        base += chunk;
+        own = b < a.sq.rows ? items_of<C>(a, seq_at<false>(a.sq, a.pg.logp, b)).total : 0;
+        int64_t all;
+        pre = total + scan_items(own, &all, lds);
+        total += all;
     }
+    const int64_t nw = total < a.workers ? (total > 0 ? total : 1) : a.workers;
+    const int64_t w = blockIdx.x;
+    p.total = total;
+    p.nw = nw;
+    p.i0 = w < nw ? w * total / nw : total;
+    p.i1 = w < nw ? (w + 1) * total / nw : total;
+    if (tid == 0) lds[4] = -1;
+    int64_t base = 0;
+    for (int c = 0; c < a.sq.rows; c += 256) {
+        const int b = c + tid;
+        if (a.sq.rows > 256) {
+            own = b < a.sq.rows ? items_of<C>(a, seq_at<false>(a.sq, a.pg.logp, b)).total : 0;
+            int64_t all;
+            pre = base + scan_items(own, &all, lds);
+            base += all;
+        }
+        __syncthreads();
+        if (p.i0 >= pre && p.i0 < pre + own) {
+            lds[4] = b;
+            lds[5] = pre;
+        }
+        __syncthreads();
+        if (lds[4] >= 0) break;
+    }
+    p.b = lds[4] >= 0 ? static_cast<int>(lds[4]) : a.sq.rows;
+    p.before = lds[5];
     __syncthreads();
     return p;
 }
@@ -1003,144 +1061,108 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
     return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
 }
 
-// How many workgroups share `total` items: at most one each.
-__device__ __forceinline__ int64_t sharers(const CacheAttnArgs& a, int64_t total) {
-    return total < a.workers ? (total > 0 ? total : 1) : a.workers;
-}
-// First item of workgroup w of nw.
-__device__ __forceinline__ int64_t first_item(int64_t w, int64_t nw, int64_t total) { return w * total / nw; }
-
 // The workgroup that holds item u.
 __device__ __forceinline__ int64_t holder(int64_t u, int64_t nw, int64_t total) {
     int64_t w = u * nw / total;
-    while (w + 1 < nw && first_item(w + 1, nw, total) <= u) ++w;
-    while (w > 0 && first_item(w, nw, total) > u) --w;
+    while (w + 1 < nw && (w + 1) * total / nw <= u) ++w;
+    while (w > 0 && w * total / nw > u) --w;
     return w;
 }
 
-// Split form: workgroup w takes items [first_item(w), first_item(w + 1)).  A
-// unit that it does not hold whole goes to scratch slot 2 w + 1 if it begins
-// here, else 2 w.
+// What the joining launch needs of a unit that begins in a workgroup and goes
+// on in the next ones.
+struct Cut {
+    int start, n;    // the sequence's first token and number of tokens
+    int h, r0;       // kv head, first query row
+    int last;        // the workgroup that ends it; -1: nothing to join
+};
+
+// Split form: workgroup w takes an equal share of all items.  A unit that it
+// does not hold whole goes to scratch slot 2 w + 1 if it begins here, else 2 w.
 template <class C, class T>
 __global__ void __launch_bounds__(256, C::WAVES) cache_attn_split(const CacheAttnArgs a) {
-    __shared__ float lds[join_floats<C>() > 16 ? join_floats<C>() : 16];
-    int64_t i0 = 0, i1 = 0;
-    const Place p = place<C>(a, reinterpret_cast<int64_t*>(lds), [&](int64_t total) {
-        const int64_t nw = sharers(a, total);
-        if (blockIdx.x >= nw) return total;
-        i0 = first_item(blockIdx.x, nw, total);
-        i1 = first_item(blockIdx.x + 1, nw, total);
-        return i0;
-    });
-    i0 = uniform64(i0);
-    i1 = uniform64(i1);
+    __shared__ float lds[join_floats<C>()];
+    const Place p = place<C>(a, reinterpret_cast<int64_t*>(lds));
+    int64_t i0 = uniform64(p.i0);
+    const int64_t i1 = uniform64(p.i1);
     int64_t before = uniform64(p.before);
+    constexpr int SLOT = C::ROWS * part_stride<C>();
+    Cut* cuts = reinterpret_cast<Cut*>(a.work + static_cast<int64_t>(a.workers) * 2 * SLOT);
+    Cut cut = {0, 0, 0, 0, -1};
     for (int b = __builtin_amdgcn_readfirstlane(p.b); b < a.sq.rows && i0 < i1; ++b) {
         const Seq s = seq_at<true>(a.sq, a.pg.logp, b);
         const Items it = items_of<C>(a, s);
+        const int size = it.blocks + kSetup;
         while (i0 < i1 && i0 < before + it.total) {
             const int64_t at = i0 - before;
-            const int unit = static_cast<int>(at / it.blocks), k = static_cast<int>(at % it.blocks);
-            const int64_t left = i1 - i0;
-            const int end = left < it.blocks - k ? k + static_cast<int>(left) : it.blocks;
-            const int h = unit / it.rbs, rb = unit % it.rbs;
+            const int unit = static_cast<int>(at / size), from = static_cast<int>(at % size);
+            const int64_t share = i1 - i0;
+            const int to = share < size - from ? from + static_cast<int>(share) : size;
+            i0 += to - from;
+            const int k = max(from - kSetup, 0), end = to - kSetup;
+            if (end <= k) continue;      // only items of the unit's start
+            const int h = unit / it.rbs, r0 = unit % it.rbs * C::ROWS;
             float* part = nullptr;
-            if (k > 0 || end < it.blocks)
-                part = a.work + (2 * static_cast<int64_t>(blockIdx.x) + (k == 0 ? 1 : 0)) * (C::ROWS * (C::D + 2));
-            segment<C, T>(a, s, b, h, rb * C::ROWS, it.first + k * C::KEYS, it.first + end * C::KEYS, part, lds);
-            i0 += end - k;
+            if (k > 0 || end < it.blocks) part = a.work + (2 * static_cast<int64_t>(blockIdx.x) + (k == 0 ? 1 : 0)) * SLOT;
+            if (k == 0 && end < it.blocks)
+                cut = {s.start, s.n, h, r0,
+                       static_cast<int>(holder(before + static_cast<int64_t>(unit + 1) * size - 1, p.nw, p.total))};
+            segment<C, T>(a, s, b, h, r0, it.first + k * C::KEYS, it.first + end * C::KEYS, part, lds);
         }
         before += it.total;
     }
+    if (threadIdx.x == 0) cuts[blockIdx.x] = cut;
 }
 
-// Joins the parts of units that were cut: a workgroup for a row, its four
-// waves along the parts, the lanes along the dimensions.
+// Joins the parts of units that were cut, in the order of their keys:
+// blockIdx.x = w takes the unit that begins in workgroup w, a wave for a row.
+// D / 4 lanes read a part, four dimensions each, the others the next ones, and
+// four parts are on their way at a time.
 template <class C, class T>
 __global__ void __launch_bounds__(256) cache_attn_join(const CacheAttnArgs a) {
-    constexpr int D = C::D, E = D / 64;
-    __shared__ int64_t lds[8];
-    __shared__ float sm[4], sl[4], so[4][D];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    for (int64_t id = blockIdx.x; id < static_cast<int64_t>(a.sq.tokens) * a.hq; id += gridDim.x) {
-        const int64_t token = id / a.hq;
-        const int head = static_cast<int>(id % a.hq), h = head / a.rep;
-        // the token's sequence: the last one that starts at or before it
-        int b = 0;
-        if (a.sq.cu) {
-            int hi = a.sq.rows - 1;
-            while (b < hi) {
-                const int mid = (b + hi + 1) / 2;
-                if (cu_at<true>(a.sq, mid) <= token) b = mid;
-                else hi = mid - 1;
-            }
-        } else {
-            b = static_cast<int>(min(token / a.sq.per, static_cast<int64_t>(a.sq.rows - 1)));
-        }
-        const Seq s = seq_at<true>(a.sq, a.pg.logp, b);
-        if (token < s.start || token >= s.start + s.n) continue;
-        const Items it = items_of<C>(a, s);
-        // items before the sequence, and of the call
-        int64_t sum = 0, pre = 0;
-        for (int x = tid; x < a.sq.rows; x += 256) {
-            const int64_t t = items_of<C>(a, seq_at<false>(a.sq, a.pg.logp, x)).total;
-            sum += t;
-            if (x < b) pre += t;
-        }
-        for (int x = 1; x < 64; x *= 2) {
-            sum += __shfl_xor(sum, x);
-            pre += __shfl_xor(pre, x);
-        }
-        __syncthreads();
-        if (lane == 0) {
-            lds[wave] = sum;
-            lds[4 + wave] = pre;
-        }
-        __syncthreads();
-        const int64_t total = lds[0] + lds[1] + lds[2] + lds[3], before = lds[4] + lds[5] + lds[6] + lds[7];
-        const int64_t nw = sharers(a, total);
-        const int row = static_cast<int>(token - s.start) * a.rep + head % a.rep;
-        const int rb = row / C::ROWS;
-        const int64_t u0 = before + (static_cast<int64_t>(h) * it.rbs + rb) * it.blocks, u1 = u0 + it.blocks - 1;
-        const int64_t w0 = holder(u0, nw, total), w1 = holder(u1, nw, total);
-        if (w0 == w1) continue;   // finished by its workgroup
-        const float* base = a.work + static_cast<int64_t>(row % C::ROWS) * (D + 2);
-        float m = kLow, l = 0.0f, o[E];
+    constexpr int D = C::D, L = D / 4, AT = 64 / L, PS = part_stride<C>(), SLOT = C::ROWS * PS;
+    const Cut* cuts = reinterpret_cast<const Cut*>(a.work + static_cast<int64_t>(a.workers) * 2 * SLOT);
+    const Cut cut = cuts[blockIdx.x];
+    const int lane = threadIdx.x & 63, row = blockIdx.y * 4 + (threadIdx.x >> 6);
+    const int at = cut.r0 + row;
+    if (cut.last < 0 || row >= C::ROWS || at >= cut.n * a.rep) return;
+    const int parts = cut.last - static_cast<int>(blockIdx.x) + 1;
+    const float* first = a.work + 2 * static_cast<int64_t>(blockIdx.x) * SLOT + row * PS;
+    float m = kLow, l = 0.0f;
+    float4v o = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p0 = lane / L; p0 < parts; p0 += 4 * AT) {
+        float4v x[4];
+        float2 ml[4];
 #pragma unroll
-        for (int i = 0; i < E; ++i) o[i] = 0.0f;
-        for (int64_t w = w0 + wave; w <= w1; w += 4) {
-            const float* p = base + (2 * w + (w == w0 ? 1 : 0)) * (C::ROWS * (D + 2));
-            const float pm = p[0], pl = p[1];
-            const float top = fmaxf(m, pm);
-            const float f = exp2f(m - top), pf = exp2f(pm - top);
-            l = l * f + pl * pf;
+        for (int i = 0; i < 4; ++i) {
+            const int p = min(p0 + i * AT, parts - 1);
+            const float* from = first + (2 * static_cast<int64_t>(p) + (p == 0 ? 1 : 0)) * SLOT;
+            x[i] = *reinterpret_cast<const float4v*>(from + lane % L * 4);
+            ml[i] = *reinterpret_cast<const float2*>(from + D);
+        }
 #pragma unroll
-            for (int i = 0; i < E; ++i) o[i] = o[i] * f + p[2 + lane * E + i] * pf;
+        for (int i = 0; i < 4; ++i) {
+            if (p0 + i * AT >= parts) break;
+            const float top = fmaxf(m, ml[i].x), f = exp2f(m - top), pf = exp2f(ml[i].x - top);
+            l = l * f + ml[i].y * pf;
+            o = o * f + x[i] * pf;
             m = top;
         }
-        if (lane == 0) {
-            sm[wave] = m;
-            sl[wave] = l;
-        }
-#pragma unroll
-        for (int i = 0; i < E; ++i) so[wave][lane * E + i] = o[i];
-        __syncthreads();
-        float top = kLow;
-        for (int x = 0; x < 4; ++x) top = fmaxf(top, sm[x]);
-        l = 0.0f;
-        for (int x = 0; x < 4; ++x) l += sl[x] * exp2f(sm[x] - top);
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        T* out = static_cast<T*>(a.out) + token * a.o_st + static_cast<int64_t>(head) * a.o_sh;
-        if (tid < D) {
-            float x = 0.0f;
-            for (int y = 0; y < 4; ++y) x += so[y][tid] * exp2f(sm[y] - top);
-            x *= inv;
-            if constexpr (sizeof(T) == 2) out[tid] = static_cast<T>(to_bf16(x));
-            else out[tid] = x;
-        }
-        if (a.lse && tid == 0)
-            a.lse[token * a.hq + head] = l == 0.0f ? -__builtin_inff() : (top + __log2f(l)) * 0.6931471805599453f;
     }
+#pragma unroll
+    for (int x = L; x < 64; x *= 2) {
+        const float om = __shfl_xor(m, x), ol = __shfl_xor(l, x);
+        const float4v oo = {__shfl_xor(o[0], x), __shfl_xor(o[1], x), __shfl_xor(o[2], x), __shfl_xor(o[3], x)};
+        const float top = fmaxf(m, om), f = exp2f(m - top), pf = exp2f(om - top);
+        l = l * f + ol * pf;
+        o = o * f + oo * pf;
+        m = top;
+    }
+    const int tok = at / a.rep;
+    const int64_t t = cut.start + tok, head = cut.h * a.rep + at - tok * a.rep;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if (lane < L) store4<T>(static_cast<T*>(a.out) + t * a.o_st + head * a.o_sh + 4 * lane, o * inv);
+    if (a.lse && lane == 0) a.lse[t * a.hq + head] = log_sum(m, l);
 }
 
 // Whole form: a workgroup for each unit.  Unit u of a head belongs to the last
@@ -1194,9 +1216,7 @@ int family(const CacheAttnKey& k, const CacheAttnArgs* a, int* workers, void* st
         hipLaunchKernelGGL((cache_attn_split<C, T>), dim3(a->workers), dim3(256), 0, s, *a);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return static_cast<int>(e);
-        const int64_t rows = static_cast<int64_t>(a->sq.tokens) * a->hq;
-        hipLaunchKernelGGL((cache_attn_join<C, T>), dim3(static_cast<uint32_t>(rows < (1 << 20) ? rows : 1 << 20)), dim3(256),
-                           0, s, *a);
+        hipLaunchKernelGGL((cache_attn_join<C, T>), dim3(a->workers, C::ROWS / 4), dim3(256), 0, s, *a);
     } else if constexpr (C::WR == 4) {
         hipLaunchKernelGGL((cache_attn_whole<C, T>), dim3(static_cast<uint32_t>(a->units) * a->pg.hkv), dim3(256), 0, s, *a);
     } else {
