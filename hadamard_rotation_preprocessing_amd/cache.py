@@ -88,18 +88,28 @@ class CacheSpec:
 
     def layout(self) -> dict:
         """Byte sizes and offsets of the page record (hr_cache_page)."""
-        return dict(_layout(self))
+        return dict(_resolved(self).layout)
 
     @property
     def page_bytes(self) -> int:
-        return _layout(self)["page_bytes"]
+        return _resolved(self).page_bytes
 
 
-@lru_cache(maxsize=None)
-def _layout(spec: CacheSpec) -> dict:
-    p = hr_cache_page()
-    check(_cache_lib().hr_cache_page_layout(ctypes.byref(spec.c()), ctypes.byref(p)))
-    return {n: getattr(p, n) for n, _ in hr_cache_page._fields_}
+class _Resolved:
+    """What the calls need of a spec: the C struct, the page's layout, and the
+    scratch sizes asked for so far (attention's, by the sizes and device)."""
+
+    def __init__(self, spec: CacheSpec):
+        self.spec = spec.c()
+        self.ref = ctypes.byref(self.spec)
+        p = hr_cache_page()
+        check(_cache_lib().hr_cache_page_layout(self.ref, ctypes.byref(p)))
+        self.layout = {n: getattr(p, n) for n, _ in hr_cache_page._fields_}
+        self.page_bytes = p.page_bytes
+        self.work = {}
+
+
+_resolved = lru_cache(maxsize=256)(_Resolved)
 
 
 def cache_pool(spec: CacheSpec, n_pages: int, layers: int | None = None, device="cuda") -> torch.Tensor:
@@ -113,7 +123,7 @@ def cache_sections(pool: torch.Tensor, spec: CacheSpec) -> dict:
     k_codes, v_codes, k_scales, v_scales and, asymmetric, k_zeros and v_zeros.
     One head of one page is what rotate_quantize_act writes for page_size rows
     of head_dim, so dequant_check reads it (after .contiguous())."""
-    lay, q = _layout(spec), spec.qspec
+    lay, q = _resolved(spec).layout, spec.qspec
     groups = spec.page_size * spec.head_dim // q.group_size
     size = {"codes": spec.page_size * spec.head_dim // 2, "scales": groups * (4 if q.scale_dtype == "f32" else 2),
             "zeros": 0 if q.sym else groups // 2}
@@ -122,53 +132,72 @@ def cache_sections(pool: torch.Tensor, spec: CacheSpec) -> dict:
             for n, b in size.items() if b for x in "kv"}
 
 
+_DTYPES = {torch.float32: L.HR_F32, torch.bfloat16: L.HR_BF16}
+
+
 def _dt(t):
-    from . import _dt as dt
-    return dt(t)
+    if t.dtype not in _DTYPES:
+        raise ValueError("dtype must be float32 or bfloat16, got %s" % t.dtype)
+    return _DTYPES[t.dtype]
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(t):
-    return torch.cuda.current_stream(t.device).cuda_stream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _ints(t: torch.Tensor, name: str, dim: int, device) -> torch.Tensor:
-    if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous() or t.device != device:
-        raise ValueError("%s must be a contiguous int32 tensor of %d dimension(s) on %s" % (name, dim, device))
-    return t
+def _stream(device) -> int:
+    """The device's current HIP stream (without the Stream object where torch
+    has a call for that: these calls are a few microseconds long)."""
+    return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
 
 
-def _pool(pool: torch.Tensor, spec: CacheSpec, layers: bool):
+def _ints(t: torch.Tensor, name: str, shape: tuple, device) -> int:
+    """Checks a contiguous int32 tensor; its address."""
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError("%s must be a contiguous int32 tensor %s on %s, got %s %s on %s"
+                         % (name, list(shape), device, t.dtype, list(t.shape), t.device))
+    return t.data_ptr()
+
+
+def _table(t: torch.Tensor, device):
+    """(address, rows, max_pages) of a page table."""
+    if t.dim() != 2:
+        raise ValueError("table must be [rows, max_pages], got %s" % list(t.shape))
+    return (_ints(t, "table", t.shape, device), *t.shape)
+
+
+def _pages(pool: torch.Tensor, r: _Resolved, layers: bool):
     """(layers, n_pages) of a pool."""
-    if pool.dtype != torch.uint8 or not pool.is_contiguous() or pool.dim() not in ((2, 3) if layers else (2,)):
+    if pool.dtype is not torch.uint8 or not pool.is_contiguous() or not (pool.dim() == 2 or (layers and pool.dim() == 3)):
         raise ValueError("pool must be a contiguous uint8 tensor [%sn_pages, page_bytes]" % ("layers, " if layers else ""))
-    if pool.shape[-1] != spec.page_bytes:
-        raise ValueError("pool pages have %d bytes: the spec's have %d" % (pool.shape[-1], spec.page_bytes))
-    return (pool.shape[0] if pool.dim() == 3 else 1), pool.shape[-2]
+    shape = pool.shape
+    if shape[-1] != r.page_bytes:
+        raise ValueError("pool pages have %d bytes: the spec's have %d" % (shape[-1], r.page_bytes))
+    return (shape[0] if len(shape) == 3 else 1), shape[-2]
 
 
 def _seqs(table, lens, cu_q, device):
-    _ints(table, "table", 2, device)
-    if _ints(lens, "lens", 1, device).shape[0] != table.shape[0]:
-        raise ValueError("lens must have one entry for each row of the table")
-    if cu_q is not None and _ints(cu_q, "cu_q", 1, device).shape[0] != table.shape[0] + 1:
-        raise ValueError("cu_q must have one entry more than the table has rows")
-    return hr_cache_seqs(_ptr(table), _ptr(lens), _ptr(cu_q), table.shape[0], table.shape[1])
+    tp, rows, width = _table(table, device)
+    return hr_cache_seqs(tp, _ints(lens, "lens", (rows,), device),
+                         None if cu_q is None else _ints(cu_q, "cu_q", (rows + 1,), device), rows, width)
 
 
-def _vectors(x: torch.Tensor, name: str, heads: int | None, spec: CacheSpec, device):
-    """Checks a [tokens, heads, head_dim] tensor whose last dimension is
-    contiguous; returns its (token, head) strides."""
-    if x.dim() != 3 or x.shape[2] != spec.head_dim or (heads is not None and x.shape[1] != heads):
-        raise ValueError("%s must be [tokens, %s, %d]" % (name, heads if heads is not None else "heads", spec.head_dim))
+def _vectors(x: torch.Tensor, name: str, tokens, heads, d: int, device):
+    """Checks a [tokens, heads, head_dim] tensor (None: any number) whose last
+    dimension is contiguous; returns its (token, head) strides."""
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads) or (tokens is not None and shape[0] != tokens):
+        raise ValueError("%s must be [%s, %s, %d], got %s" % (name, "tokens" if tokens is None else tokens,
+                                                             "heads" if heads is None else heads, d, list(shape)))
     if x.device != device:
         raise ValueError("%s must be on %s" % (name, device))
-    if x.numel() and x.stride(2) != 1:
+    st, sh, se = x.stride()
+    if se != 1:
         raise ValueError("%s: the last dimension must be contiguous" % name)
-    return x.stride(0), x.stride(1)
+    return st, sh
 
 
 def cache_append(pool: torch.Tensor, spec: CacheSpec, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
@@ -177,14 +206,18 @@ def cache_append(pool: torch.Tensor, spec: CacheSpec, k: torch.Tensor, v: torch.
     [tokens, kv_heads, head_dim] into their pages of ``pool`` [n_pages,
     page_bytes].  ``lens`` counts the new tokens already; ``cu_q`` [rows + 1]
     bounds each row's tokens (default: the same number for each)."""
-    _, n = _pool(pool, spec, False)
-    seqs = _seqs(table, lens, cu_q, pool.device)
-    ks = _vectors(k, "k", spec.kv_heads, spec, pool.device)
-    vs = _vectors(v, "v", spec.kv_heads, spec, pool.device)
-    if k.shape != v.shape or k.dtype != v.dtype:
-        raise ValueError("k and v must have the same shape and dtype")
-    check(_cache_lib().hr_cache_append(_ptr(pool), n, ctypes.byref(spec.c()), ctypes.byref(seqs), _ptr(k), *ks, _ptr(v), *vs,
-                                       _dt(k), k.shape[0], int(rotate), _stream(pool)))
+    r, dev = _resolved(spec), pool.device
+    _, n = _pages(pool, r, False)
+    seqs = _seqs(table, lens, cu_q, dev)
+    kt, kh = _vectors(k, "k", None, spec.kv_heads, spec.head_dim, dev)
+    tokens = k.shape[0]
+    vt, vh = _vectors(v, "v", tokens, spec.kv_heads, spec.head_dim, dev)
+    if k.dtype != v.dtype:
+        raise ValueError("k and v must have the same dtype")
+    st = _cache_lib().hr_cache_append(pool.data_ptr(), n, r.ref, ctypes.byref(seqs), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                                      _dt(k), tokens, 1 if rotate else 0, _stream(dev))
+    if st:
+        check(st)
 
 
 def cache_attention(q: torch.Tensor, pool: torch.Tensor, spec: CacheSpec, table: torch.Tensor, lens: torch.Tensor,
@@ -196,40 +229,52 @@ def cache_attention(q: torch.Tensor, pool: torch.Tensor, spec: CacheSpec, table:
     tensor.  ``max_q``: an upper bound of a row's new tokens, if known (it
     only chooses the kernel); ``work``: scratch of cache_attention_work bytes
     (allocated if not given)."""
-    _, n = _pool(pool, spec, False)
-    dev = pool.device
+    r, dev, l = _resolved(spec), pool.device, _cache_lib()
+    _, n = _pages(pool, r, False)
     seqs = _seqs(table, lens, cu_q, dev)
-    qs = _vectors(q, "q", None, spec, dev)
+    qt, qh = _vectors(q, "q", None, None, spec.head_dim, dev)
     tokens, heads = q.shape[0], q.shape[1]
+    dt = _dt(q)
     if out is None:
-        out = torch.empty((tokens, heads, spec.head_dim), dtype=q.dtype, device=dev)
-    os_ = _vectors(out, "out", heads, spec, dev)
-    if out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must have q's shape and dtype")
-    want = lse is not None and lse is not False
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    elif out.dtype != q.dtype:
+        raise ValueError("out must have q's dtype")
+    ot, oh = _vectors(out, "out", tokens, heads, spec.head_dim, dev)
+    lp = None
     if lse is True:
         lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
-    elif want and (lse.dtype != torch.float32 or lse.shape != (tokens, heads) or not lse.is_contiguous() or lse.device != dev):
-        raise ValueError("lse must be a contiguous float32 tensor [tokens, q_heads]")
-    dt, l = _dt(q), _cache_lib()
-    cs = spec.c()
-    with torch.cuda.device(dev):
-        if work is None:
-            need = ctypes.c_int64()
-            check(l.hr_cache_attention_work(dt, tokens, heads, ctypes.byref(cs), table.shape[0], max_q, ctypes.byref(need)))
-            work = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
-        check(l.hr_cache_attention(_ptr(q), *qs, dt, tokens, heads, _ptr(pool), n, ctypes.byref(cs), ctypes.byref(seqs),
-                                   0.0 if scale is None else scale, int(causal), window, int(rotate), _ptr(out), *os_,
-                                   _ptr(lse) if want else None, max_q, _ptr(work), 0 if work is None else work.numel(),
-                                   _stream(pool)))
-    return (out, lse) if want else out
+    if lse is not None and lse is not False:
+        if lse.dtype is not torch.float32 or lse.shape != (tokens, heads) or not lse.is_contiguous() or lse.device != dev:
+            raise ValueError("lse must be a contiguous float32 tensor [tokens, q_heads]")
+        lp = lse.data_ptr()
+    if torch.cuda.current_device() != dev.index:   # (kernels and scratch are chosen for the current device)
+        with torch.cuda.device(dev):
+            return cache_attention(q, pool, spec, table, lens, cu_q, max_q, scale, causal, window, rotate, out,
+                                   lse if lp else None, work)
+    if work is None:
+        key = (dt, tokens, heads, seqs.rows, max_q, dev.index)
+        need = r.work.get(key)
+        if need is None:
+            need = cache_attention_work(q.dtype, tokens, heads, spec, seqs.rows, max_q)
+            if len(r.work) > 4096:
+                r.work.clear()
+            r.work[key] = need
+        if need:
+            work = torch.empty(need, dtype=torch.uint8, device=dev)
+    st = l.hr_cache_attention(q.data_ptr(), qt, qh, dt, tokens, heads, pool.data_ptr(), n, r.ref, ctypes.byref(seqs),
+                              0.0 if scale is None else scale, 1 if causal else 0, window, 1 if rotate else 0, out.data_ptr(), ot,
+                              oh, lp, max_q, None if work is None else work.data_ptr(), 0 if work is None else work.numel(),
+                              _stream(dev))
+    if st:
+        check(st)
+    return (out, lse) if lp else out
 
 
 def cache_attention_work(dtype: torch.dtype, tokens: int, q_heads: int, spec: CacheSpec, rows: int, max_q: int = 0) -> int:
     """Bytes of scratch of a cache_attention call on the current device."""
-    dt = {torch.float32: L.HR_F32, torch.bfloat16: L.HR_BF16}[dtype]
     need = ctypes.c_int64()
-    check(_cache_lib().hr_cache_attention_work(dt, tokens, q_heads, ctypes.byref(spec.c()), rows, max_q, ctypes.byref(need)))
+    check(_cache_lib().hr_cache_attention_work(_DTYPES[dtype], tokens, q_heads, _resolved(spec).ref, rows, max_q,
+                                               ctypes.byref(need)))
     return need.value
 
 
@@ -246,26 +291,26 @@ def cache_update(pool: torch.Tensor, spec: CacheSpec, table: torch.Tensor, lens:
     partly filled ones that two rows would write, hands out free pages in
     ascending order; rows that are nobody's parent give theirs up.  Returns
     dict(table, lens, refs, status): holders of each page, and int32 [4] =
-    pages in use, lacking, copied, free."""
-    layers, n = _pool(pool, spec, True)
-    dev = pool.device
-    _seqs(table, lens, None, dev)
-    rows = _ints(parents, "parents", 1, dev).shape[0]
-    if _ints(grow, "grow", 1, dev).shape[0] != rows:
-        raise ValueError("parents and grow must have the same length")
-    i32 = dict(dtype=torch.int32, device=dev)
+    pages in use, lacking, copied, free.  ``out``: those four tensors, if the
+    caller has them; ``work``: scratch of hr_cache_update_work bytes."""
+    r, dev, l = _resolved(spec), pool.device, _cache_lib()
+    layers, n = _pages(pool, r, True)
+    tp, rows, width = _table(table, dev)
+    lp = _ints(lens, "lens", (rows,), dev)
+    new = parents.numel()
+    pp = _ints(parents, "parents", (new,), dev)
+    gp = _ints(grow, "grow", (new,), dev)
     if out is None:
-        out = {"table": torch.empty((rows, table.shape[1]), **i32), "lens": torch.empty(rows, **i32),
-               "refs": torch.empty(n, **i32), "status": torch.empty(4, **i32)}
-    for name, shape in (("table", (rows, table.shape[1])), ("lens", (rows,)), ("refs", (n,)), ("status", (4,))):
-        if _ints(out[name], name, len(shape), dev).shape != shape:
-            raise ValueError("out[%r] must be %s" % (name, shape))
-    l = _cache_lib()
+        out = {"table": torch.empty((new, width), dtype=torch.int32, device=dev)}
+        out["lens"], out["refs"], out["status"] = torch.empty(new + n + 4, dtype=torch.int32, device=dev).split((new, n, 4))
     if work is None:
-        work = _scratch(l.hr_cache_update_work, dev, n, rows)
-    check(l.hr_cache_update(_ptr(pool), layers, n, ctypes.byref(spec.c()), _ptr(table), _ptr(lens), table.shape[0],
-                            table.shape[1], _ptr(parents), _ptr(grow), rows, _ptr(out["table"]), _ptr(out["lens"]),
-                            _ptr(out["refs"]), _ptr(out["status"]), _ptr(work), work.numel(), _stream(pool)))
+        work = _scratch(l.hr_cache_update_work, dev, n, new)
+    st = l.hr_cache_update(pool.data_ptr(), layers, n, r.ref, tp, lp, rows, width, pp, gp, new,
+                           _ints(out["table"], "out['table']", (new, width), dev), _ints(out["lens"], "out['lens']", (new,), dev),
+                           _ints(out["refs"], "out['refs']", (n,), dev), _ints(out["status"], "out['status']", (4,), dev),
+                           work.data_ptr(), work.numel(), _stream(dev))
+    if st:
+        check(st)
     return out
 
 
@@ -274,26 +319,26 @@ def cache_compact(pool: torch.Tensor, spec: CacheSpec, table: torch.Tensor, lens
     """Moves the live pages to the front of the pool, or copies them into the
     pool ``into``.  Returns dict(table, refs, status): the table in the new
     places, holders of each place, and int32 [4] = live pages, pages without a
-    place, moved, free."""
-    layers, n = _pool(pool, spec, True)
-    dev = pool.device
-    _seqs(table, lens, None, dev)
+    place, moved, free.  ``out``: those three tensors, if the caller has them;
+    ``work``: scratch of hr_cache_compact_work bytes."""
+    r, dev, l = _resolved(spec), pool.device, _cache_lib()
+    layers, n = _pages(pool, r, True)
+    tp, rows, width = _table(table, dev)
+    lp = _ints(lens, "lens", (rows,), dev)
     places = n
     if into is not None:
-        ll, places = _pool(into, spec, True)
+        ll, places = _pages(into, r, True)
         if ll != layers or into.device != dev:
             raise ValueError("into must have the pool's layers and device")
-    i32 = dict(dtype=torch.int32, device=dev)
     if out is None:
-        out = {"table": torch.empty(tuple(table.shape), **i32), "refs": torch.empty(places, **i32),
-               "status": torch.empty(4, **i32)}
-    for name, shape in (("table", tuple(table.shape)), ("refs", (places,)), ("status", (4,))):
-        if tuple(_ints(out[name], name, len(shape), dev).shape) != shape:
-            raise ValueError("out[%r] must be %s" % (name, shape))
-    l = _cache_lib()
+        out = {"table": torch.empty((rows, width), dtype=torch.int32, device=dev)}
+        out["refs"], out["status"] = torch.empty(places + 4, dtype=torch.int32, device=dev).split((places, 4))
     if work is None:
         work = _scratch(l.hr_cache_compact_work, dev, n)
-    check(l.hr_cache_compact(_ptr(pool), layers, n, ctypes.byref(spec.c()), _ptr(table), _ptr(lens), table.shape[0],
-                             table.shape[1], _ptr(into), places if into is not None else 0, _ptr(out["table"]),
-                             _ptr(out["refs"]), _ptr(out["status"]), _ptr(work), work.numel(), _stream(pool)))
+    st = l.hr_cache_compact(pool.data_ptr(), layers, n, r.ref, tp, lp, rows, width, _ptr(into), 0 if into is None else places,
+                            _ints(out["table"], "out['table']", (rows, width), dev),
+                            _ints(out["refs"], "out['refs']", (places,), dev), _ints(out["status"], "out['status']", (4,), dev),
+                            work.data_ptr(), work.numel(), _stream(dev))
+    if st:
+        check(st)
     return out

@@ -101,8 +101,8 @@ int launch_cache_attn(const CacheAttnKey& k, const CacheAttnArgs& a, void* strea
 int cache_attn_workers(const CacheAttnKey& k, int* workers);
 
 // int32 words of scratch
-constexpr int64_t cache_update_words(int64_t n_pages, int64_t new_rows) { return 3 * n_pages + 4 * new_rows + 64; }
-constexpr int64_t cache_compact_words(int64_t n_pages) { return 3 * n_pages + 64; }
+constexpr int64_t cache_update_words(int64_t n_pages, int64_t new_rows) { return 4 * n_pages + 4 * new_rows + 16; }
+constexpr int64_t cache_compact_words(int64_t n_pages) { return 5 * n_pages + 16; }
 
 // Message and status of a failing call on this thread (api.cpp).
 int set_error(int status, const char* text);

@@ -53,6 +53,7 @@ namespace hr {
 namespace {
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bfloat8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
@@ -392,6 +393,22 @@ struct Rows {
     int e;                      // exponent of the value scales in o
 };
 
+// The sign matrix of the index bits that a lane's eight elements and its lane
+// group make (5 of them, H_32) as the A operand of a bfloat16 product: row m of
+// half a is the element 8 (m >> 2) + 4 a + (m & 3), so that the product leaves
+// every result in the lane and register of its input.
+__device__ __forceinline__ uint4v hadamard32(int a) {
+    const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+    const int j = 4 * a + (m & 3);
+    // bit i of byte j: parity of i & j
+    uint32_t s = (j & 1 ? 0xAAu : 0u) ^ (j & 2 ? 0xCCu : 0u) ^ (j & 4 ? 0xF0u : 0u);
+    if (__popc((m >> 2) & g) & 1) s ^= 0xFFu;
+    uint4v f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = 0x3F803F80u | ((s >> (2 * i) & 1u) << 15) | ((s >> (2 * i + 1) & 1u) << 31);
+    return f;
+}
+
 // Loads rows r0 + 16 rt + (lane & 15) of kv head h, rotates them and makes
 // them operands.  Rows past the sequence's repeat its last one.
 template <class C, class T>
@@ -400,6 +417,7 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     float v[C::RT][N];
     float top = 0.0f;
+    const uint4v h0 = hadamard32(0), h1 = hadamard32(1);
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt) {
         const int row = min(r0 + 16 * rt + n, s.n * a.rep - 1);
@@ -415,10 +433,23 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
             if constexpr (sizeof(T) == 2) {
                 uint32_t x[4];
                 load_words<4>(reinterpret_cast<const uint8_t*>(p + at), x);
+                if (a.rotate) {
+                    // bfloat16 times +-1 is exact, and the sums are float32
+                    const uint4v in = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[rt][8 * i + 2 * j] = __uint_as_float(x[j] << 16);
-                    v[rt][8 * i + 2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+                    for (int y = 0; y < 2; ++y) {
+                        const float4v out = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bfloat8, y ? h1 : h0), __builtin_bit_cast(bfloat8, in),
+                            float4v{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[rt][8 * i + 4 * y + j] = out[j];
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[rt][8 * i + 2 * j] = __uint_as_float(x[j] << 16);
+                        v[rt][8 * i + 2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+                    }
                 }
             } else {
                 uint32_t x[8];
@@ -428,10 +459,11 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
             }
         }
         if (a.rotate) {
-            // H over the dimension's bits: those inside the lane, then the two
-            // that are the lane group's
+            // H over the dimension's bits.  bfloat16 rows have those of the
+            // eight elements and of the lane group from the products above, and
+            // want those of the run; float32 rows want all.
 #pragma unroll
-            for (int st = 1; st < N; st *= 2)
+            for (int st = sizeof(T) == 2 ? 8 : 1; st < N; st *= 2)
 #pragma unroll
                 for (int j = 0; j < N; ++j)
                     if (!(j & st)) {
@@ -439,12 +471,16 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
                         v[rt][j] = x + y;
                         v[rt][j + st] = x - y;
                     }
-            // (+ in the lower of two lanes, lower - upper in the other)
-            const uint32_t s0 = (lane & 16) << 27, s1 = (lane & 32) << 26;
-            const auto diff0 = [s0](float x, float y) { return x + __uint_as_float(__float_as_uint(y) ^ s0); };
-            const auto diff1 = [s1](float x, float y) { return x + __uint_as_float(__float_as_uint(y) ^ s1); };
+            if constexpr (sizeof(T) == 4) {
+                // (+ in the lower of two lanes, lower - upper in the other)
+                const uint32_t s0 = (lane & 16) << 27, s1 = (lane & 32) << 26;
+                const auto diff0 = [s0](float x, float y) { return x + __uint_as_float(__float_as_uint(y) ^ s0); };
+                const auto diff1 = [s1](float x, float y) { return x + __uint_as_float(__float_as_uint(y) ^ s1); };
 #pragma unroll
-            for (int j = 0; j < N; ++j) v[rt][j] = over_halves(over_rows(v[rt][j], diff0), diff1) * a.norm;
+                for (int j = 0; j < N; ++j) v[rt][j] = over_halves(over_rows(v[rt][j], diff0), diff1);
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[rt][j] *= a.norm;
         }
         // (a row of infinities or NaN scales nothing: it gives NaN all the same)
         float own = 0.0f;
@@ -959,6 +995,12 @@ __device__ __forceinline__ void segment(const CacheAttnArgs& a, const Seq& s, in
     else put_rows<C, T>(a, s, h, row, st, part, row - r0);
 }
 
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+    return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
 // The items of a sequence: for each kv head and row block a unit of kSetup items
 // that stand for its start and end, then one for each block of keys, at least
 // one so that rows that see nothing are written too.
@@ -978,7 +1020,7 @@ __device__ __forceinline__ Items items_of(const CacheAttnArgs& a, const Seq& s) 
         it.first = min(sp.lo, sp.hi) & ~31;
         it.blocks = max((sp.hi - it.first + C::KEYS - 1) / C::KEYS, 1);
     }
-    it.total = static_cast<int64_t>(a.pg.hkv) * it.rbs * (it.blocks + kSetup);
+    it.total = static_cast<int64_t>(a.pg.hkv * it.rbs) * (it.blocks + kSetup);
     return it;
 }
 
@@ -1005,68 +1047,77 @@ __device__ __forceinline__ int64_t scan_items(int64_t v, int64_t* all, int64_t* 
     return before + inc - v;
 }
 
+// How the items are shared out: every workgroup of the first nw has `share`,
+// and the first `rest` of them one more.
+struct Shares {
+    int64_t total, share, rest;
+    __device__ __forceinline__ int64_t first(int64_t w) const { return w * share + min(w, rest); }
+    // the workgroup that holds item u
+    __device__ __forceinline__ int64_t holder(int64_t u) const {
+        const int64_t longer = rest * (share + 1);
+        return u < longer ? u / (share + 1) : rest + (u - longer) / share;
+    }
+};
+
 // Workgroup w of the split form: its items [i0, i1), the sequence b that holds
 // the first and the items before that sequence.  Every thread takes part.
 struct Place {
-    int64_t total, nw;    // items of the call, workgroups that share them
+    Shares sh;
     int64_t i0, i1, before;
     int b;
+    Seq s;                // sequence b
 };
 template <class C>
 __device__ __forceinline__ Place place(const CacheAttnArgs& a, int64_t* lds) {
     const int tid = threadIdx.x;
     Place p;
     int64_t total = 0, own = 0, pre = 0;
+    Seq s = {0, 0, 0};
+    const auto items = [&](int b) {
+        if (b >= a.sq.rows) return int64_t{0};
+        s = seq_at<false>(a.sq, a.pg.logp, b);
+        return items_of<C>(a, s).total;
+    };
     // (a call of up to 256 sequences is scanned once)
     for (int c = 0; c < a.sq.rows; c += 256) {
-        const int b = c + tid;
-        own = b < a.sq.rows ? items_of<C>(a, seq_at<false>(a.sq, a.pg.logp, b)).total : 0;
+        own = items(c + tid);
         int64_t all;
         pre = total + scan_items(own, &all, lds);
         total += all;
     }
-    const int64_t nw = total < a.workers ? (total > 0 ? total : 1) : a.workers;
-    const int64_t w = blockIdx.x;
-    p.total = total;
-    p.nw = nw;
-    p.i0 = w < nw ? w * total / nw : total;
-    p.i1 = w < nw ? (w + 1) * total / nw : total;
+    total = uniform64(total);
+    const uint32_t nw = total < a.workers ? static_cast<uint32_t>(max(total, int64_t{1})) : a.workers;
+    p.sh.total = total;
+    p.sh.share = total < (int64_t{1} << 31) ? static_cast<int64_t>(static_cast<uint32_t>(total) / nw) : total / nw;
+    p.sh.rest = total - p.sh.share * nw;
+    const int64_t w = min(blockIdx.x, nw);
+    p.i0 = p.sh.first(w);
+    p.i1 = min(p.sh.first(w + 1), total);
     if (tid == 0) lds[4] = -1;
     int64_t base = 0;
     for (int c = 0; c < a.sq.rows; c += 256) {
-        const int b = c + tid;
         if (a.sq.rows > 256) {
-            own = b < a.sq.rows ? items_of<C>(a, seq_at<false>(a.sq, a.pg.logp, b)).total : 0;
+            own = items(c + tid);
             int64_t all;
             pre = base + scan_items(own, &all, lds);
             base += all;
         }
         __syncthreads();
         if (p.i0 >= pre && p.i0 < pre + own) {
-            lds[4] = b;
+            lds[4] = c + tid;
             lds[5] = pre;
+            lds[6] = s.start;
+            lds[7] = static_cast<int64_t>(s.n) << 32 | static_cast<uint32_t>(s.len);
         }
         __syncthreads();
         if (lds[4] >= 0) break;
     }
-    p.b = lds[4] >= 0 ? static_cast<int>(lds[4]) : a.sq.rows;
-    p.before = lds[5];
+    p.b = lds[4] >= 0 ? __builtin_amdgcn_readfirstlane(static_cast<int>(lds[4])) : a.sq.rows;
+    p.before = uniform64(lds[5]);
+    const int64_t nl = uniform64(lds[7]);
+    p.s = {__builtin_amdgcn_readfirstlane(static_cast<int>(lds[6])), static_cast<int>(nl >> 32), static_cast<int>(nl)};
     __syncthreads();
     return p;
-}
-
-__device__ __forceinline__ int64_t uniform64(int64_t v) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
-    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
-    return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
-}
-
-// The workgroup that holds item u.
-__device__ __forceinline__ int64_t holder(int64_t u, int64_t nw, int64_t total) {
-    int64_t w = u * nw / total;
-    while (w + 1 < nw && (w + 1) * total / nw <= u) ++w;
-    while (w > 0 && w * total / nw > u) --w;
-    return w;
 }
 
 // What the joining launch needs of a unit that begins in a workgroup and goes
@@ -1083,19 +1134,26 @@ template <class C, class T>
 __global__ void __launch_bounds__(256, C::WAVES) cache_attn_split(const CacheAttnArgs a) {
     __shared__ float lds[join_floats<C>()];
     const Place p = place<C>(a, reinterpret_cast<int64_t*>(lds));
-    int64_t i0 = uniform64(p.i0);
-    const int64_t i1 = uniform64(p.i1);
-    int64_t before = uniform64(p.before);
+    int64_t i0 = p.i0;
+    const int64_t i1 = p.i1;
+    int64_t before = p.before;
     constexpr int SLOT = C::ROWS * part_stride<C>();
     Cut* cuts = reinterpret_cast<Cut*>(a.work + static_cast<int64_t>(a.workers) * 2 * SLOT);
     Cut cut = {0, 0, 0, 0, -1};
-    for (int b = __builtin_amdgcn_readfirstlane(p.b); b < a.sq.rows && i0 < i1; ++b) {
-        const Seq s = seq_at<true>(a.sq, a.pg.logp, b);
+    for (int b = p.b; b < a.sq.rows && i0 < i1; ++b) {
+        const Seq s = b == p.b ? p.s : seq_at<true>(a.sq, a.pg.logp, b);
         const Items it = items_of<C>(a, s);
         const int size = it.blocks + kSetup;
         while (i0 < i1 && i0 < before + it.total) {
             const int64_t at = i0 - before;
-            const int unit = static_cast<int>(at / size), from = static_cast<int>(at % size);
+            int unit, from;
+            if (at < (int64_t{1} << 31)) {
+                unit = static_cast<uint32_t>(at) / static_cast<uint32_t>(size);
+                from = static_cast<int>(at) - unit * size;
+            } else {
+                unit = static_cast<int>(at / size);
+                from = static_cast<int>(at % size);
+            }
             const int64_t share = i1 - i0;
             const int to = share < size - from ? from + static_cast<int>(share) : size;
             i0 += to - from;
@@ -1106,7 +1164,7 @@ __global__ void __launch_bounds__(256, C::WAVES) cache_attn_split(const CacheAtt
             if (k > 0 || end < it.blocks) part = a.work + (2 * static_cast<int64_t>(blockIdx.x) + (k == 0 ? 1 : 0)) * SLOT;
             if (k == 0 && end < it.blocks)
                 cut = {s.start, s.n, h, r0,
-                       static_cast<int>(holder(before + static_cast<int64_t>(unit + 1) * size - 1, p.nw, p.total))};
+                       static_cast<int>(p.sh.holder(before + static_cast<int64_t>(unit + 1) * size - 1))};
             segment<C, T>(a, s, b, h, r0, it.first + k * C::KEYS, it.first + end * C::KEYS, part, lds);
         }
         before += it.total;

@@ -246,15 +246,16 @@ int append_dim(const CacheAppendArgs& a, hipStream_t s) {
 // update and compact
 //
 // Both count the holders of every page from the table itself (integer
-// additions, so the order of the atomics does not matter), number the free or
-// live pages by a scan in ascending order in one workgroup, and then write the
-// new table and copy the pages in one launch.
+// additions, so the order of the atomics does not matter) and number the free
+// or live pages in ascending order.  One workgroup does that, its counters in
+// LDS where the pool's pages fit (kPlanPages) and in the scratch otherwise; a
+// second launch writes the new table and copies the pages.  The plan is a few
+// dependent passes over some ten thousand integers: in LDS it takes 5 to 9 us,
+// where counting by one launch and scanning by another took 20 to 25 with the
+// gaps between them.
 
-constexpr int kScan = 1024;  // threads of a scanning workgroup
-
-__global__ void __launch_bounds__(256) fill_words(int32_t* p, int64_t n, int32_t v) {
-    for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) p[i] = v;
-}
+constexpr int kScan = 1024;        // threads of the planning workgroup
+constexpr int kPlanPages = 12288;  // pages whose three counters fit LDS
 
 // exclusive sum of v over the workgroup's kScan threads, and the total
 __device__ __forceinline__ int scan_wg(int v, int* total, int* lds) {
@@ -303,121 +304,166 @@ __device__ __forceinline__ int page_in(int32_t page, int64_t n) {
     return page >= 0 && page < n ? page : -1;
 }
 
-// refs: entries of the new rows that inherit a page; writers, lowest: how many
-// rows go on in it, and the lowest of them.  A workgroup a row.
-__global__ void __launch_bounds__(256) update_count(const CacheUpdateArgs a, int32_t* writers, int32_t* lowest) {
-    for (int i = blockIdx.x; i < a.new_rows; i += gridDim.x) {
+// Entries of the table are taken by groups of 16 lanes, a row each at a time.
+constexpr int kRowLanes = 16;
+
+// The plan of an update: which row copies its last page (copies[i], the page
+// or -1), the number base[i] of free pages handed out before row i's, the free
+// pages in ascending order as far as they are needed, the copies (from, to)
+// with their number, refs and status.
+template <bool LDS>
+__global__ void __launch_bounds__(kScan) update_plan(const CacheUpdateArgs a, int32_t* base, int32_t* copies, int32_t* free_list,
+                                                     int32_t* moves, int32_t* counters) {
+    extern __shared__ int32_t counts[];
+    __shared__ int lds[kScan / 64];
+    const int n = static_cast<int>(a.n_pages), tid = threadIdx.x;
+    int32_t* held = LDS ? counts : counters;       // entries of the new rows that inherit a page
+    int32_t* writers = held + n;                   // rows that go on in it
+    int32_t* lowest = writers + n;                 // the lowest of them
+    for (int p = tid; p < n; p += kScan) {
+        held[p] = 0;
+        writers[p] = 0;
+        lowest[p] = 0x7FFFFFFF;
+    }
+    __threadfence_block();
+    __syncthreads();
+    for (int i = tid / kRowLanes; i < a.new_rows; i += kScan / kRowLanes) {
         const Kept k = kept_of(a, i);
-        for (int j = threadIdx.x; j < k.kept; j += 256) {
-            const int p = page_in(k.row[j], a.n_pages);
+#pragma unroll 4
+        for (int j = tid % kRowLanes; j < k.kept; j += kRowLanes) {
+            const int p = page_in(k.row[j], n);
             if (p < 0) continue;
-            atomicAdd(a.refs + p, 1);
+            atomicAdd(held + p, 1);
             if (j == k.last) {
                 atomicAdd(writers + p, 1);
                 atomicMin(lowest + p, i);
             }
         }
     }
-}
-
-// Which row copies its last page, how many pages each row needs before it,
-// and the free pages in ascending order (as many as are needed).
-__global__ void __launch_bounds__(kScan) update_plan(const CacheUpdateArgs a, const int32_t* writers, const int32_t* lowest,
-                                                     int32_t* base, int32_t* copies, int32_t* free_list, int32_t* counts) {
-    __shared__ int lds[kScan / 64];
-    int need = 0;
+    __threadfence_block();
+    __syncthreads();
+    int need = 0, done = 0, total;
     for (int c = 0; c < a.new_rows; c += kScan) {
-        const int i = c + threadIdx.x;
-        int mine = 0, copy = 0;
+        const int i = c + tid;
+        int mine = 0, copy = -1;
         if (i < a.new_rows) {
             const Kept k = kept_of(a, i);
             if (k.last >= 0) {
-                const int p = page_in(k.row[k.last], a.n_pages);
-                copy = p >= 0 && !(lowest[p] == i && a.refs[p] == writers[p]);
+                const int p = page_in(k.row[k.last], n);
+                if (p >= 0 && !(lowest[p] == i && held[p] == writers[p])) copy = p;
             }
-            mine = copy + k.held - k.kept;
+            mine = (copy >= 0) + k.held - k.kept;
             copies[i] = copy;
         }
-        int total;
         const int before = scan_wg(mine, &total, lds);
         if (i < a.new_rows) base[i] = need + before;
         need += total;
     }
-    int found = 0;
-    for (int64_t c = 0; c < a.n_pages; c += kScan) {
-        const int64_t p = c + threadIdx.x;
-        const int is = p < a.n_pages && a.refs[p] == 0;
-        int total;
-        const int before = scan_wg(is, &total, lds);
-        if (is && found + before < need) free_list[found + before] = static_cast<int32_t>(p);
-        found += total;
-    }
-    if (threadIdx.x == 0) {
-        counts[0] = need;
-        counts[1] = found;
-    }
-}
-
-// Copies n 16-byte words with the workgroup.
-__device__ __forceinline__ void copy_words(const uint4v* from, uint4v* to, int64_t n) {
-    for (int64_t i = threadIdx.x; i < n; i += 256) to[i] = from[i];
-}
-
-// blockIdx.y = 0: row i of the new table; above: the row's copy, one layer each.
-__global__ void __launch_bounds__(256) update_write(const CacheUpdateArgs a, const int32_t* base, const int32_t* copies,
-                                                    const int32_t* free_list, const int32_t* counts) {
-    const int found = counts[1];
-    for (int i = blockIdx.x; i < a.new_rows; i += gridDim.x) {
-        const Kept k = kept_of(a, i);
-        const int at = base[i], copy = copies[i];
-        const int own = copy ? (at < found ? free_list[at] : -1) : -1;
-        if (blockIdx.y > 0) {
-            const int src = copy ? page_in(k.row[k.last], a.n_pages) : -1;
-            if (own < 0 || src < 0) continue;
-            for (int64_t l = blockIdx.y - 1; l < a.layers; l += gridDim.y - 1) {
-                uint8_t* layer = a.pool + l * a.n_pages * a.page_bytes;
-                copy_words(reinterpret_cast<const uint4v*>(layer + src * a.page_bytes),
-                           reinterpret_cast<uint4v*>(layer + own * a.page_bytes), a.page_bytes / 16);
+    // free pages: a thread numbers a run of neighbouring pages.  (writers is
+    // no longer needed and takes the counts of the rows that copy.)
+    __syncthreads();
+    for (int p = tid; p < n; p += kScan) writers[p] = 0;
+    __threadfence_block();
+    __syncthreads();
+    const int run = (n + kScan - 1) / kScan, p0 = min(tid * run, n), p1 = min(p0 + run, n);
+    int mine = 0;
+    for (int p = p0; p < p1; ++p) mine += held[p] == 0;
+    int found;
+    int rank = scan_wg(mine, &found, lds);
+    for (int p = p0; p < p1; ++p)
+        if (held[p] == 0) {
+            if (rank < need) {
+                free_list[rank] = p;
+                lowest[p] = -1;          // handed out
             }
-            continue;
+            ++rank;
         }
+    __threadfence_block();
+    for (int c = 0; c < a.new_rows; c += kScan) {
+        const int i = c + tid;
+        int at = 0, src = -1;
+        if (i < a.new_rows) {            // (this thread's own stores of the first loop)
+            at = base[i];
+            src = copies[i];
+            if (src >= 0) atomicAdd(writers + src, 1);
+        }
+        const bool does = src >= 0 && at < found;
+        const int m = done + scan_wg(does, &total, lds);   // (its barriers make the free pages visible)
+        if (does) {
+            moves[2 * m] = src;
+            moves[2 * m + 1] = free_list[at];
+        }
+        done += total;
+    }
+    __threadfence_block();
+    __syncthreads();
+    for (int p = tid; p < n; p += kScan) a.refs[p] = lowest[p] < 0 ? 1 : held[p] - writers[p];
+    if (tid == 0) {
+        const int given = min(need, found), used = n - found + given;
+        a.status[0] = used;
+        a.status[1] = need - given;
+        a.status[2] = done;
+        moves[2 * a.new_rows] = done;
+        a.status[3] = n - used;
+        base[a.new_rows] = found;
+    }
+}
+
+// Copies bytes [b0, b1) of a page (multiples of 16), eight loads on their way
+// in every thread.
+constexpr int kChunk = 256 * 8 * 16;
+__device__ __forceinline__ void copy_chunk(const uint8_t* from, uint8_t* to, int64_t b0, int64_t bytes) {
+    const int64_t at = b0 + threadIdx.x * 16;
+    if (b0 + kChunk <= bytes) {
+        uint4v x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __builtin_nontemporal_load(reinterpret_cast<const uint4v*>(from + at + i * 4096));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) __builtin_nontemporal_store(x[i], reinterpret_cast<uint4v*>(to + at + i * 4096));
+    } else {
+        for (int64_t i = at; i < bytes; i += 4096)
+            *reinterpret_cast<uint4v*>(to + i) = *reinterpret_cast<const uint4v*>(from + i);
+    }
+}
+
+// Copies pages: workgroup b of n takes every n-th chunk of a page of one layer.
+__device__ __forceinline__ void copy_pages(const uint8_t* from, int64_t from_pages, uint8_t* to, int64_t to_pages, int64_t bytes,
+                                           int64_t layers, const int32_t* moves, int n_moves, int b, int n) {
+    const int64_t chunks = (bytes + kChunk - 1) / kChunk, units = n_moves * layers * chunks;
+    for (int64_t u = b; u < units; u += n) {
+        const int64_t page = u / chunks, m = page / layers, l = page % layers;
+        copy_chunk(from + (l * from_pages + moves[2 * m]) * bytes, to + (l * to_pages + moves[2 * m + 1]) * bytes,
+                   u % chunks * kChunk, bytes);
+    }
+}
+constexpr int kCopyGrid = 1024;  // workgroups that copy: 16 waves with eight loads each on a CU
+
+// The first `rows` workgroups write the new table, a row each at a time; the
+// others copy.
+__global__ void __launch_bounds__(256) update_write(const CacheUpdateArgs a, const int32_t* base, const int32_t* copies,
+                                                    const int32_t* free_list, const int32_t* moves, int rows) {
+    if (static_cast<int>(blockIdx.x) >= rows) {
+        copy_pages(a.pool, a.n_pages, a.pool, a.n_pages, a.page_bytes, a.layers, moves, moves[2 * a.new_rows], blockIdx.x - rows,
+                   gridDim.x - rows);
+        return;
+    }
+    const int found = base[a.new_rows];
+    for (int i = blockIdx.x; i < a.new_rows; i += rows) {
+        const int at = base[i];
+        const bool copy = copies[i] >= 0;
+        const Kept k = kept_of(a, i);
         int32_t* row = a.new_table + static_cast<int64_t>(i) * a.max_pages;
         for (int j = threadIdx.x; j < a.max_pages; j += 256) {
             int p = -1;
-            if (j < k.kept) {
+            if (j < k.kept && !(copy && j == k.last)) {
                 p = page_in(k.row[j], a.n_pages);
-                if (copy && j == k.last) {
-                    atomicAdd(a.refs + p, -1);   // copy: p is a page
-                    p = own;
-                    if (p >= 0) a.refs[p] = 1;
-                }
             } else if (j < k.held) {
-                const int64_t f = static_cast<int64_t>(at) + copy + j - k.kept;
+                const int64_t f = at + (j < k.kept ? int64_t{0} : static_cast<int64_t>(copy) + j - k.kept);
                 p = f < found ? free_list[f] : -1;
-                if (p >= 0) a.refs[p] = 1;
             }
             row[j] = p;
         }
         if (threadIdx.x == 0) a.new_lens[i] = k.after;
-    }
-}
-
-// status: in use = inherited pages (all but the free ones) + those handed out
-__global__ void __launch_bounds__(kScan) update_status(const CacheUpdateArgs a, const int32_t* base, const int32_t* copies,
-                                                       const int32_t* counts) {
-    __shared__ int lds[kScan / 64];
-    const int need = counts[0], found = counts[1];
-    int done = 0;
-    for (int i = threadIdx.x; i < a.new_rows; i += kScan) done += copies[i] && base[i] < found;
-    int total;
-    scan_wg(done, &total, lds);
-    if (threadIdx.x == 0) {
-        const int given = min(need, found);
-        const int used = static_cast<int>(a.n_pages) - found + given;
-        a.status[0] = used;
-        a.status[1] = need - given;
-        a.status[2] = total;
-        a.status[3] = static_cast<int>(a.n_pages) - used;
     }
 }
 
@@ -427,68 +473,90 @@ __device__ __forceinline__ int held_pages(const CacheCompactArgs& a, int i) {
     return static_cast<int>((len + a.page - 1) / a.page);
 }
 
-// counts[p]: entries of the table that hold page p
-__global__ void __launch_bounds__(256) compact_count(const CacheCompactArgs a, int32_t* counts) {
-    for (int i = blockIdx.x; i < a.rows; i += gridDim.x) {
-        const int held = held_pages(a, i);
-        const int32_t* row = a.table + static_cast<int64_t>(i) * a.max_pages;
-        for (int j = threadIdx.x; j < held; j += 256) {
-            const int p = page_in(row[j], a.n_pages);
-            if (p >= 0) atomicAdd(counts + p, 1);
-        }
-    }
-}
-
-// to[p]: the new place of page p, or -1.  Within the pool also the list of
-// holes (places below the number of live pages that are free), ascending.
-__global__ void __launch_bounds__(kScan) compact_plan(const CacheCompactArgs a, const int32_t* counts, int32_t* to,
-                                                      int32_t* holes) {
+// The plan of a compaction: to[p], the new place of page p or -1; the moves
+// (from, to) with their number; refs and status.
+template <bool LDS>
+__global__ void __launch_bounds__(kScan) compact_plan(const CacheCompactArgs a, int32_t* to, int32_t* moves, int32_t* counters) {
+    extern __shared__ int32_t counts[];
     __shared__ int lds[kScan / 64];
-    int live = 0;
-    for (int64_t p = threadIdx.x; p < a.n_pages; p += kScan) live += counts[p] > 0;
-    int total;
-    scan_wg(live, &total, lds);
-    live = total;
-    int rank = 0, moved = 0, free = 0;
-    if (!a.into) {
-        for (int64_t c = 0; c < live; c += kScan) {
-            const int64_t p = c + threadIdx.x;
-            const int is = p < live && counts[p] == 0;
-            const int before = scan_wg(is, &total, lds);
-            if (is) holes[free + before] = static_cast<int32_t>(p);
-            free += total;
+    const int n = static_cast<int>(a.n_pages), places = static_cast<int>(a.into_pages), tid = threadIdx.x;
+    int32_t* held = LDS ? counts : counters;     // entries of the table that hold a page
+    int32_t* holes = held + n;                   // free places below the number of live pages
+    for (int p = tid; p < n; p += kScan) held[p] = 0;
+    for (int p = tid; p < places; p += kScan) a.refs[p] = 0;
+    __threadfence_block();
+    __syncthreads();
+    for (int i = tid / kRowLanes; i < a.rows; i += kScan / kRowLanes) {
+        const int k = held_pages(a, i);
+        const int32_t* row = a.table + static_cast<int64_t>(i) * a.max_pages;
+#pragma unroll 4
+        for (int j = tid % kRowLanes; j < k; j += kRowLanes) {
+            const int p = page_in(row[j], n);
+            if (p >= 0) atomicAdd(held + p, 1);
         }
-        __threadfence_block();
-        __syncthreads();
     }
-    for (int64_t c = 0; c < a.n_pages; c += kScan) {
-        const int64_t p = c + threadIdx.x;
-        const bool is = p < a.n_pages && counts[p] > 0;
-        const bool counted = is && (a.into || p >= live);
-        const int before = scan_wg(counted, &total, lds);
-        if (p < a.n_pages) {
+    __threadfence_block();
+    __syncthreads();
+    // a thread numbers a run of neighbouring pages
+    const int run = (n + kScan - 1) / kScan, p0 = min(tid * run, n), p1 = min(p0 + run, n);
+    int mine = 0, live;
+    for (int p = p0; p < p1; ++p) mine += held[p] > 0;
+    const int live_before = scan_wg(mine, &live, lds);
+    int moved;
+    if (a.into) {
+        moved = min(live, places);
+        int rank = live_before;
+        for (int p = p0; p < p1; ++p) {
             int t = -1;
-            if (is && a.into) t = rank + before < a.into_pages ? rank + before : -1;
-            else if (is) t = p < live ? static_cast<int>(p) : holes[rank + before];
+            if (held[p] > 0 && rank++ < places) {
+                t = rank - 1;
+                a.refs[t] = held[p];
+                moves[2 * t] = p;
+                moves[2 * t + 1] = t;
+            }
             to[p] = t;
         }
-        rank += total;
+    } else {
+        // holes below `live`: as many as live pages at and above it
+        const int free_before = p0 - live_before;
+        int rank = free_before;
+        for (int p = p0; p < min(p1, live); ++p)
+            if (held[p] == 0) holes[rank++] = p;
+        mine = 0;
+        for (int p = max(p0, live); p < p1; ++p) mine += held[p] > 0;
+        rank = scan_wg(mine, &moved, lds);       // (its barriers make the holes visible)
+        __threadfence_block();
+        __syncthreads();
+        for (int p = p0; p < p1; ++p) {
+            int t = -1;
+            if (held[p] > 0) {
+                t = p;
+                if (p >= live) {
+                    t = holes[rank];
+                    moves[2 * rank] = p;
+                    moves[2 * rank + 1] = t;
+                    ++rank;
+                }
+                a.refs[t] = held[p];
+            }
+            to[p] = t;
+        }
     }
-    moved = a.into ? static_cast<int>(min(static_cast<int64_t>(rank), a.into_pages)) : rank;
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
         const int placed = a.into ? moved : live;
         a.status[0] = live;
         a.status[1] = live - placed;
         a.status[2] = moved;
-        a.status[3] = static_cast<int>(a.into_pages) - placed;
+        a.status[3] = places - placed;
+        moves[2 * n] = moved;
     }
 }
 
-// The new table (blockIdx.y = 0), the counts in the new places (1) and the pages
-// themselves (2 and above: a layer each).
-__global__ void __launch_bounds__(256) compact_write(const CacheCompactArgs a, const int32_t* counts, const int32_t* to) {
-    if (blockIdx.y == 0) {
-        for (int i = blockIdx.x; i < a.rows; i += gridDim.x) {
+// The first `rows` workgroups write the new table, a row each; the others copy
+// the pages, a chunk of a page of one layer at a time.
+__global__ void __launch_bounds__(256) compact_write(const CacheCompactArgs a, const int32_t* to, const int32_t* moves, int rows) {
+    if (static_cast<int>(blockIdx.x) < rows) {
+        for (int i = blockIdx.x; i < a.rows; i += rows) {
             const int held = held_pages(a, i);
             const int64_t at = static_cast<int64_t>(i) * a.max_pages;
             for (int j = threadIdx.x; j < a.max_pages; j += 256) {
@@ -498,26 +566,24 @@ __global__ void __launch_bounds__(256) compact_write(const CacheCompactArgs a, c
         }
         return;
     }
-    if (blockIdx.y == 1) {
-        for (int64_t p = blockIdx.x * 256 + threadIdx.x; p < a.n_pages; p += static_cast<int64_t>(gridDim.x) * 256)
-            if (to[p] >= 0) a.refs[to[p]] = counts[p];
-        return;
-    }
-    for (int64_t p = blockIdx.x; p < a.n_pages; p += gridDim.x) {
-        const int t = to[p];
-        if (t < 0 || (!a.into && t == p)) continue;
-        for (int64_t l = blockIdx.y - 2; l < a.layers; l += gridDim.y - 2) {
-            const uint8_t* from = a.pool + (l * a.n_pages + p) * a.page_bytes;
-            uint8_t* dst = (a.into ? a.into + l * a.into_pages * a.page_bytes : a.pool + l * a.n_pages * a.page_bytes) +
-                           t * a.page_bytes;
-            copy_words(reinterpret_cast<const uint4v*>(from), reinterpret_cast<uint4v*>(dst), a.page_bytes / 16);
-        }
-    }
+    copy_pages(a.pool, a.n_pages, a.into ? a.into : a.pool, a.into_pages, a.page_bytes, a.layers, moves, moves[2 * a.n_pages],
+               blockIdx.x - rows, gridDim.x - rows);
 }
 
-int fill(int32_t* p, int64_t n, int32_t v, hipStream_t s) {
-    const int64_t grid = (n + 255) / 256;
-    hipLaunchKernelGGL(fill_words, dim3(static_cast<uint32_t>(grid < 1024 ? grid : 1024)), dim3(256), 0, s, p, n, v);
+// Launches a planning kernel: in LDS if its counters fit, else in the scratch.
+template <class A, class... P>
+int plan(void (*in_lds)(A, P...), void (*in_scratch)(A, P...), int words, const A& a, hipStream_t s, P... args) {
+    const size_t bytes = static_cast<size_t>(words) * a.n_pages * 4;
+    if (a.n_pages <= kPlanPages) {
+        if (bytes > 65536) {
+            const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(in_lds), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                     static_cast<int>(bytes));
+            if (e != hipSuccess) return static_cast<int>(e);
+        }
+        hipLaunchKernelGGL(in_lds, dim3(1), dim3(kScan), bytes, s, a, args...);
+    } else {
+        hipLaunchKernelGGL(in_scratch, dim3(1), dim3(kScan), 0, s, a, args...);
+    }
     return static_cast<int>(hipGetLastError());
 }
 
@@ -530,38 +596,26 @@ int launch_cache_append(const CacheAppendArgs& a, int bf16, void* stream) {
 
 int launch_cache_update(const CacheUpdateArgs& a, void* stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    int32_t* writers = a.work;
-    int32_t* lowest = writers + a.n_pages;
-    int32_t* free_list = lowest + a.n_pages;
-    int32_t* base = free_list + a.n_pages;
-    int32_t* copies = base + a.new_rows;
-    int32_t* counts = copies + a.new_rows;
-    int e;
-    if ((e = fill(a.refs, a.n_pages, 0, s)) || (e = fill(writers, a.n_pages, 0, s)) ||
-        (e = fill(lowest, a.n_pages, 0x7FFFFFFF, s)))
-        return e;
-    const uint32_t rows = static_cast<uint32_t>(a.new_rows < 65536 ? (a.new_rows > 0 ? a.new_rows : 1) : 65536);
-    hipLaunchKernelGGL(update_count, dim3(rows), dim3(256), 0, s, a, writers, lowest);
-    hipLaunchKernelGGL(update_plan, dim3(1), dim3(kScan), 0, s, a, writers, lowest, base, copies, free_list, counts);
-    hipLaunchKernelGGL(update_write, dim3(rows, static_cast<uint32_t>(a.layers < 1024 ? a.layers : 1024) + 1), dim3(256), 0, s, a,
-                       base, copies, free_list, counts);
-    hipLaunchKernelGGL(update_status, dim3(1), dim3(kScan), 0, s, a, base, copies, counts);
+    int32_t* base = a.work;                       // new_rows + 1
+    int32_t* copies = base + a.new_rows + 1;      // new_rows
+    int32_t* moves = copies + a.new_rows;         // 2 new_rows + 1
+    int32_t* free_list = moves + 2 * a.new_rows + 1;
+    const int e = plan(update_plan<true>, update_plan<false>, 3, a, s, base, copies, free_list, moves, free_list + a.n_pages);
+    if (e || a.new_rows == 0) return e;
+    const int rows = a.new_rows < 4096 ? a.new_rows : 4096;
+    hipLaunchKernelGGL(update_write, dim3(static_cast<uint32_t>(rows + kCopyGrid)), dim3(256), 0, s, a, base, copies, free_list, moves,
+                       rows);
     return static_cast<int>(hipGetLastError());
 }
 
 int launch_cache_compact(const CacheCompactArgs& a, void* stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    int32_t* counts = a.work;
-    int32_t* to = counts + a.n_pages;
-    int32_t* holes = to + a.n_pages;
-    int e;
-    if ((e = fill(counts, a.n_pages, 0, s)) || (e = fill(a.refs, a.into_pages, 0, s))) return e;
-    const uint32_t rows = static_cast<uint32_t>(a.rows < 65536 ? (a.rows > 0 ? a.rows : 1) : 65536);
-    hipLaunchKernelGGL(compact_count, dim3(rows), dim3(256), 0, s, a, counts);
-    hipLaunchKernelGGL(compact_plan, dim3(1), dim3(kScan), 0, s, a, counts, to, holes);
-    const uint32_t pages = static_cast<uint32_t>(a.n_pages < 4096 ? a.n_pages : 4096);
-    hipLaunchKernelGGL(compact_write, dim3(pages, static_cast<uint32_t>(a.layers < 1024 ? a.layers : 1024) + 2), dim3(256), 0, s, a,
-                       counts, to);
+    int32_t* to = a.work;
+    int32_t* moves = to + a.n_pages;              // 2 n_pages + 1
+    const int e = plan(compact_plan<true>, compact_plan<false>, 2, a, s, to, moves, moves + 2 * a.n_pages + 1);
+    if (e) return e;
+    const int rows = a.rows < 4096 ? a.rows : 4096;
+    hipLaunchKernelGGL(compact_write, dim3(static_cast<uint32_t>(rows + kCopyGrid)), dim3(256), 0, s, a, to, moves, rows);
     return static_cast<int>(hipGetLastError());
 }
 

@@ -487,7 +487,8 @@ def run_update(rows, new_rows, n_pages, max_pages, page, layers, seed, grow_to=4
 
 @pytest.mark.parametrize("rows,new_rows,n_pages,max_pages,page,layers", [
     (1, 1, 4, 2, 16, 1), (5, 8, 40, 6, 16, 2), (30, 20, 100, 7, 32, 1), (64, 64, 500, 9, 16, 3), (3, 700, 900, 5, 16, 1),
-    (700, 40, 3000, 5, 16, 1), (300, 1500, 9000, 8, 16, 1), (20, 20, 33, 6, 16, 1)])
+    (700, 40, 3000, 5, 16, 1), (300, 1500, 9000, 8, 16, 1), (20, 20, 33, 6, 16, 1), (40, 1100, 12288, 30, 16, 1),
+    (40, 1100, 13001, 30, 16, 1)])
 def test_update(rows, new_rows, n_pages, max_pages, page, layers):
     for seed in range(3):
         run_update(rows, new_rows, n_pages, max_pages, page, layers, seed)
@@ -530,7 +531,8 @@ def run_compact(rows, n_pages, max_pages, page, layers, seed, into=None):
 
 
 @pytest.mark.parametrize("into", [None, 1, 17, 4000])
-@pytest.mark.parametrize("rows,n_pages,max_pages,layers", [(1, 1, 1, 1), (4, 30, 5, 2), (50, 400, 9, 1), (600, 5000, 7, 2), (3, 9000, 4, 1)])
+@pytest.mark.parametrize("rows,n_pages,max_pages,layers", [(1, 1, 1, 1), (4, 30, 5, 2), (50, 400, 9, 1), (600, 5000, 7, 2), (3, 9000, 4, 1),
+                                                           (300, 12288, 30, 1), (300, 12290, 30, 1)])
 def test_compact(rows, n_pages, max_pages, layers, into):
     for seed in range(2):
         run_compact(rows, n_pages, max_pages, 16, layers, seed, into)
