@@ -191,7 +191,12 @@ struct Cfg {
     static constexpr int DT = D / 16;              // dimension tiles of O^T
     static constexpr int VW = D == 256 ? 2 : 1;    // 32-bit words of a V row per lane (64: half a word)
     static constexpr int ROWS = 16 * RT * WR;      // query rows of a unit
-    static constexpr int KEYS = 32 * WT;           // keys of an item
+    static constexpr bool SHARED = WR > 1;         // keys become operands once for all waves
+    static constexpr bool VLO = WIDE && NG > 1;    // scaled values as pairs of float16
+    // shared: 32-key tiles of a pass, so that two workgroups' fit LDS
+    static constexpr int TILE = (2 * KS + DT * (VLO ? 2 : 1)) * 1024 + (NG + 1) * 128 + 16;
+    static constexpr int TILES = !SHARED ? 1 : 4 * TILE <= 80 * 1024 ? 4 : 2;
+    static constexpr int KEYS = SHARED ? 32 * TILES : 32 * WT;  // keys of an item
     static constexpr int ES = SF32 ? 4 : 2;
     static constexpr int KSW = NG * ES;            // 32-bit words of four positions' scales
     static constexpr int WAVES = 2;  // waves per SIMD
@@ -360,9 +365,10 @@ __device__ __forceinline__ Zeros zeros_of(const CacheAttnArgs& a) {
 }
 
 // Four operand words of eight codes: (0,4) (1,5) (2,6) (3,7).  Subnormal: in
-// units of 2^-24, the second and fourth word with a factor of 16.  Ordinary
-// numbers: less the zero point, z0 = its float16 1024 + z twice, z1 = 64 + z.
-template <bool SUB>
+// units of 2^-24, the second and fourth word with a factor of 16.  CENTRED:
+// less the zero point, z0 = it twice, z1 = 16 times that; of ordinary numbers
+// the float16 1024 + z and 64 + z.
+template <bool SUB, bool CENTRED>
 __device__ __forceinline__ uint4v code_operand(uint32_t w, uint32_t flip, uint32_t z0, uint32_t z1) {
     const uint32_t f0 = SUB ? flip : flip | 0x64006400u, f1 = SUB ? flip << 4 : flip << 4 | 0x54005400u;
     uint4v f;
@@ -371,7 +377,7 @@ __device__ __forceinline__ uint4v code_operand(uint32_t w, uint32_t flip, uint32
     w >>= 8;
     f.z = (w & 0x000F000Fu) ^ f0;
     f.w = (w & 0x00F000F0u) ^ f1;
-    if constexpr (!SUB) {
+    if constexpr (CENTRED) {
         f.x = pk_sub(f.x, z0);
         f.y = pk_sub(f.y, z1);
         f.z = pk_sub(f.z, z0);
@@ -380,11 +386,75 @@ __device__ __forceinline__ uint4v code_operand(uint32_t w, uint32_t flip, uint32
     return f;
 }
 
+// The operands of V^T of 32 keys: pair() gives the two dimensions of byte b of
+// the lane's words, each over the lane's eight keys.
+template <class C>
+struct Values {
+    uint32_t f0, f1;          // XORed into the masked codes
+    uint32_t z0[4], z1[4];    // zero points of key pairs, for the low and the high nibble
+    uint32_t s0[4], s1[4];    // several groups: the pairs' scales, and what float16 loses of them
+
+    // vs: several groups only, scales times a power of two
+    __device__ __forceinline__ Values(const Zeros& zs, const Raw<C>& w, const float (&vs)[8]) {
+        const int lane = threadIdx.x & 63;
+        f0 = C::SUBV ? zs.flip : zs.flip | 0x64006400u;
+        f1 = C::SUBV ? zs.flip << 4 : zs.flip << 4 | 0x54005400u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t u;
+            if constexpr (C::NG == 1) {
+                u = w.vz[i / 2] >> (8 * (i & 1));
+                u |= u << 12;
+            } else {
+                const int gi = (lane & 15) / (16 / C::NG);
+                u = (w.vz[2 * i] | (w.vz[2 * i + 1] << 16)) >> (4 * (gi & 1));
+            }
+            z0[i] = (u & zs.mask) | zs.fixed;
+            z1[i] = z0[i] << 4;
+            if constexpr (!C::SUBV) {
+                z0[i] |= 0x64006400u;
+                z1[i] |= 0x54005400u;
+            }
+            if constexpr (C::NG > 1) {
+                s0[i] = pack_f16(vs[2 * i], vs[2 * i + 1]);
+                if constexpr (C::WIDE && C::SF32) s1[i] = pack_f16(vs[2 * i] - lo_f32(s0[i]), vs[2 * i + 1] - hi_f32(s0[i]));
+            }
+        }
+    }
+    // x: the byte of the four key pairs, side by side
+    __device__ __forceinline__ void bytes(const Raw<C>& w, int b, uint32_t (&x)[4]) const {
+        const uint32_t sel = 0x0C040C00u + 0x00010001u * (b & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = __builtin_amdgcn_perm(w.v[2 * i + 1][b / 4], w.v[2 * i][b / 4], sel);
+    }
+    __device__ __forceinline__ uint4v operand(const uint32_t (&x)[4], int half, uint4v* lo) const {
+        uint4v f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t d = pk_sub(half ? (x[i] & 0x00F000F0u) ^ f1 : (x[i] & 0x000F000Fu) ^ f0, half ? z1[i] : z0[i]);
+            if constexpr (C::NG == 1) {
+                f[i] = d;
+            } else {
+                f[i] = pk_mul(d, s0[i]);
+                if constexpr (C::WIDE) {
+                    (*lo)[i] = pk_fma(d, s0[i], f[i] ^ 0x80008000u);
+                    if constexpr (C::SF32) (*lo)[i] = pk_fma(d, s1[i], (*lo)[i]);
+                }
+            }
+        }
+        return f;
+    }
+};
+template <class C>
+__device__ __forceinline__ constexpr int value_bytes() {
+    return C::D == 64 ? 2 : 4 * C::VW;
+}
+
 // The state of a wave's rows: queries as operands and the running softmax.
 template <class C>
 struct Rows {
     uint4v q[C::RT][C::P][C::KS];
-    uint4v qz[C::RT][C::SUBK ? C::NG : 1];  // -sum(q) of a group as an operand (subnormal codes)
+    uint4v qz[C::RT][C::SUBK && !C::SHARED ? C::NG : 1];  // -sum(q) of a group as an operand (subnormal codes)
     float c;                    // log2 units of one raw score unit
     int lim[C::RT], lo[C::RT];  // keys [lo, lim) are seen
     float mc[C::RT];            // running maximum, log2 units
@@ -412,7 +482,7 @@ __device__ __forceinline__ uint4v hadamard32(int a) {
 // Loads rows r0 + 16 rt + (lane & 15) of kv head h, rotates them and makes
 // them operands.  Rows past the sequence's repeat its last one.
 template <class C, class T>
-__device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, int h, int r0, Rows<C>& w) {
+__device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, int h, int r0, Rows<C>& w, float* lds) {
     constexpr int D = C::D, N = D / 4;
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     float v[C::RT][N];
@@ -492,6 +562,14 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
     // 2^5 .. 2^6 (a group's sum then stays in float16's range); an element
     // 2^-20 of it still has all eleven bits, one of 2^-30 still one
     top = max_wave(top);
+    if constexpr (C::SHARED) {   // (of the workgroup: the shared scales carry c)
+        __syncthreads();
+        if (lane == 0) lds[threadIdx.x >> 6] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, lds[i]);
+        __syncthreads();
+    }
     int e = 0;
     if (top > 0.0f) e = min(max(6 - (static_cast<int>(__float_as_uint(top) >> 23) - 126), -100), 100);
     e = __builtin_amdgcn_readfirstlane(e);
@@ -523,7 +601,7 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
             w.q[rt][0][i] = uint4v{hi[0], hi[1], hi[2], hi[3]};
             if constexpr (C::WIDE) w.q[rt][1][i] = uint4v{lo[0], lo[1], lo[2], lo[3]};
         }
-        if constexpr (C::SUBK) {
+        if constexpr (C::SUBK && !C::SHARED) {
             // the zero point's operand has z in k slots 0 and 1 of lane group
             // 0: -sum(q) there as two float16
 #pragma unroll
@@ -569,7 +647,7 @@ __device__ __forceinline__ void scores(const Zeros& zs, const Raw<C>& w, const R
             }
 #pragma unroll
             for (int i = gi * C::KG; i < (gi + 1) * C::KG; ++i) {
-                const uint4v f = code_operand<C::SUBK>(w.k[s][i], zs.flip, z0, z1);
+                const uint4v f = code_operand<C::SUBK, !C::SUBK>(w.k[s][i], zs.flip, z0, z1);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     acc[rt] = mfma(f, st.q[rt][0][i], acc[rt]);
@@ -624,6 +702,41 @@ __device__ __forceinline__ void exponentials(Rows<C>& st, int rt, float (&x)[8],
     }
 }
 
+// Scores to probabilities as an operand (hi, and lo for pairs of float16): one
+// group: times the value scales vs.
+template <class C>
+__device__ __forceinline__ void probabilities(Rows<C>& st, int rt, float (&x)[8], const float (&mul)[8], const float (&vs)[8],
+                                              uint4v& hi, uint4v& lo) {
+    exponentials<C>(st, rt, x, mul);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float p[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) p[j] = x[2 * i + j] * (C::NG == 1 ? vs[2 * i + j] : C::SHARED ? vs[0] : static_cast<float>(1 << kPExp));
+        hi[i] = pack_f16(p[0], p[1]);
+        if constexpr (C::WIDE) lo[i] = pack_f16(p[0] - lo_f32(hi[i]), p[1] - hi_f32(hi[i]));
+    }
+}
+
+// Raises the exponent of the value scales in o to e.
+template <class C>
+__device__ __forceinline__ void raise_exponent(Rows<C>& st, int e) {
+    const float f = ldexpf(1.0f, st.e - e);
+#pragma unroll
+    for (int rt = 0; rt < C::RT; ++rt)
+#pragma unroll
+        for (int j = 0; j < C::DT; ++j) st.o[rt][j] *= f;
+    st.e = e;
+}
+// The least exponent, at least `least`, that covers the wave's finite scales.
+__device__ __forceinline__ int exponent_of(const float (&vs)[8], int least) {
+    float big = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) big = fmaxf(big, fabsf(vs[t]) < __builtin_inff() ? fabsf(vs[t]) : 0.0f);
+    big = max_wave(big);
+    return __builtin_amdgcn_readfirstlane(max(static_cast<int>(__float_as_uint(big) >> 23) - 126, least));
+}
+
 // Makes the exponent of the value scales in o cover |vs| < 2^e and returns
 // 2^(shift - e), the factor that the scales are taken with.
 template <class C>
@@ -631,20 +744,7 @@ __device__ __forceinline__ float cover_scales(Rows<C>& st, const float (&vs)[8],
     float big = fabsf(vs[0]);
 #pragma unroll
     for (int t = 1; t < 8; ++t) big = fmaxf(big, fabsf(vs[t]));
-    if (__any(big > __uint_as_float(static_cast<uint32_t>(127 + st.e) << 23))) {
-        // (scales that are not finite say nothing about the range)
-        big = 0.0f;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) big = fmaxf(big, fabsf(vs[t]) < __builtin_inff() ? fabsf(vs[t]) : 0.0f);
-        big = max_wave(big);
-        const int e = __builtin_amdgcn_readfirstlane(max(static_cast<int>(__float_as_uint(big) >> 23) - 126, st.e));
-        const float f = ldexpf(1.0f, st.e - e);
-#pragma unroll
-        for (int rt = 0; rt < C::RT; ++rt)
-#pragma unroll
-            for (int j = 0; j < C::DT; ++j) st.o[rt][j] *= f;
-        st.e = e;
-    }
+    if (__any(big > __uint_as_float(static_cast<uint32_t>(127 + st.e) << 23))) raise_exponent<C>(st, exponent_of(vs, st.e));
     return ldexpf(1.0f, shift - st.e);
 }
 
@@ -707,85 +807,29 @@ __device__ __forceinline__ void step(const CacheAttnArgs& a, const Raw<C>& w, co
             }
         }
     }
-    // probabilities as operands
     uint4v ph[RT], pl[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         HR_PHASE();
-        exponentials<C>(st, rt, x[rt], mul);
-        uint32_t hw[4], lw[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float p[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) p[j] = x[rt][2 * i + j] * (NG == 1 ? vs[2 * i + j] : static_cast<float>(1 << kPExp));
-            hw[i] = pack_f16(p[0], p[1]);
-            if constexpr (C::WIDE) lw[i] = pack_f16(p[0] - lo_f32(hw[i]), p[1] - hi_f32(hw[i]));
-        }
-        ph[rt] = uint4v{hw[0], hw[1], hw[2], hw[3]};
-        if constexpr (C::WIDE) pl[rt] = uint4v{lw[0], lw[1], lw[2], lw[3]};
-    }
-    // zero points of key pairs, in the low and in the second nibble
-    uint32_t z0[4], z1[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t u;
-        if constexpr (NG == 1) {
-            u = w.vz[i / 2] >> (8 * (i & 1));
-            u |= u << 12;
-        } else {
-            const int gi = (lane & 15) / (16 / NG);
-            u = (w.vz[2 * i] | (w.vz[2 * i + 1] << 16)) >> (4 * (gi & 1));
-        }
-        z0[i] = (u & zs.mask) | zs.fixed;
-        z1[i] = z0[i] << 4;
-        if constexpr (!C::SUBV) {
-            z0[i] |= 0x64006400u;
-            z1[i] |= 0x54005400u;
-        }
-    }
-    uint32_t s0[4], s1[4];   // several groups: the pairs' scales, and what float16 loses of them
-    if constexpr (NG > 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s0[i] = pack_f16(vs[2 * i], vs[2 * i + 1]);
-            if constexpr (C::WIDE && C::SF32) s1[i] = pack_f16(vs[2 * i] - lo_f32(s0[i]), vs[2 * i + 1] - hi_f32(s0[i]));
-        }
+        probabilities<C>(st, rt, x[rt], mul, vs, ph[rt], pl[rt]);
     }
     // O^T += V^T P^T, two dimensions a byte
-    const uint32_t f0 = C::SUBV ? zs.flip : zs.flip | 0x64006400u, f1 = C::SUBV ? zs.flip << 4 : zs.flip << 4 | 0x54005400u;
+    const Values<C> values(zs, w, vs);
 #pragma unroll
-    for (int b = 0; b < (C::D == 64 ? 2 : 4 * C::VW); ++b) {
+    for (int b = 0; b < value_bytes<C>(); ++b) {
         HR_PHASE();
-        const uint32_t sel = 0x0C040C00u + 0x00010001u * (b & 3);
         uint32_t y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = __builtin_amdgcn_perm(w.v[2 * i + 1][b / 4], w.v[2 * i][b / 4], sel);
+        values.bytes(w, b, y);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            uint32_t f[4], fl[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f[i] = half ? (y[i] & 0x00F000F0u) ^ f1 : (y[i] & 0x000F000Fu) ^ f0;
-                f[i] = pk_sub(f[i], half ? z1[i] : z0[i]);
-                if constexpr (NG > 1) {
-                    const uint32_t d = f[i];
-                    f[i] = pk_mul(d, s0[i]);
-                    if constexpr (C::WIDE) {
-                        fl[i] = pk_fma(d, s0[i], f[i] ^ 0x80008000u);
-                        if constexpr (C::SF32) fl[i] = pk_fma(d, s1[i], fl[i]);
-                    }
-                }
-            }
-            const uint4v av = {f[0], f[1], f[2], f[3]};
+            uint4v vl;
+            const uint4v vh = values.operand(y, half, &vl);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 float4v& o = st.o[rt][2 * b + half];
-                o = mfma(av, ph[rt], o);
-                if constexpr (C::WIDE) {
-                    o = mfma(av, pl[rt], o);
-                    if constexpr (NG > 1) o = mfma(uint4v{fl[0], fl[1], fl[2], fl[3]}, ph[rt], o);
-                }
+                o = mfma(vh, ph[rt], o);
+                if constexpr (C::WIDE) o = mfma(vh, pl[rt], o);
+                if constexpr (C::VLO) o = mfma(vl, ph[rt], o);
             }
         }
     }
@@ -907,7 +951,7 @@ __device__ __forceinline__ void settle(Rows<C>& st) {
 // through LDS in a few rows at a time, 16 threads to a row.
 template <class C>
 constexpr int join_floats() {
-    return C::WT == 1 ? 16 : 2 * 4 * 16 + 4 * 16 * (C::D + 4);
+    return 2 * 4 * 16 + 4 * 16 * (C::D + 4);
 }
 template <class C, class T>
 __device__ __forceinline__ void join_waves(const CacheAttnArgs& a, const Seq& s, int h, int r0, Rows<C>& st, float* part,
@@ -972,27 +1016,238 @@ __device__ __forceinline__ void join_waves(const CacheAttnArgs& a, const Seq& s,
     }
 }
 
+// A 32-key tile as operands, in LDS.
+template <class C>
+struct Tile {
+    uint4v k[2 * C::KS][64];
+    uint4v v[C::DT][64];
+    uint4v vl[C::VLO ? C::DT : 1][C::VLO ? 64 : 1];
+    float4v mul[C::NG][8];     // key scales times c: [4 s + g] holds keys 16 s + 4 g ...
+    float4v vs[8];             // one group: value scales times 2^-e
+    int e, here;               // here: bit s set if subtile s is on a present page
+};
+template <class C>
+constexpr int lds_floats() {
+    if constexpr (C::SHARED) return C::TILES * static_cast<int>(sizeof(Tile<C>)) / 4;
+    else return join_floats<C>();
+}
+
+// Makes a tile of the 32 keys in w.
+template <class C>
+__device__ __forceinline__ void make_tile(const CacheAttnArgs& a, const Raw<C>& w, const Pages& pages, int t0, int end, float c,
+                                          Tile<C>& tile) {
+    constexpr int NG = C::NG;
+    const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+    const Zeros zs = zeros_of(a);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < C::KS; ++i) {
+            const int gi = i / C::KG;
+            const uint32_t z = NG == 1 ? w.kz[s] >> (4 * (lane & 1)) : w.kz[s] >> (4 * gi);
+            uint32_t z0 = (((z << 16) | (z & 0xFFFFu)) & zs.mask) | zs.fixed, z1 = z0 << 4;
+            if constexpr (!C::SUBK) {
+                z0 |= 0x64006400u;
+                z1 |= 0x54005400u;
+            }
+            tile.k[s * C::KS + i][lane] = code_operand<C::SUBK, true>(w.k[s][i], zs.flip, z0, z1);
+        }
+    HR_PHASE();
+    // scales; those past the sequence or on an absent page are not looked at
+    float vs[8];
+    bool odd = false;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+        if constexpr (NG == 1) vs[t] = scale_at<C::SF32>(w.vs[t / 4], t & 3);
+        else vs[t] = __uint_as_float(C::SF32 ? w.vs[t][0] : w.vs[t][0] << 16);
+        if (t0 + 16 * (t / 4) + 4 * g + t % 4 >= end || !present(a, pages.p[t / 4])) vs[t] = 0.0f;
+        odd |= !(fabsf(vs[t]) < __builtin_inff());
+    }
+    // a value scale that is not finite must reach the queries that see its key
+    // and no others: it leaves the tile, and the key's score becomes NaN
+    uint32_t bad = 0;
+    if (__any(odd)) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const bool mine = !(fabsf(vs[t]) < __builtin_inff());
+            if (mine) vs[t] = 0.0f;
+            if ((__ballot(mine) >> (16 * g)) & 0xFFFFu) bad |= 1u << t;
+        }
+    }
+    const int e = exponent_of(vs, -100);
+    const float down = ldexpf(1.0f, (NG == 1 ? 0 : kSExp) - e);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) vs[t] *= down;
+    if (m == 0) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi) {
+                float4v x;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    x[r] = scale_at<C::SF32>(w.ks[s], r * NG + gi) * c;
+                    if (bad >> (4 * s + r) & 1) x[r] = __builtin_nanf("");
+                }
+                tile.mul[gi][4 * s + g] = x;
+            }
+            if constexpr (NG == 1) tile.vs[4 * s + g] = float4v{vs[4 * s], vs[4 * s + 1], vs[4 * s + 2], vs[4 * s + 3]};
+        }
+    }
+    if (lane == 0) {
+        tile.e = e;
+        tile.here = (present(a, pages.p[0]) ? 1 : 0) | (present(a, pages.p[1]) ? 2 : 0);
+    }
+    const Values<C> values(zs, w, vs);
+#pragma unroll
+    for (int b = 0; b < value_bytes<C>(); ++b) {
+        HR_PHASE();
+        uint32_t y[4];
+        values.bytes(w, b, y);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint4v vl;
+            tile.v[2 * b + half][lane] = values.operand(y, half, &vl);
+            if constexpr (C::VLO) tile.vl[2 * b + half][lane] = vl;
+        }
+    }
+}
+
+// One step over a tile; the keys that all rows of the wave see: [flo, fhi).
+template <class C>
+__device__ __forceinline__ void tile_step(const Tile<C>& tile, int t0, const Span& sp, Rows<C>& st) {
+    constexpr int NG = C::NG, RT = C::RT;
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    float x[RT][8], mul[8];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) {
+            float4v acc[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) acc[rt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = gi * C::KG; i < (gi + 1) * C::KG; ++i) {
+                const uint4v f = tile.k[s * C::KS + i][lane];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    acc[rt] = mfma(f, st.q[rt][0][i], acc[rt]);
+                    if constexpr (C::WIDE) acc[rt] = mfma(f, st.q[rt][1][i], acc[rt]);
+                }
+            }
+            const float4v ks = tile.mul[gi][4 * s + g];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                mul[4 * s + r] = NG == 1 ? ks[r] : 1.0f;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    if constexpr (NG == 1) x[rt][4 * s + r] = acc[rt][r];
+                    else x[rt][4 * s + r] = gi == 0 ? acc[rt][r] * ks[r] : fmaf(acc[rt][r], ks[r], x[rt][4 * s + r]);
+                }
+            }
+        }
+    const int here = __builtin_amdgcn_readfirstlane(tile.here);
+    if (!(t0 >= sp.flo && t0 + 32 <= sp.fhi && here == 3)) {
+        // unseen scores become -inf, whatever they are
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const int key = t0 + 16 * (t / 4) + 4 * g + t % 4;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const bool seen = (here >> (t / 4) & 1) && key < st.lim[rt] && key >= st.lo[rt];
+                x[rt][t] = seen ? x[rt][t] * mul[t] : -__builtin_inff();
+            }
+            mul[t] = 1.0f;
+        }
+    }
+    const int e = __builtin_amdgcn_readfirstlane(tile.e);
+    if (e > st.e) raise_exponent<C>(st, e);
+    const float f = ldexpf(1.0f, kPExp + e - st.e);
+    float vs[8];
+    if constexpr (NG == 1) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const float4v y = tile.vs[4 * s + g];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) vs[4 * s + r] = y[r] * f;
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) vs[t] = f;
+    }
+    uint4v ph[RT], pl[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) probabilities<C>(st, rt, x[rt], mul, vs, ph[rt], pl[rt]);
+#pragma unroll
+    for (int j = 0; j < C::DT; ++j) {
+        const uint4v vh = tile.v[j][lane];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            float4v& o = st.o[rt][j];
+            o = mfma(vh, ph[rt], o);
+            if constexpr (C::WIDE) o = mfma(vh, pl[rt], o);
+            if constexpr (C::VLO) o = mfma(tile.vl[j][lane], ph[rt], o);
+        }
+    }
+}
+
 // Rows [r0, r0 + ROWS) of kv head h of a sequence over the keys [k0, k1);
 // part: where a partial result goes (else the rows are finished here).
 template <class C, class T>
 __device__ __forceinline__ void segment(const CacheAttnArgs& a, const Seq& s, int b, int h, int r0, int k0, int k1,
                                         float* part, float* lds) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wr = wave % C::WR, wt = wave / C::WR;
-    const int row = r0 + wr * 16 * C::RT;
-    const int rows = min(row + 16 * C::RT, s.n * a.rep);
-    if (C::WT == 1 && row >= rows) return;   // (no barriers along the rows)
-    const Span sp = span_of(a, s, row, rows);
-    Walk<C> keys;
-    keys.table = a.sq.table + static_cast<int64_t>(b) * a.sq.max_pages;
-    keys.h = h;
-    keys.start(a, sp, k0, k1, wt);
+    const int32_t* table = a.sq.table + static_cast<int64_t>(b) * a.sq.max_pages;
     Rows<C> st;
-    load_rows<C, T>(a, s, h, row, st);
-    keys.run(a, sp, st);
-    settle<C>(st);
-    if constexpr (C::WT > 1) join_waves<C, T>(a, s, h, row, st, part, lds);
-    else put_rows<C, T>(a, s, h, row, st, part, row - r0);
+    if constexpr (!C::SHARED) {
+        const Span sp = span_of(a, s, r0, min(r0 + C::ROWS, s.n * a.rep));
+        Walk<C> keys;
+        keys.table = table;
+        keys.h = h;
+        keys.start(a, sp, k0, k1, wave);
+        load_rows<C, T>(a, s, h, r0, st, lds);
+        keys.run(a, sp, st);
+        settle<C>(st);
+        join_waves<C, T>(a, s, h, r0, st, part, lds);
+    } else {
+        // the waves make a tile each and then take all of them; the next
+        // tiles' keys are on their way meanwhile
+        constexpr int S = 32 * C::TILES;
+        Tile<C>* tiles = reinterpret_cast<Tile<C>*>(lds);
+        const int row = r0 + wave * 16 * C::RT, last = s.n * a.rep;
+        const Span all = span_of(a, s, r0, min(r0 + C::ROWS, last));
+        Span sp = {0, 0, 0, 0};
+        if (row < last) sp = span_of(a, s, row, min(row + 16 * C::RT, last));
+        int t = max(k0, all.lo & ~31);
+        const int end = min(k1, all.hi);
+        const bool makes = wave < C::TILES;
+        const int own = 32 * wave;
+        Raw<C> w;
+        Pages now = {{-1, -1}}, next = {{-1, -1}};
+        if (makes && t + own < end) {
+            now = pages_at(a, table, t + own);
+            load_keys<C>(a, now, h, t + own, w);
+        }
+        if (makes && t + S + own < end) next = pages_at(a, table, t + S + own);
+        load_rows<C, T>(a, s, h, row, st, lds);
+        for (; t < end; t += S) {
+            if (makes && t + own < end) make_tile<C>(a, w, now, t + own, end, st.c, tiles[wave]);
+            if (makes && t + S + own < end) {
+                now = next;
+                load_keys<C>(a, now, h, t + S + own, w);
+                if (t + 2 * S + own < end) next = pages_at(a, table, t + 2 * S + own);
+            }
+            __syncthreads();
+#pragma unroll 1
+            for (int i = 0; i < C::TILES; ++i) {
+                const int at = t + 32 * i;
+                if (at < min(end, sp.hi) && at + 32 > sp.lo) tile_step<C>(tiles[i], at, sp, st);
+            }
+            __syncthreads();
+        }
+        settle<C>(st);
+        put_rows<C, T>(a, s, h, row, st, part, row - r0);
+    }
 }
 
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
@@ -1132,7 +1387,8 @@ struct Cut {
 // does not hold whole goes to scratch slot 2 w + 1 if it begins here, else 2 w.
 template <class C, class T>
 __global__ void __launch_bounds__(256, C::WAVES) cache_attn_split(const CacheAttnArgs a) {
-    __shared__ float lds[join_floats<C>()];
+    __shared__ float4v lds4[lds_floats<C>() / 4 + 1];
+    float* lds = reinterpret_cast<float*>(lds4);
     const Place p = place<C>(a, reinterpret_cast<int64_t*>(lds));
     int64_t i0 = p.i0;
     const int64_t i1 = p.i1;
@@ -1228,6 +1484,7 @@ __global__ void __launch_bounds__(256) cache_attn_join(const CacheAttnArgs a) {
 // as many units as that bound leaves it.
 template <class C, class T>
 __global__ void __launch_bounds__(256, C::WAVES) cache_attn_whole(const CacheAttnArgs a) {
+    __shared__ float4v lds[lds_floats<C>() / 4 + 1];
     const int u = blockIdx.x % a.units, h = blockIdx.x / a.units;
     auto first = [&](int b) { return static_cast<int64_t>(cu_at<true>(a.sq, b)) * a.rep / C::ROWS + b; };
     int b = 0, hi = a.sq.rows - 1;
@@ -1241,7 +1498,7 @@ __global__ void __launch_bounds__(256, C::WAVES) cache_attn_whole(const CacheAtt
     // the last row blocks see the most keys: they go first
     const int64_t rb = rbs - 1 - (u - first(b));
     if (rb < 0 || rb >= rbs) return;
-    segment<C, T>(a, s, b, h, static_cast<int>(rb) * C::ROWS, 0, s.len, nullptr, nullptr);
+    segment<C, T>(a, s, b, h, static_cast<int>(rb) * C::ROWS, 0, s.len, nullptr, reinterpret_cast<float*>(lds));
 }
 
 template <class C, class T>
