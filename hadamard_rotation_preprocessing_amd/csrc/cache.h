@@ -44,7 +44,7 @@ struct CacheAttnArgs {
     void* out;
     float* lse;                // nullable
     const uint8_t* pool;
-    float* work;               // partial results (split kernels)
+    float* work;               // partial results
     int64_t q_st, q_sh, o_st, o_sh;   // element strides
     CachePage pg;
     CacheSeqs sq;
@@ -52,8 +52,8 @@ struct CacheAttnArgs {
     float norm;                // 1 / sqrt(d) (rotate)
     int32_t hq, rep;           // query heads; query heads per kv head
     int32_t causal, window, rotate;
-    int32_t units;             // row blocks per kv head (an upper bound)
-    int32_t workers;           // workgroups of the split kernels
+    int32_t workers;           // workgroups
+    int32_t step, over;        // a unit's rows = step rep + over (set with the kernel)
 };
 
 // Which attention kernel a call takes.
@@ -61,7 +61,6 @@ struct CacheAttnKey {
     int32_t d, ng, sf32;       // of the cache
     int32_t wide;              // float32 activations
     int32_t rt, wr;            // row tiles of a wave, waves along the rows
-    int32_t split;             // units cut over the workgroups (else one unit each)
 };
 
 struct CacheUpdateArgs {
@@ -97,7 +96,7 @@ int launch_cache_append(const CacheAppendArgs& a, int bf16, void* stream);
 int launch_cache_update(const CacheUpdateArgs& a, void* stream);
 int launch_cache_compact(const CacheCompactArgs& a, void* stream);
 int launch_cache_attn(const CacheAttnKey& k, const CacheAttnArgs& a, void* stream);
-// workgroups that a split kernel keeps in flight on the current device
+// workgroups that an attention kernel keeps in flight on the current device
 int cache_attn_workers(const CacheAttnKey& k, int* workers);
 
 // int32 words of scratch

@@ -41,6 +41,7 @@ constexpr int64_t kMaxCount = int64_t{1} << 30;
 constexpr int64_t kMaxHeads = 1 << 16;
 // workgroups of 256 threads of a launch (a grid holds fewer than 2^32 threads)
 constexpr int64_t kMaxGrid = 1 << 24;
+constexpr int64_t kMaxKeys = int64_t{1} << 31;
 
 int check_ptr(const void* p, const char* name, size_t align) {
     if (!p) return fail(HR_EINVAL, "%s is NULL", name);
@@ -178,38 +179,37 @@ int check_distinct(const char* name, int64_t st, int64_t sh, int64_t tokens, int
     return fail(HR_EINVAL, "%s strides %lld, %lld make rows overlap", name, (long long)st, (long long)sh);
 }
 
-// The kernel of a call.  rows = query heads per kv head x new tokens of a
-// sequence at most.
-void attn_key(const hr::CachePage& pg, int dtype, int64_t tokens, int32_t q_heads, int64_t max_q,
+// The kernel of a call, by its query rows (query heads per kv head x new tokens
+// of a sequence at most) and its scores at most (query rows x keys; the lengths
+// are on the device, so keys are what the table or the window allows).
+// Few rows: a workgroup's waves take different keys of the same 16 or 32 rows
+// (32: one group per vector, heads up to 128; the registers of more do not fit).
+// Many: the waves take different rows of the same keys, whose operands they
+// share, 256 or 128 to a workgroup.  Measured, few-row kernel against shared, us:
+//   rows of a sequence (32 sequences, 8000 keys, 8 kv heads; bfloat16, heads of
+//   128): one group 32: 89, 225; 64: 136, 229; 128: 254, 228.  float32 64: 262,
+//   429; 128: 505, 458.  Groups of 32 (4 kv heads) 28: 102, 137; 42: 143, 141;
+//   56: 172, 143.  Heads of 256 (16 sequences, 4000 keys) 32: 68, 63; 64: 101, 73.
+//   scores of all heads (millions): one group 8: 31, 42; 33: 53, 56 and 54, 62;
+//   65: 83, 78; 134: 118, 101.  float32 13: 38, 51; 17: 79, 87; 33: 104, 90 and
+//   77, 80; 67: 239, 197.  Groups of 32 7: 39, 51; 14: 62, 55; 17: 72, 47.  Heads
+//   of 256 8: 63, 45; 33: 79, 58.
+void attn_key(const hr::CachePage& pg, int dtype, int64_t tokens, int32_t q_heads, int64_t max_q, int64_t keys,
               hr::CacheAttnKey* k) {
     memset(k, 0, sizeof *k);
-    const int64_t rep = q_heads / pg.hkv;
-    const int64_t most = max_q > 0 && max_q < tokens ? max_q : tokens;
+    const int64_t most = max_q > 0 && max_q < tokens ? max_q : tokens, rows = most * (q_heads / pg.hkv);
     k->d = pg.d;
     k->ng = pg.ng;
     k->sf32 = pg.sf32;
     k->wide = dtype == HR_F32;
-    const int64_t rows = most * rep;
-    // a second row tile in a wave needs its registers: not with pairs of
-    // operands, and not at 256
-    const bool one = k->wide || pg.d == 256;
-    if (rows <= 16) {
-        k->rt = 1;
-        k->wr = 1;
-    } else if (rows <= 32 && !one) {
-        k->rt = 2;
+    const bool two = !k->wide && pg.d <= 128 && pg.ng == 1, light = k->wide || two;
+    if (rows <= (light ? 96 : 32) || tokens * q_heads < (int64_t{1} << (light ? 25 : 23)) / (keys > 0 ? keys : 1)) {
+        k->rt = rows > 16 && two ? 2 : 1;
         k->wr = 1;
     } else {
-        k->rt = one ? 1 : 2;
-        k->wr = 4;
+        k->rt = k->wide || pg.d == 256 ? 1 : 2;
+        k->wr = 8;
     }
-    const int64_t block = 16 * k->rt * k->wr;
-    // with many units each takes one to itself; few are cut over the device
-    k->split = !(k->wr == 4 && (tokens * rep / block) * pg.hkv >= 1024);
-}
-
-int64_t attn_units(const hr::CacheAttnKey& k, int64_t tokens, int64_t rep, int64_t rows) {
-    return tokens * rep / (16 * k.rt * k.wr) + rows;
 }
 
 int attn_sizes(int dtype, int64_t tokens, int32_t q_heads, const hr::CachePage& pg, int64_t max_q) {
@@ -223,9 +223,6 @@ int attn_sizes(int dtype, int64_t tokens, int32_t q_heads, const hr::CachePage& 
 }
 
 int attn_work_bytes(const hr::CacheAttnKey& k, int* workers, int64_t* bytes) {
-    *workers = 0;
-    *bytes = 0;
-    if (!k.split) return HR_OK;
     const int e = hr::cache_attn_workers(k, workers);
     if (e != 0) return fail(HR_EDEVICE, "occupancy query failed: %s", hipGetErrorString(static_cast<hipError_t>(e)));
     // two partial results per workgroup, rows of d sums, a maximum and a sum of
@@ -301,9 +298,15 @@ int hr_cache_attention_work(int dtype, int64_t tokens, int32_t q_heads, const hr
     *bytes = 0;
     if (tokens == 0) return ok();
     hr::CacheAttnKey key;
-    attn_key(pg, dtype, tokens, q_heads, max_q, &key);
-    int workers;
-    if ((st = attn_work_bytes(key, &workers, bytes))) return st;
+    // what suffices for any length and window: of the kernels of no keys and of
+    // all that there can be
+    int64_t need[2];
+    for (int i = 0; i < 2; ++i) {
+        int workers;
+        attn_key(pg, dtype, tokens, q_heads, max_q, i ? kMaxKeys : 0, &key);
+        if ((st = attn_work_bytes(key, &workers, &need[i]))) return st;
+    }
+    *bytes = need[0] > need[1] ? need[0] : need[1];
     return ok();
 }
 
@@ -328,28 +331,32 @@ int hr_cache_attention(const void* q, int64_t q_stride_token, int64_t q_stride_h
         (st = check_distinct("out", out_stride_token, out_stride_head, tokens, q_heads, a.pg.d)) ||
         (st = check_ptr(pool, "pool", 16)) || (lse && (st = check_ptr(lse, "lse", 4))))
         return st;
-    hr::CacheAttnKey key;
-    attn_key(a.pg, dtype, tokens, q_heads, max_q, &key);
-    int workers;
-    int64_t need;
-    if ((st = attn_work_bytes(key, &workers, &need))) return st;
-    if (need > 0) {
-        if ((st = check_ptr(work, "work", 16))) return st;
-        if (work_bytes < need)
-            return fail(HR_EINVAL, "work_bytes = %lld: %lld are needed", (long long)work_bytes, (long long)need);
-    }
     const bool in_place = q == out && q_stride_token == out_stride_token && q_stride_head == out_stride_head;
     // in place is safe: the rows of a unit are read by the workgroups that
     // work on it alone, and written by the last of them or, where the unit is
     // cut over several, by the joining launch
-    const Range r[] = {{"out", out, ob, true},
-                       {"lse", lse, lse ? tokens * q_heads * 4 : 0, true},
-                       {"work", need > 0 ? work : nullptr, need, true},
-                       {"q", in_place ? nullptr : q, qb, false},
-                       {"pool", pool, n_pages * a.pg.page_bytes, false},
-                       {"table", seqs->table, seqs->rows * seqs->max_pages * 4, false},
-                       {"lens", seqs->lens, seqs->rows * 4, false},
-                       {"cu_q", seqs->cu_q, (seqs->rows + 1) * 4, false}};
+    Range r[] = {{"out", out, ob, true},
+                 {"lse", lse, lse ? tokens * q_heads * 4 : 0, true},
+                 {"q", in_place ? nullptr : q, qb, false},
+                 {"pool", pool, n_pages * a.pg.page_bytes, false},
+                 {"table", seqs->table, seqs->rows * seqs->max_pages * 4, false},
+                 {"lens", seqs->lens, seqs->rows * 4, false},
+                 {"cu_q", seqs->cu_q, (seqs->rows + 1) * 4, false},
+                 {"work", nullptr, 0, true}};
+    if ((st = check_overlap(r, 7))) return st;
+    int64_t keys = int64_t{seqs->max_pages} << a.pg.logp;
+    if (window > 0 && window < keys - tokens) keys = window + (max_q > 0 && max_q < tokens ? max_q : tokens);
+    hr::CacheAttnKey key;
+    attn_key(a.pg, dtype, tokens, q_heads, max_q, keys, &key);
+    int workers;
+    int64_t need;
+    if ((st = attn_work_bytes(key, &workers, &need))) return st;
+    if ((st = check_ptr(work, "work", 16))) return st;
+    if (work_bytes < need)
+        return fail(HR_EINVAL, "work_bytes = %lld: %lld are needed", (long long)work_bytes, (long long)need);
+    r[0].written = r[1].written = false;   // (compared above)
+    r[2].p = q;
+    r[7] = {"work", work, need, true};
     if ((st = check_overlap(r, 8))) return st;
     a.q = q;
     a.out = out;
@@ -367,9 +374,6 @@ int hr_cache_attention(const void* q, int64_t q_stride_token, int64_t q_stride_h
     a.causal = causal != 0;
     a.window = window >= (int64_t{1} << 31) ? 0 : static_cast<int32_t>(window);
     a.rotate = rotate != 0;
-    const int64_t units = attn_units(key, tokens, a.rep, seqs->rows);
-    if (units * a.pg.hkv >= kMaxGrid) return fail(HR_EUNSUPPORTED, "too many rows, tokens and heads for one launch");
-    a.units = static_cast<int32_t>(units);
     a.workers = workers;
     return launched(hr::launch_cache_attn(key, a, stream));
 }

@@ -12,8 +12,10 @@
 // the value's scale multiplies the probability, so that o is a matrix product
 // over the integers c - z too; with several groups it multiplies the values.
 //
-// Layout.  No tile is staged: a wave turns the packed codes it has loaded into
-// operands of v_mfma_f32_16x16x32_f16 in its registers.
+// Layout.  With few rows no tile is staged: a wave turns the packed codes it has
+// loaded into operands of v_mfma_f32_16x16x32_f16 in its registers.  With many
+// rows the waves take different rows of the same keys, and an operand is made
+// once for all of them, in LDS (see Tile).
 //   Scores are formed transposed, S^T = K Q^T: the codes are the A operand
 //   (lane l: key l & 15), the queries the B operand.  The result has the query
 //   in the lane (l & 15) and four consecutive keys 4 (l >> 4) + r in its
@@ -36,15 +38,17 @@
 //
 // Split.  A unit is a kv head of a sequence with a block of its query rows
 // (new tokens x query heads of that kv head).  Units are cut into items of as
-// many keys as a workgroup's waves take at once, and every workgroup takes an
-// equal, contiguous run of all items, whatever the lengths; partial results
-// are joined in key order by cache_attn_join.
+// many keys as a workgroup takes at once, and every workgroup takes an equal,
+// contiguous run of all items, whatever the lengths; partial results are joined
+// in key order by cache_attn_join.  Where there are units enough they are shared
+// out whole instead.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "cache.h"
 #include "plan.h"
@@ -184,25 +188,26 @@ __device__ __forceinline__ Span span_of(const CacheAttnArgs& a, const Seq& s, in
 
 template <int D_, int NG_, bool SF32_, bool WIDE_, int RT_, int WR_>
 struct Cfg {
-    static constexpr int D = D_, NG = NG_, RT = RT_, WR = WR_, WT = 4 / WR_;
+    static constexpr int D = D_, NG = NG_, RT = RT_, WR = WR_;
     static constexpr bool SF32 = SF32_, WIDE = WIDE_;
+    static constexpr bool SHARED = WR > 1;         // keys become operands once for all waves
+    static constexpr int THREADS = SHARED ? 64 * WR : 256;
+    static constexpr int WT = SHARED ? 1 : 4;      // waves along the keys
     static constexpr int KS = D / 32;              // matrix steps over a vector
     static constexpr int KG = KS / NG;             // of one group
     static constexpr int DT = D / 16;              // dimension tiles of O^T
     static constexpr int VW = D == 256 ? 2 : 1;    // 32-bit words of a V row per lane (64: half a word)
     static constexpr int ROWS = 16 * RT * WR;      // query rows of a unit
-    static constexpr bool SHARED = WR > 1;         // keys become operands once for all waves
-    static constexpr bool VLO = WIDE && NG > 1;    // scaled values as pairs of float16
-    // shared: 32-key tiles of a pass, so that two workgroups' fit LDS
-    static constexpr int TILE = (2 * KS + DT * (VLO ? 2 : 1)) * 1024 + (NG + 1) * 128 + 16;
-    static constexpr int TILES = !SHARED ? 1 : 4 * TILE <= 80 * 1024 ? 4 : 2;
+    static constexpr int P = WIDE ? 2 : 1;         // float16 terms of an operand
+    // shared: 32-key tiles of a pass, so that two passes' operands fit LDS
+    static constexpr int TILES = P * D <= 128 ? 4 : P * D == 256 ? 2 : 1;
     static constexpr int KEYS = SHARED ? 32 * TILES : 32 * WT;  // keys of an item
     static constexpr int ES = SF32 ? 4 : 2;
     static constexpr int KSW = NG * ES;            // 32-bit words of four positions' scales
-    static constexpr int WAVES = 2;  // waves per SIMD
-    static constexpr int P = WIDE ? 2 : 1;         // float16 terms of an operand
+    static constexpr int WAVES = 2;                // waves per SIMD
     static constexpr bool SUBK = !WIDE;            // subnormal codes of K
     static constexpr bool SUBV = !WIDE && NG == 1; // and of V
+    static constexpr bool VLO = WIDE && NG > 1;    // scaled values as pairs of float16
 };
 
 // What a wave holds of 32 keys before it works on them.
@@ -287,22 +292,53 @@ __device__ __forceinline__ uint32_t buffer_u8(__amdgpu_buffer_rsrc_t r, int lane
     return static_cast<uint8_t>(__builtin_amdgcn_raw_buffer_load_b8(r, lane_at, at, 0));
 }
 
-// Loads 32 keys from t0.  The buffer is a head's part of a page; an absent
-// page's has no bytes, so that its loads give zeros.
+// A head's part of a page; an absent page's has no bytes, so that its loads give
+// zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t head_buffer(const CacheAttnArgs& a, int page, int h) {
+    const bool here = present(a, page);
+    const uint8_t* base = a.pool + (here ? page : 0) * a.pg.page_bytes + h * a.pg.head_bytes;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, here ? static_cast<int>(a.pg.head_bytes) : 0, 0x00020000);
+}
+
+// The values of subtile s, at position off of their page: D/16 dimensions of
+// keys 4 g + r, their scales and zero points.
+template <class C, class W>
+__device__ __forceinline__ void load_values(const CacheAttnArgs& a, __amdgpu_buffer_rsrc_t r, int off, int s, W& w) {
+    constexpr int D = C::D, NG = C::NG;
+    const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+    const int vc = a.pg.vc + off * (D / 2), vs = a.pg.vs + off * (NG * C::ES), vz = a.pg.vz + off * NG / 2;
+    int vl = 4 * g * (D / 2) + m * (D / 32);
+    HR_KEEP(vl);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (D == 64) w.v[4 * s + i][0] = buffer_u16(r, vl + i * (D / 2), vc);
+        else buffer_words<C::VW>(r, vl + i * (D / 2), vc, w.v[4 * s + i]);
+    }
+    if constexpr (NG == 1) {
+        buffer_words<C::KSW>(r, 4 * g * C::ES, vs, w.vs[s]);
+        w.vz[s] = buffer_u16(r, 2 * g, vz);
+    } else {
+        int at = 4 * g * NG + m / (16 / NG);  // the lane's group of key 4g
+        HR_KEEP(at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (C::SF32) buffer_words<1>(r, 4 * at + 4 * i * NG, vs, w.vs[4 * s + i]);
+            else w.vs[4 * s + i][0] = buffer_u16(r, 2 * at + 2 * i * NG, vs);
+            w.vz[4 * s + i] = buffer_u8(r, at / 2 + i * (NG / 2), vz);
+        }
+    }
+}
+
+// Loads 32 keys from t0.
 template <class C>
 __device__ __forceinline__ void load_keys(const CacheAttnArgs& a, const Pages& pages, int h, int t0, Raw<C>& w) {
     constexpr int D = C::D, NG = C::NG;
     const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const bool here = present(a, pages.p[s]);
+        const __amdgpu_buffer_rsrc_t r = head_buffer(a, pages.p[s], h);
         const int off = (t0 + 16 * s) & (a.pg.page - 1);
-        const uint8_t* base = a.pool + (here ? pages.p[s] : 0) * a.pg.page_bytes + h * a.pg.head_bytes;
-        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint8_t*>(base), 0, here ? static_cast<int>(a.pg.head_bytes) : 0, 0x00020000);
-        const int kc = a.pg.kc + off * (D / 2), vc = a.pg.vc + off * (D / 2);
-        const int ks = a.pg.ks + off * (NG * C::ES), vs = a.pg.vs + off * (NG * C::ES);
-        const int kz = a.pg.kz + off * NG / 2, vz = a.pg.vz + off * NG / 2;
+        const int kc = a.pg.kc + off * (D / 2), ks = a.pg.ks + off * (NG * C::ES), kz = a.pg.kz + off * NG / 2;
         // keys: a lane holds D/4 dimensions of key m, one run with one group,
         // eight of every 32 with several (a matrix step is then one group's)
         int kl = m * (D / 2) + g * (NG == 1 ? D / 8 : 4);
@@ -318,27 +354,7 @@ __device__ __forceinline__ void load_keys(const CacheAttnArgs& a, const Pages& p
         else if constexpr (NG == 2) w.kz[s] = buffer_u8(r, m, kz);
         else if constexpr (NG == 4) w.kz[s] = buffer_u16(r, 2 * m, kz);
         else buffer_words<1>(r, 4 * m, kz, &w.kz[s]);
-        // values: D/16 dimensions of keys 4g + r
-        int vl = 4 * g * (D / 2) + m * (D / 32);
-        HR_KEEP(vl);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (D == 64) w.v[4 * s + i][0] = buffer_u16(r, vl + i * (D / 2), vc);
-            else buffer_words<C::VW>(r, vl + i * (D / 2), vc, w.v[4 * s + i]);
-        }
-        if constexpr (NG == 1) {
-            buffer_words<C::KSW>(r, 4 * g * C::ES, vs, w.vs[s]);
-            w.vz[s] = buffer_u16(r, 2 * g, vz);
-        } else {
-            int at = 4 * g * NG + m / (16 / NG);  // the lane's group of key 4g
-            HR_KEEP(at);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (C::SF32) buffer_words<1>(r, 4 * at + 4 * i * NG, vs, w.vs[4 * s + i]);
-                else w.vs[4 * s + i][0] = buffer_u16(r, 2 * at + 2 * i * NG, vs);
-                w.vz[4 * s + i] = buffer_u8(r, at / 2 + i * (NG / 2), vz);
-            }
-        }
+        load_values<C>(a, r, off, s, w);
     }
 }
 
@@ -388,17 +404,19 @@ __device__ __forceinline__ uint4v code_operand(uint32_t w, uint32_t flip, uint32
 
 // The operands of V^T of 32 keys: pair() gives the two dimensions of byte b of
 // the lane's words, each over the lane's eight keys.
-template <class C>
+template <class C, bool SCALED>
 struct Values {
+    static constexpr bool SUB = !C::WIDE && !SCALED;   // subnormal codes
     uint32_t f0, f1;          // XORed into the masked codes
     uint32_t z0[4], z1[4];    // zero points of key pairs, for the low and the high nibble
-    uint32_t s0[4], s1[4];    // several groups: the pairs' scales, and what float16 loses of them
+    uint32_t s0[4], s1[4];    // SCALED: the pairs' scales, and what float16 loses of them
 
-    // vs: several groups only, scales times a power of two
-    __device__ __forceinline__ Values(const Zeros& zs, const Raw<C>& w, const float (&vs)[8]) {
+    // vs: SCALED only, scales times a power of two
+    template <class W>
+    __device__ __forceinline__ Values(const Zeros& zs, const W& w, const float (&vs)[8]) {
         const int lane = threadIdx.x & 63;
-        f0 = C::SUBV ? zs.flip : zs.flip | 0x64006400u;
-        f1 = C::SUBV ? zs.flip << 4 : zs.flip << 4 | 0x54005400u;
+        f0 = SUB ? zs.flip : zs.flip | 0x64006400u;
+        f1 = SUB ? zs.flip << 4 : zs.flip << 4 | 0x54005400u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t u;
@@ -411,18 +429,19 @@ struct Values {
             }
             z0[i] = (u & zs.mask) | zs.fixed;
             z1[i] = z0[i] << 4;
-            if constexpr (!C::SUBV) {
+            if constexpr (!SUB) {
                 z0[i] |= 0x64006400u;
                 z1[i] |= 0x54005400u;
             }
-            if constexpr (C::NG > 1) {
+            if constexpr (SCALED) {
                 s0[i] = pack_f16(vs[2 * i], vs[2 * i + 1]);
                 if constexpr (C::WIDE && C::SF32) s1[i] = pack_f16(vs[2 * i] - lo_f32(s0[i]), vs[2 * i + 1] - hi_f32(s0[i]));
             }
         }
     }
     // x: the byte of the four key pairs, side by side
-    __device__ __forceinline__ void bytes(const Raw<C>& w, int b, uint32_t (&x)[4]) const {
+    template <class W>
+    __device__ __forceinline__ void bytes(const W& w, int b, uint32_t (&x)[4]) const {
         const uint32_t sel = 0x0C040C00u + 0x00010001u * (b & 3);
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = __builtin_amdgcn_perm(w.v[2 * i + 1][b / 4], w.v[2 * i][b / 4], sel);
@@ -432,7 +451,7 @@ struct Values {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t d = pk_sub(half ? (x[i] & 0x00F000F0u) ^ f1 : (x[i] & 0x000F000Fu) ^ f0, half ? z1[i] : z0[i]);
-            if constexpr (C::NG == 1) {
+            if constexpr (!SCALED) {
                 f[i] = d;
             } else {
                 f[i] = pk_mul(d, s0[i]);
@@ -461,6 +480,11 @@ struct Rows {
     float l[C::RT];             // sum of exponentials (this lane's keys)
     float4v o[C::RT][C::DT];
     int e;                      // exponent of the value scales in o
+    // shared operands: scores start from start[] = kPExp - mc (from: in all four
+    // registers of a matrix operand); lsum is the sum of exponentials as a
+    // matrix result
+    float start[C::SHARED ? C::RT : 1];
+    float4v from[C::SHARED ? C::RT : 1], lsum[C::SHARED ? C::RT : 1];
 };
 
 // The sign matrix of the index bits that a lane's eight elements and its lane
@@ -560,21 +584,22 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
     }
     // one power of two for all rows of the wave puts the largest element at
     // 2^5 .. 2^6 (a group's sum then stays in float16's range); an element
-    // 2^-20 of it still has all eleven bits, one of 2^-30 still one
+    // 2^-20 of it still has all eleven bits, one of 2^-30 still one.  With
+    // shared operands, at 2 .. 4: their scaled keys have range to spare too.
     top = max_wave(top);
     if constexpr (C::SHARED) {   // (of the workgroup: the shared scales carry c)
         __syncthreads();
         if (lane == 0) lds[threadIdx.x >> 6] = top;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, lds[i]);
+        for (int i = 0; i < C::WR; ++i) top = fmaxf(top, lds[i]);
         __syncthreads();
     }
     int e = 0;
-    if (top > 0.0f) e = min(max(6 - (static_cast<int>(__float_as_uint(top) >> 23) - 126), -100), 100);
+    if (top > 0.0f) e = min(max((C::SHARED ? 2 : 6) - (static_cast<int>(__float_as_uint(top) >> 23) - 126), -100), 100);
     e = __builtin_amdgcn_readfirstlane(e);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    w.c = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + (C::SUBK ? 24 : 0) - e) << 23);
+    w.c = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + (C::SUBK && !C::SHARED ? 24 : 0) - e) << 23);
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt) {
         float sum[C::NG];
@@ -589,11 +614,11 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float f = C::SUBK && (j & 1) ? up * 0.0625f : up;
+                const float f = C::SUBK && !C::SHARED && (j & 1) ? up * 0.0625f : up;
                 const float x = v[rt][8 * i + j] * f, y = v[rt][8 * i + j + 4] * f;
                 hi[j] = pack_f16(x, y);
                 if constexpr (C::WIDE) lo[j] = pack_f16(x - lo_f32(hi[j]), y - hi_f32(hi[j]));
-                if constexpr (C::SUBK) {
+                if constexpr (C::SUBK && !C::SHARED) {
                     const float back = lo_f32(hi[j]) + hi_f32(hi[j]);
                     sum[C::NG == 1 ? 0 : i / C::KG] += (j & 1) ? back * 16.0f : back;
                 }
@@ -613,6 +638,12 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
         }
         w.mc[rt] = kLow;
         w.l[rt] = 0.0f;
+        if constexpr (C::SHARED) {
+            constexpr float s = kPExp;
+            w.start[rt] = s;
+            w.from[rt] = float4v{s, s, s, s};
+            w.lsum[rt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+        }
 #pragma unroll
         for (int j = 0; j < C::DT; ++j) w.o[rt][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -814,7 +845,7 @@ __device__ __forceinline__ void step(const CacheAttnArgs& a, const Raw<C>& w, co
         probabilities<C>(st, rt, x[rt], mul, vs, ph[rt], pl[rt]);
     }
     // O^T += V^T P^T, two dimensions a byte
-    const Values<C> values(zs, w, vs);
+    const Values<C, (NG > 1)> values(zs, w, vs);
 #pragma unroll
     for (int b = 0; b < value_bytes<C>(); ++b) {
         HR_PHASE();
@@ -1016,89 +1047,188 @@ __device__ __forceinline__ void join_waves(const CacheAttnArgs& a, const Seq& s,
     }
 }
 
-// A 32-key tile as operands, in LDS.
+// ---------------------------------------------------------------------------
+// Many rows: shared operands.  Eight waves have 16 or 32 rows each, one after
+// the other of the same unit.  For every pass of TILES x 32 keys some of the
+// waves turn the keys' or the values' codes of a tile into operands in LDS,
+// scaled: k times the factor that gives log2 units, v times a power of two that
+// covers the values so far.  That is done once for all rows, and leaves a row's
+// wave for each score one exponential, half a maximum and half a conversion:
+//   - the running maximum is the start value of the matrix product, so that
+//     its result is the exponent (kPExp - mc + score) itself;
+//   - the sum of exponentials is a matrix product with ones.
+// Two passes' operands are in LDS: a pass is made while the one before it is
+// computed.  The waves that make values do so first (their scales are looked
+// at again at the end of a pass), those that make keys last: the two of a SIMD
+// are one of each, so that its matrix unit and its vector unit both have work.
+// Scaled operands are rounded to float16 (2^-12, as the queries are); float32
+// activations take pairs of float16 throughout.
+
 template <class C>
 struct Tile {
-    uint4v k[2 * C::KS][64];
-    uint4v v[C::DT][64];
-    uint4v vl[C::VLO ? C::DT : 1][C::VLO ? 64 : 1];
-    float4v mul[C::NG][8];     // key scales times c: [4 s + g] holds keys 16 s + 4 g ...
-    float4v vs[8];             // one group: value scales times 2^-e
-    int e, here;               // here: bit s set if subtile s is on a present page
+    uint4v k[C::P][2 * C::KS][64];
+    uint4v v[C::P][C::DT][64];
+};
+template <class C>
+struct Passes {
+    Tile<C> tile[2][C::TILES];
+    int keys[2][4];             // of a tile's keys: bit s: subtile s is on an absent page;
+                                // 4 x shift: they are times 2^-shift (extreme scales)
+    uint32_t odd[2][4];         // keys whose value scale is not finite
+    int e[2][C::TILES];         // exponent that covers a tile's value scales
+    float top[C::WR];
 };
 template <class C>
 constexpr int lds_floats() {
-    if constexpr (C::SHARED) return C::TILES * static_cast<int>(sizeof(Tile<C>)) / 4;
+    if constexpr (C::SHARED) return static_cast<int>(sizeof(Passes<C>)) / 4;
     else return join_floats<C>();
 }
 
-// Makes a tile of the 32 keys in w.
+// Codes and scales of a tile's keys: key m in the lane.
 template <class C>
-__device__ __forceinline__ void make_tile(const CacheAttnArgs& a, const Raw<C>& w, const Pages& pages, int t0, int end, float c,
-                                          Tile<C>& tile) {
-    constexpr int NG = C::NG;
+struct RawK {
+    uint32_t k[2][C::KS];
+    uint32_t ks[2][(C::NG * C::ES + 3) / 4];
+    uint32_t kz[2];
+};
+// Codes and scales of its values: keys 4 g + r of a subtile.
+template <class C>
+struct RawV {
+    uint32_t v[8][C::VW];
+    uint32_t vs[C::NG == 1 ? 2 : 8][C::NG == 1 ? C::KSW : 1];
+    uint32_t vz[C::NG == 1 ? 2 : 8];
+};
+
+template <class C>
+__device__ __forceinline__ void load_raw(const CacheAttnArgs& a, const Pages& pages, int h, int t0, RawK<C>& w) {
+    constexpr int D = C::D, NG = C::NG;
     const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const __amdgpu_buffer_rsrc_t r = head_buffer(a, pages.p[s], h);
+        const int off = (t0 + 16 * s) & (a.pg.page - 1);
+        const int kc = a.pg.kc + off * (D / 2), ks = a.pg.ks + off * (NG * C::ES), kz = a.pg.kz + off * NG / 2;
+        int kl = m * (D / 2) + g * (NG == 1 ? D / 8 : 4);
+        HR_KEEP(kl);
+        if constexpr (NG == 1) {
+            buffer_words<C::KS>(r, kl, kc, w.k[s]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < C::KS; ++i) buffer_words<1>(r, kl + i * 16, kc, &w.k[s][i]);
+        }
+        if constexpr (NG * C::ES == 2) w.ks[s][0] = buffer_u16(r, 2 * m, ks);
+        else buffer_words<NG * C::ES / 4>(r, NG * C::ES * m, ks, w.ks[s]);
+        if constexpr (NG == 1) w.kz[s] = buffer_u8(r, m / 2, kz);
+        else if constexpr (NG == 2) w.kz[s] = buffer_u8(r, m, kz);
+        else if constexpr (NG == 4) w.kz[s] = buffer_u16(r, 2 * m, kz);
+        else buffer_words<1>(r, 4 * m, kz, &w.kz[s]);
+    }
+}
+
+template <class C>
+__device__ __forceinline__ void load_raw(const CacheAttnArgs& a, const Pages& pages, int h, int t0, RawV<C>& w) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+        load_values<C>(a, head_buffer(a, pages.p[s], h), (t0 + 16 * s) & (a.pg.page - 1), s, w);
+}
+
+// Makes the key operands of a tile.  (c: log2 units of a product with the
+// queries as they are held.)
+template <class C>
+__device__ __forceinline__ void make_keys(const CacheAttnArgs& a, const RawK<C>& w, const Pages& pages, int t0, int end, float c,
+                                          Tile<C>& tile, int* special) {
+    constexpr int NG = C::NG;
+    const int lane = threadIdx.x & 63, m = lane & 15;
     const Zeros zs = zeros_of(a);
+    float ks[2][NG], big = 0.0f;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) {
+            ks[s][gi] = t0 + 16 * s + m < end ? scale_at<C::SF32>(w.ks[s], gi) * c : 0.0f;
+            big = fmaxf(big, fabsf(ks[s][gi]) < __builtin_inff() ? fabsf(ks[s][gi]) : 0.0f);
+        }
+    // c - z is at most 15: scales of 2^-13 .. 2^12 keep within float16, and
+    // others are moved there
+    big = max_wave(big);
+    int e = 0;
+    if (big > 4096.0f || (big < 0x1p-13f && big > 0.0f)) e = static_cast<int>(__float_as_uint(big) >> 23) - 126;
+    e = __builtin_amdgcn_readfirstlane(e);
+    if (e != 0) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi) ks[s][gi] = ldexpf(ks[s][gi], -e);
+    }
+    if (lane == 0) *special = (present(a, pages.p[0]) ? 0 : 1) | (present(a, pages.p[1]) ? 0 : 2) | e * 4;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int i = 0; i < C::KS; ++i) {
             const int gi = i / C::KG;
             const uint32_t z = NG == 1 ? w.kz[s] >> (4 * (lane & 1)) : w.kz[s] >> (4 * gi);
-            uint32_t z0 = (((z << 16) | (z & 0xFFFFu)) & zs.mask) | zs.fixed, z1 = z0 << 4;
-            if constexpr (!C::SUBK) {
-                z0 |= 0x64006400u;
-                z1 |= 0x54005400u;
+            uint32_t z0 = (((z << 16) | (z & 0xFFFFu)) & zs.mask) | zs.fixed;
+            const uint32_t z1 = (z0 << 4) | 0x54005400u;
+            z0 |= 0x64006400u;
+            const uint32_t hi = pack_f16(ks[s][gi], ks[s][gi]);
+            const uint4v d = code_operand<false, true>(w.k[s][i], zs.flip, z0, z1);
+            uint4v f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = pk_mul(d[j], hi);
+            tile.k[0][s * C::KS + i][lane] = f;
+            if constexpr (C::WIDE) {
+                const float rest = ks[s][gi] - lo_f32(hi);
+                const uint32_t lo = pack_f16(rest, rest);
+                uint4v fl;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) fl[j] = pk_fma(d[j], lo, pk_fma(d[j], hi, f[j] ^ 0x80008000u));
+                tile.k[1][s * C::KS + i][lane] = fl;
             }
-            tile.k[s * C::KS + i][lane] = code_operand<C::SUBK, true>(w.k[s][i], zs.flip, z0, z1);
         }
-    HR_PHASE();
-    // scales; those past the sequence or on an absent page are not looked at
-    float vs[8];
-    bool odd = false;
+}
+
+// Value scales of a tile; those past the sequence or on an absent page are 0.
+template <class C>
+__device__ __forceinline__ void value_scales(const CacheAttnArgs& a, const RawV<C>& w, const Pages& pages, int t0, int end,
+                                             float (&vs)[8]) {
+    const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-        if constexpr (NG == 1) vs[t] = scale_at<C::SF32>(w.vs[t / 4], t & 3);
+        if constexpr (C::NG == 1) vs[t] = scale_at<C::SF32>(w.vs[t / 4], t & 3);
         else vs[t] = __uint_as_float(C::SF32 ? w.vs[t][0] : w.vs[t][0] << 16);
         if (t0 + 16 * (t / 4) + 4 * g + t % 4 >= end || !present(a, pages.p[t / 4])) vs[t] = 0.0f;
-        odd |= !(fabsf(vs[t]) < __builtin_inff());
     }
+}
+
+// Makes the value operands of a tile, times 2^(kSExp - e).
+template <class C>
+__device__ __forceinline__ void make_values(const CacheAttnArgs& a, const RawV<C>& w, const Pages& pages, int t0, int end, int e,
+                                            Tile<C>& tile, uint32_t* odd) {
+    const int lane = threadIdx.x & 63;
+    float vs[8];
+    value_scales<C>(a, w, pages, t0, end, vs);
     // a value scale that is not finite must reach the queries that see its key
-    // and no others: it leaves the tile, and the key's score becomes NaN
-    uint32_t bad = 0;
-    if (__any(odd)) {
+    // and no others: it leaves the tile, and the key is marked
+    bool any = false;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) any |= !(fabsf(vs[t]) < __builtin_inff());
+    uint32_t marks = 0;
+    if (__any(any)) {
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             const bool mine = !(fabsf(vs[t]) < __builtin_inff());
             if (mine) vs[t] = 0.0f;
-            if ((__ballot(mine) >> (16 * g)) & 0xFFFFu) bad |= 1u << t;
+            const uint64_t who = __ballot(mine);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if ((who >> (16 * y)) & 0xFFFFu) marks |= 1u << (16 * (t / 4) + 4 * y + t % 4);
         }
     }
-    const int e = exponent_of(vs, -100);
-    const float down = ldexpf(1.0f, (NG == 1 ? 0 : kSExp) - e);
+    if (lane == 0) *odd = marks;
+    const float down = ldexpf(1.0f, kSExp - e);
 #pragma unroll
     for (int t = 0; t < 8; ++t) vs[t] *= down;
-    if (m == 0) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-#pragma unroll
-            for (int gi = 0; gi < NG; ++gi) {
-                float4v x;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    x[r] = scale_at<C::SF32>(w.ks[s], r * NG + gi) * c;
-                    if (bad >> (4 * s + r) & 1) x[r] = __builtin_nanf("");
-                }
-                tile.mul[gi][4 * s + g] = x;
-            }
-            if constexpr (NG == 1) tile.vs[4 * s + g] = float4v{vs[4 * s], vs[4 * s + 1], vs[4 * s + 2], vs[4 * s + 3]};
-        }
-    }
-    if (lane == 0) {
-        tile.e = e;
-        tile.here = (present(a, pages.p[0]) ? 1 : 0) | (present(a, pages.p[1]) ? 2 : 0);
-    }
-    const Values<C> values(zs, w, vs);
+    const Values<C, true> values(zeros_of(a), w, vs);
 #pragma unroll
     for (int b = 0; b < value_bytes<C>(); ++b) {
         HR_PHASE();
@@ -1107,88 +1237,264 @@ __device__ __forceinline__ void make_tile(const CacheAttnArgs& a, const Raw<C>& 
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             uint4v vl;
-            tile.v[2 * b + half][lane] = values.operand(y, half, &vl);
-            if constexpr (C::VLO) tile.vl[2 * b + half][lane] = vl;
+            tile.v[0][2 * b + half][lane] = values.operand(y, half, &vl);
+            if constexpr (C::WIDE) tile.v[1][2 * b + half][lane] = vl;
         }
     }
 }
 
-// One step over a tile; the keys that all rows of the wave see: [flo, fhi).
+// Operands of a tile on their way from LDS: GROUP of them at a time, while the
+// products of the group before them run.
 template <class C>
-__device__ __forceinline__ void tile_step(const Tile<C>& tile, int t0, const Span& sp, Rows<C>& st) {
-    constexpr int NG = C::NG, RT = C::RT;
+struct Fetch {
+    static constexpr int GROUP = 4;
+    uint4v f[C::P][GROUP];
+    __device__ __forceinline__ void keys(const Tile<C>& tile, int first) {
+#pragma unroll
+        for (int p = 0; p < C::P; ++p)
+#pragma unroll
+            for (int i = 0; i < GROUP; ++i)
+                if (first + i < 2 * C::KS) f[p][i] = tile.k[p][first + i][threadIdx.x & 63];
+    }
+    __device__ __forceinline__ void values(const Tile<C>& tile, int first) {
+#pragma unroll
+        for (int p = 0; p < C::P; ++p)
+#pragma unroll
+            for (int i = 0; i < GROUP; ++i) f[p][i] = tile.v[p][first + i][threadIdx.x & 63];
+    }
+};
+
+// One step over a tile.  special: what the makers noted of it, odd: keys with
+// bad value scales; unset: some row has not seen a key yet.
+template <class C>
+__device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint32_t odd, int t0, const Span& sp, Rows<C>& st,
+                                          bool& unset) {
+    constexpr int RT = C::RT, GROUP = Fetch<C>::GROUP;
     const int lane = threadIdx.x & 63, g = lane >> 4;
-    float x[RT][8], mul[8];
+    float x[RT][8];
+    // scores as exponents: the products start from kPExp - mc.  (float32
+    // activations: added at the end, it would cost the sums bits; extreme
+    // scales: their unit is not 1)
+    const int shift = special >> 2;
+    const bool late = C::WIDE || shift != 0;
+    if (late) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+        for (int rt = 0; rt < RT; ++rt) st.from[rt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    float4v acc[2][RT];
+    Fetch<C> now, next;
+    now.keys(tile, 0);
 #pragma unroll
-        for (int gi = 0; gi < NG; ++gi) {
-            float4v acc[RT];
+    for (int first = 0; first < 2 * C::KS; first += GROUP) {
+        HR_PHASE();
+        if (first + GROUP < 2 * C::KS) next.keys(tile, first + GROUP);
+        else next.values(tile, 0);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) acc[rt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int i = gi * C::KG; i < (gi + 1) * C::KG; ++i) {
-                const uint4v f = tile.k[s * C::KS + i][lane];
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    acc[rt] = mfma(f, st.q[rt][0][i], acc[rt]);
-                    if constexpr (C::WIDE) acc[rt] = mfma(f, st.q[rt][1][i], acc[rt]);
-                }
-            }
-            const float4v ks = tile.mul[gi][4 * s + g];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                mul[4 * s + r] = NG == 1 ? ks[r] : 1.0f;
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    if constexpr (NG == 1) x[rt][4 * s + r] = acc[rt][r];
-                    else x[rt][4 * s + r] = gi == 0 ? acc[rt][r] * ks[r] : fmaf(acc[rt][r], ks[r], x[rt][4 * s + r]);
-                }
-            }
-        }
-    const int here = __builtin_amdgcn_readfirstlane(tile.here);
-    if (!(t0 >= sp.flo && t0 + 32 <= sp.fhi && here == 3)) {
-        // unseen scores become -inf, whatever they are
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const int key = t0 + 16 * (t / 4) + 4 * g + t % 4;
+        for (int i = first; i < first + GROUP && i < 2 * C::KS; ++i) {
+            const int s = i / C::KS, k = i % C::KS;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const bool seen = (here >> (t / 4) & 1) && key < st.lim[rt] && key >= st.lo[rt];
-                x[rt][t] = seen ? x[rt][t] * mul[t] : -__builtin_inff();
+                acc[s][rt] = mfma(now.f[0][i - first], st.q[rt][0][k], k == 0 ? st.from[rt] : acc[s][rt]);
+                if constexpr (C::WIDE) {
+                    acc[s][rt] = mfma(now.f[0][i - first], st.q[rt][1][k], acc[s][rt]);
+                    acc[s][rt] = mfma(now.f[1][i - first], st.q[rt][0][k], acc[s][rt]);
+                }
             }
-            mul[t] = 1.0f;
+        }
+        now = next;
+    }
+    HR_PHASE();
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[rt][k] = acc[k / 4][rt][k % 4];
+    if (late) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[rt][k] = (C::WIDE && shift == 0 ? x[rt][k] : ldexpf(x[rt][k], shift)) + st.start[rt];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) st.from[rt] = float4v{st.start[rt], st.start[rt], st.start[rt], st.start[rt]};
+    }
+    if (!(t0 >= sp.flo && t0 + 32 <= sp.fhi && (special & 3) == 0 && odd == 0)) {
+        // unseen scores become -inf, whatever they are
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int at = 16 * (k / 4) + 4 * g + k % 4, key = t0 + at;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const bool seen = !(special >> (k / 4) & 1) && key < st.lim[rt] && key >= st.lo[rt];
+                if (odd >> at & 1) x[rt][k] = __builtin_nanf("");
+                if (!seen) x[rt][k] = -__builtin_inff();
+            }
         }
     }
-    const int e = __builtin_amdgcn_readfirstlane(tile.e);
-    if (e > st.e) raise_exponent<C>(st, e);
-    const float f = ldexpf(1.0f, kPExp + e - st.e);
-    float vs[8];
-    if constexpr (NG == 1) {
+    float p[RT][8], top = 0.0f;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const float4v y = tile.vs[4 * s + g];
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) vs[4 * s + r] = y[r] * f;
+        for (int k = 0; k < 8; ++k) {
+            p[rt][k] = __builtin_amdgcn_exp2f(x[rt][k]);
+            top = fmaxf(top, p[rt][k]);
         }
-    } else {
+    if (unset || __any(top > static_cast<float>(1 << (kPExp + kSlack)))) {
+        bool left = false;
 #pragma unroll
-        for (int t = 0; t < 8; ++t) vs[t] = f;
+        for (int rt = 0; rt < RT; ++rt) {
+            float w = -__builtin_inff();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w = fmaxf(w, x[rt][k]);
+            w = max_groups(w) - kPExp;                       // how far the running maximum moves
+            const bool fresh = st.mc[rt] == kLow;
+            const float d = w > 0.0f || (fresh && w > -__builtin_inff()) ? w : 0.0f;
+            if (fresh && !(w > -__builtin_inff())) left = true;
+            else st.mc[rt] = fresh ? d : st.mc[rt] + d;
+            const float f = fresh ? 1.0f : exp2f(-d);        // (nothing to scale before the first key)
+            st.start[rt] -= d;
+            st.from[rt] = float4v{st.start[rt], st.start[rt], st.start[rt], st.start[rt]};
+            st.lsum[rt] *= f;
+#pragma unroll
+            for (int j = 0; j < C::DT; ++j) st.o[rt][j] *= f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) p[rt][k] = __builtin_amdgcn_exp2f(x[rt][k] - d);
+        }
+        unset = __any(left);
     }
     uint4v ph[RT], pl[RT];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) probabilities<C>(st, rt, x[rt], mul, vs, ph[rt], pl[rt]);
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-    for (int j = 0; j < C::DT; ++j) {
-        const uint4v vh = tile.v[j][lane];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            float4v& o = st.o[rt][j];
-            o = mfma(vh, ph[rt], o);
-            if constexpr (C::WIDE) o = mfma(vh, pl[rt], o);
-            if constexpr (C::VLO) o = mfma(tile.vl[j][lane], ph[rt], o);
+        for (int k = 0; k < 4; ++k) {
+            ph[rt][k] = pack_f16(p[rt][2 * k], p[rt][2 * k + 1]);
+            if constexpr (C::WIDE) pl[rt][k] = pack_f16(p[rt][2 * k] - lo_f32(ph[rt][k]), p[rt][2 * k + 1] - hi_f32(ph[rt][k]));
         }
+    const uint4v ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        st.lsum[rt] = mfma(ones, ph[rt], st.lsum[rt]);
+        if constexpr (C::WIDE) st.lsum[rt] = mfma(ones, pl[rt], st.lsum[rt]);
     }
+#pragma unroll
+    for (int first = 0; first < C::DT; first += GROUP) {
+        HR_PHASE();
+        if (first + GROUP < C::DT) next.values(tile, first + GROUP);
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                float4v& o = st.o[rt][first + i];
+                o = mfma(now.f[0][i], ph[rt], o);
+                if constexpr (C::WIDE) {
+                    o = mfma(now.f[0][i], pl[rt], o);
+                    o = mfma(now.f[1][i], ph[rt], o);
+                }
+            }
+        now = next;
+    }
+    HR_PHASE();
+}
+
+// What a wave makes for the passes, besides computing: keys or values of tile
+// `tile`, or nothing.  (Each is a loop of its own, so that a wave holds only
+// what it loads, and no value of a load on its way passes through a branch.)
+enum { kMakeKeys, kMakeValues, kMakeNothing };
+
+template <class C, int ROLE>
+__device__ __forceinline__ void passes(const CacheAttnArgs& a, const int32_t* table, int h, int tile, int begin, int end, const Span& sp,
+                                       Rows<C>& st, Passes<C>& ps) {
+    constexpr int S = 32 * C::TILES, N = C::TILES;
+    const int lane = threadIdx.x & 63, mine = 32 * tile;
+    std::conditional_t<ROLE == kMakeKeys, RawK<C>, RawV<C>> w;
+    Pages now, next = pages_at(a, table, min(begin + mine, max(end - 1, 0) & ~15));
+    // the tile of the pass at t, and the pages of the next.  Past the end there
+    // is no page, so that nothing is read.
+    const auto load = [&](int t) {
+        if constexpr (ROLE == kMakeNothing) return;
+        now = next;
+        if (t + mine >= end) now.p[0] = now.p[1] = -1;
+        load_raw<C>(a, now, h, t + mine, w);
+        next = pages_at(a, table, min(t + S + mine, max(end - 1, 0) & ~15));
+    };
+    const auto announce = [&](int t, int buf) {   // the value scales' exponent of the loaded tile
+        if constexpr (ROLE == kMakeValues) {
+            float vs[8];
+            value_scales<C>(a, w, now, t + mine, end, vs);
+            const int e = exponent_of(vs, -100);
+            if (lane == 0) ps.e[buf][tile] = e;
+        }
+    };
+    int made = -100;                    // the exponent of the pass made last
+    const auto make = [&](int t, int buf) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) made = max(made, __builtin_amdgcn_readfirstlane(ps.e[buf][i]));
+        if constexpr (ROLE == kMakeKeys) {
+            if (t + mine < end) make_keys<C>(a, w, now, t + mine, end, st.c, ps.tile[buf][tile], &ps.keys[buf][tile]);
+        } else if constexpr (ROLE == kMakeValues) {
+            if (t + mine < end) make_values<C>(a, w, now, t + mine, end, made, ps.tile[buf][tile], &ps.odd[buf][tile]);
+        }
+    };
+    load(begin);
+    announce(begin, 0);
+    __syncthreads();
+    make(begin, 0);
+    load(begin + S);
+    announce(begin + S, 1);
+    __syncthreads();
+    bool unset = true;
+    int buf = 0;
+    for (int t = begin; t < end; t += S, buf ^= 1) {
+        const int e = made;             // of this pass; make() may raise it for the next
+        if constexpr (ROLE != kMakeKeys) {
+            make(t + S, buf ^ 1);
+            load(t + 2 * S);
+        }
+        if (e > st.e) raise_exponent<C>(st, e);
+        // (tiles that no row of the wave sees are left out)
+        const int first = max(sp.lo - t, 0) >> 5, stop = (min(min(end, sp.hi) - t, S) + 31) >> 5;
+#pragma unroll 1
+        for (int i = first; i < stop; ++i)
+            tile_step<C>(ps.tile[buf][i], __builtin_amdgcn_readfirstlane(ps.keys[buf][i]), __builtin_amdgcn_readfirstlane(ps.odd[buf][i]),
+                         t + 32 * i, sp, st, unset);
+        if constexpr (ROLE == kMakeKeys) {
+            make(t + S, buf ^ 1);
+            load(t + 2 * S);
+        }
+        // (the exponents of the next pass were read above by every wave before
+        // its own barrier, those after it go to this pass's place)
+        announce(t + 2 * S, buf);
+        __syncthreads();
+    }
+}
+
+// Rows [r0, r0 + ROWS) of kv head h of a sequence over the keys [k0, k1);
+// part: where a partial result goes (else the rows are finished here).
+template <class C, class T>
+__device__ __forceinline__ void shared_segment(const CacheAttnArgs& a, const Seq& s, int b, int h, int r0, int k0, int k1,
+                                               float* part, float* lds) {
+    constexpr int N = C::TILES;
+    Passes<C>& ps = *reinterpret_cast<Passes<C>*>(lds);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t* table = a.sq.table + static_cast<int64_t>(b) * a.sq.max_pages;
+    const int row = r0 + wave * 16 * C::RT, last = s.n * a.rep;
+    const Span all = span_of(a, s, r0, min(r0 + C::ROWS, last));
+    Span sp = {0, 0, 0, 0};
+    if (row < last) sp = span_of(a, s, row, min(row + 16 * C::RT, last));
+    const int begin = max(k0, all.lo & ~31), end = min(k1, all.hi);
+    Rows<C> st;
+    load_rows<C, T>(a, s, h, row, st, ps.top);
+    if (wave < N) passes<C, kMakeKeys>(a, table, h, wave, begin, end, sp, st, ps);
+    else if (wave < 2 * N) passes<C, kMakeValues>(a, table, h, wave - N, begin, end, sp, st, ps);
+    else passes<C, kMakeNothing>(a, table, h, 0, begin, end, sp, st, ps);
+    // to value units, as the other kernels leave them
+#pragma unroll
+    for (int rt = 0; rt < C::RT; ++rt) {
+        st.l[rt] = ldexpf(st.lsum[rt][0], -kPExp);
+#pragma unroll
+        for (int j = 0; j < C::DT; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) st.o[rt][j][r] = ldexpf(st.o[rt][j][r], st.e - kPExp - kSExp);
+    }
+    put_rows<C, T>(a, s, h, row, st, part, row - r0);
 }
 
 // Rows [r0, r0 + ROWS) of kv head h of a sequence over the keys [k0, k1);
@@ -1196,57 +1502,20 @@ __device__ __forceinline__ void tile_step(const Tile<C>& tile, int t0, const Spa
 template <class C, class T>
 __device__ __forceinline__ void segment(const CacheAttnArgs& a, const Seq& s, int b, int h, int r0, int k0, int k1,
                                         float* part, float* lds) {
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int32_t* table = a.sq.table + static_cast<int64_t>(b) * a.sq.max_pages;
-    Rows<C> st;
-    if constexpr (!C::SHARED) {
+    if constexpr (C::SHARED) {
+        shared_segment<C, T>(a, s, b, h, r0, k0, k1, part, lds);
+    } else {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const Span sp = span_of(a, s, r0, min(r0 + C::ROWS, s.n * a.rep));
+        Rows<C> st;
         Walk<C> keys;
-        keys.table = table;
+        keys.table = a.sq.table + static_cast<int64_t>(b) * a.sq.max_pages;
         keys.h = h;
         keys.start(a, sp, k0, k1, wave);
         load_rows<C, T>(a, s, h, r0, st, lds);
         keys.run(a, sp, st);
         settle<C>(st);
         join_waves<C, T>(a, s, h, r0, st, part, lds);
-    } else {
-        // the waves make a tile each and then take all of them; the next
-        // tiles' keys are on their way meanwhile
-        constexpr int S = 32 * C::TILES;
-        Tile<C>* tiles = reinterpret_cast<Tile<C>*>(lds);
-        const int row = r0 + wave * 16 * C::RT, last = s.n * a.rep;
-        const Span all = span_of(a, s, r0, min(r0 + C::ROWS, last));
-        Span sp = {0, 0, 0, 0};
-        if (row < last) sp = span_of(a, s, row, min(row + 16 * C::RT, last));
-        int t = max(k0, all.lo & ~31);
-        const int end = min(k1, all.hi);
-        const bool makes = wave < C::TILES;
-        const int own = 32 * wave;
-        Raw<C> w;
-        Pages now = {{-1, -1}}, next = {{-1, -1}};
-        if (makes && t + own < end) {
-            now = pages_at(a, table, t + own);
-            load_keys<C>(a, now, h, t + own, w);
-        }
-        if (makes && t + S + own < end) next = pages_at(a, table, t + S + own);
-        load_rows<C, T>(a, s, h, row, st, lds);
-        for (; t < end; t += S) {
-            if (makes && t + own < end) make_tile<C>(a, w, now, t + own, end, st.c, tiles[wave]);
-            if (makes && t + S + own < end) {
-                now = next;
-                load_keys<C>(a, now, h, t + S + own, w);
-                if (t + 2 * S + own < end) next = pages_at(a, table, t + 2 * S + own);
-            }
-            __syncthreads();
-#pragma unroll 1
-            for (int i = 0; i < C::TILES; ++i) {
-                const int at = t + 32 * i;
-                if (at < min(end, sp.hi) && at + 32 > sp.lo) tile_step<C>(tiles[i], at, sp, st);
-            }
-            __syncthreads();
-        }
-        settle<C>(st);
-        put_rows<C, T>(a, s, h, row, st, part, row - r0);
     }
 }
 
@@ -1256,50 +1525,137 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
     return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
 }
 
-// The items of a sequence: for each kv head and row block a unit of kSetup items
-// that stand for its start and end, then one for each block of keys, at least
-// one so that rows that see nothing are written too.
-constexpr int kSetup = 4;  // a unit's start and end cost about four blocks of keys (7 against 1.7 us)
-struct Items {
-    int first, blocks, rbs;   // first key (a multiple of 32), key blocks, row blocks
-    int64_t total;
-};
+// A walk over the row blocks of a sequence: their rows and the keys that they
+// see.  (Tokens are counted along, as a division for each block would cost more
+// than the rest.)
 template <class C>
-__device__ __forceinline__ Items items_of(const CacheAttnArgs& a, const Seq& s) {
-    Items it;
-    it.rbs = (s.n * a.rep + C::ROWS - 1) / C::ROWS;
-    it.first = 0;
-    it.blocks = 1;
-    if (s.n > 0) {
-        const Span sp = span_of(a, s, 0, s.n * a.rep);
-        it.first = min(sp.lo, sp.hi) & ~31;
-        it.blocks = max((sp.hi - it.first + C::KEYS - 1) / C::KEYS, 1);
+__device__ __forceinline__ uint32_t row_blocks(const CacheAttnArgs& a, const Seq& s) {
+    return (static_cast<uint32_t>(s.n) * static_cast<uint32_t>(a.rep) + C::ROWS - 1) / C::ROWS;
+}
+template <class C>
+struct RowBlocks {
+    int rep, step, over;      // ROWS = step rep + over
+    int past, len, last;      // keys before the new tokens (may be negative), all keys, the last token
+    int window;
+    bool causal;
+    int tok, rem;             // the token of the block's first row, and how far the row is into it
+    int first, blocks;        // first key (a multiple of 32), key blocks (at least one, so that rows that see nothing are written)
+    __device__ __forceinline__ RowBlocks(const CacheAttnArgs& a, const Seq& s, uint32_t i) {
+        rep = a.rep;
+        step = a.step;
+        over = a.over;
+        past = s.len - s.n;
+        len = s.len;
+        last = s.n - 1;
+        window = a.window;
+        causal = a.causal != 0;
+        tok = rem = 0;
+        if (i > 0) {
+            const uint32_t r0 = i * C::ROWS;
+            tok = static_cast<int>(r0 / static_cast<uint32_t>(rep));
+            rem = static_cast<int>(r0) - tok * rep;
+        }
+        see();
     }
-    it.total = static_cast<int64_t>(a.pg.hkv * it.rbs) * (it.blocks + kSetup);
-    return it;
+    __device__ __forceinline__ void next() {
+        tok += step;
+        rem += over;
+        if (rem >= rep) {
+            rem -= rep;
+            ++tok;
+        }
+        see();
+    }
+    __device__ __forceinline__ void see() {
+        const int x = rem + over;   // the last row's token: ceil((rem + ROWS) / rep) - 1 past tok
+        const int to = min(tok + step + (x > 0 ? 1 : 0) + (x > rep ? 1 : 0) - 1, last);
+        const int hi = causal ? min(max(past + to + 1, 0), len) : len;
+        const int lo = window ? max(past + tok - window + 1, 0) : 0;
+        first = min(lo, hi) & ~31;
+        blocks = max((hi - first + C::KEYS - 1) / C::KEYS, 1);
+    }
+};
+
+// Work is counted in items.  For each kv head and row block a unit has kSetup
+// items that stand for its start and end, then one for each block of keys.
+constexpr int kSetup = 4;  // a unit's start and end cost about four blocks of keys (7 against 1.7 us)
+// the items of row blocks [i, n) for one kv head; most: the largest unit
+template <class C>
+__device__ __forceinline__ int64_t items_of(const CacheAttnArgs& a, const Seq& s, uint32_t i, uint32_t n, int* most) {
+    if (i >= n) return 0;
+    RowBlocks<C> rb(a, s, i);
+    int64_t sum = rb.blocks + kSetup;
+    *most = max(*most, rb.blocks + kSetup);
+    for (++i; i < n; ++i) {
+        rb.next();
+        sum += rb.blocks + kSetup;
+        *most = max(*most, rb.blocks + kSetup);
+    }
+    return sum;
 }
 
-// sum of v over the workgroup's threads before this one, and over all
-__device__ __forceinline__ int64_t scan_items(int64_t v, int64_t* all, int64_t* lds) {
+// f over the values of this lane and those before it, by moves between lanes
+// (a general shuffle goes through LDS); 0 is f's identity.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int moved(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t moved(int64_t v) {
+    const uint32_t lo = moved<CTRL, ROWS>(static_cast<int>(v)), hi = moved<CTRL, ROWS>(static_cast<int>(v >> 32));
+    return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+template <class V, class F>
+__device__ __forceinline__ V scan_wave(V v, F f) {
+    v = f(v, moved<0x111, 0xF>(v));   // the lane 1, 2, 4, 8 before, in a row of 16
+    v = f(v, moved<0x112, 0xF>(v));
+    v = f(v, moved<0x114, 0xF>(v));
+    v = f(v, moved<0x118, 0xF>(v));
+    v = f(v, moved<0x142, 0xA>(v));   // a row's last lane to the row after it, in the second and fourth
+    v = f(v, moved<0x143, 0xC>(v));   // lane 31 to the upper half
+    return v;
+}
+struct Add {
+    __device__ __forceinline__ int64_t operator()(int64_t x, int64_t y) const { return x + y; }
+};
+struct Most {
+    __device__ __forceinline__ int operator()(int x, int y) const { return max(x, y); }
+};
+
+// Sums of N values over the workgroup's threads before this one, and over all;
+// the largest of another (N = 2).
+template <int THREADS, int N>
+__device__ __forceinline__ void scan_items(int64_t (&v)[2], int64_t (&all)[2], int* most, int64_t* lds) {
+    constexpr int W = THREADS / 64;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int64_t inc = v;
+    int64_t inc[N];
 #pragma unroll
-    for (int x = 1; x < 64; x *= 2) {
-        const int64_t y = __shfl_up(inc, x);
-        if (lane >= x) inc += y;
+    for (int i = 0; i < N; ++i) inc[i] = scan_wave(v[i], Add());
+    int m = 0;
+    if constexpr (N == 2) m = scan_wave(*most, Most());
+    __syncthreads();
+    if (lane == 63) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) lds[i * W + wave] = inc[i];
+        if constexpr (N == 2) lds[2 * W + wave] = m;
     }
     __syncthreads();
-    if (lane == 63) lds[wave] = inc;
-    __syncthreads();
-    int64_t before = 0, sum = 0;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        const int64_t y = lds[x];
-        if (x < wave) before += y;
-        sum += y;
+    for (int i = 0; i < N; ++i) {
+        int64_t before = 0;
+        all[i] = 0;
+#pragma unroll
+        for (int x = 0; x < W; ++x) {
+            const int64_t y = lds[i * W + x];
+            if (x < wave) before += y;
+            all[i] += y;
+        }
+        v[i] = before + inc[i] - v[i];
     }
-    *all = sum;
-    return before + inc - v;
+    if constexpr (N == 2) {
+#pragma unroll
+        for (int x = 0; x < W; ++x) *most = max(*most, static_cast<int>(lds[2 * W + x]));
+    }
 }
 
 // How the items are shared out: every workgroup of the first nw has `share`,
@@ -1313,66 +1669,153 @@ struct Shares {
         return u < longer ? u / (share + 1) : rest + (u - longer) / share;
     }
 };
+__device__ __forceinline__ Shares shares_of(int64_t total, int workers) {
+    const uint32_t nw = total < workers ? static_cast<uint32_t>(max(total, int64_t{1})) : workers;
+    Shares sh;
+    sh.total = total;
+    sh.share = total < (int64_t{1} << 31) ? static_cast<int64_t>(static_cast<uint32_t>(total) / nw) : total / nw;
+    sh.rest = total - sh.share * nw;
+    return sh;
+}
 
-// Workgroup w of the split form: its items [i0, i1), the sequence b that holds
-// the first and the items before that sequence.  Every thread takes part.
+// What cutting costs a workgroup, in items: a second unit's start and end, and
+// the joining launch.
+constexpr int kCut = 8;
+
+// Workgroup w: its items [i0, i1), the sequence b that holds the first and the
+// items before that sequence.  Every thread takes part.  whole: units are not
+// cut, as sharing them out whole is no longer for the workgroup that has most;
+// each counts as one item then.
 struct Place {
     Shares sh;
     int64_t i0, i1, before;
     int b;
+    bool whole;
     Seq s;                // sequence b
 };
 template <class C>
 __device__ __forceinline__ Place place(const CacheAttnArgs& a, int64_t* lds) {
+    constexpr int OUT = 3 * C::THREADS / 64, N = C::SHARED ? 2 : 1;
     const int tid = threadIdx.x;
+    // few sequences: 2^per threads for each, with a part of its row blocks
+    int per = 0;
+    while (per < 6 && (2 << per) * a.sq.rows <= C::THREADS) ++per;
+    const int nth = tid >> per, part = tid & ((1 << per) - 1), step = C::THREADS >> per;
     Place p;
-    int64_t total = 0, own = 0, pre = 0;
     Seq s = {0, 0, 0};
+    int most = 0;
+    int64_t total[2] = {0, 0}, own[2], pre[2], all[2];
     const auto items = [&](int b) {
-        if (b >= a.sq.rows) return int64_t{0};
-        s = seq_at<false>(a.sq, a.pg.logp, b);
-        return items_of<C>(a, s).total;
+        own[0] = own[1] = 0;
+        uint32_t n = 0;
+        if (b < a.sq.rows) {
+            s = seq_at<false>(a.sq, a.pg.logp, b);
+            n = row_blocks<C>(a, s);
+            const uint32_t each = (n + (1u << per) - 1) >> per, i = part * each;
+            own[0] = items_of<C>(a, s, i, min(i + each, n), &most);
+        }
+        if (__any(n > 1))
+            for (int x = 1; x < 1 << per; x *= 2) own[0] += __shfl_xor(own[0], x);
+        if (part == 0) own[1] = static_cast<int64_t>(n) * a.pg.hkv;
+        pre[0] = own[0] = part == 0 ? own[0] * a.pg.hkv : 0;
+        pre[1] = own[1];
+        scan_items<C::THREADS, N>(pre, all, &most, lds);
     };
-    // (a call of up to 256 sequences is scanned once)
-    for (int c = 0; c < a.sq.rows; c += 256) {
-        own = items(c + tid);
-        int64_t all;
-        pre = total + scan_items(own, &all, lds);
-        total += all;
+    // (a call of no more sequences than threads is scanned once)
+    for (int c = 0; c < a.sq.rows; c += step) {
+        items(c + nth);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            pre[i] += total[i];
+            total[i] += all[i];
+        }
     }
-    total = uniform64(total);
-    const uint32_t nw = total < a.workers ? static_cast<uint32_t>(max(total, int64_t{1})) : a.workers;
-    p.sh.total = total;
-    p.sh.share = total < (int64_t{1} << 31) ? static_cast<int64_t>(static_cast<uint32_t>(total) / nw) : total / nw;
-    p.sh.rest = total - p.sh.share * nw;
-    const int64_t w = min(blockIdx.x, nw);
-    p.i0 = p.sh.first(w);
-    p.i1 = min(p.sh.first(w + 1), total);
-    if (tid == 0) lds[4] = -1;
-    int64_t base = 0;
-    for (int c = 0; c < a.sq.rows; c += 256) {
-        if (a.sq.rows > 256) {
-            own = items(c + tid);
-            int64_t all;
-            pre = base + scan_items(own, &all, lds);
-            base += all;
+    p.sh = shares_of(uniform64(total[0]), a.workers);
+    p.whole = false;
+    if constexpr (N == 2) {
+        const Shares whole = shares_of(uniform64(total[1]), a.workers);
+        p.whole = (whole.share + (whole.rest > 0 ? 1 : 0)) * __builtin_amdgcn_readfirstlane(most) <= p.sh.share + kCut;
+        if (p.whole) p.sh = whole;
+    }
+    const int64_t w = blockIdx.x;
+    p.i0 = min(p.sh.first(w), p.sh.total);
+    p.i1 = min(p.sh.first(w + 1), p.sh.total);
+    if (tid == 0) lds[OUT] = -1;
+    int64_t base[2] = {0, 0};
+    for (int c = 0; c < a.sq.rows; c += step) {
+        if (a.sq.rows > step) {
+            items(c + nth);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                pre[i] += base[i];
+                base[i] += all[i];
+            }
         }
         __syncthreads();
-        if (p.i0 >= pre && p.i0 < pre + own) {
-            lds[4] = c + tid;
-            lds[5] = pre;
-            lds[6] = s.start;
-            lds[7] = static_cast<int64_t>(s.n) << 32 | static_cast<uint32_t>(s.len);
+        const int64_t at = p.whole ? pre[1] : pre[0];
+        if (p.i0 >= at && p.i0 < at + (p.whole ? own[1] : own[0])) {
+            lds[OUT] = c + nth;
+            lds[OUT + 1] = at;
+            lds[OUT + 2] = s.start;
+            lds[OUT + 3] = static_cast<int64_t>(s.n) << 32 | static_cast<uint32_t>(s.len);
         }
         __syncthreads();
-        if (lds[4] >= 0) break;
+        if (lds[OUT] >= 0) break;
     }
-    p.b = lds[4] >= 0 ? __builtin_amdgcn_readfirstlane(static_cast<int>(lds[4])) : a.sq.rows;
-    p.before = uniform64(lds[5]);
-    const int64_t nl = uniform64(lds[7]);
-    p.s = {__builtin_amdgcn_readfirstlane(static_cast<int>(lds[6])), static_cast<int>(nl >> 32), static_cast<int>(nl)};
+    p.b = lds[OUT] >= 0 ? __builtin_amdgcn_readfirstlane(static_cast<int>(lds[OUT])) : a.sq.rows;
+    p.before = uniform64(lds[OUT + 1]);
+    const int64_t nl = uniform64(lds[OUT + 3]);
+    p.s = {__builtin_amdgcn_readfirstlane(static_cast<int>(lds[OUT + 2])), static_cast<int>(nl >> 32), static_cast<int>(nl)};
     __syncthreads();
     return p;
+}
+
+// Where item `at` of a sequence is: its kv head, row block and unit's first
+// item; each: the items of a kv head.  Every lane of the wave takes part.
+struct Found {
+    int h;
+    uint32_t rb;
+    int64_t first, each;
+};
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {   // (of small numbers, mostly)
+    return x < (int64_t{1} << 31) && y < (int64_t{1} << 31) ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y)) : x / y;
+}
+template <class C>
+__device__ __forceinline__ Found find_item(const CacheAttnArgs& a, const Seq& s, uint32_t n, int64_t at, bool whole) {
+    Found f;
+    if (whole) {
+        f.each = n;
+        f.h = static_cast<int>(divide(at, n));
+        f.rb = static_cast<uint32_t>(at - f.h * f.each);
+        f.first = at;
+        return f;
+    }
+    if (n == 1) {
+        f.each = RowBlocks<C>(a, s, 0).blocks + kSetup;
+        f.h = static_cast<int>(divide(at, f.each));
+        f.rb = 0;
+        f.first = f.h * f.each;
+        return f;
+    }
+    int most = 0;
+    const uint32_t part = (n + 63) / 64, i = min((threadIdx.x & 63) * part, n);
+    const int64_t own = items_of<C>(a, s, i, min(i + part, n), &most), inc = scan_wave(own, Add());
+    f.each = uniform64(__shfl(inc, 63));
+    f.h = static_cast<int>(divide(at, f.each));
+    at -= f.h * f.each;
+    // the lane that has it, and from there on
+    const uint64_t who = __ballot(at >= inc - own && at < inc);
+    const int l = who ? __builtin_ctzll(who) : 0;
+    f.rb = __builtin_amdgcn_readfirstlane(__shfl(i, l));
+    f.first = uniform64(__shfl(inc - own, l));
+    RowBlocks<C> rb(a, s, f.rb);
+    while (f.first + rb.blocks + kSetup <= at) {
+        f.first += rb.blocks + kSetup;
+        ++f.rb;
+        rb.next();
+    }
+    f.first += f.h * f.each;
+    return f;
 }
 
 // What the joining launch needs of a unit that begins in a workgroup and goes
@@ -1386,7 +1829,7 @@ struct Cut {
 // Split form: workgroup w takes an equal share of all items.  A unit that it
 // does not hold whole goes to scratch slot 2 w + 1 if it begins here, else 2 w.
 template <class C, class T>
-__global__ void __launch_bounds__(256, C::WAVES) cache_attn_split(const CacheAttnArgs a) {
+__global__ void __launch_bounds__(C::THREADS, C::WAVES) cache_attn_split(const CacheAttnArgs a) {
     __shared__ float4v lds4[lds_floats<C>() / 4 + 1];
     float* lds = reinterpret_cast<float*>(lds4);
     const Place p = place<C>(a, reinterpret_cast<int64_t*>(lds));
@@ -1398,32 +1841,29 @@ __global__ void __launch_bounds__(256, C::WAVES) cache_attn_split(const CacheAtt
     Cut cut = {0, 0, 0, 0, -1};
     for (int b = p.b; b < a.sq.rows && i0 < i1; ++b) {
         const Seq s = b == p.b ? p.s : seq_at<true>(a.sq, a.pg.logp, b);
-        const Items it = items_of<C>(a, s);
-        const int size = it.blocks + kSetup;
-        while (i0 < i1 && i0 < before + it.total) {
-            const int64_t at = i0 - before;
-            int unit, from;
-            if (at < (int64_t{1} << 31)) {
-                unit = static_cast<uint32_t>(at) / static_cast<uint32_t>(size);
-                from = static_cast<int>(at) - unit * size;
-            } else {
-                unit = static_cast<int>(at / size);
-                from = static_cast<int>(at % size);
+        const uint32_t n = row_blocks<C>(a, s);
+        if (n == 0) continue;
+        Found f = find_item<C>(a, s, n, i0 - before, p.whole);
+        int64_t unit = before + f.first;
+        for (int h = f.h; h < a.pg.hkv && i0 < i1; ++h, f.rb = 0) {
+            RowBlocks<C> rb(a, s, f.rb);
+            for (uint32_t i = f.rb; i < n && i0 < i1; ++i) {
+                const int size = p.whole ? 1 : rb.blocks + kSetup;
+                const int from = static_cast<int>(i0 - unit), to = static_cast<int>(min(i1 - unit, static_cast<int64_t>(size)));
+                const int k = p.whole ? 0 : max(from - kSetup, 0), end = p.whole ? rb.blocks : to - kSetup;
+                if (end > k) {           // (else only items of the unit's start)
+                    const int r0 = static_cast<int>(i * C::ROWS);
+                    float* part = nullptr;
+                    if (k > 0 || end < rb.blocks) part = a.work + (2 * static_cast<int64_t>(blockIdx.x) + (k == 0 ? 1 : 0)) * SLOT;
+                    if (k == 0 && end < rb.blocks) cut = {s.start, s.n, h, r0, static_cast<int>(p.sh.holder(unit + size - 1))};
+                    segment<C, T>(a, s, b, h, r0, rb.first + k * C::KEYS, rb.first + end * C::KEYS, part, lds);
+                }
+                i0 = unit + to;
+                unit += size;
+                rb.next();
             }
-            const int64_t share = i1 - i0;
-            const int to = share < size - from ? from + static_cast<int>(share) : size;
-            i0 += to - from;
-            const int k = max(from - kSetup, 0), end = to - kSetup;
-            if (end <= k) continue;      // only items of the unit's start
-            const int h = unit / it.rbs, r0 = unit % it.rbs * C::ROWS;
-            float* part = nullptr;
-            if (k > 0 || end < it.blocks) part = a.work + (2 * static_cast<int64_t>(blockIdx.x) + (k == 0 ? 1 : 0)) * SLOT;
-            if (k == 0 && end < it.blocks)
-                cut = {s.start, s.n, h, r0,
-                       static_cast<int>(p.sh.holder(before + static_cast<int64_t>(unit + 1) * size - 1))};
-            segment<C, T>(a, s, b, h, r0, it.first + k * C::KEYS, it.first + end * C::KEYS, part, lds);
         }
-        before += it.total;
+        before += f.each * a.pg.hkv;
     }
     if (threadIdx.x == 0) cuts[blockIdx.x] = cut;
 }
@@ -1479,28 +1919,6 @@ __global__ void __launch_bounds__(256) cache_attn_join(const CacheAttnArgs a) {
     if (a.lse && lane == 0) a.lse[t * a.hq + head] = log_sum(m, l);
 }
 
-// Whole form: a workgroup for each unit.  Unit u of a head belongs to the last
-// sequence b with floor(cu(b) rep / ROWS) + b <= u; a sequence has at most
-// as many units as that bound leaves it.
-template <class C, class T>
-__global__ void __launch_bounds__(256, C::WAVES) cache_attn_whole(const CacheAttnArgs a) {
-    __shared__ float4v lds[lds_floats<C>() / 4 + 1];
-    const int u = blockIdx.x % a.units, h = blockIdx.x / a.units;
-    auto first = [&](int b) { return static_cast<int64_t>(cu_at<true>(a.sq, b)) * a.rep / C::ROWS + b; };
-    int b = 0, hi = a.sq.rows - 1;
-    while (b < hi) {
-        const int mid = (b + hi + 1) / 2;
-        if (first(mid) <= u) b = mid;
-        else hi = mid - 1;
-    }
-    const Seq s = seq_at<true>(a.sq, a.pg.logp, b);
-    const int64_t rbs = (static_cast<int64_t>(s.n) * a.rep + C::ROWS - 1) / C::ROWS;
-    // the last row blocks see the most keys: they go first
-    const int64_t rb = rbs - 1 - (u - first(b));
-    if (rb < 0 || rb >= rbs) return;
-    segment<C, T>(a, s, b, h, static_cast<int>(rb) * C::ROWS, 0, s.len, nullptr, reinterpret_cast<float*>(lds));
-}
-
 template <class C, class T>
 int split_workers(int* workers) {
     static std::atomic<int> slots[kMaxDevices];
@@ -1512,7 +1930,7 @@ int split_workers(int* workers) {
     if (n == 0) {
         int cus = 0, per = 0;
         if ((e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev)) != hipSuccess) return static_cast<int>(e);
-        if ((e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&per, cache_attn_split<C, T>, 256, 0)) != hipSuccess)
+        if ((e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&per, cache_attn_split<C, T>, C::THREADS, 0)) != hipSuccess)
             return static_cast<int>(e);
         n = cus * (per > 0 ? per : 1);
         slots[dev].store(n, std::memory_order_relaxed);
@@ -1524,35 +1942,31 @@ int split_workers(int* workers) {
 // One kernel family: launches it, or with workers set only asks how many
 // workgroups it keeps in flight.
 template <class C, class T>
-int family(const CacheAttnKey& k, const CacheAttnArgs* a, int* workers, void* stream) {
+int family(const CacheAttnArgs* a, int* workers, void* stream) {
     if (workers) return split_workers<C, T>(workers);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (k.split) {
-        hipLaunchKernelGGL((cache_attn_split<C, T>), dim3(a->workers), dim3(256), 0, s, *a);
-        hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return static_cast<int>(e);
-        hipLaunchKernelGGL((cache_attn_join<C, T>), dim3(a->workers, C::ROWS / 4), dim3(256), 0, s, *a);
-    } else if constexpr (C::WR == 4) {
-        hipLaunchKernelGGL((cache_attn_whole<C, T>), dim3(static_cast<uint32_t>(a->units) * a->pg.hkv), dim3(256), 0, s, *a);
-    } else {
-        return static_cast<int>(hipErrorInvalidValue);
-    }
+    CacheAttnArgs args = *a;
+    args.step = C::ROWS / a->rep;
+    args.over = C::ROWS % a->rep;
+    hipLaunchKernelGGL((cache_attn_split<C, T>), dim3(a->workers), dim3(C::THREADS), 0, s, args);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return static_cast<int>(e);
+    hipLaunchKernelGGL((cache_attn_join<C, T>), dim3(a->workers, C::ROWS / 4), dim3(256), 0, s, args);
     return static_cast<int>(hipGetLastError());
 }
 
 template <int D, int NG, bool SF32>
 int pick_shape(const CacheAttnKey& k, const CacheAttnArgs* a, int* workers, void* stream) {
     if (k.wide) {
-        if (k.wr == 1) return family<Cfg<D, NG, SF32, true, 1, 1>, float>(k, a, workers, stream);
-        return family<Cfg<D, NG, SF32, true, 1, 4>, float>(k, a, workers, stream);
+        if (k.wr == 1) return family<Cfg<D, NG, SF32, true, 1, 1>, float>(a, workers, stream);
+        return family<Cfg<D, NG, SF32, true, 1, 8>, float>(a, workers, stream);
     }
-    if (k.rt == 1 && k.wr == 1) return family<Cfg<D, NG, SF32, false, 1, 1>, uint16_t>(k, a, workers, stream);
-    if constexpr (D == 256) {
-        return family<Cfg<D, NG, SF32, false, 1, 4>, uint16_t>(k, a, workers, stream);
-    } else {
-        if (k.wr == 1) return family<Cfg<D, NG, SF32, false, 2, 1>, uint16_t>(k, a, workers, stream);
-        return family<Cfg<D, NG, SF32, false, 2, 4>, uint16_t>(k, a, workers, stream);
+    if (k.wr == 1) {
+        if constexpr (D <= 128 && NG == 1)
+            if (k.rt == 2) return family<Cfg<D, NG, SF32, false, 2, 1>, uint16_t>(a, workers, stream);
+        return family<Cfg<D, NG, SF32, false, 1, 1>, uint16_t>(a, workers, stream);
     }
+    return family<Cfg<D, NG, SF32, false, D == 256 ? 1 : 2, 8>, uint16_t>(a, workers, stream);
 }
 
 template <int D, int NG>

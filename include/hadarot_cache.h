@@ -117,7 +117,7 @@ int hr_cache_append(void* pool, int64_t n_pages, const hr_cache_spec* spec, cons
  *           only chooses the kernel: a larger row is still computed in full.
  *   work    device scratch of at least the bytes that
  *           hr_cache_attention_work gives for the same arguments, 16-byte
- *           aligned; may be NULL if that is 0.  Contents do not matter.
+ *           aligned.  Contents do not matter.
  * Products use float16 operands with float32 sums for HR_BF16 (the 4-bit
  * codes are exact, the queries and probabilities carry 11 bits) and pairs of
  * float16 (22 bits) for HR_F32.  The result does not depend on scheduling:
