@@ -136,6 +136,8 @@ __device__ __forceinline__ uint32_t to_bf16(float f) {
 // The phases of a step stay in order: left alone, the scheduler forms all
 // operands of a step at once, and spills.
 #define HR_PHASE() __builtin_amdgcn_sched_barrier(0)
+// A rare case stays a branch, instead of being computed always and selected.
+#define HR_BRANCH() asm volatile("")
 
 constexpr float kLow = -3.0e38f;      // running maximum of nothing
 constexpr float kLog2e = 1.4426950408889634f;
@@ -1264,6 +1266,34 @@ struct Fetch {
     }
 };
 
+// Moves the running maxima to what the scores (exponents, from kPExp - mc) of a
+// tile have, where that is more, and the sums and the scores with them.  Whether
+// some row has not seen a key yet.
+template <class C>
+__device__ __forceinline__ bool move_maximum(float4v (&x)[C::RT][2], Rows<C>& st) {
+    bool left = false;
+#pragma unroll
+    for (int rt = 0; rt < C::RT; ++rt) {
+        float w = -__builtin_inff();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w = fmaxf(w, x[rt][k / 4][k % 4]);
+        w = max_groups(w) - kPExp;                       // how far the running maximum moves
+        const bool fresh = st.mc[rt] == kLow;
+        const float d = w > 0.0f || (fresh && w > -__builtin_inff()) ? w : 0.0f;
+        if (fresh && !(w > -__builtin_inff())) left = true;
+        else st.mc[rt] = fresh ? d : st.mc[rt] + d;
+        const float f = fresh ? 1.0f : exp2f(-d);        // (nothing to scale before the first key)
+        st.start[rt] -= d;
+        st.from[rt] = float4v{st.start[rt], st.start[rt], st.start[rt], st.start[rt]};
+        st.lsum[rt] *= f;
+#pragma unroll
+        for (int j = 0; j < C::DT; ++j) st.o[rt][j] *= f;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) x[rt][s] -= d;
+    }
+    return __any(left);
+}
+
 // One step over a tile.  special: what the makers noted of it, odd: keys with
 // bad value scales; unset: some row has not seen a key yet.
 template <class C>
@@ -1271,17 +1301,17 @@ __device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint
                                           bool& unset) {
     constexpr int RT = C::RT, GROUP = Fetch<C>::GROUP;
     const int lane = threadIdx.x & 63, g = lane >> 4;
-    float x[RT][8];
-    // scores as exponents: the products start from kPExp - mc.  (float32
-    // activations: added at the end, it would cost the sums bits; extreme
-    // scales: their unit is not 1)
+    // scores as exponents: the products start from kPExp - mc.  (Not so for float32
+    // activations, where it would cost the sums bits, and extreme scales, whose
+    // unit is not 1: it is added at the end.)
     const int shift = special >> 2;
     const bool late = C::WIDE || shift != 0;
     if (late) {
+        HR_BRANCH();
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) st.from[rt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    float4v acc[2][RT];
+    float4v acc[RT][2];
     Fetch<C> now, next;
     now.keys(tile, 0);
 #pragma unroll
@@ -1294,25 +1324,22 @@ __device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint
             const int s = i / C::KS, k = i % C::KS;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                acc[s][rt] = mfma(now.f[0][i - first], st.q[rt][0][k], k == 0 ? st.from[rt] : acc[s][rt]);
+                acc[rt][s] = mfma(now.f[0][i - first], st.q[rt][0][k], k == 0 ? st.from[rt] : acc[rt][s]);
                 if constexpr (C::WIDE) {
-                    acc[s][rt] = mfma(now.f[0][i - first], st.q[rt][1][k], acc[s][rt]);
-                    acc[s][rt] = mfma(now.f[1][i - first], st.q[rt][0][k], acc[s][rt]);
+                    acc[rt][s] = mfma(now.f[0][i - first], st.q[rt][1][k], acc[rt][s]);
+                    acc[rt][s] = mfma(now.f[1][i - first], st.q[rt][0][k], acc[rt][s]);
                 }
             }
         }
         now = next;
     }
     HR_PHASE();
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[rt][k] = acc[k / 4][rt][k % 4];
     if (late) {
+        HR_BRANCH();
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[rt][k] = (C::WIDE && shift == 0 ? x[rt][k] : ldexpf(x[rt][k], shift)) + st.start[rt];
+            for (int k = 0; k < 8; ++k) acc[rt][k / 4][k % 4] = (C::WIDE && shift == 0 ? acc[rt][k / 4][k % 4] : ldexpf(acc[rt][k / 4][k % 4], shift)) + st.start[rt];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) st.from[rt] = float4v{st.start[rt], st.start[rt], st.start[rt], st.start[rt]};
     }
@@ -1324,8 +1351,8 @@ __device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 const bool seen = !(special >> (k / 4) & 1) && key < st.lim[rt] && key >= st.lo[rt];
-                if (odd >> at & 1) x[rt][k] = __builtin_nanf("");
-                if (!seen) x[rt][k] = -__builtin_inff();
+                if (odd >> at & 1) acc[rt][k / 4][k % 4] = __builtin_nanf("");
+                if (!seen) acc[rt][k / 4][k % 4] = -__builtin_inff();
             }
         }
     }
@@ -1334,31 +1361,15 @@ __device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            p[rt][k] = __builtin_amdgcn_exp2f(x[rt][k]);
+            p[rt][k] = __builtin_amdgcn_exp2f(acc[rt][k / 4][k % 4]);
             top = fmaxf(top, p[rt][k]);
         }
     if (unset || __any(top > static_cast<float>(1 << (kPExp + kSlack)))) {
-        bool left = false;
+        unset = move_maximum<C>(acc, st);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            float w = -__builtin_inff();
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w = fmaxf(w, x[rt][k]);
-            w = max_groups(w) - kPExp;                       // how far the running maximum moves
-            const bool fresh = st.mc[rt] == kLow;
-            const float d = w > 0.0f || (fresh && w > -__builtin_inff()) ? w : 0.0f;
-            if (fresh && !(w > -__builtin_inff())) left = true;
-            else st.mc[rt] = fresh ? d : st.mc[rt] + d;
-            const float f = fresh ? 1.0f : exp2f(-d);        // (nothing to scale before the first key)
-            st.start[rt] -= d;
-            st.from[rt] = float4v{st.start[rt], st.start[rt], st.start[rt], st.start[rt]};
-            st.lsum[rt] *= f;
-#pragma unroll
-            for (int j = 0; j < C::DT; ++j) st.o[rt][j] *= f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) p[rt][k] = __builtin_amdgcn_exp2f(x[rt][k] - d);
-        }
-        unset = __any(left);
+            for (int k = 0; k < 8; ++k) p[rt][k] = __builtin_amdgcn_exp2f(acc[rt][k / 4][k % 4]);
     }
     uint4v ph[RT], pl[RT];
 #pragma unroll
@@ -1391,6 +1402,101 @@ __device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint
             }
         now = next;
     }
+    HR_PHASE();
+}
+
+// The same for two row tiles, one half a step behind the other, so that the
+// exponentials of one are formed while the matrix unit works for the other.
+// Everything else (keys that some rows do not see, extreme scales, a maximum
+// that moves) is in one branch between the scores and the values.
+#define HR_GROUP(what, n) __builtin_amdgcn_sched_group_barrier(what, n, 0)
+enum { kMatrix = 0x8, kLdsRead = 0x100, kTranscendental = 0x400 };
+__device__ __forceinline__ uint4v exponentials(const float4v (&acc)[2]) {
+    uint4v ph;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        ph[k] = pack_f16(__builtin_amdgcn_exp2f(acc[k / 2][2 * k % 4]), __builtin_amdgcn_exp2f(acc[k / 2][2 * k % 4 + 1]));
+    return ph;
+}
+template <class C>
+__device__ __forceinline__ void pair_step(const Tile<C>& tile, int special, uint32_t odd, int t0, const Span& sp, Rows<C>& st,
+                                          bool& unset) {
+    constexpr int N = C::DT;   // operands of keys, and of values
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    const uint4v ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+    uint4v k[N], v[N];
+    float4v acc[2][2];
+    HR_PHASE();
+#pragma unroll
+    for (int i = 0; i < N; ++i) k[i] = tile.k[0][i][lane];
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+        for (int i = 0; i < C::KS; ++i)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                acc[rt][s] = mfma(k[s * C::KS + i], st.q[rt][0][i], i == 0 ? st.from[rt] : acc[rt][s]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = tile.v[0][i][lane];
+    uint4v p0 = exponentials(acc[0]);
+    asm volatile("" : "+v"(p0));   // (here, and not after the branch)
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, acc[i / 8][i / 4 % 2][i % 4]);
+    HR_GROUP(kLdsRead, N);
+    HR_GROUP(kMatrix, N + 2);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        HR_GROUP(kTranscendental, 8 / N);
+        HR_GROUP(kMatrix, 1);
+        HR_GROUP(kLdsRead, 1);
+    }
+    const bool all = t0 >= sp.flo && t0 + 32 <= sp.fhi && (special | odd) == 0;
+    if (!all || unset || __any(top > static_cast<float>(kPExp + kSlack))) {
+        HR_BRANCH();
+        const int shift = special >> 2;
+        if (shift != 0) {
+            // extreme scales: the scores' unit is not 1, and they start from 0
+            HR_BRANCH();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float4v& x = acc[i / 2][i % 2];
+                x = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < C::KS; ++j) x = mfma(tile.k[0][i % 2 * C::KS + j][lane], st.q[i / 2][0][j], x);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[r] = ldexpf(x[r], shift) + st.start[i / 2];
+            }
+        }
+        if (!all) {
+            // unseen scores become -inf, whatever they are
+            HR_BRANCH();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int at = 16 * (i / 4) + 4 * g + i % 4, key = t0 + at;
+#pragma unroll
+                for (int rt = 0; rt < 2; ++rt) {
+                    float& x = reinterpret_cast<float*>(&acc[rt][i / 4])[i % 4];
+                    if (odd >> at & 1) x = __builtin_nanf("");
+                    if ((special >> (i / 4) & 1) || key >= st.lim[rt] || key < st.lo[rt]) x = -__builtin_inff();
+                }
+            }
+        }
+        unset = move_maximum<C>(acc, st);
+        p0 = exponentials(acc[0]);
+    }
+    st.lsum[0] = mfma(ones, p0, st.lsum[0]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) st.o[0][i] = mfma(v[i], p0, st.o[0][i]);
+    const uint4v p1 = exponentials(acc[1]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        HR_GROUP(kMatrix, 1);
+        HR_GROUP(kTranscendental, 8 / N);
+    }
+    st.lsum[1] = mfma(ones, p1, st.lsum[1]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) st.o[1][i] = mfma(v[i], p1, st.o[1][i]);
     HR_PHASE();
 }
 
@@ -1452,9 +1558,12 @@ __device__ __forceinline__ void passes(const CacheAttnArgs& a, const int32_t* ta
         // (tiles that no row of the wave sees are left out)
         const int first = max(sp.lo - t, 0) >> 5, stop = (min(min(end, sp.hi) - t, S) + 31) >> 5;
 #pragma unroll 1
-        for (int i = first; i < stop; ++i)
-            tile_step<C>(ps.tile[buf][i], __builtin_amdgcn_readfirstlane(ps.keys[buf][i]), __builtin_amdgcn_readfirstlane(ps.odd[buf][i]),
-                         t + 32 * i, sp, st, unset);
+        for (int i = first; i < stop; ++i) {
+            const int special = __builtin_amdgcn_readfirstlane(ps.keys[buf][i]), t0 = t + 32 * i;
+            const uint32_t odd = __builtin_amdgcn_readfirstlane(ps.odd[buf][i]);
+            if constexpr (C::RT == 2) pair_step<C>(ps.tile[buf][i], special, odd, t0, sp, st, unset);
+            else tile_step<C>(ps.tile[buf][i], special, odd, t0, sp, st, unset);
+        }
         if constexpr (ROLE == kMakeKeys) {
             make(t + S, buf ^ 1);
             load(t + 2 * S);
