@@ -21,19 +21,26 @@ typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
 // elements each: four bits of the Hadamard transform are inside the lane, the
 // other two to four are lane bits, and a group of 32 to 256 elements is 2 to
 // 16 consecutive lanes.  The stages go in the order of the index bits.
+//
+// Every element is read once and every code written once, so the floor is the
+// copy of those bytes; what comes next is the instruction stream, 690 vector
+// instructions for a lane's 32 elements.  32768 tokens x 32 heads of 128 (683 MB):
+// 154 us, 4.4 TB/s where a large copy has 4.95; with selections in the lane
+// stages and codes packed one by one (820 instructions) it was 175.  One token of
+// each of 64 sequences: 6 us, the launch and the chain of loads to the page.
 
-template <int CTRL, int BANKS = 0xF>
-__device__ __forceinline__ float dpp(float old, float v) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, 0xF, BANKS, false));
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
 }
 
 // the value of lane ^ X (X = 1, 2, 4, 8, inside 16 lanes)
 template <int X>
 __device__ __forceinline__ float lane_xor(float v) {
-    if constexpr (X == 1) return dpp<0xB1>(v, v);         // quad_perm [1,0,3,2]
-    if constexpr (X == 2) return dpp<0x4E>(v, v);         // quad_perm [2,3,0,1]
-    if constexpr (X == 4) return dpp<0x114, 0xA>(dpp<0x104, 0x5>(v, v), v);  // banks of four: shl 4 into even, shr 4 into odd
-    return dpp<0x128>(v, v);                               // row_ror 8
+    if constexpr (X == 1) return dpp<0xB1>(v);         // quad_perm [1,0,3,2]
+    if constexpr (X == 2) return dpp<0x4E>(v);         // quad_perm [2,3,0,1]
+    if constexpr (X == 4) return dpp<0x141>(dpp<0x1B>(v));  // quad_perm [3,2,1,0], then the row's half mirrored: ^ 3 ^ 7
+    return dpp<0x128>(v);                               // row_ror 8
 }
 
 template <int LANES, class F>
@@ -45,13 +52,14 @@ __device__ __forceinline__ float over_lanes(float v, F f) {
     return v;
 }
 
+// (a product with 1 or -1 is exact, and costs less than a selection; the move
+// between lanes is part of the addition)
 template <int X>
 __device__ __forceinline__ void lane_stage(float (&v)[16], int lane) {
+#pragma clang fp contract(off)
+    const float sign = (lane & X) ? -1.0f : 1.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float y = lane_xor<X>(v[i]);
-        v[i] = (lane & X) ? y - v[i] : v[i] + y;
-    }
+    for (int i = 0; i < 16; ++i) v[i] = lane_xor<X>(v[i]) + v[i] * sign;
 }
 
 template <int D>
@@ -101,7 +109,8 @@ __device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
 // t = y r the remainder fma(-t, s, y) is exact, so fma(remainder, r, t) rounds
 // to y / s (P. Markstein, IBM J. Res. Dev. 34, 1990).  That keeps every code
 // equal to the definition's, ties included, at two more instructions than a
-// product with the reciprocal.
+// product with the reciprocal.  Codes are packed as float32, four of them to an
+// integer below 2^16; symmetric ones with 8 added, which an XOR takes back.
 template <int LANES, bool SYM>
 __device__ __forceinline__ uint2v quantize(const float (&v)[16], bool sf32, uint32_t* scale, uint32_t* zero) {
 #pragma clang fp contract(off)
@@ -132,20 +141,29 @@ __device__ __forceinline__ uint2v quantize(const float (&v)[16], bool sf32, uint
         s = bf2f(*scale);
     }
     const float r = 1.0f / s;
-    float least = -8.0f, most = 7.0f;
-    if constexpr (!SYM) {
+    if constexpr (SYM) {
+        z = 8.0f;
+    } else {
         z = fminf(fmaxf(rintf(-z / s), 0.0f), 15.0f);
         *zero = static_cast<uint32_t>(static_cast<int>(z));
-        least = 0.0f;
-        most = 15.0f;
     }
-    uint2v w = {0u, 0u};
+    uint2v w;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float t = v[i] * r;
-        const float q = rintf(__builtin_fmaf(__builtin_fmaf(-t, s, v[i]), r, t));
-        const int c = static_cast<int>(fminf(fmaxf(q + z, least), most));
-        w[i / 8] |= (static_cast<uint32_t>(c) & 15u) << (4 * (i & 7));
+    for (int i = 0; i < 16; i += 8) {
+        uint32_t half[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int k = 3; k >= 0; --k) {
+                const float y = v[i + 4 * j + k], t = y * r;
+                const float q = rintf(__builtin_fmaf(__builtin_fmaf(-t, s, y), r, t));
+                const float c = __builtin_amdgcn_fmed3f(q + z, 0.0f, 15.0f);   // (NaN: 0)
+                sum = k == 3 ? c : __builtin_fmaf(sum, 16.0f, c);
+            }
+            half[j] = static_cast<uint32_t>(sum);
+        }
+        w[i / 8] = (half[1] << 16 | half[0]) ^ (SYM ? 0x88888888u : 0u);
     }
     return w;
 }
@@ -252,7 +270,8 @@ int append_dim(const CacheAppendArgs& a, hipStream_t s) {
 // second launch writes the new table and copies the pages.  The plan is a few
 // dependent passes over some ten thousand integers: in LDS it takes 5 to 9 us,
 // where counting by one launch and scanning by another took 20 to 25 with the
-// gaps between them.
+// gaps between them (14 us with 256 rows of 128 pages over 12000).  The copies are
+// bound by memory: 100 MB in 19 us, 400 MB in 70 to 77, 5.3 to 5.7 TB/s.
 
 constexpr int kScan = 1024;        // threads of the planning workgroup
 constexpr int kPlanPages = 12288;  // pages whose three counters fit LDS
