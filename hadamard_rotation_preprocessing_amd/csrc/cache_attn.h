@@ -1826,7 +1826,7 @@ __device__ __forceinline__ Place place(const CacheAttnArgs& a, int64_t* lds) {
     const int tid = threadIdx.x;
     // few sequences: 2^per threads for each, with a part of its row blocks
     int per = 0;
-    while (per < 6 && (2 << per) * a.sq.rows <= C::THREADS) ++per;
+    while (per < 6 && a.sq.rows <= C::THREADS >> (per + 1)) ++per;
     const int nth = tid >> per, part = tid & ((1 << per) - 1), step = C::THREADS >> per;
     Place p;
     Seq s = {0, 0, 0};
