@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "cache.h"
+#include "cache_index.h"
 #include "codes.h"
 
 namespace hr {
@@ -177,27 +178,14 @@ __global__ void __launch_bounds__(256) cache_append(const CacheAppendArgs a) {
     const int h = static_cast<int>(blockIdx.x % groups) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int u = blockIdx.x / groups;
     if (h >= a.pg.hkv) return;
-    // the block's sequence: the last b with floor(cu(b) / POS) + 2 b <= u, a
-    // bound that leaves every sequence at least the blocks it touches
-    auto cu = [&](int b) { return min(max(a.sq.cu ? a.sq.cu[b] : b * a.sq.per, 0), a.sq.tokens); };
-    int b = 0, hi = a.sq.rows - 1;
-    while (b < hi) {
-        const int mid = (b + hi + 1) / 2;
-        if (cu(mid) / POS + 2 * mid <= u) b = mid;
-        else hi = mid - 1;
-    }
-    const int start = cu(b), n = max(cu(b + 1) - start, 0);
-    const int len = min(max(a.sq.lens[b], 0), a.sq.max_pages << a.pg.logp);
-    const int first = len - n;  // position of the first new token; may lie before 0
-    const int nth = u - (start / POS + 2 * b);
-    const int p0 = (max(first, 0) / POS + nth) * POS;
-    if (nth < 0 || p0 >= len) return;
-    const int page = a.sq.table[static_cast<int64_t>(b) * a.sq.max_pages + (p0 >> a.pg.logp)];
+    const AppendBlock blk = append_block<POS>(a.sq, a.pg.logp, u);
+    if (!blk.any) return;
+    const int page = a.sq.table[static_cast<int64_t>(blk.b) * a.sq.max_pages + (blk.p0 >> a.pg.logp)];
     if (static_cast<uint32_t>(page) >= static_cast<uint64_t>(a.sq.n_pages)) return;
     uint8_t* base = a.pool + page * a.pg.page_bytes + h * a.pg.head_bytes;
-    const int pos = p0 + lane / LPV, off = pos & (a.pg.page - 1), e = lane % LPV;
-    const bool mine = pos >= max(first, 0) && pos < len;
-    const int64_t tok = start + min(max(pos - first, 0), n - 1);
+    const int pos = blk.p0 + lane / LPV, off = pos & (a.pg.page - 1), e = lane % LPV;
+    const bool mine = blk.holds(pos);
+    const int64_t tok = blk.token(pos);
     float k[16], v[16];
     load16(static_cast<const T*>(a.k) + tok * a.k_st + h * a.k_sh + 16 * e, k);
     load16(static_cast<const T*>(a.v) + tok * a.v_st + h * a.v_sh + 16 * e, v);
