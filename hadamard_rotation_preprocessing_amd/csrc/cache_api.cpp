@@ -125,6 +125,14 @@ int check_table(int64_t rows, int64_t max_pages, int page, const char* name) {
     return HR_OK;
 }
 
+// A table whose entries are counted (holders of a page, pages handed out): the
+// kernels do that in 31 bits.
+int check_counted(int64_t rows, int64_t max_pages, const char* name) {
+    if (rows * max_pages >= (int64_t{1} << 31))
+        return fail(HR_EUNSUPPORTED, "%s x max_pages = %lld x %lld must be below 2^31", name, (long long)rows, (long long)max_pages);
+    return HR_OK;
+}
+
 int check_seqs(const hr_cache_seqs* s, const hr::CachePage& pg, int64_t n_pages, int64_t tokens, hr::CacheSeqs* o) {
     if (!s) return fail(HR_EINVAL, "seqs is NULL");
     int st;
@@ -395,7 +403,8 @@ int hr_cache_update(void* pool, int64_t layers, int64_t n_pages, const hr_cache_
     int st = check_spec(spec, &pg);
     if (st) return st;
     if ((st = check_pages(n_pages, layers)) || (st = check_table(rows, max_pages, pg.page, "rows")) ||
-        (st = check_table(new_rows, max_pages, pg.page, "new_rows")))
+        (st = check_table(new_rows, max_pages, pg.page, "new_rows")) || (st = check_counted(rows, max_pages, "rows")) ||
+        (st = check_counted(new_rows, max_pages, "new_rows")))
         return st;
     if ((st = check_ptr(pool, "pool", 16)) || (st = check_ptr(refs, "refs", 4)) || (st = check_ptr(status, "status", 4)))
         return st;
@@ -452,7 +461,9 @@ int hr_cache_compact(void* pool, int64_t layers, int64_t n_pages, const hr_cache
     hr::CachePage pg;
     int st = check_spec(spec, &pg);
     if (st) return st;
-    if ((st = check_pages(n_pages, layers)) || (st = check_table(rows, max_pages, pg.page, "rows"))) return st;
+    if ((st = check_pages(n_pages, layers)) || (st = check_table(rows, max_pages, pg.page, "rows")) ||
+        (st = check_counted(rows, max_pages, "rows")))
+        return st;
     if (into && (into_pages <= 0 || into_pages > kMaxCount))
         return fail(HR_EINVAL, "into_pages = %lld must be in 1..2^30", (long long)into_pages);
     if ((st = check_ptr(pool, "pool", 16)) || (into && (st = check_ptr(into, "into", 16))) ||

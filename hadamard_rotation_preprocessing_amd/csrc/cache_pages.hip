@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kScan) update_plan(const CacheUpdateArgs a, in
         a.status[0] = used;
         a.status[1] = need - given;
         a.status[2] = done;
-        moves[2 * a.new_rows] = done;
+        moves[2 * int64_t{a.new_rows}] = done;
         a.status[3] = n - used;
         base[a.new_rows] = found;
     }
@@ -450,7 +450,7 @@ constexpr int kCopyGrid = 1024;  // workgroups that copy: 16 waves with eight lo
 __global__ void __launch_bounds__(256) update_write(const CacheUpdateArgs a, const int32_t* base, const int32_t* copies,
                                                     const int32_t* free_list, const int32_t* moves, int rows) {
     if (static_cast<int>(blockIdx.x) >= rows) {
-        copy_pages(a.pool, a.n_pages, a.pool, a.n_pages, a.page_bytes, a.layers, moves, moves[2 * a.new_rows], blockIdx.x - rows,
+        copy_pages(a.pool, a.n_pages, a.pool, a.n_pages, a.page_bytes, a.layers, moves, moves[2 * int64_t{a.new_rows}], blockIdx.x - rows,
                    gridDim.x - rows);
         return;
     }
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kScan) compact_plan(const CacheCompactArgs a, 
         a.status[1] = live - placed;
         a.status[2] = moved;
         a.status[3] = places - placed;
-        moves[2 * n] = moved;
+        moves[2 * int64_t{n}] = moved;
     }
 }
 
@@ -606,7 +606,7 @@ int launch_cache_update(const CacheUpdateArgs& a, void* stream) {
     int32_t* base = a.work;                       // new_rows + 1
     int32_t* copies = base + a.new_rows + 1;      // new_rows
     int32_t* moves = copies + a.new_rows;         // 2 new_rows + 1
-    int32_t* free_list = moves + 2 * a.new_rows + 1;
+    int32_t* free_list = moves + 2 * int64_t{a.new_rows} + 1;
     const int e = plan(update_plan<true>, update_plan<false>, 3, a, s, base, copies, free_list, moves, free_list + a.n_pages);
     if (e || a.new_rows == 0) return e;
     const int rows = a.new_rows < 4096 ? a.new_rows : 4096;

@@ -156,7 +156,8 @@ int hr_cache_attention_work(int dtype, int64_t tokens, int32_t q_heads, const hr
  *   status     device, int32 [4]: pages in use, pages that were lacking,
  *              pages copied, pages left free.
  *   work       device scratch of hr_cache_update_work bytes, 16-byte aligned.
- * The old table and lens are only read and may not overlap the new ones.
+ * The old table and lens are only read and may not overlap the new ones; each
+ * has fewer than 2^31 entries.
  */
 int hr_cache_update(void* pool, int64_t layers, int64_t n_pages, const hr_cache_spec* spec,
                     const int32_t* table, const int32_t* lens, int64_t rows, int64_t max_pages,
@@ -180,7 +181,7 @@ int hr_cache_update_work(int64_t n_pages, int64_t new_rows, int64_t* bytes);
  *              pages moved, places left free.
  *   work       device scratch of hr_cache_compact_work bytes, 16-byte aligned.
  * Lengths do not change.  The old table is only read and may not overlap the
- * new one; `into` may not overlap the pool.
+ * new one; each has fewer than 2^31 entries; `into` may not overlap the pool.
  */
 int hr_cache_compact(void* pool, int64_t layers, int64_t n_pages, const hr_cache_spec* spec,
                      const int32_t* table, const int32_t* lens, int64_t rows, int64_t max_pages,
