@@ -35,13 +35,24 @@ int launched(int e) {
 bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
-// No count of rows, pages, tokens or heads above these; every product that the
-// calls form of them then stays within 63 bits, every index within 31.
+// No count of rows, pages, tokens or heads above these; every index then stays
+// within 31 bits.  Products with strides and page sizes need not stay within 63:
+// size_of and sum_of hold them at the largest.
 constexpr int64_t kMaxCount = int64_t{1} << 30;
 constexpr int64_t kMaxHeads = 1 << 16;
 // workgroups of 256 threads of a launch (a grid holds fewer than 2^32 threads)
 constexpr int64_t kMaxGrid = 1 << 24;
 constexpr int64_t kMaxKeys = int64_t{1} << 31;
+
+int64_t size_of(int64_t a, int64_t b, int64_t c = 1) {   // a b c, none negative
+    int64_t r;
+    if (__builtin_mul_overflow(a, b, &r) || __builtin_mul_overflow(r, c, &r)) return INT64_MAX;
+    return r;
+}
+int64_t sum_of(int64_t a, int64_t b) {
+    int64_t r;
+    return __builtin_add_overflow(a, b, &r) ? INT64_MAX : r;
+}
 
 int check_ptr(const void* p, const char* name, size_t align) {
     if (!p) return fail(HR_EINVAL, "%s is NULL", name);
@@ -62,7 +73,8 @@ int check_overlap(const Range* r, int n) {
         for (int j = i + 1; j < n; ++j) {
             if (!r[i].p || !r[j].p || !(r[i].written || r[j].written) || r[i].bytes <= 0 || r[j].bytes <= 0) continue;
             const uintptr_t a = reinterpret_cast<uintptr_t>(r[i].p), b = reinterpret_cast<uintptr_t>(r[j].p);
-            if (a < b + static_cast<uintptr_t>(r[j].bytes) && b < a + static_cast<uintptr_t>(r[i].bytes))
+            // (by distance: an end may lie past the last address)
+            if (a < b ? b - a < static_cast<uintptr_t>(r[i].bytes) : a - b < static_cast<uintptr_t>(r[j].bytes))
                 return fail(HR_EINVAL, "%s overlaps %s", r[i].name, r[j].name);
         }
     return HR_OK;
@@ -175,7 +187,7 @@ int check_rows(const void* p, const char* name, int64_t st, int64_t sh, int64_t 
         return fail(HR_EINVAL, "%s rows are not 16-byte aligned (strides %lld, %lld)", name, (long long)st, (long long)sh);
     if ((heads > 1 && sh < d) || (tokens > 1 && st < d))
         return fail(HR_EINVAL, "%s strides %lld, %lld are smaller than a row of %d", name, (long long)st, (long long)sh, d);
-    *bytes = ((tokens - 1) * st + (heads - 1) * sh + d) * es;
+    *bytes = size_of(sum_of(size_of(tokens - 1, st), (heads - 1) * sh + d), es);
     return HR_OK;
 }
 
@@ -183,7 +195,7 @@ int check_rows(const void* p, const char* name, int64_t st, int64_t sh, int64_t 
 // of the two strides has to span the whole of the other dimension.
 int check_distinct(const char* name, int64_t st, int64_t sh, int64_t tokens, int64_t heads, int d) {
     if (tokens <= 1 || heads <= 1) return HR_OK;
-    if (st >= (heads - 1) * sh + d || sh >= (tokens - 1) * st + d) return HR_OK;
+    if (st >= (heads - 1) * sh + d || sh >= sum_of(size_of(tokens - 1, st), d)) return HR_OK;
     return fail(HR_EINVAL, "%s strides %lld, %lld make rows overlap", name, (long long)st, (long long)sh);
 }
 
@@ -272,7 +284,7 @@ int hr_cache_append(void* pool, int64_t n_pages, const hr_cache_spec* spec, cons
         (st = check_rows(k, "k", k_stride_token, k_stride_head, tokens, a.pg.hkv, a.pg.d, dtype, &kb)) ||
         (st = check_rows(v, "v", v_stride_token, v_stride_head, tokens, a.pg.hkv, a.pg.d, dtype, &vb)))
         return st;
-    const Range r[] = {{"pool", pool, n_pages * a.pg.page_bytes, true},
+    const Range r[] = {{"pool", pool, size_of(n_pages, a.pg.page_bytes), true},
                        {"k", k, kb, false},
                        {"v", v, vb, false},
                        {"table", seqs->table, seqs->rows * seqs->max_pages * 4, false},
@@ -346,7 +358,7 @@ int hr_cache_attention(const void* q, int64_t q_stride_token, int64_t q_stride_h
     Range r[] = {{"out", out, ob, true},
                  {"lse", lse, lse ? tokens * q_heads * 4 : 0, true},
                  {"q", in_place ? nullptr : q, qb, false},
-                 {"pool", pool, n_pages * a.pg.page_bytes, false},
+                 {"pool", pool, size_of(n_pages, a.pg.page_bytes), false},
                  {"table", seqs->table, seqs->rows * seqs->max_pages * 4, false},
                  {"lens", seqs->lens, seqs->rows * 4, false},
                  {"cu_q", seqs->cu_q, (seqs->rows + 1) * 4, false},
@@ -415,7 +427,7 @@ int hr_cache_update(void* pool, int64_t layers, int64_t n_pages, const hr_cache_
     const int64_t need = hr::cache_update_words(n_pages, new_rows) * 4;
     if ((st = check_ptr(work, "work", 16))) return st;
     if (work_bytes < need) return fail(HR_EINVAL, "work_bytes = %lld: %lld are needed", (long long)work_bytes, (long long)need);
-    const Range r[] = {{"pool", pool, layers * n_pages * pg.page_bytes, true},
+    const Range r[] = {{"pool", pool, size_of(layers, n_pages, pg.page_bytes), true},
                        {"new_table", new_table, new_rows * max_pages * 4, true},
                        {"new_lens", new_lens, new_rows * 4, true},
                        {"refs", refs, n_pages * 4, true},
@@ -475,8 +487,8 @@ int hr_cache_compact(void* pool, int64_t layers, int64_t n_pages, const hr_cache
     const int64_t need = hr::cache_compact_words(n_pages) * 4;
     if ((st = check_ptr(work, "work", 16))) return st;
     if (work_bytes < need) return fail(HR_EINVAL, "work_bytes = %lld: %lld are needed", (long long)work_bytes, (long long)need);
-    const Range r[] = {{"pool", pool, layers * n_pages * pg.page_bytes, true},
-                       {"into", into, into ? layers * into_pages * pg.page_bytes : 0, true},
+    const Range r[] = {{"pool", pool, size_of(layers, n_pages, pg.page_bytes), true},
+                       {"into", into, into ? size_of(layers, into_pages, pg.page_bytes) : 0, true},
                        {"new_table", new_table, rows * max_pages * 4, true},
                        {"refs", refs, (into ? into_pages : n_pages) * 4, true},
                        {"status", status, 16, true},
