@@ -195,7 +195,7 @@ def _vectors(x: torch.Tensor, name: str, tokens, heads, d: int, device):
     if x.device != device:
         raise ValueError("%s must be on %s" % (name, device))
     st, sh, se = x.stride()
-    if se != 1:
+    if se != 1 and x.numel():
         raise ValueError("%s: the last dimension must be contiguous" % name)
     return st, sh
 
@@ -240,17 +240,17 @@ def cache_attention(q: torch.Tensor, pool: torch.Tensor, spec: CacheSpec, table:
     elif out.dtype != q.dtype:
         raise ValueError("out must have q's dtype")
     ot, oh = _vectors(out, "out", tokens, heads, spec.head_dim, dev)
-    lp = None
+    lp, with_lse = None, lse is not None and lse is not False
     if lse is True:
         lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
-    if lse is not None and lse is not False:
+    if with_lse:
         if lse.dtype is not torch.float32 or lse.shape != (tokens, heads) or not lse.is_contiguous() or lse.device != dev:
             raise ValueError("lse must be a contiguous float32 tensor [tokens, q_heads]")
         lp = lse.data_ptr()
     if torch.cuda.current_device() != dev.index:   # (kernels and scratch are chosen for the current device)
         with torch.cuda.device(dev):
             return cache_attention(q, pool, spec, table, lens, cu_q, max_q, scale, causal, window, rotate, out,
-                                   lse if lp else None, work)
+                                   lse if with_lse else None, work)
     if work is None:
         key = (dt, tokens, heads, seqs.rows, max_q, dev.index)
         need = r.work.get(key)
@@ -267,7 +267,7 @@ def cache_attention(q: torch.Tensor, pool: torch.Tensor, spec: CacheSpec, table:
                               _stream(dev))
     if st:
         check(st)
-    return (out, lse) if lp else out
+    return (out, lse) if with_lse else out
 
 
 def cache_attention_work(dtype: torch.dtype, tokens: int, q_heads: int, spec: CacheSpec, rows: int, max_q: int = 0) -> int:

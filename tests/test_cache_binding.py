@@ -1,0 +1,70 @@
+"""CPU tests of the paged cache's binding (cache.py): what it hands to the C
+calls and returns, with the library's entry points replaced by recorders."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+import hadamard_rotation_preprocessing_amd as hr
+from hadamard_rotation_preprocessing_amd import cache as K
+
+SPEC = hr.CacheSpec(2, 64, 16, hr.QSpec("int", 4, 64, False, "bf16"))
+
+
+class Calls:
+    """Stand-in for the library: notes every call and the device it ran on."""
+
+    def __init__(self):
+        self.seen, self.device = [], "current"
+        self.real = K._cache_lib()
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.seen.append((name, self.device, args))
+            if name.endswith("_work"):
+                args[-1]._obj.value = 64
+            return 0
+        return call
+
+    @contextlib.contextmanager
+    def on(self, device):
+        self.device, before = device, self.device
+        yield
+        self.device = before
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    SPEC.layout()   # (by the real library)
+    c = Calls()
+    K._resolved(SPEC).work.clear()
+    monkeypatch.setattr(K, "_cache_lib", lambda: c)
+    monkeypatch.setattr(K, "_stream", lambda device: 0)
+    monkeypatch.setattr(torch.cuda, "device", c.on)
+    # the tensors here are on the CPU, whose device has no index: None is "theirs"
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    yield c
+    K._resolved(SPEC).work.clear()
+
+
+def state(tokens=2, rows=1):
+    i32 = dict(dtype=torch.int32)
+    return types.SimpleNamespace(pool=hr.cache_pool(SPEC, 4, device="cpu"), table=torch.zeros((rows, 3), **i32),
+                                 lens=torch.zeros(rows, **i32), q=torch.zeros((tokens, 4, 64)), k=torch.zeros((tokens, 2, 64)),
+                                 cu=torch.zeros(rows + 1, **i32), parents=torch.zeros(rows, **i32))
+
+
+def test_no_tokens(calls):
+    """An empty call returns what a call returns: out, and lse where asked for."""
+    s = state(tokens=0)
+    out, lse = hr.cache_attention(s.q, s.pool, SPEC, s.table, s.lens, cu_q=s.cu, lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    given = torch.empty((0, 4))
+    out, lse = hr.cache_attention(s.q, s.pool, SPEC, s.table, s.lens, cu_q=s.cu, lse=given)
+    assert lse is given
+    assert isinstance(hr.cache_attention(s.q, s.pool, SPEC, s.table, s.lens, cu_q=s.cu, lse=False), torch.Tensor)
+    # (a tensor without elements may have any strides)
+    e = torch.zeros((64, 2, 0)).permute(2, 1, 0)
+    hr.cache_append(s.pool, SPEC, e, e, s.table, s.lens, cu_q=s.cu)
+    hr.cache_attention(e, s.pool, SPEC, s.table, s.lens, cu_q=s.cu)
