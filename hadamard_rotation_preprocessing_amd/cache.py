@@ -162,6 +162,14 @@ def _ints(t: torch.Tensor, name: str, shape: tuple, device) -> int:
     return t.data_ptr()
 
 
+def _bytes(work: torch.Tensor, device):
+    """(address, bytes) of a caller's scratch."""
+    if work.device != device or not work.is_contiguous():
+        raise ValueError("work must be a contiguous tensor on %s, got one on %s%s"
+                         % (device, work.device, "" if work.is_contiguous() else " with strides %s" % list(work.stride())))
+    return work.data_ptr(), work.numel() * work.element_size()
+
+
 def _table(t: torch.Tensor, device):
     """(address, rows, max_pages) of a page table."""
     if t.dim() != 2:
@@ -251,7 +259,10 @@ def cache_attention(q: torch.Tensor, pool: torch.Tensor, spec: CacheSpec, table:
         with torch.cuda.device(dev):
             return cache_attention(q, pool, spec, table, lens, cu_q, max_q, scale, causal, window, rotate, out,
                                    lse if with_lse else None, work)
-    if work is None:
+    wp = wb = 0
+    if work is not None:
+        wp, wb = _bytes(work, dev)
+    else:
         key = (dt, tokens, heads, seqs.rows, max_q, dev.index)
         need = r.work.get(key)
         if need is None:
@@ -261,10 +272,10 @@ def cache_attention(q: torch.Tensor, pool: torch.Tensor, spec: CacheSpec, table:
             r.work[key] = need
         if need:
             work = torch.empty(need, dtype=torch.uint8, device=dev)
+            wp, wb = work.data_ptr(), need
     st = l.hr_cache_attention(q.data_ptr(), qt, qh, dt, tokens, heads, pool.data_ptr(), n, r.ref, ctypes.byref(seqs),
                               0.0 if scale is None else scale, 1 if causal else 0, window, 1 if rotate else 0, out.data_ptr(), ot,
-                              oh, lp, max_q, None if work is None else work.data_ptr(), 0 if work is None else work.numel(),
-                              _stream(dev))
+                              oh, lp, max_q, wp, wb, _stream(dev))
     if st:
         check(st)
     return (out, lse) if with_lse else out
@@ -305,10 +316,11 @@ def cache_update(pool: torch.Tensor, spec: CacheSpec, table: torch.Tensor, lens:
         out["lens"], out["refs"], out["status"] = torch.empty(new + n + 4, dtype=torch.int32, device=dev).split((new, n, 4))
     if work is None:
         work = _scratch(l.hr_cache_update_work, dev, n, new)
+    wp, wb = _bytes(work, dev)
     st = l.hr_cache_update(pool.data_ptr(), layers, n, r.ref, tp, lp, rows, width, pp, gp, new,
                            _ints(out["table"], "out['table']", (new, width), dev), _ints(out["lens"], "out['lens']", (new,), dev),
                            _ints(out["refs"], "out['refs']", (n,), dev), _ints(out["status"], "out['status']", (4,), dev),
-                           work.data_ptr(), work.numel(), _stream(dev))
+                           wp, wb, _stream(dev))
     if st:
         check(st)
     return out
@@ -335,10 +347,11 @@ def cache_compact(pool: torch.Tensor, spec: CacheSpec, table: torch.Tensor, lens
         out["refs"], out["status"] = torch.empty(places + 4, dtype=torch.int32, device=dev).split((places, 4))
     if work is None:
         work = _scratch(l.hr_cache_compact_work, dev, n)
+    wp, wb = _bytes(work, dev)
     st = l.hr_cache_compact(pool.data_ptr(), layers, n, r.ref, tp, lp, rows, width, _ptr(into), 0 if into is None else places,
                             _ints(out["table"], "out['table']", (rows, width), dev),
                             _ints(out["refs"], "out['refs']", (places,), dev), _ints(out["status"], "out['status']", (4,), dev),
-                            work.data_ptr(), work.numel(), _stream(dev))
+                            wp, wb, _stream(dev))
     if st:
         check(st)
     return out

@@ -68,3 +68,26 @@ def test_no_tokens(calls):
     e = torch.zeros((64, 2, 0)).permute(2, 1, 0)
     hr.cache_append(s.pool, SPEC, e, e, s.table, s.lens, cu_q=s.cu)
     hr.cache_attention(e, s.pool, SPEC, s.table, s.lens, cu_q=s.cu)
+
+
+BAD_WORK = {
+    "another device": lambda: torch.empty(1 << 16, dtype=torch.uint8, device="meta"),
+    "strided": lambda: torch.empty(1 << 16, dtype=torch.uint8)[::2],
+}
+
+
+@pytest.mark.parametrize("work", BAD_WORK.values(), ids=BAD_WORK)
+def test_scratch_of_the_caller_is_checked(calls, work):
+    s = state()
+    for f in (lambda w: hr.cache_attention(s.q, s.pool, SPEC, s.table, s.lens, work=w),
+              lambda w: hr.cache_update(s.pool, SPEC, s.table, s.lens, s.parents, s.parents, work=w),
+              lambda w: hr.cache_compact(s.pool, SPEC, s.table, s.lens, work=w)):
+        before = len(calls.seen)
+        with pytest.raises(ValueError, match="work must be"):
+            f(work())
+        assert len(calls.seen) == before
+        # and its size is given in bytes, whatever its type
+        w = torch.empty(100, dtype=torch.float32)
+        f(w)
+        args = calls.seen[-1][2]
+        assert args[-3:-1] == (w.data_ptr(), 400)
