@@ -154,6 +154,21 @@ def _stream(device) -> int:
     return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
 
 
+_current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # (the latter also initializes: 0.4 us)
+
+
+def _call(device, fn, *args) -> None:
+    """Makes a C call with the tensors' device current: kernels, their sizes and
+    the default stream are those of the current device."""
+    if _current() == device.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st:
+        check(st)
+
+
 def _ints(t: torch.Tensor, name: str, shape: tuple, device) -> int:
     """Checks a contiguous int32 tensor; its address."""
     if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != device:
@@ -222,10 +237,8 @@ def cache_append(pool: torch.Tensor, spec: CacheSpec, k: torch.Tensor, v: torch.
     vt, vh = _vectors(v, "v", tokens, spec.kv_heads, spec.head_dim, dev)
     if k.dtype != v.dtype:
         raise ValueError("k and v must have the same dtype")
-    st = _cache_lib().hr_cache_append(pool.data_ptr(), n, r.ref, ctypes.byref(seqs), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
-                                      _dt(k), tokens, 1 if rotate else 0, _stream(dev))
-    if st:
-        check(st)
+    _call(dev, _cache_lib().hr_cache_append, pool.data_ptr(), n, r.ref, ctypes.byref(seqs), k.data_ptr(), kt, kh, v.data_ptr(),
+          vt, vh, _dt(k), tokens, 1 if rotate else 0, _stream(dev))
 
 
 def cache_attention(q: torch.Tensor, pool: torch.Tensor, spec: CacheSpec, table: torch.Tensor, lens: torch.Tensor,
@@ -255,10 +268,6 @@ def cache_attention(q: torch.Tensor, pool: torch.Tensor, spec: CacheSpec, table:
         if lse.dtype is not torch.float32 or lse.shape != (tokens, heads) or not lse.is_contiguous() or lse.device != dev:
             raise ValueError("lse must be a contiguous float32 tensor [tokens, q_heads]")
         lp = lse.data_ptr()
-    if torch.cuda.current_device() != dev.index:   # (kernels and scratch are chosen for the current device)
-        with torch.cuda.device(dev):
-            return cache_attention(q, pool, spec, table, lens, cu_q, max_q, scale, causal, window, rotate, out,
-                                   lse if with_lse else None, work)
     wp = wb = 0
     if work is not None:
         wp, wb = _bytes(work, dev)
@@ -266,18 +275,18 @@ def cache_attention(q: torch.Tensor, pool: torch.Tensor, spec: CacheSpec, table:
         key = (dt, tokens, heads, seqs.rows, max_q, dev.index)
         need = r.work.get(key)
         if need is None:
-            need = cache_attention_work(q.dtype, tokens, heads, spec, seqs.rows, max_q)
+            bytes_ = ctypes.c_int64()
+            _call(dev, l.hr_cache_attention_work, dt, tokens, heads, r.ref, seqs.rows, max_q, ctypes.byref(bytes_))
+            need = bytes_.value
             if len(r.work) > 4096:
                 r.work.clear()
             r.work[key] = need
         if need:
             work = torch.empty(need, dtype=torch.uint8, device=dev)
             wp, wb = work.data_ptr(), need
-    st = l.hr_cache_attention(q.data_ptr(), qt, qh, dt, tokens, heads, pool.data_ptr(), n, r.ref, ctypes.byref(seqs),
-                              0.0 if scale is None else scale, 1 if causal else 0, window, 1 if rotate else 0, out.data_ptr(), ot,
-                              oh, lp, max_q, wp, wb, _stream(dev))
-    if st:
-        check(st)
+    _call(dev, l.hr_cache_attention, q.data_ptr(), qt, qh, dt, tokens, heads, pool.data_ptr(), n, r.ref, ctypes.byref(seqs),
+          0.0 if scale is None else scale, 1 if causal else 0, window, 1 if rotate else 0, out.data_ptr(), ot, oh, lp, max_q,
+          wp, wb, _stream(dev))
     return (out, lse) if with_lse else out
 
 
@@ -317,12 +326,9 @@ def cache_update(pool: torch.Tensor, spec: CacheSpec, table: torch.Tensor, lens:
     if work is None:
         work = _scratch(l.hr_cache_update_work, dev, n, new)
     wp, wb = _bytes(work, dev)
-    st = l.hr_cache_update(pool.data_ptr(), layers, n, r.ref, tp, lp, rows, width, pp, gp, new,
-                           _ints(out["table"], "out['table']", (new, width), dev), _ints(out["lens"], "out['lens']", (new,), dev),
-                           _ints(out["refs"], "out['refs']", (n,), dev), _ints(out["status"], "out['status']", (4,), dev),
-                           wp, wb, _stream(dev))
-    if st:
-        check(st)
+    _call(dev, l.hr_cache_update, pool.data_ptr(), layers, n, r.ref, tp, lp, rows, width, pp, gp, new,
+          _ints(out["table"], "out['table']", (new, width), dev), _ints(out["lens"], "out['lens']", (new,), dev),
+          _ints(out["refs"], "out['refs']", (n,), dev), _ints(out["status"], "out['status']", (4,), dev), wp, wb, _stream(dev))
     return out
 
 
@@ -348,10 +354,7 @@ def cache_compact(pool: torch.Tensor, spec: CacheSpec, table: torch.Tensor, lens
     if work is None:
         work = _scratch(l.hr_cache_compact_work, dev, n)
     wp, wb = _bytes(work, dev)
-    st = l.hr_cache_compact(pool.data_ptr(), layers, n, r.ref, tp, lp, rows, width, _ptr(into), 0 if into is None else places,
-                            _ints(out["table"], "out['table']", (rows, width), dev),
-                            _ints(out["refs"], "out['refs']", (places,), dev), _ints(out["status"], "out['status']", (4,), dev),
-                            wp, wb, _stream(dev))
-    if st:
-        check(st)
+    _call(dev, l.hr_cache_compact, pool.data_ptr(), layers, n, r.ref, tp, lp, rows, width, _ptr(into),
+          0 if into is None else places, _ints(out["table"], "out['table']", (rows, width), dev),
+          _ints(out["refs"], "out['refs']", (places,), dev), _ints(out["status"], "out['status']", (4,), dev), wp, wb, _stream(dev))
     return out

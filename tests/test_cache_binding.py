@@ -43,7 +43,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(K, "_stream", lambda device: 0)
     monkeypatch.setattr(torch.cuda, "device", c.on)
     # the tensors here are on the CPU, whose device has no index: None is "theirs"
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(K, "_current", lambda: None)
     yield c
     K._resolved(SPEC).work.clear()
 
@@ -91,3 +91,19 @@ def test_scratch_of_the_caller_is_checked(calls, work):
         f(w)
         args = calls.seen[-1][2]
         assert args[-3:-1] == (w.data_ptr(), 400)
+
+
+def test_calls_run_on_the_device_of_their_tensors(calls, monkeypatch):
+    """With another device current, every entry point makes its C calls with
+    the tensors' device current: the default stream is address 0 on each."""
+    monkeypatch.setattr(K, "_current", lambda: 5)
+    s = state()
+    here = s.pool.device
+    hr.cache_append(s.pool, SPEC, s.k, s.k, s.table, s.lens)
+    hr.cache_attention(s.q, s.pool, SPEC, s.table, s.lens, lse=True)
+    hr.cache_update(s.pool, SPEC, s.table, s.lens, s.parents, s.parents, work=torch.empty(64, dtype=torch.uint8))
+    hr.cache_compact(s.pool, SPEC, s.table, s.lens, work=torch.empty(64, dtype=torch.uint8))
+    assert [n for n, _, _ in calls.seen] == ["hr_cache_append", "hr_cache_attention_work", "hr_cache_attention",
+                                             "hr_cache_update", "hr_cache_compact"]
+    assert all(device == here for _, device, _ in calls.seen), calls.seen
+    assert calls.device == "current"
