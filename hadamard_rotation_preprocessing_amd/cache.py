@@ -248,8 +248,8 @@ def cache_attention(q: torch.Tensor, pool: torch.Tensor, spec: CacheSpec, table:
     """Attention of q [tokens, q_heads, head_dim] over the cache; returns out
     (like q), or (out, lse) with ``lse`` True or a float32 [tokens, q_heads]
     tensor.  ``max_q``: an upper bound of a row's new tokens, if known (it
-    only chooses the kernel); ``work``: scratch of cache_attention_work bytes
-    (allocated if not given)."""
+    only chooses the kernel); ``scale``: None or 0 means 1 / sqrt(head_dim);
+    ``work``: scratch of cache_attention_work bytes (allocated if not given)."""
     r, dev, l = _resolved(spec), pool.device, _cache_lib()
     _, n = _pages(pool, r, False)
     seqs = _seqs(table, lens, cu_q, dev)
@@ -268,6 +268,8 @@ def cache_attention(q: torch.Tensor, pool: torch.Tensor, spec: CacheSpec, table:
         if lse.dtype is not torch.float32 or lse.shape != (tokens, heads) or not lse.is_contiguous() or lse.device != dev:
             raise ValueError("lse must be a contiguous float32 tensor [tokens, q_heads]")
         lp = lse.data_ptr()
+    if scale is not None and scale != 0 and ctypes.c_float(scale).value == 0:
+        raise ValueError("scale = %r is 0 in float32" % scale)   # (which would mean the default)
     wp = wb = 0
     if work is not None:
         wp, wb = _bytes(work, dev)

@@ -107,3 +107,13 @@ def test_calls_run_on_the_device_of_their_tensors(calls, monkeypatch):
                                              "hr_cache_update", "hr_cache_compact"]
     assert all(device == here for _, device, _ in calls.seen), calls.seen
     assert calls.device == "current"
+
+
+def test_scale_that_float32_does_not_hold(calls):
+    """0 means 1 / sqrt(head_dim); a scale that only rounds to 0 does not."""
+    s = state()
+    with pytest.raises(ValueError, match="scale"):
+        hr.cache_attention(s.q, s.pool, SPEC, s.table, s.lens, scale=1e-60)
+    for given, want in ((None, 0.0), (0.0, 0.0), (0.25, 0.25), (1e-40, 1e-40)):
+        hr.cache_attention(s.q, s.pool, SPEC, s.table, s.lens, scale=given)
+        assert calls.seen[-1][2][10] == want
