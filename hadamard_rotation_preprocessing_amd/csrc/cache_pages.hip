@@ -104,50 +104,12 @@ __device__ __forceinline__ void load16(const T* p, float (&v)[16]) {
     }
 }
 
-// Quantizes the lane's 16 elements: scale s = range / steps of the group,
-// stored (f32 or nearest-even bf16), codes from the stored scale.  y / s is
-// the correctly rounded quotient: one division gives r = 1 / s, and with
-// t = y r the remainder fma(-t, s, y) is exact, so fma(remainder, r, t) rounds
-// to y / s (P. Markstein, IBM J. Res. Dev. 34, 1990).  That keeps every code
-// equal to the definition's, ties included, at two more instructions than a
-// product with the reciprocal.  Codes are packed as float32, four of them to an
-// integer below 2^16; symmetric ones with 8 added, which an XOR takes back.
-template <int LANES, bool SYM>
-__device__ __forceinline__ uint2v quantize(const float (&v)[16], bool sf32, uint32_t* scale, uint32_t* zero) {
+// The codes of 16 elements y: quotient(y) is y / s, rounded to an integer.
+// Codes are packed as float32, four of them to an integer below 2^16; symmetric
+// ones with 8 added, which an XOR takes back.
+template <bool SYM, class Q>
+__device__ __forceinline__ uint2v pack_codes(const float (&v)[16], float z, Q quotient) {
 #pragma clang fp contract(off)
-    float s, z = 0.0f;
-    if constexpr (SYM) {
-        float top = fabsf(v[0]);
-#pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(top, fabsf(v[i]));
-        top = over_lanes<LANES>(top, [](float a, float b) { return fmaxf(a, b); });
-        s = top / 7.0f;
-    } else {
-        float lo = fminf(v[0], 0.0f), hi = fmaxf(v[0], 0.0f);
-#pragma unroll
-        for (int i = 1; i < 16; ++i) {
-            lo = fminf(lo, v[i]);
-            hi = fmaxf(hi, v[i]);
-        }
-        lo = over_lanes<LANES>(lo, [](float a, float b) { return fminf(a, b); });
-        hi = over_lanes<LANES>(hi, [](float a, float b) { return fmaxf(a, b); });
-        s = (hi - lo) / 15.0f;
-        z = lo;
-    }
-    if (s == 0.0f) s = 1.0f;
-    if (sf32) {
-        *scale = __float_as_uint(s);
-    } else {
-        *scale = f2bf(s);
-        s = bf2f(*scale);
-    }
-    const float r = 1.0f / s;
-    if constexpr (SYM) {
-        z = 8.0f;
-    } else {
-        z = fminf(fmaxf(rintf(-z / s), 0.0f), 15.0f);
-        *zero = static_cast<uint32_t>(static_cast<int>(z));
-    }
     uint2v w;
 #pragma unroll
     for (int i = 0; i < 16; i += 8) {
@@ -157,8 +119,7 @@ __device__ __forceinline__ uint2v quantize(const float (&v)[16], bool sf32, uint
             float sum = 0.0f;
 #pragma unroll
             for (int k = 3; k >= 0; --k) {
-                const float y = v[i + 4 * j + k], t = y * r;
-                const float q = rintf(__builtin_fmaf(__builtin_fmaf(-t, s, y), r, t));
+                const float q = quotient(v[i + 4 * j + k]);
                 const float c = __builtin_amdgcn_fmed3f(q + z, 0.0f, 15.0f);   // (NaN: 0)
                 sum = k == 3 ? c : __builtin_fmaf(sum, 16.0f, c);
             }
@@ -167,6 +128,64 @@ __device__ __forceinline__ uint2v quantize(const float (&v)[16], bool sf32, uint
         w[i / 8] = (half[1] << 16 | half[0]) ^ (SYM ? 0x88888888u : 0u);
     }
     return w;
+}
+
+// Quantizes the lane's 16 elements: scale s = range / steps of the group,
+// stored (f32 or nearest-even bf16), codes from the stored scale.  A group with
+// a NaN has a NaN scale, so that whoever reads it sees one.  y / s is the
+// correctly rounded quotient: one division gives r = 1 / s, and with t = y r the
+// remainder fma(-t, s, y) is exact, so fma(remainder, r, t) rounds to y / s (P.
+// Markstein, IBM J. Res. Dev. 34, 1990).  That keeps every code equal to the
+// definition's, ties included, at two more instructions than a product with the
+// reciprocal.  Where r or the remainder could leave the normal numbers, and for
+// scales that are not finite, each element is divided.
+template <int LANES, bool SYM>
+__device__ __forceinline__ uint2v quantize(const float (&v)[16], bool sf32, uint32_t* scale, uint32_t* zero) {
+#pragma clang fp contract(off)
+    float s, z = 0.0f;
+    bool nan;
+    if constexpr (SYM) {
+        float top = fabsf(v[0]);
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = __builtin_elementwise_maximum(top, fabsf(v[i]));   // (keeps a NaN)
+        nan = top != top;
+        top = over_lanes<LANES>(top, [](float a, float b) { return fmaxf(a, b); });
+        s = top / 7.0f;
+    } else {
+        float lo = fminf(v[0], 0.0f), hi = __builtin_elementwise_maximum(v[0], 0.0f);
+#pragma unroll
+        for (int i = 1; i < 16; ++i) {
+            lo = fminf(lo, v[i]);
+            hi = __builtin_elementwise_maximum(hi, v[i]);
+        }
+        nan = hi != hi;
+        lo = over_lanes<LANES>(lo, [](float a, float b) { return fminf(a, b); });
+        hi = over_lanes<LANES>(hi, [](float a, float b) { return fmaxf(a, b); });
+        s = (hi - lo) / 15.0f;
+        z = lo;
+    }
+    if (s == 0.0f) s = 1.0f;
+    const bool odd = __any(nan || !(s >= 0x1p-64f && s <= 0x1p64f));
+    if (odd && over_lanes<LANES>(nan ? 1.0f : 0.0f, [](float a, float b) { return fmaxf(a, b); }) != 0.0f)
+        s = __uint_as_float(0x7FC00000u);
+    if (sf32) {
+        *scale = __float_as_uint(s);
+    } else {
+        *scale = f2bf(s);
+        s = bf2f(*scale);
+    }
+    if constexpr (SYM) {
+        z = 8.0f;
+    } else {
+        z = fminf(fmaxf(rintf(-z / s), 0.0f), 15.0f);
+        *zero = static_cast<uint32_t>(static_cast<int>(z));
+    }
+    if (odd) return pack_codes<SYM>(v, z, [s](float y) { return rintf(y / s); });
+    const float r = 1.0f / s;
+    return pack_codes<SYM>(v, z, [s, r](float y) {
+        const float t = y * r;
+        return rintf(__builtin_fmaf(__builtin_fmaf(-t, s, y), r, t));
+    });
 }
 
 template <int D, int G, bool SYM, class T>

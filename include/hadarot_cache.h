@@ -80,7 +80,9 @@ int hr_cache_page_layout(const hr_cache_spec* spec, hr_cache_page* out);
  * Writes the new tokens' keys and values into their pages: each key vector
  * is rotated by H / sqrt(head_dim) if `rotate` is not 0 (R3; the value
  * vectors never are), and both are quantized with spec->q as in
- * rotate_quantize_act, from the float32 values.
+ * rotate_quantize_act, from the float32 values.  A group with a NaN gets a NaN
+ * scale (its codes do not matter then), so attention gives NaN to the tokens
+ * that see it.
  *   pool    device, [n_pages, page_bytes], 16-byte aligned.
  *   k, v    device, element (t, h, i) at t * stride_token + h * stride_head
  *           + i (strides in elements, so a slice of a fused projection's

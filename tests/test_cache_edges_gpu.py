@@ -1,8 +1,11 @@
 """The paged 4-bit cache on the GPU where one sequence, key or row could reach
 another's result: idle sequences, scales and queries of very different sizes.
 Oracle and bounds as in test_cache_gpu.py."""
+import numpy as np
 import pytest
+import torch
 
+import oracle
 import test_cache_gpu as T
 from oracle import cache as O
 from test_cache_gpu import BF, F32, gpu_ready  # noqa: F401
@@ -27,3 +30,75 @@ def test_calls_without_tokens():
     pool = T.gpu(O.random_pool(c, 4, 1))
     out, lse = T.hr.cache_attention(q, pool, T.spec_of(c), T.ints([[0, 1]]), T.ints([20]), cu_q=T.ints([0, 0]), lse=True)
     assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+
+
+def definition(v, c):
+    """Codes, scale bytes and zero points of float32 vectors [tokens, d] by the
+    definition, step for step in float32."""
+    y = v.reshape(len(v), c.ng, c.group)
+    with np.errstate(all="ignore"):
+        if c.sym:
+            lo, s = None, np.abs(y).max(-1) / np.float32(7)
+        else:
+            lo, hi = np.minimum(y.min(-1), np.float32(0)), np.maximum(y.max(-1), np.float32(0))
+            s = (hi - lo) / np.float32(15)
+        s = np.where(s == 0, np.float32(1), s).astype(np.float32)
+        stored = torch.from_numpy(s) if c.sdt == "f32" else torch.from_numpy(s).to(BF)
+        s = stored.float().numpy()
+        q = np.rint(y / s[..., None])
+        z = np.zeros(s.shape, dtype=np.float32) if c.sym else np.clip(np.rint(-lo / s), 0, 15)
+        q = np.clip(q, -8, 7) if c.sym else np.clip(q + z[..., None], 0, 15)
+    return q, stored, z
+
+
+@pytest.mark.parametrize("sdt", ["bf16", "f32"])
+@pytest.mark.parametrize("sym", [False, True], ids=["asym", "sym"])
+@pytest.mark.parametrize("d,group", [(64, 64), (128, 32), (256, 256)])
+def test_append_at_the_ends_of_float32(d, group, sym, sdt):
+    """Vectors whose scale is subnormal, next to it, next to the largest number
+    or infinite: the definition's codes; a NaN marks the scale of its group."""
+    c = O.CacheDef(1, d, 16, group, sym, sdt)
+    rng = np.random.default_rng(d)
+    v = rng.standard_normal((48, 1, d)).astype(np.float32)
+    for i, e in enumerate([-149, -146, -140, -133, -130, -128, -127, -126, -125, -120, -110, -100, -70, -66, -64, -62, -60, -30,
+                           30, 60, 64, 66, 100, 120, 123, 124, 125]):
+        v[i] = np.ldexp(v[i] / np.abs(v[i]).max(), e)
+    v[30, 0, 3] = np.inf
+    v[31, 0, d - 1] = -np.inf
+    nan = [(35, 0), (36, 17), (37, d - 1), (38, d // 2 + 5), (39, d // 2 - 1)]
+    for t, i in nan:
+        v[t, 0, i] = np.nan
+    v[40, 0, 5:9] = np.nan, np.inf, -np.inf, 1.0
+    k = torch.zeros((48, 1, d)).to(T.DEV)
+    pool = T.hr.cache_pool(T.spec_of(c), 3)
+    T.hr.cache_append(pool, T.spec_of(c), k, torch.from_numpy(v).to(T.DEV), T.ints([[2, 0, 1]]), T.ints([48]))
+    out, zeros = T.read_rows(pool.cpu().numpy(), c, np.array([[2, 0, 1]]), 0, 0, "v", 0, 48)
+    q, s, z = definition(v[:, 0], c)
+    want_nan = np.zeros((48, c.ng), dtype=bool)
+    for t, i in nan + [(40, 5)]:
+        want_nan[t, i // group] = True
+    got = out["scales"].float()
+    assert (torch.isnan(got).numpy() == want_nan).all()
+    s = s.float().numpy()
+    same = ~want_nan
+    assert (got.numpy()[same] == s[same]).all()
+    # codes of groups whose elements and scale are finite
+    fine = same & np.isfinite(v[:, 0].reshape(48, c.ng, group)).all(-1)
+    codes = oracle.unpack_nibbles(out["codes"].numpy().reshape(-1), 48 * d, sym).reshape(48, c.ng, group)
+    # (a scale that bfloat16 rounds to 0 leaves 0 / 0 without a code)
+    assert ((codes == q) | np.isnan(q))[fine].all(), np.argwhere(((codes != q) & ~np.isnan(q)).any(-1) & fine)
+    if not sym:
+        assert (zeros.reshape(48, c.ng)[fine] == z[fine]).all()
+
+
+def test_a_nan_that_was_appended_is_seen():
+    """A NaN in one key, or value, reaches the rows that see it and no others."""
+    c = O.CacheDef(2, 128, 16, 32, False, "bf16")
+    for x in range(2):
+        kv = [T.make_q(40, 2, 128, BF, 3 + y, 1.0).to(T.DEV) for y in range(2)]
+        kv[x][20, 1, 77] = float("nan")
+        pool, table = T.hr.cache_pool(T.spec_of(c), 3), T.ints([[1, 2, 0]])
+        T.hr.cache_append(pool, T.spec_of(c), *kv, table, T.ints([40]))
+        out = T.hr.cache_attention(T.make_q(30, 4, 128, BF, 9).to(T.DEV), pool, T.spec_of(c), table, T.ints([40])).cpu()
+        assert torch.isnan(out[10:, 2:]).any(-1).all()
+        assert not torch.isnan(out[:10]).any() and not torch.isnan(out[:, :2]).any()
