@@ -199,6 +199,17 @@ int check_distinct(const char* name, int64_t st, int64_t sh, int64_t tokens, int
     return fail(HR_EINVAL, "%s strides %lld, %lld make rows overlap", name, (long long)st, (long long)sh);
 }
 
+// The new tokens that a sequence of the call has, for the choice of a kernel: the
+// caller's bound, or without one the mean (which they are where cu_q is NULL).
+// One token in each of 64 sequences of up to 32768 positions: 94 us, where all
+// tokens counted as one sequence's took 313.  A prompt among 63 single tokens (4000
+// positions, 32 heads over 8 of 128), few-row kernel against shared, us: 128 tokens
+// 93, 98; 512 166, 360; 1400 (rows by the mean: shared) 314, 415.
+int64_t new_tokens(int64_t tokens, int64_t seqs, int64_t max_q) {
+    if (max_q > 0) return max_q < tokens ? max_q : tokens;
+    return seqs > 0 ? (tokens + seqs - 1) / seqs : tokens;
+}
+
 // The kernel of a call, by its query rows (query heads per kv head x new tokens
 // of a sequence at most) and its scores at most (query rows x keys; the lengths
 // are on the device, so keys are what the table or the window allows).
@@ -214,10 +225,10 @@ int check_distinct(const char* name, int64_t st, int64_t sh, int64_t tokens, int
 //   65: 83, 78; 134: 118, 101.  float32 13: 38, 51; 17: 79, 87; 33: 104, 90 and
 //   77, 80; 67: 239, 197.  Groups of 32 7: 39, 51; 14: 62, 55; 17: 72, 47.  Heads
 //   of 256 8: 63, 45; 33: 79, 58.
-void attn_key(const hr::CachePage& pg, int dtype, int64_t tokens, int32_t q_heads, int64_t max_q, int64_t keys,
+void attn_key(const hr::CachePage& pg, int dtype, int64_t tokens, int32_t q_heads, int64_t seqs, int64_t max_q, int64_t keys,
               hr::CacheAttnKey* k) {
     memset(k, 0, sizeof *k);
-    const int64_t most = max_q > 0 && max_q < tokens ? max_q : tokens, rows = most * (q_heads / pg.hkv);
+    const int64_t rows = new_tokens(tokens, seqs, max_q) * (q_heads / pg.hkv);
     k->d = pg.d;
     k->ng = pg.ng;
     k->sf32 = pg.sf32;
@@ -323,7 +334,7 @@ int hr_cache_attention_work(int dtype, int64_t tokens, int32_t q_heads, const hr
     int64_t need[2];
     for (int i = 0; i < 2; ++i) {
         int workers;
-        attn_key(pg, dtype, tokens, q_heads, max_q, i ? kMaxKeys : 0, &key);
+        attn_key(pg, dtype, tokens, q_heads, rows, max_q, i ? kMaxKeys : 0, &key);
         if ((st = attn_work_bytes(key, &workers, &need[i]))) return st;
     }
     *bytes = need[0] > need[1] ? need[0] : need[1];
@@ -365,9 +376,9 @@ int hr_cache_attention(const void* q, int64_t q_stride_token, int64_t q_stride_h
                  {"work", nullptr, 0, true}};
     if ((st = check_overlap(r, 7))) return st;
     int64_t keys = int64_t{seqs->max_pages} << a.pg.logp;
-    if (window > 0 && window < keys - tokens) keys = window + (max_q > 0 && max_q < tokens ? max_q : tokens);
+    if (window > 0 && window < keys - tokens) keys = window + new_tokens(tokens, seqs->rows, max_q);
     hr::CacheAttnKey key;
-    attn_key(a.pg, dtype, tokens, q_heads, max_q, keys, &key);
+    attn_key(a.pg, dtype, tokens, q_heads, seqs->rows, max_q, keys, &key);
     int workers;
     int64_t need;
     if ((st = attn_work_bytes(key, &workers, &need))) return st;

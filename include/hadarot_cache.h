@@ -115,8 +115,9 @@ int hr_cache_append(void* pool, int64_t n_pages, const hr_cache_spec* spec, cons
  *   scale   positive and finite; 0 means 1 / sqrt(head_dim).
  *   lse     device float32 [tokens, q_heads] or NULL: the natural logarithm of
  *           the softmax's sum of exponentials.
- *   max_q   an upper bound of one row's new tokens, or 0 if not known.  It
- *           only chooses the kernel: a larger row is still computed in full.
+ *   max_q   an upper bound of one row's new tokens, or 0 if not known (the
+ *           mean is taken).  It only chooses the kernel: a larger row is
+ *           still computed in full.
  *   work    device scratch of at least the bytes that
  *           hr_cache_attention_work gives for the same arguments, 16-byte
  *           aligned.  Contents do not matter.
