@@ -93,6 +93,16 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 __device__ __forceinline__ float lo_f32(uint32_t h) { return static_cast<float>(__builtin_bit_cast(half2v, h).x); }
 __device__ __forceinline__ float hi_f32(uint32_t h) { return static_cast<float>(__builtin_bit_cast(half2v, h).y); }
 
+// Two floats as pairs of float16: hi, and what it loses of them.  They pass an
+// empty asm as values: a product would be rounded to float16 in one instruction
+// where it makes hi, and through float32 where lo takes hi from it, which in one
+// of some thousand elements are neighbouring numbers, 2^-11 apart.
+__device__ __forceinline__ void split_f16(float a, float b, uint32_t& hi, uint32_t& lo) {
+    asm("" : "+v"(a), "+v"(b));
+    hi = pack_f16(a, b);
+    lo = pack_f16(a - lo_f32(hi), b - hi_f32(hi));
+}
+
 // The value of lane ^ X inside 32 lanes: a swizzle, whose pattern is in the
 // instruction (a general shuffle would hold its addresses in registers).
 template <int X>
@@ -443,8 +453,8 @@ struct Values {
                 z1[i] |= 0x54005400u;
             }
             if constexpr (SCALED) {
-                s0[i] = pack_f16(vs[2 * i], vs[2 * i + 1]);
-                if constexpr (C::WIDE && C::SF32) s1[i] = pack_f16(vs[2 * i] - lo_f32(s0[i]), vs[2 * i + 1] - hi_f32(s0[i]));
+                if constexpr (C::WIDE && C::SF32) split_f16(vs[2 * i], vs[2 * i + 1], s0[i], s1[i]);
+                else s0[i] = pack_f16(vs[2 * i], vs[2 * i + 1]);
             }
         }
     }
@@ -625,8 +635,8 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
             for (int j = 0; j < 4; ++j) {
                 const float f = C::SUBK && !C::SHARED && (j & 1) ? up * 0.0625f : up;
                 const float x = v[rt][8 * i + j] * f, y = v[rt][8 * i + j + 4] * f;
-                hi[j] = pack_f16(x, y);
-                if constexpr (C::WIDE) lo[j] = pack_f16(x - lo_f32(hi[j]), y - hi_f32(hi[j]));
+                if constexpr (C::WIDE) split_f16(x, y, hi[j], lo[j]);
+                else hi[j] = pack_f16(x, y);
                 if constexpr (C::SUBK && !C::SHARED) {
                     const float back = lo_f32(hi[j]) + hi_f32(hi[j]);
                     sum[C::NG == 1 ? 0 : i / C::KG] += (j & 1) ? back * 16.0f : back;
@@ -641,8 +651,9 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
 #pragma unroll
             for (int i = 0; i < C::NG; ++i) {
                 const float t = -sum_groups(sum[i]);
-                const uint32_t hi = pack_f16(t, 0.0f);
-                w.qz[rt][i] = uint4v{g == 0 ? (hi & 0xFFFFu) | (pack_f16(t - lo_f32(hi), 0.0f) << 16) : 0u, 0u, 0u, 0u};
+                uint32_t hi, lo;
+                split_f16(t, 0.0f, hi, lo);
+                w.qz[rt][i] = uint4v{g == 0 ? (hi & 0xFFFFu) | (lo << 16) : 0u, 0u, 0u, 0u};
             }
         }
         w.mc[rt] = kLow;
@@ -753,8 +764,11 @@ __device__ __forceinline__ void probabilities(Rows<C>& st, int rt, float (&x)[8]
         float p[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) p[j] = x[2 * i + j] * (C::NG == 1 ? vs[2 * i + j] : C::SHARED ? vs[0] : static_cast<float>(1 << kPExp));
-        hi[i] = pack_f16(p[0], p[1]);
-        if constexpr (C::WIDE) lo[i] = pack_f16(p[0] - lo_f32(hi[i]), p[1] - hi_f32(hi[i]));
+        uint32_t h, l = 0;
+        if constexpr (C::WIDE) split_f16(p[0], p[1], h, l);
+        else h = pack_f16(p[0], p[1]);
+        hi[i] = h;
+        lo[i] = l;
     }
 }
 
@@ -1184,15 +1198,15 @@ __device__ __forceinline__ void make_keys(const CacheAttnArgs& a, const RawK<C>&
             uint32_t z0 = (((z << 16) | (z & 0xFFFFu)) & zs.mask) | zs.fixed;
             const uint32_t z1 = (z0 << 4) | 0x54005400u;
             z0 |= 0x64006400u;
-            const uint32_t hi = pack_f16(ks[s][gi], ks[s][gi]);
+            uint32_t hi, lo = 0;
+            if constexpr (C::WIDE) split_f16(ks[s][gi], ks[s][gi], hi, lo);
+            else hi = pack_f16(ks[s][gi], ks[s][gi]);
             const uint4v d = code_operand<false, true>(w.k[s][i], zs.flip, z0, z1);
             uint4v f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[j] = pk_mul(d[j], hi);
             tile.k[0][s * C::KS + i][lane] = f;
             if constexpr (C::WIDE) {
-                const float rest = ks[s][gi] - lo_f32(hi);
-                const uint32_t lo = pack_f16(rest, rest);
                 uint4v fl;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) fl[j] = pk_fma(d[j], lo, pk_fma(d[j], hi, f[j] ^ 0x80008000u));
@@ -1388,8 +1402,11 @@ __device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            ph[rt][k] = pack_f16(p[rt][2 * k], p[rt][2 * k + 1]);
-            if constexpr (C::WIDE) pl[rt][k] = pack_f16(p[rt][2 * k] - lo_f32(ph[rt][k]), p[rt][2 * k + 1] - hi_f32(ph[rt][k]));
+            uint32_t h, l = 0;
+            if constexpr (C::WIDE) split_f16(p[rt][2 * k], p[rt][2 * k + 1], h, l);
+            else h = pack_f16(p[rt][2 * k], p[rt][2 * k + 1]);
+            ph[rt][k] = h;
+            pl[rt][k] = l;
         }
     const uint4v ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
 #pragma unroll

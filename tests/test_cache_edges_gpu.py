@@ -102,3 +102,52 @@ def test_a_nan_that_was_appended_is_seen():
         out = T.hr.cache_attention(T.make_q(30, 4, 128, BF, 9).to(T.DEV), pool, T.spec_of(c), table, T.ints([40])).cpu()
         assert torch.isnan(out[10:, 2:]).any(-1).all()
         assert not torch.isnan(out[:10]).any() and not torch.isnan(out[:, :2]).any()
+
+
+# ---------------------------------------------------------------------------
+# attention: nothing of another row or of an unseen key in a row's result
+
+KERNELS = ["few", "shared"]
+SHAPES = [(64, 32), (128, 128), (128, 32), (256, 256), (256, 64)]
+
+
+def attend(many, c, pool, table, lens, cu, q, **kw):
+    """One call, by the kernel of few rows or by that of many (which a table of
+    2^22 positions and a large bound of new tokens ask for)."""
+    if many == "shared":
+        wide = np.full((len(lens), (1 << 22) // c.page), -1, dtype=np.int32)
+        wide[:, :table.shape[1]] = table
+        table = wide
+    return T.hr.cache_attention(q.to(T.DEV), T.gpu(pool), T.spec_of(c), T.gpu(table), T.ints(lens), cu_q=T.ints(cu),
+                                max_q=1 << 20 if many == "shared" else 1, lse=True, **kw)
+
+
+def row_errors(out, ref):
+    """Relative error of each (token, head)."""
+    g = out.detach().cpu().double().numpy()
+    return np.linalg.norm(g - ref, axis=-1) / np.maximum(np.linalg.norm(ref, axis=-1), 1e-30)
+
+
+# A row's error where its scores are of order 1: rounding the result once is at
+# most 2^-9 (bfloat16) of it, and 11-bit operands (2^-11 / sqrt(12) each, of some
+# ten score units at random signs) are a quarter of that.  float32: as in
+# test_cache_gpu.py.
+ROW = {BF: 1.5 * 2.0 ** -9, F32: 2e-5}
+
+
+@pytest.mark.parametrize("d,group", SHAPES)
+@pytest.mark.parametrize("many", KERNELS)
+def test_no_row_loses_a_pair_of_float16(many, d, group):
+    """float32 rows, each by itself: one key whose probability, scale or query
+    is a pair of float16 that do not belong together errs by 2^-11."""
+    c = O.CacheDef(2, d, 16, group, False, "f32")
+    lens, cu = [300, 90], np.array([0, 150, 240], dtype=np.int32)
+    table, n_pages = T.make_table(c, lens, 4)
+    pool = O.random_pool(c, n_pages, 4)
+    q = T.make_q(240, 4, d, F32, 6)
+    ref, rlse, err = O.attention(q.double().numpy(), pool, c, table, lens, cu)
+    out, lse = attend(many, c, pool, table, lens, cu, q)
+    T.check_attention(out, lse, ref, rlse, err, q, c, 300)
+    e = row_errors(out, ref)
+    T.say("  largest row error %.3g" % e.max())
+    assert e.max() <= ROW[F32], np.unravel_index(e.argmax(), e.shape)
