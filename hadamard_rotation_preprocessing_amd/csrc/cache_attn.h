@@ -743,8 +743,13 @@ __device__ __forceinline__ void exponentials(Rows<C>& st, int rt, float (&x)[8],
         st.l[rt] *= f;
 #pragma unroll
         for (int j = 0; j < C::DT; ++j) st.o[rt][j] *= f;
+        // (the products rounded as mc is: beside it an unrounded one of 2^30 may be
+        // 2^6 larger)
 #pragma unroll
-        for (int t = 0; t < 8; ++t) p[t] = __builtin_amdgcn_exp2f(fmaf(x[t], mul[t], -mc));
+        for (int t = 0; t < 8; ++t) {
+#pragma clang fp contract(off)
+            p[t] = __builtin_amdgcn_exp2f(x[t] * mul[t] - mc);
+        }
     }
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
@@ -1303,7 +1308,9 @@ __device__ __forceinline__ bool move_maximum(float4v (&x)[C::RT][2], Rows<C>& st
         float w = -__builtin_inff();
 #pragma unroll
         for (int k = 0; k < 8; ++k) w = fmaxf(w, x[rt][k / 4][k % 4]);
-        w = max_groups(w) - kPExp;                       // how far the running maximum moves
+        const float most = max_groups(w);
+        w = most - kPExp;                                // how far the running maximum moves
+        if (most - w > kPExp + kSlack) w = most;         // (where the unit in the last place is 16)
         const bool fresh = st.mc[rt] == kLow;
         const float d = w > 0.0f || (fresh && w > -__builtin_inff()) ? w : 0.0f;
         if (fresh && !(w > -__builtin_inff())) left = true;

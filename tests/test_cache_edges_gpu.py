@@ -151,3 +151,33 @@ def test_no_row_loses_a_pair_of_float16(many, d, group):
     e = row_errors(out, ref)
     T.say("  largest row error %.3g" % e.max())
     assert e.max() <= ROW[F32], np.unravel_index(e.argmax(), e.shape)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d,group", SHAPES)
+@pytest.mark.parametrize("many", KERNELS)
+def test_scores_beyond_the_bits_of_float32(many, d, group, dtype):
+    """Scores of 1e9 to 1e31, whose unit in the last place is large: one key
+    takes a row, and the result is finite."""
+    c = O.CacheDef(1, d, 16, group, False, "bf16")
+    lens, cu = [150, 70], np.array([0, 40, 60], dtype=np.int32)
+    table, n_pages = T.make_table(c, lens, 3)
+    pool = O.random_pool(c, n_pages, 3)
+    for size in (1e9, 1e20, 1e30):
+        q = (size * T.make_q(60, 4, d, F32, 5)).to(dtype)
+        ref, _, (mag, _) = O.attention(q.double().numpy(), pool, c, table, lens, cu)
+        out, _ = attend(many, c, pool, table, lens, cu, q)
+        assert torch.isfinite(out).all()
+        # rows whose best key leads by more than twice what a score errs by
+        y = oracle.rotate(q.double().numpy().reshape(-1, d), d, 0).reshape(60, 4, d)
+        lead = np.zeros((60, 4))
+        for b in range(2):
+            k = np.concatenate([O.vectors(pool[p], c, 0, "k")[0] for p in table[b] if p >= 0])[: lens[b]]
+            for t in range(cu[b], cu[b + 1]):
+                seen = lens[b] - (cu[b + 1] - t) + 1
+                s = np.sort(y[t] @ k[:seen].T / np.sqrt(d), -1)
+                lead[t] = s[:, -1] - s[:, -2] if seen > 1 else np.inf
+        sure = lead > 2 * (2.0 ** -21 if dtype == F32 else 2.0 ** -11) * mag + 2 * d * 2.0 ** -24 * mag
+        assert sure.mean() > 0.5
+        e = np.where(sure, row_errors(out, ref), 0)
+        assert e.max() <= ROW[dtype], np.unravel_index(e.argmax(), e.shape)
