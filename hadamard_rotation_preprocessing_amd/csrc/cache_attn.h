@@ -530,6 +530,10 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     float v[C::RT][N];
     float top = 0.0f;
+    // shared operands: the scores' factor is a fraction, which goes into the rows,
+    // and a power of two, so that the keys' scales are taken as they are
+    const float factor = a.scale * kLog2e;
+    const float fraction = C::SHARED ? __builtin_amdgcn_frexp_mantf(factor) : 1.0f;
     const uint4v h0 = hadamard32(0), h1 = hadamard32(1);
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt) {
@@ -595,6 +599,10 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
 #pragma unroll
             for (int j = 0; j < N; ++j) v[rt][j] *= a.norm;
         }
+        if constexpr (C::SHARED) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[rt][j] *= fraction;
+        }
         // (a row of infinities or NaN scales nothing: it gives NaN all the same)
         float own = 0.0f;
 #pragma unroll
@@ -618,7 +626,8 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
     if (top > 0.0f) e = min(max((C::SHARED ? 2 : 6) - (static_cast<int>(__float_as_uint(top) >> 23) - 126), -100), 100);
     e = __builtin_amdgcn_readfirstlane(e);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    w.c = a.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 + (C::SUBK && !C::SHARED ? 24 : 0) - e) << 23);
+    if constexpr (C::SHARED) w.c = ldexpf(1.0f, __builtin_amdgcn_frexp_expf(factor) - e);
+    else w.c = factor * __uint_as_float(static_cast<uint32_t>(127 + (C::SUBK ? 24 : 0) - e) << 23);
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt) {
         float sum[C::NG];
@@ -1094,8 +1103,16 @@ __device__ __forceinline__ void join_waves(const CacheAttnArgs& a, const Seq& s,
 // computed.  The waves that make values do so first (their scales are looked
 // at again at the end of a pass), those that make keys last: the two of a SIMD
 // are one of each, so that its matrix unit and its vector unit both have work.
-// Scaled operands are rounded to float16 (2^-12, as the queries are); float32
-// activations take pairs of float16 throughout.
+// Scaled operands s (c - z) are rounded to float16 for bfloat16 activations: with
+// bfloat16 scales (8 bits) that is exact but for |c - z| of 9, 11, 13 and 15 (4 bits
+// more), and then each element's own, of 2^-12 at most; float32 scales are rounded
+// with their elements (keys) or before them (values).  The sum of exponentials is
+// that of the probabilities as they are multiplied, 11 bits each, so what rounding
+// does to all of a row cancels; the log-sum-exp errs by 2^-12 at most.  Scales
+// applied to the results and probabilities instead, in float32, took 755 us for the
+// call above and do not change its error, 1.70e-3 (1.66e-3 of it bfloat16's own
+// rounding); with scales times the scores' factor rounded for a whole key it was
+// 1.99e-3.  float32 activations take pairs of float16 throughout.
 
 template <class C>
 struct Tile {
@@ -1204,12 +1221,17 @@ __device__ __forceinline__ void make_keys(const CacheAttnArgs& a, const RawK<C>&
             const uint32_t z1 = (z0 << 4) | 0x54005400u;
             z0 |= 0x64006400u;
             uint32_t hi, lo = 0;
-            if constexpr (C::WIDE) split_f16(ks[s][gi], ks[s][gi], hi, lo);
-            else hi = pack_f16(ks[s][gi], ks[s][gi]);
+            if constexpr (C::WIDE || C::SF32) split_f16(ks[s][gi], ks[s][gi], hi, lo);
+            else hi = pack_f16(ks[s][gi], ks[s][gi]);   // (exact)
             const uint4v d = code_operand<false, true>(w.k[s][i], zs.flip, z0, z1);
             uint4v f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = pk_mul(d[j], hi);
+            for (int j = 0; j < 4; ++j) {
+                // (what float16 loses of a float32 scale would be lost of all the
+                // key's elements at once, and move its score by up to 2^-11)
+                if constexpr (!C::WIDE && C::SF32) f[j] = pk_fma(d[j], hi, pk_mul(d[j], lo));
+                else f[j] = pk_mul(d[j], hi);
+            }
             tile.k[0][s * C::KS + i][lane] = f;
             if constexpr (C::WIDE) {
                 uint4v fl;

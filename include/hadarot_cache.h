@@ -121,9 +121,13 @@ int hr_cache_append(void* pool, int64_t n_pages, const hr_cache_spec* spec, cons
  *   work    device scratch of at least the bytes that
  *           hr_cache_attention_work gives for the same arguments, 16-byte
  *           aligned.  Contents do not matter.
- * Products use float16 operands with float32 sums for HR_BF16 (the 4-bit
- * codes are exact, the queries and probabilities carry 11 bits) and pairs of
- * float16 (22 bits) for HR_F32.  The result does not depend on scheduling:
+ * Products use float16 operands with float32 sums for HR_BF16: the queries and
+ * probabilities carry 11 bits, and so do scale (c - z) of values in several
+ * groups and, where a call has many new tokens, of all keys and values (which
+ * is exact with bfloat16 scales but for |c - z| of 9, 11, 13 and 15); the codes
+ * are exact otherwise.  The log-sum-exp of such a call errs by up to 2^-12 by
+ * the rounding of its probabilities.  HR_F32 takes pairs of float16 (22 bits).
+ * The result does not depend on scheduling:
  * partial sums over a long sequence are joined in a fixed order.
  */
 int hr_cache_attention(const void* q, int64_t q_stride_token, int64_t q_stride_head,

@@ -128,10 +128,9 @@ def row_errors(out, ref):
     return np.linalg.norm(g - ref, axis=-1) / np.maximum(np.linalg.norm(ref, axis=-1), 1e-30)
 
 
-# A row's error where its scores are of order 1: rounding the result once is at
-# most 2^-9 (bfloat16) of it, and 11-bit operands (2^-11 / sqrt(12) each, of some
-# ten score units at random signs) are a quarter of that.  float32: as in
-# test_cache_gpu.py.
+# A row's error where nothing cancels: rounding the result once leaves at most
+# 2^-8 / sqrt(3) in the root mean square (bfloat16, of elements at the lower end of
+# their binades), times 1.3.  float32: as in test_cache_gpu.py.
 ROW = {BF: 1.5 * 2.0 ** -9, F32: 2e-5}
 
 
@@ -181,3 +180,40 @@ def test_scores_beyond_the_bits_of_float32(many, d, group, dtype):
         assert sure.mean() > 0.5
         e = np.where(sure, row_errors(out, ref), 0)
         assert e.max() <= ROW[dtype], np.unravel_index(e.argmax(), e.shape)
+
+
+@pytest.mark.parametrize("sdt", ["bf16", "f32"])
+@pytest.mark.parametrize("d,group", SHAPES)
+@pytest.mark.parametrize("many", KERNELS)
+def test_a_key_is_not_scaled_as_a_whole(many, d, group, sdt):
+    """Rows that see one key: the log-sum-exp is the score.  Queries of the
+    key's signs, so that nothing cancels.  A float16 operand is rounded by a unit
+    in the last place / sqrt(12) in the root mean square, 2^-10 / sqrt(12) of a
+    number at the lower end of its binade and less of others.  What is left of
+    these errors in a score: independent ones of the queries, and of the keys one
+    for every odd part of c - z (powers of two are rounded alike).  A scale that
+    is rounded for a whole key, or a rounded factor of all scores, has one error
+    for the score as a whole and leaves more."""
+    c = O.CacheDef(2, d, 16, group, False, sdt)
+    rows, hq = 96, 4
+    rng = np.random.default_rng(d + group)
+    table = rng.permutation(rows).astype(np.int32)[:, None]
+    pool = O.random_pool(c, rows, 7)
+    q = np.abs(rng.standard_normal((rows, hq, d))) + 0.2
+    want, sigma = np.zeros((rows, hq)), np.zeros((rows, hq))
+    for b in range(rows):
+        for h in range(hq):
+            k, n, _ = (x[0] for x in O.vectors(pool[table[b, 0]], c, h // 2, "k"))
+            x = torch.from_numpy(q[b, h] * np.where(k < 0, -1, 1)).to(BF).double().numpy()
+            q[b, h] = x
+            w = np.abs(x * k)
+            want[b, h] = w.sum() / np.sqrt(d)
+            odd = np.abs(n).astype(int)
+            while ((odd > 0) & (odd % 2 == 0)).any():
+                odd = np.where((odd > 0) & (odd % 2 == 0), odd // 2, odd)
+            classes = [w[g * group: (g + 1) * group][odd[g * group: (g + 1) * group] == v].sum() for g in range(c.ng) for v in range(1, 16, 2)]
+            sigma[b, h] = np.sqrt((w ** 2).sum() + (np.array(classes) ** 2).sum()) / w.sum()
+    out, lse = attend(many, c, pool, table, [1] * rows, np.arange(rows + 1), torch.from_numpy(q).to(BF), rotate=False)
+    e = (lse.cpu().double().numpy() / want - 1) / sigma / (2.0 ** -10 / 12 ** 0.5)
+    T.say("  root mean square of the errors, of its bound: %.3g; largest %.3g" % (np.sqrt((e ** 2).mean()), np.abs(e).max()))
+    assert np.sqrt((e ** 2).mean()) <= 1
