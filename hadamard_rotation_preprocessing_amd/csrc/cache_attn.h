@@ -493,7 +493,9 @@ template <class C>
 struct Rows {
     uint4v q[C::RT][C::P][C::KS];
     uint4v qz[C::RT][C::SUBK && !C::SHARED ? C::NG : 1];  // -sum(q) of a group as an operand (subnormal codes)
-    float c;                    // log2 units of one raw score unit
+    float c;                    // log2 units of one raw score unit, of rows in the common unit
+    int own;                    // kOwnUnit if some row of the wave is not, else 0
+    int unit[C::SHARED && C::WIDE ? C::RT : 1];   // shared, float32: scores are times 2^-unit
     int lim[C::RT], lo[C::RT];  // keys [lo, lim) are seen
     float mc[C::RT];            // running maximum, log2 units
     float l[C::RT];             // sum of exponentials (this lane's keys)
@@ -505,6 +507,10 @@ struct Rows {
     float start[C::SHARED ? C::RT : 1];
     float4v from[C::SHARED ? C::RT : 1], lsum[C::SHARED ? C::RT : 1];
 };
+
+// What the makers of a tile's key operands note of it (see Passes): bits 0 and 1
+// absent subtiles, kOwnUnit (added by the waves), the rest the keys' exponent.
+enum { kOwnUnit = 4, kShiftBits = 3 };
 
 // The sign matrix of the index bits that a lane's eight elements and its lane
 // group make (5 of them, H_32) as the A operand of a bfloat16 product: row m of
@@ -523,13 +529,14 @@ __device__ __forceinline__ uint4v hadamard32(int a) {
 }
 
 // Loads rows r0 + 16 rt + (lane & 15) of kv head h, rotates them and makes
-// them operands.  Rows past the sequence's repeat its last one.
+// them operands.  Rows past the sequence's repeat its last one.  units: for the
+// exponents of the wave's 16 RT rows against the common one.
 template <class C, class T>
-__device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, int h, int r0, Rows<C>& w, float* lds) {
+__device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, int h, int r0, Rows<C>& w, float* lds, int* units) {
     constexpr int D = C::D, N = D / 4;
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     float v[C::RT][N];
-    float top = 0.0f;
+    float top[C::RT];   // a row's largest element
     // shared operands: the scores' factor is a fraction, which goes into the rows,
     // and a power of two, so that the keys' scales are taken as they are
     const float factor = a.scale * kLog2e;
@@ -603,33 +610,51 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
 #pragma unroll
             for (int j = 0; j < N; ++j) v[rt][j] *= fraction;
         }
-        // (a row of infinities or NaN scales nothing: it gives NaN all the same)
         float own = 0.0f;
 #pragma unroll
         for (int j = 0; j < N; ++j) own = fmaxf(own, fabsf(v[rt][j]));
-        if (own < __builtin_inff()) top = fmaxf(top, own);
+        own = max_groups(own);
+        top[rt] = own < __builtin_inff() ? own : 0.0f;   // (a row of infinities or NaN scales nothing: it gives NaN all the same)
     }
-    // one power of two for all rows of the wave puts the largest element at
-    // 2^5 .. 2^6 (a group's sum then stays in float16's range); an element
-    // 2^-20 of it still has all eleven bits, one of 2^-30 still one.  With
-    // shared operands, at 2 .. 4: their scaled keys have range to spare too.
-    top = max_wave(top);
-    if constexpr (C::SHARED) {   // (of the workgroup: the shared scales carry c)
+    // A power of two puts the largest element of the wave's rows at 2^5 .. 2^6 (a
+    // group's sum then stays in float16's range); with shared operands, of the
+    // workgroup's at 2 .. 4: their scaled keys, which carry c, have range to spare
+    // too.  A row that is not much smaller shares that unit: float16 loses nothing
+    // above 2^-25, which is 2^-16 of a row's largest element at a distance of
+    // 2^RANGE (pairs: 2^-22).  Other rows have a unit of their own, put right in
+    // their scores, so that a result does not depend on the rows beside it.  The
+    // scores of pairs in shared operands are put right in any case.
+    constexpr int TO = C::SHARED ? 2 : 6, RANGE = !C::WIDE ? 10 : C::SHARED ? 0 : 8;
+    const auto exponent = [](float x) { return min(max(TO - (static_cast<int>(__float_as_uint(x) >> 23) - 126), -100), 100); };
+    float all = top[0];
+#pragma unroll
+    for (int rt = 1; rt < C::RT; ++rt) all = fmaxf(all, top[rt]);
+    all = max_wave(all);
+    if constexpr (C::SHARED) {
         __syncthreads();
-        if (lane == 0) lds[threadIdx.x >> 6] = top;
+        if (lane == 0) lds[threadIdx.x >> 6] = all;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < C::WR; ++i) top = fmaxf(top, lds[i]);
+        for (int i = 0; i < C::WR; ++i) all = fmaxf(all, lds[i]);
         __syncthreads();
     }
-    int e = 0;
-    if (top > 0.0f) e = min(max((C::SHARED ? 2 : 6) - (static_cast<int>(__float_as_uint(top) >> 23) - 126), -100), 100);
-    e = __builtin_amdgcn_readfirstlane(e);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    if constexpr (C::SHARED) w.c = ldexpf(1.0f, __builtin_amdgcn_frexp_expf(factor) - e);
-    else w.c = factor * __uint_as_float(static_cast<uint32_t>(127 + (C::SUBK ? 24 : 0) - e) << 23);
+    const int common = __builtin_amdgcn_readfirstlane(all > 0.0f ? exponent(all) : 0);
+    int e[C::RT];
+    bool others = false;
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt) {
+        e[rt] = top[rt] > 0.0f ? exponent(top[rt]) : common;
+        if (e[rt] - common <= RANGE) e[rt] = common;
+        others |= e[rt] != common;
+        if constexpr (C::SHARED && C::WIDE) w.unit[rt] = e[rt] - common;
+        else if (g == 0) units[16 * rt + n] = e[rt] - common;
+    }
+    w.own = !(C::SHARED && C::WIDE) && __any(others) ? kOwnUnit : 0;
+    if constexpr (C::SHARED) w.c = ldexpf(1.0f, __builtin_amdgcn_frexp_expf(factor) - common);
+    else w.c = factor * __uint_as_float(static_cast<uint32_t>(127 + (C::SUBK ? 24 : 0) - common) << 23);
+#pragma unroll
+    for (int rt = 0; rt < C::RT; ++rt) {
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + e[rt]) << 23);
         float sum[C::NG];
 #pragma unroll
         for (int i = 0; i < C::NG; ++i) sum[i] = 0.0f;
@@ -816,15 +841,26 @@ __device__ __forceinline__ float cover_scales(Rows<C>& st, const float (&vs)[8],
     return ldexpf(1.0f, shift - st.e);
 }
 
-// One step over 32 keys; mask: some of them are not seen by every row.
+// One step over 32 keys; mask: some of them are not seen by every row; units: of
+// the wave's rows.
 template <class C>
-__device__ __forceinline__ void step(const CacheAttnArgs& a, const Raw<C>& w, const Pages& pages, bool mask, int t0, Rows<C>& st) {
+__device__ __forceinline__ void step(const CacheAttnArgs& a, const Raw<C>& w, const Pages& pages, bool mask, const int* units, int t0,
+                                     Rows<C>& st) {
     constexpr int NG = C::NG, RT = C::RT;
     const int lane = threadIdx.x & 63, g = lane >> 4;
     const Zeros zs = zeros_of(a);
     float x[RT][8], mul[8];
     scores<C>(zs, w, st, x, mul);
     HR_PHASE();
+    if (st.own) {
+        HR_BRANCH();
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const int unit = -units[16 * rt + (lane & 15)];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) x[rt][t] = ldexpf(x[rt][t], unit);
+        }
+    }
     float vs[8];
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
@@ -923,7 +959,7 @@ struct Walk {
         next = pages_at(a, table, t + S);
         load_keys<C>(a, now, h, t, w);
     }
-    __device__ __forceinline__ void run(const CacheAttnArgs& a, const Span& sp, Rows<C>& st) {
+    __device__ __forceinline__ void run(const CacheAttnArgs& a, const Span& sp, const int* units, Rows<C>& st) {
         if (t >= end) return;
         while (true) {
             Raw<C> n;
@@ -931,7 +967,7 @@ struct Walk {
             if (more) load_keys<C>(a, next, h, t + S, n);
             const Pages after = pages_at(a, table, t + 2 * S);
             const bool all = t >= sp.flo && t + 32 <= sp.fhi && present(a, now.p[0]) && present(a, now.p[1]);
-            step<C>(a, w, now, !all, t, st);
+            step<C>(a, w, now, !all, units, t, st);
             if (!more) return;
             t += S;
             w = n;
@@ -1123,15 +1159,16 @@ template <class C>
 struct Passes {
     Tile<C> tile[2][C::TILES];
     int keys[2][4];             // of a tile's keys: bit s: subtile s is on an absent page;
-                                // 4 x shift: they are times 2^-shift (extreme scales)
+                                // 2^kShiftBits x shift: they are times 2^-shift (extreme scales)
     uint32_t odd[2][4];         // keys whose value scale is not finite
     int e[2][C::TILES];         // exponent that covers a tile's value scales
     float top[C::WR];
+    int unit[C::WR][16 * C::RT];   // exponents of the rows' units (bfloat16 activations)
 };
 template <class C>
 constexpr int lds_floats() {
     if constexpr (C::SHARED) return static_cast<int>(sizeof(Passes<C>)) / 4;
-    else return join_floats<C>();
+    else return join_floats<C>() + 4 * 16 * C::RT;   // (and the units of each wave's rows)
 }
 
 // Codes and scales of a tile's keys: key m in the lane.
@@ -1210,7 +1247,7 @@ __device__ __forceinline__ void make_keys(const CacheAttnArgs& a, const RawK<C>&
 #pragma unroll
             for (int gi = 0; gi < NG; ++gi) ks[s][gi] = ldexpf(ks[s][gi], -e);
     }
-    if (lane == 0) *special = (present(a, pages.p[0]) ? 0 : 1) | (present(a, pages.p[1]) ? 0 : 2) | e * 4;
+    if (lane == 0) *special = (present(a, pages.p[0]) ? 0 : 1) | (present(a, pages.p[1]) ? 0 : 2) | e * (1 << kShiftBits);
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -1350,17 +1387,17 @@ __device__ __forceinline__ bool move_maximum(float4v (&x)[C::RT][2], Rows<C>& st
 }
 
 // One step over a tile.  special: what the makers noted of it, odd: keys with
-// bad value scales; unset: some row has not seen a key yet.
+// bad value scales; units: of the wave's rows; unset: some row has not seen a
+// key yet.
 template <class C>
-__device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint32_t odd, int t0, const Span& sp, Rows<C>& st,
-                                          bool& unset) {
+__device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint32_t odd, const int* units, int t0, const Span& sp,
+                                          Rows<C>& st, bool& unset) {
     constexpr int RT = C::RT, GROUP = Fetch<C>::GROUP;
     const int lane = threadIdx.x & 63, g = lane >> 4;
     // scores as exponents: the products start from kPExp - mc.  (Not so for float32
-    // activations, where it would cost the sums bits, and extreme scales, whose
-    // unit is not 1: it is added at the end.)
-    const int shift = special >> 2;
-    const bool late = C::WIDE || shift != 0;
+    // activations, where it would cost the sums bits, and extreme scales and rows,
+    // whose unit is not 1: it is added at the end.)
+    const bool late = C::WIDE || (special & ~3) != 0;
     if (late) {
         HR_BRANCH();
 #pragma unroll
@@ -1392,9 +1429,11 @@ __device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint
     if (late) {
         HR_BRANCH();
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int rt = 0; rt < RT; ++rt) {
+            const int unit = (special >> kShiftBits) - (C::WIDE ? st.unit[rt] : units[16 * rt + (lane & 15)]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) acc[rt][k / 4][k % 4] = (C::WIDE && shift == 0 ? acc[rt][k / 4][k % 4] : ldexpf(acc[rt][k / 4][k % 4], shift)) + st.start[rt];
+            for (int k = 0; k < 8; ++k) acc[rt][k / 4][k % 4] = ldexpf(acc[rt][k / 4][k % 4], unit) + st.start[rt];
+        }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) st.from[rt] = float4v{st.start[rt], st.start[rt], st.start[rt], st.start[rt]};
     }
@@ -1477,8 +1516,8 @@ __device__ __forceinline__ uint4v exponentials(const float4v (&acc)[2]) {
     return ph;
 }
 template <class C>
-__device__ __forceinline__ void pair_step(const Tile<C>& tile, int special, uint32_t odd, int t0, const Span& sp, Rows<C>& st,
-                                          bool& unset) {
+__device__ __forceinline__ void pair_step(const Tile<C>& tile, int special, uint32_t odd, const int* units, int t0, const Span& sp,
+                                          Rows<C>& st, bool& unset) {
     constexpr int N = C::DT;   // operands of keys, and of values
     const int lane = threadIdx.x & 63, g = lane >> 4;
     const uint4v ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
@@ -1512,9 +1551,8 @@ __device__ __forceinline__ void pair_step(const Tile<C>& tile, int special, uint
     const bool all = t0 >= sp.flo && t0 + 32 <= sp.fhi && (special | odd) == 0;
     if (!all || unset || __any(top > static_cast<float>(kPExp + kSlack))) {
         HR_BRANCH();
-        const int shift = special >> 2;
-        if (shift != 0) {
-            // extreme scales: the scores' unit is not 1, and they start from 0
+        if ((special & ~3) != 0) {
+            // extreme scales or rows: the scores' unit is not 1, and they start from 0
             HR_BRANCH();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -1523,7 +1561,8 @@ __device__ __forceinline__ void pair_step(const Tile<C>& tile, int special, uint
 #pragma unroll
                 for (int j = 0; j < C::KS; ++j) x = mfma(tile.k[0][i % 2 * C::KS + j][lane], st.q[i / 2][0][j], x);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = ldexpf(x[r], shift) + st.start[i / 2];
+                for (int r = 0; r < 4; ++r)
+                    x[r] = ldexpf(x[r], (special >> kShiftBits) - units[i / 2 * 16 + (lane & 15)]) + st.start[i / 2];
             }
         }
         if (!all) {
@@ -1587,6 +1626,7 @@ __device__ __forceinline__ void passes(const CacheAttnArgs& a, const int32_t* ta
             if (lane == 0) ps.e[buf][tile] = e;
         }
     };
+    const int* units = ps.unit[threadIdx.x >> 6];
     int made = -100;                    // the exponent of the pass made last
     const auto make = [&](int t, int buf) {
 #pragma unroll
@@ -1617,10 +1657,10 @@ __device__ __forceinline__ void passes(const CacheAttnArgs& a, const int32_t* ta
         const int first = max(sp.lo - t, 0) >> 5, stop = (min(min(end, sp.hi) - t, S) + 31) >> 5;
 #pragma unroll 1
         for (int i = first; i < stop; ++i) {
-            const int special = __builtin_amdgcn_readfirstlane(ps.keys[buf][i]), t0 = t + 32 * i;
+            const int special = __builtin_amdgcn_readfirstlane(ps.keys[buf][i]) | st.own, t0 = t + 32 * i;
             const uint32_t odd = __builtin_amdgcn_readfirstlane(ps.odd[buf][i]);
-            if constexpr (C::RT == 2) pair_step<C>(ps.tile[buf][i], special, odd, t0, sp, st, unset);
-            else tile_step<C>(ps.tile[buf][i], special, odd, t0, sp, st, unset);
+            if constexpr (C::RT == 2) pair_step<C>(ps.tile[buf][i], special, odd, units, t0, sp, st, unset);
+            else tile_step<C>(ps.tile[buf][i], special, odd, units, t0, sp, st, unset);
         }
         if constexpr (ROLE == kMakeKeys) {
             make(t + S, buf ^ 1);
@@ -1648,7 +1688,7 @@ __device__ __forceinline__ void shared_segment(const CacheAttnArgs& a, const Seq
     if (row < last) sp = span_of(a, s, row, min(row + 16 * C::RT, last));
     const int begin = max(k0, all.lo & ~31), end = min(k1, all.hi);
     Rows<C> st;
-    load_rows<C, T>(a, s, h, row, st, ps.top);
+    load_rows<C, T>(a, s, h, row, st, ps.top, ps.unit[wave]);
     if (wave < N) passes<C, kMakeKeys>(a, table, h, wave, begin, end, sp, st, ps);
     else if (wave < 2 * N) passes<C, kMakeValues>(a, table, h, wave - N, begin, end, sp, st, ps);
     else passes<C, kMakeNothing>(a, table, h, 0, begin, end, sp, st, ps);
@@ -1679,8 +1719,9 @@ __device__ __forceinline__ void segment(const CacheAttnArgs& a, const Seq& s, in
         keys.table = a.sq.table + static_cast<int64_t>(b) * a.sq.max_pages;
         keys.h = h;
         keys.start(a, sp, k0, k1, wave);
-        load_rows<C, T>(a, s, h, r0, st, lds);
-        keys.run(a, sp, st);
+        int* units = reinterpret_cast<int*>(lds + join_floats<C>()) + wave * 16 * C::RT;
+        load_rows<C, T>(a, s, h, r0, st, lds, units);
+        keys.run(a, sp, units, st);
         settle<C>(st);
         join_waves<C, T>(a, s, h, r0, st, part, lds);
     }

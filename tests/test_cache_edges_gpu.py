@@ -217,3 +217,59 @@ def test_a_key_is_not_scaled_as_a_whole(many, d, group, sdt):
     e = (lse.cpu().double().numpy() / want - 1) / sigma / (2.0 ** -10 / 12 ** 0.5)
     T.say("  root mean square of the errors, of its bound: %.3g; largest %.3g" % (np.sqrt((e ** 2).mean()), np.abs(e).max()))
     assert np.sqrt((e ** 2).mean()) <= 1
+
+
+def check_rows(many, out, lse, ref, rlse, err, q, c, keys, rows):
+    """check_attention of some (token, head) rows.  The log-sum-exp of a bfloat16
+    call by the kernel of many rows is that of probabilities rounded to float16:
+    2^-11 more."""
+    mag, vabs = (x[rows] for x in err)
+    loose = many == "shared" and q.dtype == BF
+    T.check_attention(out.cpu()[rows], None if loose else lse.cpu()[rows], ref[rows], rlse[rows], (mag, vabs), q, c, keys, rms=False)
+    if loose:
+        e = (2.0 ** -11 + c.d * 2.0 ** -24) * mag + 2.0 ** -20 + 2.0 ** -18 * (1 + np.abs(rlse[rows])) + 2.0 ** -11
+        assert (np.abs(lse.cpu().double().numpy()[rows] - rlse[rows]) <= e).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d,group", SHAPES)
+@pytest.mark.parametrize("many", KERNELS)
+def test_rows_of_all_sizes(many, d, group, dtype):
+    """Queries of sizes from 1e-30 to 1e30 in one block of rows: each is as
+    precise as its own size allows."""
+    c = O.CacheDef(1, d, 16, group, False, "bf16")
+    lens, cu = [150, 70], np.array([0, 40, 60], dtype=np.int32)
+    table, n_pages = T.make_table(c, lens, 3)
+    pool = O.random_pool(c, n_pages, 3)
+    rng = np.random.default_rng(d)
+    for top in (100.0, 1e4, 1e7, 1e30):
+        size = rng.choice([1e-4, 1e-2, 0.3, 1.0, top], (60, 4))
+        size[5:9] = 1e-30
+        size[9, 1] = 0.0
+        q = (T.make_q(60, 4, d, F32, 5) * torch.from_numpy(size[..., None]).float()).to(dtype)
+        ref, rlse, err = O.attention(q.double().numpy(), pool, c, table, lens, cu)
+        out, lse = attend(many, c, pool, table, lens, cu, q)
+        assert torch.isfinite(out).all()
+        small = size <= 1.0
+        check_rows(many, out, lse, ref, rlse, err, q, c, 150, small)
+        if dtype == F32:
+            assert row_errors(out, ref)[small].max() <= ROW[F32]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("many", KERNELS)
+def test_rows_of_infinities(many, dtype):
+    """A query with an infinity or a NaN gives NaN, and changes no other row."""
+    c = O.CacheDef(1, 128, 16, 128, False, "bf16")
+    lens, cu = [150], np.array([0, 60], dtype=np.int32)
+    table, n_pages = T.make_table(c, lens, 3)
+    pool = O.random_pool(c, n_pages, 3)
+    q = T.make_q(60, 4, 128, dtype, 5)
+    ref, rlse, err = O.attention(q.double().numpy(), pool, c, table, lens, cu)
+    fine = np.ones((60, 4), dtype=bool)
+    for t, h, x in ((3, 0, float("inf")), (17, 2, float("nan")), (40, 3, -float("inf"))):
+        q[t, h, 70] = x
+        fine[t, h] = False
+    out, lse = attend(many, c, pool, table, lens, cu, q)
+    assert torch.isnan(out.cpu()[torch.from_numpy(~fine)]).all()
+    check_rows(many, out, lse, ref, rlse, err, q, c, 150, fine)
