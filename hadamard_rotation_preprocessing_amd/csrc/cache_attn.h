@@ -1356,9 +1356,30 @@ struct Fetch {
     }
 };
 
-// Moves the running maxima to what the scores (exponents, from kPExp - mc) of a
-// tile have, where that is more, and the sums and the scores with them.  Whether
-// some row has not seen a key yet.
+// The scores of a tile, in log2 units.
+template <class C>
+__device__ __forceinline__ void raw_scores(const Tile<C>& tile, int special, const int* units, const Rows<C>& st,
+                                           float4v (&x)[C::RT][2]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < 2 * C::RT; ++i) {
+        float4v& y = x[i / 2][i % 2];
+        y = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < C::KS; ++j) y = mfma(tile.k[0][i % 2 * C::KS + j][lane], st.q[i / 2][0][j], y);
+        if ((special & ~3) != 0) {   // (extreme scales or rows: their unit is not 1)
+            HR_BRANCH();
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y[r] = ldexpf(y[r], (special >> kShiftBits) - units[i / 2 * 16 + (lane & 15)]);
+        }
+    }
+}
+
+// Moves the running maxima to what the scores of a tile have, where that is more,
+// and the sums with them; the scores become exponents, kPExp less what they lie
+// below the maximum.  (Of the scores themselves: as a product that starts from
+// kPExp - mc, a score far above mc has lost bits of its own.)  Whether some row has
+// not seen a key yet.
 template <class C>
 __device__ __forceinline__ bool move_maximum(float4v (&x)[C::RT][2], Rows<C>& st) {
     bool left = false;
@@ -1367,21 +1388,21 @@ __device__ __forceinline__ bool move_maximum(float4v (&x)[C::RT][2], Rows<C>& st
         float w = -__builtin_inff();
 #pragma unroll
         for (int k = 0; k < 8; ++k) w = fmaxf(w, x[rt][k / 4][k % 4]);
-        const float most = max_groups(w);
-        w = most - kPExp;                                // how far the running maximum moves
-        if (most - w > kPExp + kSlack) w = most;         // (where the unit in the last place is 16)
-        const bool fresh = st.mc[rt] == kLow;
-        const float d = w > 0.0f || (fresh && w > -__builtin_inff()) ? w : 0.0f;
-        if (fresh && !(w > -__builtin_inff())) left = true;
-        else st.mc[rt] = fresh ? d : st.mc[rt] + d;
-        const float f = fresh ? 1.0f : exp2f(-d);        // (nothing to scale before the first key)
-        st.start[rt] -= d;
+        w = max_groups(w);
+        const bool fresh = st.mc[rt] == kLow, any = w > -__builtin_inff();
+        if (fresh && !any) left = true;
+        const float mc = any && (fresh || w > st.mc[rt]) ? w : st.mc[rt];
+        const float f = fresh ? 1.0f : exp2f(st.mc[rt] - mc);   // (nothing to scale before the first key)
+        if (mc != st.mc[rt]) st.start[rt] = kPExp - mc;
+        st.mc[rt] = mc;
         st.from[rt] = float4v{st.start[rt], st.start[rt], st.start[rt], st.start[rt]};
         st.lsum[rt] *= f;
 #pragma unroll
         for (int j = 0; j < C::DT; ++j) st.o[rt][j] *= f;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) x[rt][s] -= d;
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[rt][s][r] = x[rt][s][r] - mc + kPExp;
     }
     return __any(left);
 }
@@ -1432,33 +1453,38 @@ __device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint
         for (int rt = 0; rt < RT; ++rt) {
             const int unit = (special >> kShiftBits) - (C::WIDE ? st.unit[rt] : units[16 * rt + (lane & 15)]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) acc[rt][k / 4][k % 4] = ldexpf(acc[rt][k / 4][k % 4], unit) + st.start[rt];
+            for (int k = 0; k < 8; ++k) acc[rt][k / 4][k % 4] = ldexpf(acc[rt][k / 4][k % 4], unit);
         }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) st.from[rt] = float4v{st.start[rt], st.start[rt], st.start[rt], st.start[rt]};
     }
-    if (!(t0 >= sp.flo && t0 + 32 <= sp.fhi && (special & 3) == 0 && odd == 0)) {
-        // unseen scores become -inf, whatever they are
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int at = 16 * (k / 4) + 4 * g + k % 4, key = t0 + at;
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const bool seen = !(special >> (k / 4) & 1) && key < st.lim[rt] && key >= st.lo[rt];
-                if (odd >> at & 1) acc[rt][k / 4][k % 4] = __builtin_nanf("");
-                if (!seen) acc[rt][k / 4][k % 4] = -__builtin_inff();
-            }
-        }
-    }
+    const bool all = t0 >= sp.flo && t0 + 32 <= sp.fhi && (special & 3) == 0 && odd == 0;
     float p[RT][8], top = 0.0f;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            p[rt][k] = __builtin_amdgcn_exp2f(acc[rt][k / 4][k % 4]);
+            p[rt][k] = __builtin_amdgcn_exp2f(late ? acc[rt][k / 4][k % 4] + st.start[rt] : acc[rt][k / 4][k % 4]);
             top = fmaxf(top, p[rt][k]);
         }
-    if (unset || __any(top > static_cast<float>(1 << (kPExp + kSlack)))) {
+    if (!all || unset || __any(top > static_cast<float>(1 << (kPExp + kSlack)))) {
+        HR_BRANCH();
+        if constexpr (!C::WIDE)
+            if (!late) raw_scores<C>(tile, special, units, st, acc);
+        if (!all) {
+            // unseen scores become -inf, whatever they are
+            HR_BRANCH();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int at = 16 * (k / 4) + 4 * g + k % 4, key = t0 + at;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const bool seen = !(special >> (k / 4) & 1) && key < st.lim[rt] && key >= st.lo[rt];
+                    if (odd >> at & 1) acc[rt][k / 4][k % 4] = __builtin_nanf("");
+                    if (!seen) acc[rt][k / 4][k % 4] = -__builtin_inff();
+                }
+            }
+        }
         unset = move_maximum<C>(acc, st);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
@@ -1551,20 +1577,7 @@ __device__ __forceinline__ void pair_step(const Tile<C>& tile, int special, uint
     const bool all = t0 >= sp.flo && t0 + 32 <= sp.fhi && (special | odd) == 0;
     if (!all || unset || __any(top > static_cast<float>(kPExp + kSlack))) {
         HR_BRANCH();
-        if ((special & ~3) != 0) {
-            // extreme scales or rows: the scores' unit is not 1, and they start from 0
-            HR_BRANCH();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float4v& x = acc[i / 2][i % 2];
-                x = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int j = 0; j < C::KS; ++j) x = mfma(tile.k[0][i % 2 * C::KS + j][lane], st.q[i / 2][0][j], x);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    x[r] = ldexpf(x[r], (special >> kShiftBits) - units[i / 2 * 16 + (lane & 15)]) + st.start[i / 2];
-            }
-        }
+        raw_scores<C>(tile, special, units, st, acc);
         if (!all) {
             // unseen scores become -inf, whatever they are
             HR_BRANCH();

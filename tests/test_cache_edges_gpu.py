@@ -273,3 +273,27 @@ def test_rows_of_infinities(many, dtype):
     out, lse = attend(many, c, pool, table, lens, cu, q)
     assert torch.isnan(out.cpu()[torch.from_numpy(~fine)]).all()
     check_rows(many, out, lse, ref, rlse, err, q, c, 150, fine)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("below", [1e3, 1e5, 1e7])
+@pytest.mark.parametrize("many", KERNELS)
+def test_scores_far_above_the_first_ones(many, below, dtype):
+    """A sequence whose first keys have scores far below all others': the result
+    is that without them."""
+    c = O.CacheDef(1, 128, 16, 128, True, "f32")
+    lens, cu = [200], np.array([0, 60], dtype=np.int32)
+    table, n_pages = T.make_table(c, lens, 3)
+    pool = O.random_pool(c, n_pages, 3)
+    q = T.make_q(60, 4, 128, F32, 5).abs().to(dtype)
+    without = table.copy()
+    without[0, :2] = -1
+    ref, rlse, err = O.attention(q.double().numpy(), pool, c, without, lens, cu, rotate=False)
+    for pos in range(32):                     # codes of -8: their scores are -8 s sum(q) / sqrt(128)
+        O.section(pool[table[0, pos // 16]], c, 0, "k_codes").reshape(16, -1)[pos % 16] = 0x88
+        row = O.section(pool[table[0, pos // 16]], c, 0, "k_scales").reshape(16, -1)
+        row[pos % 16] = O.f32_to_bytes(np.full(1, below / 100, dtype=np.float32), "f32")
+    out, lse = attend(many, c, pool, table, lens, cu, q, rotate=False)
+    check_rows(many, out, lse, ref, rlse, err, q, c, 200, np.ones((60, 4), dtype=bool))
+    if dtype == F32:
+        assert row_errors(out, ref).max() <= ROW[F32]
