@@ -161,6 +161,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPExp = 9;              // probabilities are at most 2^kSlack and carry 2^kPExp in float16
 constexpr int kSlack = 6;             // how far (log2) a score may pass the running maximum before it moves
 constexpr int kSExp = 8;              // value scales (several groups) carry 2^kSExp
+constexpr int kFar = 32;              // value scales outside 2^-kFar .. 2^kFar are set aside
+constexpr int kNoUnit = -10000;       // the unit of value scales before the first of them
 
 // Integers read at an address that is the same in all lanes: through the scalar
 // cache, into scalar registers.
@@ -223,10 +225,36 @@ struct Cfg {
     static constexpr int KEYS = SHARED ? 32 * TILES : 32 * WT;  // keys of an item
     static constexpr int ES = SF32 ? 4 : 2;
     static constexpr int KSW = NG * ES;            // 32-bit words of four positions' scales
-    static constexpr int WAVES = 2;                // waves per SIMD
+    static constexpr int WAVES = D == 64 && NG == 1 && RT == 1 && !SHARED ? 3 : 2;   // waves per SIMD
     static constexpr bool SUBK = !WIDE;            // subnormal codes of K
     static constexpr bool SUBV = !WIDE && NG == 1; // and of V
     static constexpr bool VLO = WIDE && NG > 1;    // scaled values as pairs of float16
+    // How far (log2) value scales may lie below their unit, and scaled keys below
+    // 2^12, and keep their bits in float16.  Values: scales carry 2^kSExp, down to
+    // float16's smallest normal number, 2^-14, or for pairs to 2^-3; where they are
+    // in probabilities, of which those far below 1 lose bits anyway, 2^14 or 2^10.
+    static constexpr int VEXP = NG == 1 && !SHARED ? kPExp : kSExp;
+    static constexpr int VRANGE = NG == 1 && !SHARED ? (WIDE ? 10 : 14) : (WIDE ? 10 : 21);
+    static constexpr int KRANGE = WIDE ? 13 : 24;
+};
+
+// A workgroup's note of the segment it works on, in LDS, for sweep_rows.
+struct Todo {
+    int aside;               // whether it sets keys aside (0 between segments)
+    int b, h, r0, k0, k1;
+    float c;                 // of the rows, with shared operands
+    float* part;             // where its rows go (nullptr: they are finished)
+    float* spare;            // for the parts of rows that are finished but for such keys
+    __device__ __forceinline__ void set(int b_, int h_, int r, int from, int to, float scale, float* p, float* sp) {
+        b = b_;
+        h = h_;
+        r0 = r;
+        k0 = from;
+        k1 = to;
+        c = scale;
+        part = p;
+        spare = sp;
+    }
 };
 
 // What a wave holds of 32 keys before it works on them.
@@ -275,7 +303,7 @@ __device__ __forceinline__ Pages pages_at(const CacheAttnArgs& a, const int32_t*
     return r;
 }
 __device__ __forceinline__ bool present(const CacheAttnArgs& a, int page) {
-    return static_cast<uint32_t>(page) < static_cast<uint64_t>(a.sq.n_pages);
+    return static_cast<uint32_t>(page) < static_cast<uint32_t>(a.sq.n_pages);   // (at most 2^30)
 }
 
 // The value of a lane offset as it stands here: sums with constants formed from
@@ -500,7 +528,8 @@ struct Rows {
     float mc[C::RT];            // running maximum, log2 units
     float l[C::RT];             // sum of exponentials (this lane's keys)
     float4v o[C::RT][C::DT];
-    int e;                      // exponent of the value scales in o
+    int e;                      // unit of the value scales in o
+    float big, small;           // few rows: the largest and smallest of them in that unit
     // shared operands: scores start from start[] = kPExp - mc (from: in all four
     // registers of a matrix operand); lsum is the sum of exponentials as a
     // matrix result
@@ -701,7 +730,7 @@ __device__ __forceinline__ void load_rows(const CacheAttnArgs& a, const Seq& s, 
 #pragma unroll
         for (int j = 0; j < C::DT; ++j) w.o[rt][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    w.e = -100;
+    w.e = kNoUnit;
 }
 
 // Raw scores of 32 keys, in log2 units once multiplied by mul:
@@ -811,41 +840,145 @@ __device__ __forceinline__ void probabilities(Rows<C>& st, int rt, float (&x)[8]
     }
 }
 
-// Raises the exponent of the value scales in o to e.
+// The unit of value scales.  o is held in units of 2^e of them, and a scale takes
+// part in a float16 operand if its exponent is in [e - VRANGE, e].  With shared
+// operands the unit moves with the scales of a pass, and o with it, exactly.  A
+// few-row wave takes the one of its first step throughout, and goes through its
+// keys again with a unit for every step if some scale was not in it (a branch that
+// moves the unit in every step's code takes 8% of a single token's time).
+// Keys whose scales are too far from the others' for one unit, beyond 2^kFar either
+// way, or not finite are set aside: left out of the step, and taken one at a time
+// when the segment is done, in float32 throughout (sweep_rows).  So a key that a
+// row does not see has no influence on it, whatever its scale is, and one that it
+// sees costs the others no bits.  Whether a key is set aside depends on the scales
+// of its step (pass) alone, not on those before it: the sweep finds the same keys.
+// (Within 2^kFar no move of the unit lets a sum overflow.)
+// A token of R3's cache: 43 us; 118 and 145 with one scale in 20000 and in 1000 2^28
+// times the others', 2400 with all of them anywhere from 1 to 2^30.
+__device__ __forceinline__ int exponent(float x) {   // |x| < 2^exponent(x); x finite
+    return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 126;
+}
+__device__ __forceinline__ float power(int e) {      // 2^e, -126 <= e <= 128 (infinite)
+    return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+// The unit for exponents from lo to hi, at most RANGE apart: those in its middle.
+template <int RANGE>
+__device__ __forceinline__ int unit_for(int lo, int hi) {
+    return min(max(hi + (RANGE - (hi - lo)) / 2, RANGE - kFar), kFar);
+}
+template <int RANGE>
+__device__ __forceinline__ bool set_aside(float x, int lo) {
+    x = fabsf(x);
+    return x != 0.0f && !(x >= power(lo - 1) && x < power(min(lo + RANGE, kFar)));
+}
 template <class C>
-__device__ __forceinline__ void raise_exponent(Rows<C>& st, int e) {
-    const float f = ldexpf(1.0f, st.e - e);
+__device__ __forceinline__ void set_unit(Rows<C>& st, int e) {
+    if (st.e != kNoUnit) {
+        const float f = ldexpf(1.0f, st.e - e);
 #pragma unroll
-    for (int rt = 0; rt < C::RT; ++rt)
+        for (int rt = 0; rt < C::RT; ++rt)
 #pragma unroll
-        for (int j = 0; j < C::DT; ++j) st.o[rt][j] *= f;
+            for (int j = 0; j < C::DT; ++j) st.o[rt][j] *= f;
+    }
     st.e = e;
 }
-// The least exponent, at least `least`, that covers the wave's finite scales.
-__device__ __forceinline__ int exponent_of(const float (&vs)[8], int least) {
-    float big = 0.0f;
-#pragma unroll
-    for (int t = 0; t < 8; ++t) big = fmaxf(big, fabsf(vs[t]) < __builtin_inff() ? fabsf(vs[t]) : 0.0f);
-    big = max_wave(big);
-    return __builtin_amdgcn_readfirstlane(max(static_cast<int>(__float_as_uint(big) >> 23) - 126, least));
+__device__ __forceinline__ uint32_t max_u16(uint32_t a, uint32_t b) {   // of both halves
+    typedef uint16_t ushort2v __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2v, a), __builtin_bit_cast(ushort2v, b)));
 }
-
-// Makes the exponent of the value scales in o cover |vs| < 2^e and returns
-// 2^(shift - e), the factor that the scales are taken with.
+// Over the lanes that hold a wave's value scales (one group: 16 have the same).
 template <class C>
-__device__ __forceinline__ float cover_scales(Rows<C>& st, const float (&vs)[8], int shift) {
-    float big = fabsf(vs[0]);
+__device__ __forceinline__ float max_scales(float v) {
+    return C::NG == 1 ? max_groups(v) : max_wave(v);
+}
+// The exponents of the wave's scales, but for those that are 0, or not within
+// 2^kFar (some: there are such).  hi < lo: there are no others.
+template <class C>
+__device__ __forceinline__ void exponents_of(const float (&vs)[8], int& lo, int& hi, bool& some) {
+    // the smallest as an integer, less 1: a zero is the largest then
+    float big = 0.0f;
+    uint32_t small = ~0u;
 #pragma unroll
-    for (int t = 1; t < 8; ++t) big = fmaxf(big, fabsf(vs[t]));
-    if (__any(big > __uint_as_float(static_cast<uint32_t>(127 + st.e) << 23))) raise_exponent<C>(st, exponent_of(vs, st.e));
-    return ldexpf(1.0f, shift - st.e);
+    for (int t = 0; t < 8; ++t) {
+        big = __builtin_elementwise_maximum(big, fabsf(vs[t]));   // (keeps a NaN)
+        small = min(small, __float_as_uint(fabsf(vs[t])) - 1u);
+    }
+    some = __any(!(big < 0x1p32f) || small < 0x2F000000u - 1u);   // 2^-33
+    if (some) {
+        HR_BRANCH();
+        big = 0.0f, small = ~0u;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const float x = fabsf(vs[t]);
+            const bool in = x >= 0x1p-33f && x < 0x1p32f;
+            big = fmaxf(big, in ? x : 0.0f);
+            small = min(small, in ? __float_as_uint(x) - 1u : ~0u);
+        }
+    }
+    // both in one word: the exponent fields, of the smallest 255 less it
+    uint32_t both = __float_as_uint(big) >> 23 << 16 | (small == ~0u ? 0u : 255u - ((small + 1u) >> 23));
+    if constexpr (C::NG > 1) {
+        both = max_u16(both, swizzle_xor<1>(both));
+        both = max_u16(both, swizzle_xor<2>(both));
+        both = max_u16(both, swizzle_xor<4>(both));
+        both = max_u16(both, swizzle_xor<8>(both));
+    }
+    const auto most = [](float x, float y) { return __uint_as_float(max_u16(__float_as_uint(x), __float_as_uint(y))); };
+    both = __builtin_amdgcn_readfirstlane(__float_as_uint(over_halves(over_rows(__uint_as_float(both), most), most)));
+    hi = static_cast<int>(both >> 16) - 126;
+    lo = 129 - static_cast<int>(both & 0xFFFFu);
+}
+// The keys of 32, key 16 (t / 4) + 4 g + t % 4 in element t of lane group g, of
+// which some lane says that they are out.
+__device__ __forceinline__ uint32_t keys_of(const bool (&out)[8]) {
+    uint32_t keys = 0;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+        const uint64_t who = __ballot(out[t]);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            if (who >> (16 * g) & 0xFFFFu) keys |= 1u << (16 * (t / 4) + 4 * g + t % 4);
+    }
+    return __builtin_amdgcn_readfirstlane(keys);
+}
+// The value scales of a few-row step, and those of keys past the last that is
+// seen, or on an absent page, whatever they are, as `none`.
+template <class C, class W>
+__device__ __forceinline__ void step_scales(const W& w, float (&vs)[8]) {
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+        if constexpr (C::NG == 1) vs[t] = scale_at<C::SF32>(w.vs[t / 4], t & 3);
+        else vs[t] = __uint_as_float(C::SF32 ? w.vs[t][0] : w.vs[t][0] << 16);
+    }
+}
+__device__ __forceinline__ void drop_unseen(const CacheAttnArgs& a, const Pages& pages, int t0, int end, float none, float (&vs)[8]) {
+    const int g = (threadIdx.x & 63) >> 4;
+    const bool here[2] = {present(a, pages.p[0]), present(a, pages.p[1])};
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+        const int key = t0 + 16 * (t / 4) + 4 * g + t % 4;
+        vs[t] = key < end && here[t / 4] ? vs[t] : none;
+    }
+}
+// The keys that such a step sets aside, and the exponents lo to hi of the others.
+template <class C>
+__device__ __forceinline__ uint32_t aside_of(const float (&vs)[8], int& lo, int& hi) {
+    bool some, out[8];
+    exponents_of<C>(vs, lo, hi, some);
+    if (hi < lo) lo = hi = 0;
+    if (!some && hi - lo <= C::VRANGE) return 0;
+    hi = min(hi, lo + C::VRANGE);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) out[t] = set_aside<C::VRANGE>(vs[t], lo);
+    return keys_of(out);
 }
 
 // One step over 32 keys; mask: some of them are not seen by every row; units: of
-// the wave's rows.
-template <class C>
-__device__ __forceinline__ void step(const CacheAttnArgs& a, const Raw<C>& w, const Pages& pages, bool mask, const int* units, int t0,
-                                     Rows<C>& st) {
+// the wave's rows.  MOVES: the unit of the value scales is the step's own, and flag
+// is set if keys are set aside.
+template <class C, bool MOVES>
+__device__ __forceinline__ void step(const CacheAttnArgs& a, const Raw<C>& w, const Pages& pages, bool mask, int end, int* flag,
+                                     const int* units, int t0, Rows<C>& st) {
     constexpr int NG = C::NG, RT = C::RT;
     const int lane = threadIdx.x & 63, g = lane >> 4;
     const Zeros zs = zeros_of(a);
@@ -861,54 +994,49 @@ __device__ __forceinline__ void step(const CacheAttnArgs& a, const Raw<C>& w, co
             for (int t = 0; t < 8; ++t) x[rt][t] = ldexpf(x[rt][t], unit);
         }
     }
+    // value scales in their unit (several groups: they go into the operand that
+    // all 16 queries share)
     float vs[8];
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-        if constexpr (NG == 1) vs[t] = scale_at<C::SF32>(w.vs[t / 4], t & 3);
-        else vs[t] = __uint_as_float(C::SF32 ? w.vs[t][0] : w.vs[t][0] << 16);
-    }
+    step_scales<C>(w, vs);
     if (mask) {
-        // unseen scores become -inf, whatever they are; the scales of keys
-        // that no row may see (past the sequence or on an absent page) are
-        // not looked at
+        // unseen scores become -inf, whatever they are
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
             const int key = t0 + 16 * (t / 4) + 4 * g + t % 4;
-            bool any = false;
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 const bool seen = present(a, pages.p[t / 4]) && key < st.lim[rt] && key >= st.lo[rt];
-                any |= seen;
                 x[rt][t] = seen ? x[rt][t] * mul[t] : -__builtin_inff();
             }
             mul[t] = 1.0f;
-            // (several groups: the scale goes into the operand that all 16
-            // queries share, so it must be dropped only if none sees the key)
-            if constexpr (NG > 1) any = (__ballot(any) >> (16 * g)) & 0xFFFFu;
-            if (!any) vs[t] = 0.0f;
+        }
+        if constexpr (!MOVES) drop_unseen(a, pages, t0, end, ldexpf(1.0f, st.e - 1), vs);   // (one in the unit)
+    }
+    if constexpr (MOVES) {
+        int lo, hi;
+        drop_unseen(a, pages, t0, end, 0.0f, vs);
+        const uint32_t aside = aside_of<C>(vs, lo, hi);
+        if (!(hi <= st.e && lo >= st.e - C::VRANGE)) set_unit<C>(st, unit_for<C::VRANGE>(lo, hi));
+        if (aside) {
+            HR_BRANCH();
+            *flag = 1;
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+                if (aside >> (16 * (t / 4) + 4 * g + t % 4) & 1) {
+                    vs[t] = 0.0f;
+                    mul[t] = 1.0f;
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) x[rt][t] = -__builtin_inff();
+                }
         }
     }
-    const float down = cover_scales<C>(st, vs, NG == 1 ? kPExp : kSExp);
-    bool odd = false;
+    const float down = ldexpf(1.0f, C::VEXP - st.e);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
         vs[t] *= down;
-        odd |= !(fabsf(vs[t]) < __builtin_inff());
-    }
-    if (__any(odd)) {
-        // a value scale that is not finite must reach the queries that see its
-        // key and no others: it leaves the step, and their scores become NaN
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            const bool bad = !(fabsf(vs[t]) < __builtin_inff());
-            if (bad) vs[t] = 0.0f;
-            if ((__ballot(bad) >> (16 * g)) & 0xFFFFu) {
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const int key = t0 + 16 * (t / 4) + 4 * g + t % 4;
-                    if (key < st.lim[rt] && key >= st.lo[rt]) x[rt][t] = __builtin_nanf("");
-                }
-            }
+        if constexpr (!MOVES) {
+            st.big = __builtin_elementwise_maximum(st.big, fabsf(vs[t]));   // (keeps a NaN)
+            st.small = fminf(st.small, fabsf(vs[t]));
         }
     }
     uint4v ph[RT], pl[RT];
@@ -959,7 +1087,18 @@ struct Walk {
         next = pages_at(a, table, t + S);
         load_keys<C>(a, now, h, t, w);
     }
-    __device__ __forceinline__ void run(const CacheAttnArgs& a, const Span& sp, const int* units, Rows<C>& st) {
+    // A unit that the first step's scales are in, with room above and below.
+    __device__ __forceinline__ int first_unit(const CacheAttnArgs& a) const {
+        float vs[8], big = 0.0f;
+        step_scales<C>(w, vs);
+        drop_unseen(a, now, t, end, 0.0f, vs);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(vs[i]));
+        const int hi = __builtin_amdgcn_readfirstlane(exponent(max_scales<C>(big)));
+        return min(max((hi < -kFar ? 0 : hi) + C::VRANGE / 3, C::VRANGE - kFar), kFar);
+    }
+    template <bool MOVES>
+    __device__ __forceinline__ void run(const CacheAttnArgs& a, const Span& sp, int* flag, const int* units, Rows<C>& st) {
         if (t >= end) return;
         while (true) {
             Raw<C> n;
@@ -967,7 +1106,7 @@ struct Walk {
             if (more) load_keys<C>(a, next, h, t + S, n);
             const Pages after = pages_at(a, table, t + 2 * S);
             const bool all = t >= sp.flo && t + 32 <= sp.fhi && present(a, now.p[0]) && present(a, now.p[1]);
-            step<C>(a, w, now, !all, units, t, st);
+            step<C, MOVES>(a, w, now, !all, end, flag, units, t, st);
             if (!more) return;
             t += S;
             w = n;
@@ -1051,25 +1190,33 @@ __device__ __forceinline__ void settle(Rows<C>& st) {
 }
 
 // Joins the four waves that took different keys of the same rows and writes
-// the rows, or their part to the scratch: maxima first, then every wave's sums
-// through LDS in a few rows at a time, 16 threads to a row.
+// the rows, or their part to the scratch (to `spare` for rows that are finished
+// here but for keys set aside; returns whether there are such): maxima first,
+// then every wave's sums through LDS in a few rows at a time, 16 threads to a row.
 template <class C>
 constexpr int join_floats() {
     return 2 * 4 * 16 + 4 * 16 * (C::D + 4);
 }
 template <class C, class T>
-__device__ __forceinline__ void join_waves(const CacheAttnArgs& a, const Seq& s, int h, int r0, Rows<C>& st, float* part,
-                                           float* lds) {
+__device__ __forceinline__ bool join_waves(const CacheAttnArgs& a, const Seq& s, int h, int r0, Rows<C>& st, float* part,
+                                           float* spare, const int* flag, float* lds) {
     static_assert(C::WT == 4 && C::WR == 1, "four waves along the keys");
     constexpr int D = C::D, LD = D + 4;                    // (rows 16 bytes apart in the banks)
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, n = lane & 15, g = lane >> 4;
     float* ml = lds;                                       // [2][4][16]: maxima, sums
     float* so = lds + 128;                                 // [4][16][LD]
+    bool aside = false;
 #pragma unroll
     for (int rt = 0; rt < C::RT; ++rt) {
         const int rows = min(s.n * a.rep - r0 - 16 * rt, 16);
         if (rows <= 0) break;
         __syncthreads();
+        if (rt == 0) {
+            // (every wave has set it that will, and the next segment's may be
+            // set only after the barrier below)
+            aside = __builtin_amdgcn_readfirstlane(*flag) != 0;
+            if (aside && !part) part = spare;
+        }
         if (g == 0) {
             ml[wave * 16 + n] = st.mc[rt];
             ml[64 + wave * 16 + n] = st.l[rt];
@@ -1118,6 +1265,7 @@ __device__ __forceinline__ void join_waves(const CacheAttnArgs& a, const Seq& s,
             }
         }
     }
+    return aside;
 }
 
 // ---------------------------------------------------------------------------
@@ -1158,17 +1306,26 @@ struct Tile {
 template <class C>
 struct Passes {
     Tile<C> tile[2][C::TILES];
-    int keys[2][4];             // of a tile's keys: bit s: subtile s is on an absent page;
-                                // 2^kShiftBits x shift: they are times 2^-shift (extreme scales)
-    uint32_t odd[2][4];         // keys whose value scale is not finite
-    int e[2][C::TILES];         // exponent that covers a tile's value scales
+    // of a tile: keys (bit s: subtile s is on an absent page; 2^kShiftBits x shift:
+    // they are times 2^-shift, extreme scales), keys that are set aside for their own
+    // scales, and for their values', -
+    uint4v note[2][C::TILES];
+    uint2v range[2][C::TILES];  // exponents lo, hi of a tile's value scales
+    Todo todo;
     float top[C::WR];
     int unit[C::WR][16 * C::RT];   // exponents of the rows' units (bfloat16 activations)
 };
 template <class C>
 constexpr int lds_floats() {
     if constexpr (C::SHARED) return static_cast<int>(sizeof(Passes<C>)) / 4;
-    else return join_floats<C>() + 4 * 16 * C::RT;   // (and the units of each wave's rows)
+    // (and the units of each wave's rows, and a Todo)
+    else return join_floats<C>() + 4 * 16 * C::RT + 4 + static_cast<int>(sizeof(Todo)) / 4;
+}
+
+template <class C>
+__device__ __forceinline__ Todo* todo_at(float* lds) {
+    if constexpr (C::SHARED) return &reinterpret_cast<Passes<C>*>(lds)->todo;
+    else return reinterpret_cast<Todo*>(lds + join_floats<C>() + 4 * 16 * C::RT);
 }
 
 // Codes and scales of a tile's keys: key m in the lane.
@@ -1219,35 +1376,72 @@ __device__ __forceinline__ void load_raw(const CacheAttnArgs& a, const Pages& pa
         load_values<C>(a, head_buffer(a, pages.p[s], h), (t0 + 16 * s) & (a.pg.page - 1), s, w);
 }
 
+// The scales of a tile's keys (times c), and the power of two that they are
+// divided by.  c - z is at most 15: scales of 2^-13 .. 2^12 keep within float16, and
+// a tile of others is moved there.  Larger keys among small ones are set aside,
+// and their scales become 0.
+template <class C>
+__device__ __forceinline__ int key_unit(const RawK<C>& w, int t0, int end, float c, float (&ks)[2][C::NG], uint32_t& aside) {
+    constexpr int NG = C::NG;
+    const int m = threadIdx.x & 15;
+    float top[2];                            // the key's largest
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        top[s] = 0.0f;
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) {
+            ks[s][gi] = t0 + 16 * s + m < end ? scale_at<C::SF32>(w.ks[s], gi) * c : 0.0f;
+            top[s] = __builtin_elementwise_maximum(top[s], fabsf(ks[s][gi]));   // (keeps a NaN)
+        }
+    }
+    aside = 0;
+    const float most = __builtin_elementwise_maximum(top[0], top[1]);
+    if (!__any(!(most <= 4096.0f)) && __any(most >= 0x1p-13f)) return 0;
+    HR_BRANCH();
+    float big = 0.0f, small = __builtin_inff();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        if (top[s] < __builtin_inff()) big = fmaxf(big, top[s]);
+        if (top[s] > 0.0f) small = fminf(small, top[s]);
+    }
+    big = max_wave(big);
+    small = -max_wave(-small);
+    int e = 0;
+    if (big > 4096.0f) e = max(min(exponent(big), exponent(small) + C::KRANGE) - 12, 0);
+    else if (big > 0.0f && big < 0x1p-13f) e = exponent(big);
+    e = __builtin_amdgcn_readfirstlane(e);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const bool out = !(top[s] <= 4096.0f) && !(e + 12 < 128 && top[s] < power(e + 12));
+        aside |= static_cast<uint32_t>(__ballot(out) & 0xFFFFu) << (16 * s);   // (a key's four lanes agree)
+        if (out) {
+#pragma unroll
+            for (int gi = 0; gi < NG; ++gi) ks[s][gi] = 0.0f;
+        }
+    }
+    return e;
+}
+
 // Makes the key operands of a tile.  (c: log2 units of a product with the
 // queries as they are held.)
 template <class C>
 __device__ __forceinline__ void make_keys(const CacheAttnArgs& a, const RawK<C>& w, const Pages& pages, int t0, int end, float c,
-                                          Tile<C>& tile, int* special) {
+                                          Tile<C>& tile, uint32_t* note, int* flag) {
     constexpr int NG = C::NG;
-    const int lane = threadIdx.x & 63, m = lane & 15;
+    const int lane = threadIdx.x & 63;
     const Zeros zs = zeros_of(a);
-    float ks[2][NG], big = 0.0f;
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int gi = 0; gi < NG; ++gi) {
-            ks[s][gi] = t0 + 16 * s + m < end ? scale_at<C::SF32>(w.ks[s], gi) * c : 0.0f;
-            big = fmaxf(big, fabsf(ks[s][gi]) < __builtin_inff() ? fabsf(ks[s][gi]) : 0.0f);
-        }
-    // c - z is at most 15: scales of 2^-13 .. 2^12 keep within float16, and
-    // others are moved there
-    big = max_wave(big);
-    int e = 0;
-    if (big > 4096.0f || (big < 0x1p-13f && big > 0.0f)) e = static_cast<int>(__float_as_uint(big) >> 23) - 126;
-    e = __builtin_amdgcn_readfirstlane(e);
+    float ks[2][NG];
+    uint32_t aside;
+    const int e = key_unit<C>(w, t0, end, c, ks, aside);
+    if (aside) *flag = 1;
     if (e != 0) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int gi = 0; gi < NG; ++gi) ks[s][gi] = ldexpf(ks[s][gi], -e);
     }
-    if (lane == 0) *special = (present(a, pages.p[0]) ? 0 : 1) | (present(a, pages.p[1]) ? 0 : 2) | e * (1 << kShiftBits);
+    const int special = (present(a, pages.p[0]) ? 0 : 1) | (present(a, pages.p[1]) ? 0 : 2) | e * (1 << kShiftBits);
+    if (lane == 0) *reinterpret_cast<uint2v*>(note) = uint2v{static_cast<uint32_t>(special), aside};
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -1292,31 +1486,27 @@ __device__ __forceinline__ void value_scales(const CacheAttnArgs& a, const RawV<
     }
 }
 
-// Makes the value operands of a tile, times 2^(kSExp - e).
+// Makes the value operands of a tile, times 2^(kSExp - e).  check: some scales may
+// not be in the unit, which begins at exponent lo.
 template <class C>
 __device__ __forceinline__ void make_values(const CacheAttnArgs& a, const RawV<C>& w, const Pages& pages, int t0, int end, int e,
-                                            Tile<C>& tile, uint32_t* odd) {
+                                            bool check, int lo, Tile<C>& tile, uint32_t* set_aside_at, int* flag) {
     const int lane = threadIdx.x & 63;
     float vs[8];
     value_scales<C>(a, w, pages, t0, end, vs);
-    // a value scale that is not finite must reach the queries that see its key
-    // and no others: it leaves the tile, and the key is marked
-    bool any = false;
-#pragma unroll
-    for (int t = 0; t < 8; ++t) any |= !(fabsf(vs[t]) < __builtin_inff());
-    uint32_t marks = 0;
-    if (__any(any)) {
+    uint32_t aside = 0;
+    if (check) {
+        HR_BRANCH();
+        bool out[8];
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            const bool mine = !(fabsf(vs[t]) < __builtin_inff());
-            if (mine) vs[t] = 0.0f;
-            const uint64_t who = __ballot(mine);
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-                if ((who >> (16 * y)) & 0xFFFFu) marks |= 1u << (16 * (t / 4) + 4 * y + t % 4);
+            out[t] = set_aside<C::VRANGE>(vs[t], lo);
+            if (out[t]) vs[t] = 0.0f;
         }
+        aside = keys_of(out);
+        if (aside) *flag = 1;
     }
-    if (lane == 0) *odd = marks;
+    if (lane == 0) *set_aside_at = aside;
     const float down = ldexpf(1.0f, kSExp - e);
 #pragma unroll
     for (int t = 0; t < 8; ++t) vs[t] *= down;
@@ -1407,11 +1597,11 @@ __device__ __forceinline__ bool move_maximum(float4v (&x)[C::RT][2], Rows<C>& st
     return __any(left);
 }
 
-// One step over a tile.  special: what the makers noted of it, odd: keys with
-// bad value scales; units: of the wave's rows; unset: some row has not seen a
+// One step over a tile.  special: what the makers noted of it, aside: keys that
+// are left out; units: of the wave's rows; unset: some row has not seen a
 // key yet.
 template <class C>
-__device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint32_t odd, const int* units, int t0, const Span& sp,
+__device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint32_t aside, const int* units, int t0, const Span& sp,
                                           Rows<C>& st, bool& unset) {
     constexpr int RT = C::RT, GROUP = Fetch<C>::GROUP;
     const int lane = threadIdx.x & 63, g = lane >> 4;
@@ -1458,7 +1648,7 @@ __device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) st.from[rt] = float4v{st.start[rt], st.start[rt], st.start[rt], st.start[rt]};
     }
-    const bool all = t0 >= sp.flo && t0 + 32 <= sp.fhi && (special & 3) == 0 && odd == 0;
+    const bool all = t0 >= sp.flo && t0 + 32 <= sp.fhi && (special & 3) == 0 && aside == 0;
     float p[RT][8], top = 0.0f;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
@@ -1479,8 +1669,7 @@ __device__ __forceinline__ void tile_step(const Tile<C>& tile, int special, uint
                 const int at = 16 * (k / 4) + 4 * g + k % 4, key = t0 + at;
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    const bool seen = !(special >> (k / 4) & 1) && key < st.lim[rt] && key >= st.lo[rt];
-                    if (odd >> at & 1) acc[rt][k / 4][k % 4] = __builtin_nanf("");
+                    const bool seen = !(special >> (k / 4) & 1) && !(aside >> at & 1) && key < st.lim[rt] && key >= st.lo[rt];
                     if (!seen) acc[rt][k / 4][k % 4] = -__builtin_inff();
                 }
             }
@@ -1542,7 +1731,7 @@ __device__ __forceinline__ uint4v exponentials(const float4v (&acc)[2]) {
     return ph;
 }
 template <class C>
-__device__ __forceinline__ void pair_step(const Tile<C>& tile, int special, uint32_t odd, const int* units, int t0, const Span& sp,
+__device__ __forceinline__ void pair_step(const Tile<C>& tile, int special, uint32_t aside, const int* units, int t0, const Span& sp,
                                           Rows<C>& st, bool& unset) {
     constexpr int N = C::DT;   // operands of keys, and of values
     const int lane = threadIdx.x & 63, g = lane >> 4;
@@ -1574,7 +1763,7 @@ __device__ __forceinline__ void pair_step(const Tile<C>& tile, int special, uint
         HR_GROUP(kMatrix, 1);
         HR_GROUP(kLdsRead, 1);
     }
-    const bool all = t0 >= sp.flo && t0 + 32 <= sp.fhi && (special | odd) == 0;
+    const bool all = t0 >= sp.flo && t0 + 32 <= sp.fhi && (special | aside) == 0;
     if (!all || unset || __any(top > static_cast<float>(kPExp + kSlack))) {
         HR_BRANCH();
         raw_scores<C>(tile, special, units, st, acc);
@@ -1587,8 +1776,7 @@ __device__ __forceinline__ void pair_step(const Tile<C>& tile, int special, uint
 #pragma unroll
                 for (int rt = 0; rt < 2; ++rt) {
                     float& x = reinterpret_cast<float*>(&acc[rt][i / 4])[i % 4];
-                    if (odd >> at & 1) x = __builtin_nanf("");
-                    if ((special >> (i / 4) & 1) || key >= st.lim[rt] || key < st.lo[rt]) x = -__builtin_inff();
+                    if ((special >> (i / 4) & 1) || (aside >> at & 1) || key >= st.lim[rt] || key < st.lo[rt]) x = -__builtin_inff();
                 }
             }
         }
@@ -1609,6 +1797,26 @@ __device__ __forceinline__ void pair_step(const Tile<C>& tile, int special, uint
     for (int i = 0; i < N; ++i) st.o[1][i] = mfma(v[i], p1, st.o[1][i]);
     HR_PHASE();
 }
+
+// The exponents of a pass's value scales: those of its tiles, if they fit one
+// unit, else those from the largest of the tiles' smallest on (one odd key in a
+// tile, large or small, is then the one that is set aside).
+template <class C>
+struct PassScales {
+    int lo = 1000, hi = -1000, vote = -1000;
+    __device__ __forceinline__ void add(int l, int h) {
+        lo = min(lo, l);
+        hi = max(hi, h);
+        if (h >= l) vote = max(vote, l);
+    }
+    __device__ __forceinline__ void settle() {
+        if (hi < lo) lo = hi = 0;
+        if (hi - lo > C::VRANGE) {
+            lo = vote;
+            hi = min(hi, lo + C::VRANGE);
+        }
+    }
+};
 
 // What a wave makes for the passes, besides computing: keys or values of tile
 // `tile`, or nothing.  (Each is a loop of its own, so that a wave holds only
@@ -1631,23 +1839,37 @@ __device__ __forceinline__ void passes(const CacheAttnArgs& a, const int32_t* ta
         load_raw<C>(a, now, h, t + mine, w);
         next = pages_at(a, table, min(t + S + mine, max(end - 1, 0) & ~15));
     };
-    const auto announce = [&](int t, int buf) {   // the value scales' exponent of the loaded tile
+    int own_lo = 0, own_hi = 0;         // of the tile that was announced last
+    bool some = false;
+    const auto announce = [&](int t, int buf) {   // the value scales' exponents of the loaded tile
         if constexpr (ROLE == kMakeValues) {
             float vs[8];
             value_scales<C>(a, w, now, t + mine, end, vs);
-            const int e = exponent_of(vs, -100);
-            if (lane == 0) ps.e[buf][tile] = e;
+            exponents_of<C>(vs, own_lo, own_hi, some);
+            if (lane == 0) ps.range[buf][tile] = uint2v{static_cast<uint32_t>(own_lo), static_cast<uint32_t>(own_hi)};
         }
     };
     const int* units = ps.unit[threadIdx.x >> 6];
-    int made = -100;                    // the exponent of the pass made last
+    int made = kNoUnit;                 // the unit of the pass made last
     const auto make = [&](int t, int buf) {
+        PassScales<C> sc;
 #pragma unroll
-        for (int i = 0; i < N; ++i) made = max(made, __builtin_amdgcn_readfirstlane(ps.e[buf][i]));
+        for (int i = 0; i < N; ++i) {
+            const uint2v r = ps.range[buf][i];
+            sc.add(__builtin_amdgcn_readfirstlane(static_cast<int>(r.x)), __builtin_amdgcn_readfirstlane(static_cast<int>(r.y)));
+        }
+        if (!(sc.hi <= made && sc.lo >= made - C::VRANGE)) {
+            HR_BRANCH();
+            sc.settle();
+            if (!(sc.hi <= made && sc.lo >= made - C::VRANGE)) made = unit_for<C::VRANGE>(sc.lo, sc.hi);
+        }
+        [[maybe_unused]] uint32_t* note = reinterpret_cast<uint32_t*>(&ps.note[buf][tile]);
         if constexpr (ROLE == kMakeKeys) {
-            if (t + mine < end) make_keys<C>(a, w, now, t + mine, end, st.c, ps.tile[buf][tile], &ps.keys[buf][tile]);
+            if (t + mine < end) make_keys<C>(a, w, now, t + mine, end, st.c, ps.tile[buf][tile], note, &ps.todo.aside);
         } else if constexpr (ROLE == kMakeValues) {
-            if (t + mine < end) make_values<C>(a, w, now, t + mine, end, made, ps.tile[buf][tile], &ps.odd[buf][tile]);
+            const bool check = some || own_hi > sc.hi || own_lo < sc.lo;
+            if (t + mine < end)
+                make_values<C>(a, w, now, t + mine, end, made, check, sc.lo, ps.tile[buf][tile], note + 2, &ps.todo.aside);
         }
     };
     load(begin);
@@ -1660,20 +1882,21 @@ __device__ __forceinline__ void passes(const CacheAttnArgs& a, const int32_t* ta
     bool unset = true;
     int buf = 0;
     for (int t = begin; t < end; t += S, buf ^= 1) {
-        const int e = made;             // of this pass; make() may raise it for the next
+        const int e = made;             // of this pass; make() may move it for the next
         if constexpr (ROLE != kMakeKeys) {
             make(t + S, buf ^ 1);
             load(t + 2 * S);
         }
-        if (e > st.e) raise_exponent<C>(st, e);
+        if (e != st.e) set_unit<C>(st, e);
         // (tiles that no row of the wave sees are left out)
         const int first = max(sp.lo - t, 0) >> 5, stop = (min(min(end, sp.hi) - t, S) + 31) >> 5;
 #pragma unroll 1
         for (int i = first; i < stop; ++i) {
-            const int special = __builtin_amdgcn_readfirstlane(ps.keys[buf][i]) | st.own, t0 = t + 32 * i;
-            const uint32_t odd = __builtin_amdgcn_readfirstlane(ps.odd[buf][i]);
-            if constexpr (C::RT == 2) pair_step<C>(ps.tile[buf][i], special, odd, units, t0, sp, st, unset);
-            else tile_step<C>(ps.tile[buf][i], special, odd, units, t0, sp, st, unset);
+            const uint4v note = ps.note[buf][i];
+            const int special = __builtin_amdgcn_readfirstlane(static_cast<int>(note.x)) | st.own, t0 = t + 32 * i;
+            const uint32_t aside = __builtin_amdgcn_readfirstlane(note.y | note.z);
+            if constexpr (C::RT == 2) pair_step<C>(ps.tile[buf][i], special, aside, units, t0, sp, st, unset);
+            else tile_step<C>(ps.tile[buf][i], special, aside, units, t0, sp, st, unset);
         }
         if constexpr (ROLE == kMakeKeys) {
             make(t + S, buf ^ 1);
@@ -1686,11 +1909,164 @@ __device__ __forceinline__ void passes(const CacheAttnArgs& a, const int32_t* ta
     }
 }
 
+// One key that was set aside, at base + ... of its page, for one row (the wave's;
+// the same in all lanes): its score from its own elements s (c - z), one step of
+// the softmax on the row's part, p s (c - z) added.  A lane has D / 64 dimensions.
+template <class C, class T>
+__device__ __forceinline__ void aside_row(const CacheAttnArgs& a, const Seq& s, int h, int row, const uint8_t* base, int off, int key,
+                                          float* p) {
+    constexpr int D = C::D, NG = C::NG, E = D / 64;
+    const int lane = threadIdx.x & 63;
+    const int tok = row / a.rep, hh = row - tok * a.rep, pos = s.len - s.n + tok;
+    if (a.causal && (key > pos || (a.window && key <= pos - a.window))) return;
+    const T* from = static_cast<const T*>(a.q) + static_cast<int64_t>(s.start + tok) * a.q_st +
+                    static_cast<int64_t>(h * a.rep + hh) * a.q_sh + lane * E;
+    float q[E], k[E], v[E], sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        if constexpr (sizeof(T) == 2) q[i] = __uint_as_float(static_cast<uint32_t>(from[i]) << 16);
+        else q[i] = from[i];
+    }
+    if (a.rotate) {
+#pragma unroll
+        for (int x = 1; x < E; x *= 2)
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (!(i & x)) {
+                    const float u = q[i], w = q[i + x];
+                    q[i] = u + w;
+                    q[i + x] = u - w;
+                }
+        for (int x = 1; x < 64; x *= 2)
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float o = __shfl_xor(q[i], x);
+                q[i] = lane & x ? o - q[i] : o + q[i];
+            }
+#pragma unroll
+        for (int i = 0; i < E; ++i) q[i] *= a.norm;
+    }
+    const auto elements = [&](int codes, int scales, int zeros, float (&to)[E]) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int dim = lane * E + i, at = off * NG + dim / (D / NG);
+            uint32_t c = base[codes + off * (D / 2) + dim / 2] >> (4 * (dim & 1)) & 15u;
+            const uint32_t z = a.pg.sym ? 8u : base[zeros + at / 2] >> (4 * (at & 1)) & 15u;
+            if (a.pg.sym) c ^= 8u;
+            const float scale = C::SF32 ? reinterpret_cast<const float*>(base + scales)[at]
+                                        : __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(base + scales)[at]) << 16);
+            to[i] = scale * static_cast<float>(static_cast<int>(c) - static_cast<int>(z));
+        }
+    };
+    elements(a.pg.kc, a.pg.ks, a.pg.kz, k);
+    elements(a.pg.vc, a.pg.vs, a.pg.vz, v);
+#pragma unroll
+    for (int i = 0; i < E; ++i) sum = fmaf(q[i], k[i], sum);
+    for (int x = 1; x < 64; x *= 2) sum += __shfl_xor(sum, x);
+    float w = sum * (a.scale * kLog2e);
+    asm("" : "+v"(w));                     // (rounded, as the maximum is that it is compared with)
+    const float was = p[D];
+    const float mc = fmaxf(was, w), f = exp2f(was - mc), pr = exp2f(w - mc);
+    const float l = fmaf(p[D + 1], f, pr);
+#pragma unroll
+    for (int i = 0; i < E; ++i) p[lane * E + i] = fmaf(p[lane * E + i], f, pr * v[i]);
+    p[D] = mc;                             // (every lane its own copy of these two)
+    p[D + 1] = l;
+}
+
+// The keys of a segment that were set aside, for the rows' parts at `part`, a row
+// to a wave at a time; last: the rows are finished here.  A function of its own,
+// that is called: inlined, what it needs takes registers in the loops before it
+// (10% of a step's time, and where none are free many times that).
+typedef const CacheAttnArgs __attribute__((address_space(4)))* ConstArgs;
+template <class C, class T>
+__device__ __attribute__((noinline)) void sweep_rows(ConstArgs args, Todo* todo) {
+    const CacheAttnArgs& a = *(const CacheAttnArgs*)(args);
+    constexpr int WAVES = C::THREADS / 64, D = C::D, E = D / 64, TILES = C::SHARED ? C::TILES : 1;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int b = __builtin_amdgcn_readfirstlane(todo->b), h = __builtin_amdgcn_readfirstlane(todo->h);
+    const int r0 = __builtin_amdgcn_readfirstlane(todo->r0), k0 = todo->k0, k1 = todo->k1;
+    const float c = todo->c;
+    const bool last = todo->part == nullptr;
+    float* part = last ? todo->spare : todo->part;
+    const Seq s = seq_at<true>(a.sq, a.pg.logp, b);
+    const int rows = min(s.n * a.rep - r0, C::ROWS);
+    const Span sp = span_of(a, s, r0, r0 + rows);
+    const int32_t* table = a.sq.table + static_cast<int64_t>(b) * a.sq.max_pages;
+    const int begin = __builtin_amdgcn_readfirstlane(max(k0, sp.lo & ~31)), end = __builtin_amdgcn_readfirstlane(min(k1, sp.hi));
+    __threadfence_block();
+    __syncthreads();                       // (the parts were written by other waves)
+    for (int t = begin; t < end; t += 32 * TILES) {
+        PassScales<C> sc;
+        for (int turn = C::SHARED ? 0 : 1; turn < 2; ++turn) {   // with shared operands the pass's unit first
+            for (int t0 = t; t0 < min(t + 32 * TILES, end); t0 += 32) {
+                const Pages pages = pages_at(a, table, t0);
+                RawV<C> rv;
+                load_raw<C>(a, pages, h, t0, rv);
+                float vs[8];
+                uint32_t aside;
+                if constexpr (C::SHARED) {
+                    value_scales<C>(a, rv, pages, t0, end, vs);
+                    if (turn == 0) {
+                        int lo, hi;
+                        bool some;
+                        exponents_of<C>(vs, lo, hi, some);
+                        sc.add(lo, hi);
+                        continue;
+                    }
+                    bool out[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) out[x] = set_aside<C::VRANGE>(vs[x], sc.lo);
+                    RawK<C> rk;
+                    load_raw<C>(a, pages, h, t0, rk);
+                    float ks[2][C::NG];
+                    key_unit<C>(rk, t0, end, c, ks, aside);
+                    aside = __builtin_amdgcn_readfirstlane(aside) | keys_of(out);
+                } else {
+                    int lo, hi;
+                    step_scales<C>(rv, vs);
+                    drop_unseen(a, pages, t0, end, 0.0f, vs);
+                    aside = aside_of<C>(vs, lo, hi);
+                }
+                while (aside) {
+                    const int i = __builtin_ctz(aside), key = t0 + i, page = i < 16 ? pages.p[0] : pages.p[1];
+                    aside &= aside - 1;
+                    if (key >= end || !present(a, page)) continue;
+                    const uint8_t* base = a.pool + page * a.pg.page_bytes + h * a.pg.head_bytes;
+                    for (int row = wave; row < rows; row += WAVES)
+                        aside_row<C, T>(a, s, h, r0 + row, base, key & (a.pg.page - 1), key, part + row * part_stride<C>());
+                }
+            }
+            if (turn == 0) sc.settle();
+        }
+    }
+    if (last) {
+        for (int row = wave; row < rows; row += WAVES) {
+            const float* p = part + row * part_stride<C>();
+            const int tok = (r0 + row) / a.rep;
+            const int64_t t = s.start + tok, head = h * a.rep + (r0 + row) - tok * a.rep;
+            const float l = p[D + 1], inv = l == 0.0f ? 0.0f : 1.0f / l;
+            T* to = static_cast<T*>(a.out) + t * a.o_st + head * a.o_sh + lane * E;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float x = p[lane * E + i] * inv;
+                if constexpr (sizeof(T) == 2) to[i] = static_cast<uint16_t>(to_bf16(x));
+                else to[i] = x;
+            }
+            if (a.lse && lane == 0) a.lse[t * a.hq + head] = log_sum(p[D], l);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) todo->aside = 0;
+    __syncthreads();
+}
+
 // Rows [r0, r0 + ROWS) of kv head h of a sequence over the keys [k0, k1);
-// part: where a partial result goes (else the rows are finished here).
+// part: where a partial result goes (else the rows are finished here); spare: for
+// one of a segment that sets keys aside.
 template <class C, class T>
 __device__ __forceinline__ void shared_segment(const CacheAttnArgs& a, const Seq& s, int b, int h, int r0, int k0, int k1,
-                                               float* part, float* lds) {
+                                               float* part, float* spare, float* lds) {
     constexpr int N = C::TILES;
     Passes<C>& ps = *reinterpret_cast<Passes<C>*>(lds);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1702,6 +2078,7 @@ __device__ __forceinline__ void shared_segment(const CacheAttnArgs& a, const Seq
     const int begin = max(k0, all.lo & ~31), end = min(k1, all.hi);
     Rows<C> st;
     load_rows<C, T>(a, s, h, row, st, ps.top, ps.unit[wave]);
+    if (threadIdx.x == 0) ps.todo.set(b, h, r0, k0, k1, st.c, part, spare);
     if (wave < N) passes<C, kMakeKeys>(a, table, h, wave, begin, end, sp, st, ps);
     else if (wave < 2 * N) passes<C, kMakeValues>(a, table, h, wave - N, begin, end, sp, st, ps);
     else passes<C, kMakeNothing>(a, table, h, 0, begin, end, sp, st, ps);
@@ -1714,16 +2091,23 @@ __device__ __forceinline__ void shared_segment(const CacheAttnArgs& a, const Seq
 #pragma unroll
             for (int r = 0; r < 4; ++r) st.o[rt][j][r] = ldexpf(st.o[rt][j][r], st.e - kPExp - kSExp);
     }
+    const bool aside = __builtin_amdgcn_readfirstlane(ps.todo.aside) != 0;
+    if (aside && !part) part = spare;
     put_rows<C, T>(a, s, h, row, st, part, row - r0);
+    if (aside) {
+        HR_BRANCH();
+        sweep_rows<C, T>((ConstArgs)(__builtin_amdgcn_kernarg_segment_ptr()), &ps.todo);
+    }
 }
 
 // Rows [r0, r0 + ROWS) of kv head h of a sequence over the keys [k0, k1);
-// part: where a partial result goes (else the rows are finished here).
+// part: where a partial result goes (else the rows are finished here); spare: for
+// one of a segment that sets keys aside.
 template <class C, class T>
 __device__ __forceinline__ void segment(const CacheAttnArgs& a, const Seq& s, int b, int h, int r0, int k0, int k1,
-                                        float* part, float* lds) {
+                                        float* part, float* spare, float* lds) {
     if constexpr (C::SHARED) {
-        shared_segment<C, T>(a, s, b, h, r0, k0, k1, part, lds);
+        shared_segment<C, T>(a, s, b, h, r0, k0, k1, part, spare, lds);
     } else {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const Span sp = span_of(a, s, r0, min(r0 + C::ROWS, s.n * a.rep));
@@ -1733,10 +2117,33 @@ __device__ __forceinline__ void segment(const CacheAttnArgs& a, const Seq& s, in
         keys.h = h;
         keys.start(a, sp, k0, k1, wave);
         int* units = reinterpret_cast<int*>(lds + join_floats<C>()) + wave * 16 * C::RT;
+        Todo* todo = todo_at<C>(lds);
+        if (threadIdx.x == 0) todo->set(b, h, r0, k0, k1, 0.0f, part, spare);
         load_rows<C, T>(a, s, h, r0, st, lds, units);
-        keys.run(a, sp, units, st);
+        if (keys.t < keys.end) {
+            st.e = keys.first_unit(a);
+            st.big = 0.0f;
+            st.small = 0x1p126f;
+            keys.template run<false>(a, sp, nullptr, units, st);
+            if (__any(!(st.big < power(C::VEXP) && st.small >= power(C::VEXP - C::VRANGE - 1)))) {
+                HR_BRANCH();
+                st.e = kNoUnit;
+#pragma unroll
+                for (int rt = 0; rt < C::RT; ++rt) {
+                    st.mc[rt] = kLow;
+                    st.l[rt] = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < C::DT; ++j) st.o[rt][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+                }
+                keys.start(a, sp, k0, k1, wave);
+                keys.template run<true>(a, sp, &todo->aside, units, st);
+            }
+        }
         settle<C>(st);
-        join_waves<C, T>(a, s, h, r0, st, part, lds);
+        if (join_waves<C, T>(a, s, h, r0, st, part, spare, &todo->aside, lds)) {
+            HR_BRANCH();
+            sweep_rows<C, T>((ConstArgs)(__builtin_amdgcn_kernarg_segment_ptr()), todo);
+        }
     }
 }
 
@@ -2059,6 +2466,7 @@ template <class C, class T>
 __global__ void __launch_bounds__(C::THREADS, C::WAVES) cache_attn_split(const CacheAttnArgs a) {
     __shared__ float4v lds4[lds_floats<C>() / 4 + 1];
     float* lds = reinterpret_cast<float*>(lds4);
+    if (threadIdx.x == 0) todo_at<C>(lds)->aside = 0;
     const Place p = place<C>(a, reinterpret_cast<int64_t*>(lds));
     int64_t i0 = p.i0;
     const int64_t i1 = p.i1;
@@ -2080,10 +2488,13 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) cache_attn_split(const C
                 const int k = p.whole ? 0 : max(from - kSetup, 0), end = p.whole ? rb.blocks : to - kSetup;
                 if (end > k) {           // (else only items of the unit's start)
                     const int r0 = static_cast<int>(i * C::ROWS);
+                    // (a unit that ends here leaves the second slot free, which a
+                    // unit that goes on takes after it)
                     float* part = nullptr;
-                    if (k > 0 || end < rb.blocks) part = a.work + (2 * static_cast<int64_t>(blockIdx.x) + (k == 0 ? 1 : 0)) * SLOT;
+                    float* spare = a.work + (2 * static_cast<int64_t>(blockIdx.x) + 1) * SLOT;
+                    if (k > 0 || end < rb.blocks) part = spare - (k == 0 ? 0 : SLOT);
                     if (k == 0 && end < rb.blocks) cut = {s.start, s.n, h, r0, static_cast<int>(p.sh.holder(unit + size - 1))};
-                    segment<C, T>(a, s, b, h, r0, rb.first + k * C::KEYS, rb.first + end * C::KEYS, part, lds);
+                    segment<C, T>(a, s, b, h, r0, rb.first + k * C::KEYS, rb.first + end * C::KEYS, part, spare, lds);
                 }
                 i0 = unit + to;
                 unit += size;

@@ -108,7 +108,8 @@ int hr_cache_append(void* pool, int64_t n_pages, const hr_cache_spec* spec, cons
  *   window  0: no limit; w > 0 (causal only): the last w of those positions.
  * Positions of absent pages are not seen.  What a token does not see has no
  * influence, whatever its bytes are.  A token that sees nothing gets zeros
- * (and a log-sum-exp of -inf).
+ * (and a log-sum-exp of -inf).  Keys whose scales are far from their
+ * neighbours', by 2^10 and more, may be taken one at a time, which is slower.
  *   q, out  device, element (t, h, i) at t * stride_token + h * stride_head
  *           + i; 16-byte aligned rows; `dtype` HR_F32 or HR_BF16.  out may be
  *           q with the same strides.

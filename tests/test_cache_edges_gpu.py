@@ -297,3 +297,120 @@ def test_scores_far_above_the_first_ones(many, below, dtype):
     check_rows(many, out, lse, ref, rlse, err, q, c, 200, np.ones((60, 4), dtype=bool))
     if dtype == F32:
         assert row_errors(out, ref).max() <= ROW[F32]
+
+
+def set_scales(pool, c, table, b, head, x, pos, values):
+    """Sets the scales [ng] of one position."""
+    row = O.section(pool[table[b, pos // c.page]], c, head, x + "_scales").reshape(c.page, -1)
+    row[pos % c.page] = O.f32_to_bytes(np.broadcast_to(np.asarray(values, dtype=np.float32), (c.ng,)), c.sdt)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d,group", SHAPES)
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("many", KERNELS)
+def test_unseen_keys_have_no_influence(many, what, d, group, dtype):
+    """Scales of 1e10, 1e30, 1e-30 and infinity in keys after a row's own, before
+    its window and past the length: the rows that do not see them are the same
+    as without them, and as precise."""
+    c = O.CacheDef(2, d, 16, group, False, "f32")
+    lens, cu = [170, 70], np.array([0, 60, 130], dtype=np.int32)
+    table, n_pages = T.make_table(c, lens, 3)
+    plain = O.random_pool(c, n_pages, 3)
+    q = T.make_q(130, 4, d, dtype, 5)
+    later, before = ((0, 150), (0, 151), (0, 169), (1, 40), (1, 41), (1, 69)), ((0, 75), (0, 100), (1, 0), (1, 3))
+    for window in (0, 33):
+        ref, rlse, err = O.attention(q.double().numpy(), plain, c, table, lens, cu, window=window)
+        for extreme in (1e4, 1e10, 1e30, 1e-30, np.inf):
+            pool = plain.copy()
+            unseen = np.ones((130, 4), dtype=bool)
+            for b, pos in later + (before if window else ()):
+                set_scales(pool, c, table, b, 1, what, pos, 2.0 ** 0.3 * extreme)
+                first = lens[b] - (cu[b + 1] - cu[b])
+                t = np.arange(cu[b], cu[b + 1])
+                sees = (pos <= first + t - cu[b]) & ((window == 0) | (pos > first + t - cu[b] - window))
+                unseen[t[sees], 2:] = False
+            for pos in (170, 171, 175):
+                set_scales(pool, c, table, 0, 1, what, pos, extreme)
+            out, lse = attend(many, c, pool, table, lens, cu, q, window=window)
+            assert unseen[:, 2:].sum() >= 40
+            check_rows(many, out, lse, ref, rlse, err, q, c, 170, unseen)
+            if dtype == F32:
+                assert row_errors(out, ref)[unseen].max() <= ROW[F32]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d,group", SHAPES)
+@pytest.mark.parametrize("what", ["k", "v", "both"])
+@pytest.mark.parametrize("many", KERNELS)
+def test_scales_far_apart(many, what, d, group, dtype):
+    """Neighbouring keys whose scales are up to 2^70 apart, all of them seen: a
+    key of little weight takes no bits from the others."""
+    c = O.CacheDef(1, d, 16, group, False, "f32")
+    lens, cu = [200, 90], np.array([0, 40, 100], dtype=np.int32)
+    table, n_pages = T.make_table(c, lens, 3)
+    rng = np.random.default_rng(d + group)
+    q = T.make_q(100, 4, d, dtype, 5)
+    for spread in (8.0, 35.0):
+        pool = O.random_pool(c, n_pages, 3)
+        for b, n in enumerate(lens):
+            for pos in range(n):
+                x = 2.0 ** rng.uniform(-spread, spread, c.ng if pos % 3 else 1)
+                if what != "k":
+                    set_scales(pool, c, table, b, 0, "v", pos, x)
+                if what != "v":
+                    set_scales(pool, c, table, b, 0, "k", pos, 2.0 ** rng.uniform(-spread, 0))
+        ref, rlse, err = O.attention(q.double().numpy(), pool, c, table, lens, cu)
+        out, lse = attend(many, c, pool, table, lens, cu, q)
+        check_rows(many, out, lse, ref, rlse, err, q, c, 200, np.ones((100, 4), dtype=bool))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("many", KERNELS)
+def test_a_large_value_of_no_weight(many, dtype):
+    """A value 2^40 times the others', whose probability is 2^-60 or 0: the
+    others keep their bits."""
+    c = O.CacheDef(1, 128, 16, 128, True, "f32")
+    lens, cu = [100], np.array([0, 60], dtype=np.int32)
+    table, n_pages = T.make_table(c, lens, 3)
+    pool = O.random_pool(c, n_pages, 3)
+    q = T.make_q(60, 2, 128, F32, 5).abs().to(dtype)
+    for pos, size in ((20, 30.0), (21, 3000.0)):   # codes of -8: scores far below the others'
+        O.section(pool[table[0, 1]], c, 0, "k_codes").reshape(16, -1)[pos % 16] = 0x88
+        set_scales(pool, c, table, 0, 0, "k", pos, size / 128)
+        set_scales(pool, c, table, 0, 0, "v", pos, 2.0 ** 40)
+    ref, rlse, err = O.attention(q.double().numpy(), pool, c, table, lens, cu, rotate=False)
+    out, lse = attend(many, c, pool, table, lens, cu, q, rotate=False)
+    check_rows(many, out, lse, ref, rlse, err, q, c, 100, np.ones((60, 2), dtype=bool))
+    if dtype == F32:
+        assert row_errors(out, ref).max() <= ROW[F32]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d,group", [(64, 64), (128, 32)])
+@pytest.mark.parametrize("many", KERNELS)
+def test_keys_set_aside_anywhere(many, d, group, dtype):
+    """Extreme scales in a long sequence, whose units are cut over workgroups,
+    and in many short ones, several to a workgroup; the same bits in place."""
+    c = O.CacheDef(2, d, 64, group, False, "f32")
+    rng = np.random.default_rng(d)
+    new = rng.integers(1, 12, 90)
+    lens = new + rng.integers(0, 90, 90)
+    new[7], lens[7] = 9, 4000
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    table, n_pages = T.make_table(c, [int(n) for n in lens], 3)
+    pool = O.random_pool(c, n_pages, 3)
+    for b in rng.permutation(90)[:60].tolist() + [7] * 12:
+        pos = int(rng.integers(0, lens[b]))
+        set_scales(pool, c, table, b, int(rng.integers(0, 2)), "v" if rng.random() < 0.7 else "k", pos,
+                   2.0 ** rng.choice([-45.0, -20.0, 24.0, 40.0]) if rng.random() < 0.8 else 0.0)
+    # the same extremes everywhere in one sequence, and nothing but them
+    for pos in range(lens[8]):
+        set_scales(pool, c, table, 8, 0, "v", pos, 2.0 ** rng.uniform(35, 60))
+        set_scales(pool, c, table, 8, 1, "v", pos, 0.0)
+    q = T.make_q(int(cu[-1]), 6, d, dtype, 5)
+    ref, rlse, err = O.attention(q.double().numpy(), pool, c, table, lens, cu)
+    out, lse = attend(many, c, pool, table, [int(n) for n in lens], cu, q)
+    check_rows(many, out, lse, ref, rlse, err, q, c, 4000, np.ones((int(cu[-1]), 6), dtype=bool))
+    x = q.to(T.DEV)
+    assert torch.equal(attend(many, c, pool, table, [int(n) for n in lens], cu, x, out=x)[0], out)
