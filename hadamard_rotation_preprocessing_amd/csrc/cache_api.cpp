@@ -218,13 +218,16 @@ int64_t new_tokens(int64_t tokens, int64_t seqs, int64_t max_q) {
 // Many: the waves take different rows of the same keys, whose operands they
 // share, 256 or 128 to a workgroup.  Measured, few-row kernel against shared, us:
 //   rows of a sequence (32 sequences, 8000 keys, 8 kv heads; bfloat16, heads of
-//   128): one group 32: 89, 225; 64: 136, 229; 128: 254, 228.  float32 64: 262,
-//   429; 128: 505, 458.  Groups of 32 (4 kv heads) 28: 102, 137; 42: 143, 141;
-//   56: 172, 143.  Heads of 256 (16 sequences, 4000 keys) 32: 68, 63; 64: 101, 73.
-//   scores of all heads (millions): one group 8: 31, 42; 33: 53, 56 and 54, 62;
-//   65: 83, 78; 134: 118, 101.  float32 13: 38, 51; 17: 79, 87; 33: 104, 90 and
-//   77, 80; 67: 239, 197.  Groups of 32 7: 39, 51; 14: 62, 55; 17: 72, 47.  Heads
-//   of 256 8: 63, 45; 33: 79, 58.
+//   128): one group 32: 86, 206; 64: 134, 211; 128: 246, 218.  float32 64: 262,
+//   413; 128: 489, 448.  Groups of 32 (4 kv heads) 28: 102, 124; 42: 142, 129;
+//   56: 174, 131.  Heads of 256 (16 sequences, 4000 keys) 32: 63, 105; 64: 95, 126.
+//   scores of all heads (millions), 1 sequence of 8000 keys if nothing else is
+//   said: one group 8: 31, 42; 33: 53, 59 and (4 of 4000 keys) 56, 59; 66: 81, 76;
+//   134: 136, 112.  float32 13: 43, 72; 17 (2 of 4100 keys): 50, 68; 33: 77, 102;
+//   67: 137, 151.  Groups of 32 7: 38, 57; 14: 56, 57; 17: 63, 61.  Heads of 256 8:
+//   44, 86; 33: 91, 105.
+// So heads of 256 (64 rows, 33 million scores) and float32 calls (67 million) go to
+// the shared kernel somewhat before it is the faster one.
 void attn_key(const hr::CachePage& pg, int dtype, int64_t tokens, int32_t q_heads, int64_t seqs, int64_t max_q, int64_t keys,
               hr::CacheAttnKey* k) {
     memset(k, 0, sizeof *k);

@@ -40,15 +40,18 @@
 // (new tokens x query heads of that kv head).  Units are cut into items of as
 // many keys as a workgroup takes at once, and every workgroup takes an equal,
 // contiguous run of all items, whatever the lengths; partial results are joined
-// in key order by cache_attn_join.  Where there are units enough they are shared
-// out whole instead.
+// in key order by cache_attn_join.  Where there are units enough the kernel of many
+// rows shares them out whole instead (kCut).
 //
 // What bounds it.  Few rows: the bytes of the cache, and at small sizes some ten
 // microseconds for the chain from the lengths to the first keys, the merge of the
 // waves and the joining launch.  One token in each of 16 sequences of 2048
-// positions, 32 kv heads of 128 (140 MB): 38 us, 3.7 TB/s where a large copy has
+// positions, 32 kv heads of 128 (140 MB): 39 us, 3.6 TB/s where a large copy has
 // 4.95 (28 us); 24 sequences of up to 32768, 8 kv heads (132 MB): 42 us; one of 331:
-// 15 us.  Many rows: the vector unit beside the matrix unit (see Tile).
+// 16 us.  Heads of 256 do not fit the registers with several groups (16 sequences of
+// 4000, 8 kv heads: 41 us with one group, 60, 115 and 252 with groups of 128, 64 and
+// 32, which spill 12 to 284 registers; 376 with float32 scales, 490).
+// Many rows: neither unit alone, see Tile.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -1272,17 +1275,22 @@ __device__ __forceinline__ bool join_waves(const CacheAttnArgs& a, const Seq& s,
 // Many rows: shared operands.  Eight waves have 16 or 32 rows each, one after
 // the other of the same unit.  For every pass of TILES x 32 keys some of the
 // waves turn the keys' or the values' codes of a tile into operands in LDS,
-// scaled: k times the factor that gives log2 units, v times a power of two that
-// covers the values so far.  That is done once for all rows, and leaves a row's
-// wave for each score one exponential, half a maximum and half a conversion:
+// scaled: k by its scales and a power of two (the rest of the factor that gives log2
+// units is in the queries), v by its scales and one, the unit of the pass (VEXP).
+// That is done once for all rows, and leaves a row's wave for each score one
+// exponential, half a maximum and half a conversion:
 //   - the running maximum is the start value of the matrix product, so that
 //     its result is the exponent (kPExp - mc + score) itself;
 //   - the sum of exponentials is a matrix product with ones.
-// 2 prompts of 2048 tokens behind 6144 keys, 32 heads over 8 of 128: 565 us, 850
+// 2 prompts of 2048 tokens behind 6144 keys, 32 heads over 8 of 128: 560 us, 860
 // TFLOP/s of scores and values, where a large bfloat16 matrix product has 1216
 // (395 us); with operands made anew for every four waves it was 755.  By the
-// counters the matrix unit is busy 39% of the time and the vector unit 57%, and
-// the waves wait 37% of theirs, for LDS, results and each other.
+// counters the matrix units are busy 39% of the time (SQ_VALU_MFMA_BUSY_CYCLES over
+// the busy cycles of all SIMDs), the waves wait 36% of theirs (SQ_WAIT_ANY over
+// SQ_WAVE_CYCLES), and there are 3.4 other vector instructions for a matrix
+// instruction: neither unit is full.  A workgroup fills a CU (132 kB of LDS, 256
+// registers a lane), so nothing runs while its waves wait for each other at the end
+// of a pass.
 // Two passes' operands are in LDS: a pass is made while the one before it is
 // computed.  The waves that make values do so first (their scales are looked
 // at again at the end of a pass), those that make keys last: the two of a SIMD

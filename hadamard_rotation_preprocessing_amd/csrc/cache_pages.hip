@@ -24,9 +24,9 @@ typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
 // 16 consecutive lanes.  The stages go in the order of the index bits.
 //
 // Every element is read once and every code written once, so the floor is the
-// copy of those bytes; what comes next is the instruction stream, 690 vector
+// copy of those bytes; what comes next is the instruction stream, 700 vector
 // instructions for a lane's 32 elements.  32768 tokens x 32 heads of 128 (683 MB):
-// 154 us, 4.4 TB/s where a large copy has 4.95; with selections in the lane
+// 155 us, 4.4 TB/s where a large copy has 4.95; with selections in the lane
 // stages and codes packed one by one (820 instructions) it was 175.  One token of
 // each of 64 sequences: 6 us, the launch and the chain of loads to the page.
 
@@ -277,8 +277,12 @@ int append_dim(const CacheAppendArgs& a, hipStream_t s) {
 // second launch writes the new table and copies the pages.  The plan is a few
 // dependent passes over some ten thousand integers: in LDS it takes 5 to 9 us,
 // where counting by one launch and scanning by another took 20 to 25 with the
-// gaps between them (14 us with 256 rows of 128 pages over 12000).  The copies are
-// bound by memory: 100 MB in 19 us, 400 MB in 70 to 77, 5.3 to 5.7 TB/s.
+// gaps between them (14 us with 256 rows of 128 pages over 12000).  Counters in the
+// scratch cost a pass over global memory by that one workgroup for each of these
+// passes: whole calls of 256 rows of 128 pages over 12288, 12289, 16384, 65536 and
+// 262144 pages take 19, 35, 47, 136 and 415 us (update), and 20, 37 and 260 us over
+// 12288, 12289 and 65536 (compact).  The copies are bound by memory: 100 MB in 19
+// us, 400 MB in 70 to 77, 5.3 to 5.7 TB/s.
 
 constexpr int kScan = 1024;        // threads of the planning workgroup
 constexpr int kPlanPages = 12288;  // pages whose three counters fit LDS
