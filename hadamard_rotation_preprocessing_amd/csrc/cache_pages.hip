@@ -5,6 +5,7 @@
 
 #include "cache.h"
 #include "cache_index.h"
+#include "cache_plan.h"
 #include "codes.h"
 
 namespace hr {
@@ -284,32 +285,6 @@ int append_dim(const CacheAppendArgs& a, hipStream_t s) {
 // 12288, 12289 and 65536 (compact).  The copies are bound by memory: 100 MB in 19
 // us, 400 MB in 70 to 77, 5.3 to 5.7 TB/s.
 
-constexpr int kScan = 1024;        // threads of the planning workgroup
-constexpr int kPlanPages = 12288;  // pages whose three counters fit LDS
-
-// exclusive sum of v over the workgroup's kScan threads, and the total
-__device__ __forceinline__ int scan_wg(int v, int* total, int* lds) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int inc = v;
-#pragma unroll
-    for (int x = 1; x < 64; x *= 2) {
-        const int y = __shfl_up(inc, x);
-        if (lane >= x) inc += y;
-    }
-    __syncthreads();
-    if (lane == 63) lds[wave] = inc;
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int x = 0; x < kScan / 64; ++x) {
-        const int y = lds[x];
-        if (x < wave) before += y;
-        all += y;
-    }
-    *total = all;
-    return before + inc - v;
-}
-
 // What row i of the new table takes from the old one.
 struct Kept {
     const int32_t* row;   // the parent's entries
@@ -330,13 +305,6 @@ __device__ __forceinline__ Kept kept_of(const CacheUpdateArgs& a, int i) {
     k.last = k.after > k.before && k.before % a.page > 0 ? k.before / a.page : -1;
     return k;
 }
-__device__ __forceinline__ int page_in(int32_t page, int64_t n) {
-    return page >= 0 && page < n ? page : -1;
-}
-
-// Entries of the table are taken by groups of 16 lanes, a row each at a time.
-constexpr int kRowLanes = 16;
-
 // The plan of an update: which row copies its last page (copies[i], the page
 // or -1), the number base[i] of free pages handed out before row i's, the free
 // pages in ascending order as far as they are needed, the copies (from, to)
@@ -598,23 +566,6 @@ __global__ void __launch_bounds__(256) compact_write(const CacheCompactArgs a, c
     }
     copy_pages(a.pool, a.n_pages, a.into ? a.into : a.pool, a.into_pages, a.page_bytes, a.layers, moves, moves[2 * a.n_pages],
                blockIdx.x - rows, gridDim.x - rows);
-}
-
-// Launches a planning kernel: in LDS if its counters fit, else in the scratch.
-template <class A, class... P>
-int plan(void (*in_lds)(A, P...), void (*in_scratch)(A, P...), int words, const A& a, hipStream_t s, P... args) {
-    const size_t bytes = static_cast<size_t>(words) * a.n_pages * 4;
-    if (a.n_pages <= kPlanPages) {
-        if (bytes > 65536) {
-            const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(in_lds), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                     static_cast<int>(bytes));
-            if (e != hipSuccess) return static_cast<int>(e);
-        }
-        hipLaunchKernelGGL(in_lds, dim3(1), dim3(kScan), bytes, s, a, args...);
-    } else {
-        hipLaunchKernelGGL(in_scratch, dim3(1), dim3(kScan), 0, s, a, args...);
-    }
-    return static_cast<int>(hipGetLastError());
 }
 
 }  // namespace
