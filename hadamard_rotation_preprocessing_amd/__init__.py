@@ -18,7 +18,8 @@ int32 / int8 / int8, any subset) the first three call the ``*_mixed`` entry
 points (randomised rotations, hr_mix in the header).
 
 The paged 4-bit key/value cache that takes the rotated keys (CacheSpec,
-cache_append, cache_attention, cache_update, cache_compact) is in ``cache.py``.
+cache_append, cache_attention, cache_update, cache_compact) is in ``cache.py``,
+the eviction of positions from it (cache_weights, cache_evict) in ``evict.py``.
 """
 from __future__ import annotations
 
@@ -279,3 +280,7 @@ from .cache import (CacheSpec, cache_append, cache_attention, cache_attention_wo
 
 __all__ += ["CacheSpec", "cache_append", "cache_attention", "cache_attention_work", "cache_compact", "cache_pool",
             "cache_sections", "cache_update"]
+
+from .evict import cache_evict, cache_weights  # noqa: E402,F401
+
+__all__ += ["cache_evict", "cache_weights"]

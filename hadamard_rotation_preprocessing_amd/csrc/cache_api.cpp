@@ -5,8 +5,6 @@
 #include <stdint.h>
 #include <string.h>
 
-#include <cmath>
-
 #include "cache_check.h"
 
 namespace {
@@ -56,16 +54,6 @@ void attn_key(const hr::CachePage& pg, int dtype, int64_t tokens, int32_t q_head
         k->rt = k->wide || pg.d == 256 ? 1 : 2;
         k->wr = 8;
     }
-}
-
-int attn_sizes(int dtype, int64_t tokens, int32_t q_heads, const hr::CachePage& pg, int64_t max_q) {
-    int st;
-    if ((st = check_tokens(dtype, tokens))) return st;
-    if (q_heads <= 0 || q_heads > kMaxHeads) return fail(HR_EINVAL, "q_heads = %d must be in 1..%lld", q_heads, (long long)kMaxHeads);
-    if (q_heads % pg.hkv) return fail(HR_EINVAL, "q_heads = %d is not a multiple of kv_heads = %d", q_heads, pg.hkv);
-    if (max_q < 0) return fail(HR_EINVAL, "max_q = %lld is negative", (long long)max_q);
-    if (tokens * q_heads >= (int64_t{1} << 31)) return fail(HR_EINVAL, "tokens * q_heads must be below 2^31");
-    return HR_OK;
 }
 
 int attn_work_bytes(const hr::CacheAttnKey& k, int* workers, int64_t* bytes) {
@@ -139,7 +127,7 @@ int hr_cache_attention_work(int dtype, int64_t tokens, int32_t q_heads, const hr
     int st = check_spec(spec, &pg);
     if (st) return st;
     if (!bytes) return fail(HR_EINVAL, "bytes is NULL");
-    if ((st = attn_sizes(dtype, tokens, q_heads, pg, max_q))) return st;
+    if ((st = check_attention_sizes(dtype, tokens, q_heads, pg, max_q))) return st;
     if (rows < 0 || rows > kMaxCount) return fail(HR_EINVAL, "rows = %lld must be in 0..2^30", (long long)rows);
     *bytes = 0;
     if (tokens == 0) return ok();
@@ -164,12 +152,10 @@ int hr_cache_attention(const void* q, int64_t q_stride_token, int64_t q_stride_h
     hr::CacheAttnArgs a{};
     int st = check_spec(spec, &a.pg);
     if (st) return st;
-    if ((st = attn_sizes(dtype, tokens, q_heads, a.pg, max_q)) ||
+    if ((st = check_attention_sizes(dtype, tokens, q_heads, a.pg, max_q)) ||
         (st = check_seqs(seqs, a.pg, n_pages, tokens, &a.sq)))
         return st;
-    if (!(scale >= 0.0f) || !std::isfinite(scale)) return fail(HR_EINVAL, "scale must be positive and finite (0: 1 / sqrt(head_dim))");
-    if (window < 0) return fail(HR_EINVAL, "window = %lld is negative", (long long)window);
-    if (window > 0 && !causal) return fail(HR_EINVAL, "a window needs causal attention");
+    if ((st = check_mask(scale, causal, window))) return st;
     if (tokens == 0) return ok();
     int64_t qb, ob;
     if ((st = check_rows(q, "q", q_stride_token, q_stride_head, tokens, q_heads, a.pg.d, dtype, &qb)) ||

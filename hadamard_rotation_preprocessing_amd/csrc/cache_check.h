@@ -9,6 +9,8 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <cmath>
+
 #include "../../include/hadarot_cache.h"
 #include "cache.h"
 
@@ -196,6 +198,23 @@ int check_distinct(const char* name, int64_t st, int64_t sh, int64_t tokens, int
     if (tokens <= 1 || heads <= 1) return HR_OK;
     if (st >= (heads - 1) * sh + d || sh >= sum_of(size_of(tokens - 1, st), d)) return HR_OK;
     return fail(HR_EINVAL, "%s strides %lld, %lld make rows overlap", name, (long long)st, (long long)sh);
+}
+
+int check_attention_sizes(int dtype, int64_t tokens, int32_t q_heads, const hr::CachePage& pg, int64_t max_q) {
+    int st;
+    if ((st = check_tokens(dtype, tokens))) return st;
+    if (q_heads <= 0 || q_heads > kMaxHeads) return fail(HR_EINVAL, "q_heads = %d must be in 1..%lld", q_heads, (long long)kMaxHeads);
+    if (q_heads % pg.hkv) return fail(HR_EINVAL, "q_heads = %d is not a multiple of kv_heads = %d", q_heads, pg.hkv);
+    if (max_q < 0) return fail(HR_EINVAL, "max_q = %lld is negative", (long long)max_q);
+    if (tokens * q_heads >= (int64_t{1} << 31)) return fail(HR_EINVAL, "tokens * q_heads must be below 2^31");
+    return HR_OK;
+}
+
+int check_mask(float scale, int causal, int64_t window) {
+    if (!(scale >= 0.0f) || !std::isfinite(scale)) return fail(HR_EINVAL, "scale must be positive and finite (0: 1 / sqrt(head_dim))");
+    if (window < 0) return fail(HR_EINVAL, "window = %lld is negative", (long long)window);
+    if (window > 0 && !causal) return fail(HR_EINVAL, "a window needs causal attention");
+    return HR_OK;
 }
 
 }  // namespace

@@ -1,0 +1,59 @@
+// Argument structs shared by the eviction's host layer (evict_api.cpp) and its
+// kernels (evict_weights_*.hip, evict_pages.hip).  Plain data only.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "cache.h"
+
+namespace hr {
+
+struct CacheEvictArgs {
+    uint8_t* pool;
+    const int32_t* table;
+    const int32_t* lens;
+    float* weights;
+    int32_t* new_table;
+    int32_t* new_lens;
+    int32_t* refs;
+    int32_t* status;
+    int32_t* work;
+    CachePage pg;
+    int64_t layers, n_pages, width;
+    int32_t rows, max_pages;
+    int32_t budget, sinks, recent;
+};
+
+struct CacheWeightsArgs {
+    const void* q;
+    const uint8_t* pool;
+    const float* lse;
+    float* weights;
+    uint8_t* work;
+    int64_t q_st, q_sh;        // element strides
+    int64_t width;
+    CachePage pg;
+    CacheSeqs sq;
+    float scale;               // of the scores
+    float norm;                // 1 / sqrt(d) (rotate)
+    float decay;
+    int32_t hq, rep;           // query heads; query heads per kv head
+    int32_t causal, window, rotate;
+    int32_t workers;           // workgroups
+};
+
+// Launchers: 0 or a hipError_t.
+int launch_cache_weights(const CacheWeightsArgs& a, int bf16, void* stream);
+// workgroups that hr_cache_weights keeps in flight on the current device
+int cache_weights_workers(int* workers);
+int launch_cache_evict(const CacheEvictArgs& a, void* stream);
+
+// bytes of scratch: a row's factor and log-sum-exp, and its query as pairs of float16
+constexpr int64_t cache_weights_bytes(int64_t tokens, int32_t q_heads, int d) {
+    return (tokens * q_heads * 8 + 15) / 16 * 16 + tokens * q_heads * d * 4;
+}
+// int32 words of scratch
+constexpr int64_t cache_evict_words(int64_t n_pages, int64_t rows) { return 3 * n_pages + rows + 16; }
+
+}  // namespace hr
