@@ -19,7 +19,9 @@ points (randomised rotations, hr_mix in the header).
 
 The paged 4-bit key/value cache that takes the rotated keys (CacheSpec,
 cache_append, cache_attention, cache_update, cache_compact) is in ``cache.py``,
-the eviction of positions from it (cache_weights, cache_evict) in ``evict.py``.
+the eviction of positions from it (cache_weights, cache_evict) in ``evict.py``;
+the paged cache of latents (LatentSpec, latent_append, latent_read,
+latent_attention, latent_prompt_attention) is in ``latent.py``.
 """
 from __future__ import annotations
 
@@ -283,4 +285,7 @@ __all__ += ["CacheSpec", "cache_append", "cache_attention", "cache_attention_wor
 
 from .evict import cache_evict, cache_weights  # noqa: E402,F401
 
-__all__ += ["cache_evict", "cache_weights"]
+from .latent import (LatentSpec, latent_append, latent_attention, latent_prompt_attention, latent_read)  # noqa: E402,F401
+
+__all__ += ["cache_evict", "cache_weights", "LatentSpec", "latent_append", "latent_attention", "latent_prompt_attention",
+            "latent_read"]

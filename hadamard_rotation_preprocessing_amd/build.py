@@ -56,8 +56,11 @@ def build(verbose: bool = True) -> str:
     os.makedirs(obj_dir, exist_ok=True)
     sources = [("kernels.hip", True), ("fast.hip", True), ("colrot.hip", True), ("cache_attn_256.hip", True),
                ("cache_attn_128.hip", True), ("cache_attn_64.hip", True), ("cache_pages.hip", True), ("evict_weights.hip", True),
-               ("evict_pages.hip", True), ("api.cpp", False),
-               ("paley.cpp", False), ("cache_api.cpp", False), ("cache_attn.cpp", False), ("evict_api.cpp", False)]
+               ("evict_pages.hip", True), ("latent_attn_512_4.hip", True), ("latent_attn_512_2.hip", True),
+               ("latent_attn_512_1.hip", True), ("latent_attn_256_2.hip", True), ("latent_attn_256_1.hip", True),
+               ("latent_pages.hip", True), ("latent_prompt.hip", True), ("api.cpp", False),
+               ("paley.cpp", False), ("cache_api.cpp", False), ("cache_attn.cpp", False), ("evict_api.cpp", False),
+               ("latent_api.cpp", False), ("latent_attn.cpp", False)]
     cmds, objs = [], []
     for src, device in sources:
         out = os.path.join(obj_dir, src + ".o")

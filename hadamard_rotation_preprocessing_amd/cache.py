@@ -94,10 +94,14 @@ class CacheSpec:
     def page_bytes(self) -> int:
         return _resolved(self).page_bytes
 
+    def _make(self) -> "_Resolved":
+        return _Resolved(self)
+
 
 class _Resolved:
     """What the calls need of a spec: the C struct, the page's layout, and the
     scratch sizes asked for so far (attention's, by the sizes and device)."""
+    update, compact = "hr_cache_update", "hr_cache_compact"   # the calls that move such pages
 
     def __init__(self, spec: CacheSpec):
         self.spec = spec.c()
@@ -109,11 +113,14 @@ class _Resolved:
         self.work = {}
 
 
-_resolved = lru_cache(maxsize=256)(_Resolved)
+@lru_cache(maxsize=256)
+def _resolved(spec):
+    return spec._make()
 
 
 def cache_pool(spec: CacheSpec, n_pages: int, layers: int | None = None, device="cuda") -> torch.Tensor:
-    """Zeroed pages: uint8 [n_pages, page_bytes], or [layers, n_pages, page_bytes]."""
+    """Zeroed pages: uint8 [n_pages, page_bytes], or [layers, n_pages, page_bytes].
+    (This, cache_update and cache_compact take a LatentSpec as well.)"""
     shape = (n_pages, spec.page_bytes) if layers is None else (layers, n_pages, spec.page_bytes)
     return torch.zeros(shape, dtype=torch.uint8, device=device)
 
@@ -328,7 +335,7 @@ def cache_update(pool: torch.Tensor, spec: CacheSpec, table: torch.Tensor, lens:
     if work is None:
         work = _scratch(l.hr_cache_update_work, dev, n, new)
     wp, wb = _bytes(work, dev)
-    _call(dev, l.hr_cache_update, pool.data_ptr(), layers, n, r.ref, tp, lp, rows, width, pp, gp, new,
+    _call(dev, getattr(l, r.update), pool.data_ptr(), layers, n, r.ref, tp, lp, rows, width, pp, gp, new,
           _ints(out["table"], "out['table']", (new, width), dev), _ints(out["lens"], "out['lens']", (new,), dev),
           _ints(out["refs"], "out['refs']", (n,), dev), _ints(out["status"], "out['status']", (4,), dev), wp, wb, _stream(dev))
     return out
@@ -356,7 +363,7 @@ def cache_compact(pool: torch.Tensor, spec: CacheSpec, table: torch.Tensor, lens
     if work is None:
         work = _scratch(l.hr_cache_compact_work, dev, n)
     wp, wb = _bytes(work, dev)
-    _call(dev, l.hr_cache_compact, pool.data_ptr(), layers, n, r.ref, tp, lp, rows, width, _ptr(into),
+    _call(dev, getattr(l, r.compact), pool.data_ptr(), layers, n, r.ref, tp, lp, rows, width, _ptr(into),
           0 if into is None else places, _ints(out["table"], "out['table']", (rows, width), dev),
           _ints(out["refs"], "out['refs']", (places,), dev), _ints(out["status"], "out['status']", (4,), dev), wp, wb, _stream(dev))
     return out

@@ -103,6 +103,14 @@ int cache_attn_workers(const CacheAttnKey& k, int* workers);
 constexpr int64_t cache_update_words(int64_t n_pages, int64_t new_rows) { return 4 * n_pages + 4 * new_rows + 16; }
 constexpr int64_t cache_compact_words(int64_t n_pages) { return 5 * n_pages + 16; }
 
+// hr_cache_update and hr_cache_compact of pages of any kind (cache_api.cpp).
+int cache_update(void* pool, int64_t layers, int64_t n_pages, const CachePage& pg, const int32_t* table, const int32_t* lens,
+                 int64_t rows, int64_t max_pages, const int32_t* parents, const int32_t* grow, int64_t new_rows, int32_t* new_table,
+                 int32_t* new_lens, int32_t* refs, int32_t* status, void* work, int64_t work_bytes, void* stream);
+int cache_compact(void* pool, int64_t layers, int64_t n_pages, const CachePage& pg, const int32_t* table, const int32_t* lens,
+                  int64_t rows, int64_t max_pages, void* into, int64_t into_pages, int32_t* new_table, int32_t* refs,
+                  int32_t* status, void* work, int64_t work_bytes, void* stream);
+
 // Message and status of a failing call on this thread (api.cpp).
 int set_error(int status, const char* text);
 

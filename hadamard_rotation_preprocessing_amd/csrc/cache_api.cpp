@@ -67,6 +67,108 @@ int attn_work_bytes(const hr::CacheAttnKey& k, int* workers, int64_t* bytes) {
 
 }  // namespace
 
+namespace hr {
+
+// hr_cache_update and hr_cache_compact of pages of any kind: of a page they need
+// its positions and bytes.
+int cache_update(void* pool, int64_t layers, int64_t n_pages, const CachePage& pg, const int32_t* table,
+                    const int32_t* lens, int64_t rows, int64_t max_pages, const int32_t* parents, const int32_t* grow,
+                    int64_t new_rows, int32_t* new_table, int32_t* new_lens, int32_t* refs, int32_t* status, void* work,
+                    int64_t work_bytes, void* stream) {
+    int st;
+    if ((st = check_pages(n_pages, layers)) || (st = check_table(rows, max_pages, pg.page, "rows")) ||
+        (st = check_table(new_rows, max_pages, pg.page, "new_rows")) || (st = check_counted(rows, max_pages, "rows")) ||
+        (st = check_counted(new_rows, max_pages, "new_rows")))
+        return st;
+    if ((st = check_ptr(pool, "pool", 16)) || (st = check_ptr(refs, "refs", 4)) || (st = check_ptr(status, "status", 4)))
+        return st;
+    if (rows > 0 && ((st = check_ptr(table, "table", 4)) || (st = check_ptr(lens, "lens", 4)))) return st;
+    if (new_rows > 0 && ((st = check_ptr(parents, "parents", 4)) || (st = check_ptr(grow, "grow", 4)) ||
+                         (st = check_ptr(new_table, "new_table", 4)) || (st = check_ptr(new_lens, "new_lens", 4))))
+        return st;
+    const int64_t need = cache_update_words(n_pages, new_rows) * 4;
+    if ((st = check_ptr(work, "work", 16))) return st;
+    if (work_bytes < need) return fail(HR_EINVAL, "work_bytes = %lld: %lld are needed", (long long)work_bytes, (long long)need);
+    const Range r[] = {{"pool", pool, size_of(layers, n_pages, pg.page_bytes), true},
+                       {"new_table", new_table, new_rows * max_pages * 4, true},
+                       {"new_lens", new_lens, new_rows * 4, true},
+                       {"refs", refs, n_pages * 4, true},
+                       {"status", status, 16, true},
+                       {"work", work, need, true},
+                       {"table", table, rows * max_pages * 4, false},
+                       {"lens", lens, rows * 4, false},
+                       {"parents", parents, new_rows * 4, false},
+                       {"grow", grow, new_rows * 4, false}};
+    if ((st = check_overlap(r, 10))) return st;
+    CacheUpdateArgs a{};
+    a.pool = static_cast<uint8_t*>(pool);
+    a.table = table;
+    a.lens = lens;
+    a.parents = parents;
+    a.grow = grow;
+    a.new_table = new_table;
+    a.new_lens = new_lens;
+    a.refs = refs;
+    a.status = status;
+    a.work = static_cast<int32_t*>(work);
+    a.layers = layers;
+    a.n_pages = n_pages;
+    a.page_bytes = pg.page_bytes;
+    a.rows = static_cast<int32_t>(rows);
+    a.max_pages = static_cast<int32_t>(max_pages);
+    a.new_rows = static_cast<int32_t>(new_rows);
+    a.page = pg.page;
+    return launched(launch_cache_update(a, stream));
+}
+
+int cache_compact(void* pool, int64_t layers, int64_t n_pages, const CachePage& pg, const int32_t* table,
+                     const int32_t* lens, int64_t rows, int64_t max_pages, void* into, int64_t into_pages,
+                     int32_t* new_table, int32_t* refs, int32_t* status, void* work, int64_t work_bytes, void* stream) {
+    int st;
+    if ((st = check_pages(n_pages, layers)) || (st = check_table(rows, max_pages, pg.page, "rows")) ||
+        (st = check_counted(rows, max_pages, "rows")))
+        return st;
+    if (into && (into_pages <= 0 || into_pages > kMaxCount))
+        return fail(HR_EINVAL, "into_pages = %lld must be in 1..2^30", (long long)into_pages);
+    if ((st = check_ptr(pool, "pool", 16)) || (into && (st = check_ptr(into, "into", 16))) ||
+        (st = check_ptr(refs, "refs", 4)) || (st = check_ptr(status, "status", 4)))
+        return st;
+    if (rows > 0 && ((st = check_ptr(table, "table", 4)) || (st = check_ptr(lens, "lens", 4)) ||
+                     (st = check_ptr(new_table, "new_table", 4))))
+        return st;
+    const int64_t need = cache_compact_words(n_pages) * 4;
+    if ((st = check_ptr(work, "work", 16))) return st;
+    if (work_bytes < need) return fail(HR_EINVAL, "work_bytes = %lld: %lld are needed", (long long)work_bytes, (long long)need);
+    const Range r[] = {{"pool", pool, size_of(layers, n_pages, pg.page_bytes), true},
+                       {"into", into, into ? size_of(layers, into_pages, pg.page_bytes) : 0, true},
+                       {"new_table", new_table, rows * max_pages * 4, true},
+                       {"refs", refs, (into ? into_pages : n_pages) * 4, true},
+                       {"status", status, 16, true},
+                       {"work", work, need, true},
+                       {"table", table, rows * max_pages * 4, false},
+                       {"lens", lens, rows * 4, false}};
+    if ((st = check_overlap(r, 8))) return st;
+    CacheCompactArgs a{};
+    a.pool = static_cast<uint8_t*>(pool);
+    a.into = static_cast<uint8_t*>(into);
+    a.table = table;
+    a.lens = lens;
+    a.new_table = new_table;
+    a.refs = refs;
+    a.status = status;
+    a.work = static_cast<int32_t*>(work);
+    a.layers = layers;
+    a.n_pages = n_pages;
+    a.into_pages = into ? into_pages : n_pages;
+    a.page_bytes = pg.page_bytes;
+    a.rows = static_cast<int32_t>(rows);
+    a.max_pages = static_cast<int32_t>(max_pages);
+    a.page = pg.page;
+    return launched(launch_cache_compact(a, stream));
+}
+
+}  // namespace hr
+
 extern "C" {
 
 int hr_cache_page_layout(const hr_cache_spec* spec, hr_cache_page* out) {
@@ -224,51 +326,9 @@ int hr_cache_update(void* pool, int64_t layers, int64_t n_pages, const hr_cache_
                     int64_t new_rows, int32_t* new_table, int32_t* new_lens, int32_t* refs, int32_t* status, void* work,
                     int64_t work_bytes, void* stream) {
     hr::CachePage pg;
-    int st = check_spec(spec, &pg);
+    const int st = check_spec(spec, &pg);
     if (st) return st;
-    if ((st = check_pages(n_pages, layers)) || (st = check_table(rows, max_pages, pg.page, "rows")) ||
-        (st = check_table(new_rows, max_pages, pg.page, "new_rows")) || (st = check_counted(rows, max_pages, "rows")) ||
-        (st = check_counted(new_rows, max_pages, "new_rows")))
-        return st;
-    if ((st = check_ptr(pool, "pool", 16)) || (st = check_ptr(refs, "refs", 4)) || (st = check_ptr(status, "status", 4)))
-        return st;
-    if (rows > 0 && ((st = check_ptr(table, "table", 4)) || (st = check_ptr(lens, "lens", 4)))) return st;
-    if (new_rows > 0 && ((st = check_ptr(parents, "parents", 4)) || (st = check_ptr(grow, "grow", 4)) ||
-                         (st = check_ptr(new_table, "new_table", 4)) || (st = check_ptr(new_lens, "new_lens", 4))))
-        return st;
-    const int64_t need = hr::cache_update_words(n_pages, new_rows) * 4;
-    if ((st = check_ptr(work, "work", 16))) return st;
-    if (work_bytes < need) return fail(HR_EINVAL, "work_bytes = %lld: %lld are needed", (long long)work_bytes, (long long)need);
-    const Range r[] = {{"pool", pool, size_of(layers, n_pages, pg.page_bytes), true},
-                       {"new_table", new_table, new_rows * max_pages * 4, true},
-                       {"new_lens", new_lens, new_rows * 4, true},
-                       {"refs", refs, n_pages * 4, true},
-                       {"status", status, 16, true},
-                       {"work", work, need, true},
-                       {"table", table, rows * max_pages * 4, false},
-                       {"lens", lens, rows * 4, false},
-                       {"parents", parents, new_rows * 4, false},
-                       {"grow", grow, new_rows * 4, false}};
-    if ((st = check_overlap(r, 10))) return st;
-    hr::CacheUpdateArgs a{};
-    a.pool = static_cast<uint8_t*>(pool);
-    a.table = table;
-    a.lens = lens;
-    a.parents = parents;
-    a.grow = grow;
-    a.new_table = new_table;
-    a.new_lens = new_lens;
-    a.refs = refs;
-    a.status = status;
-    a.work = static_cast<int32_t*>(work);
-    a.layers = layers;
-    a.n_pages = n_pages;
-    a.page_bytes = pg.page_bytes;
-    a.rows = static_cast<int32_t>(rows);
-    a.max_pages = static_cast<int32_t>(max_pages);
-    a.new_rows = static_cast<int32_t>(new_rows);
-    a.page = pg.page;
-    return launched(hr::launch_cache_update(a, stream));
+    return hr::cache_update(pool, layers, n_pages, pg, table, lens, rows, max_pages, parents, grow, new_rows, new_table, new_lens, refs, status, work, work_bytes, stream);
 }
 
 int hr_cache_compact_work(int64_t n_pages, int64_t* bytes) {
@@ -283,48 +343,9 @@ int hr_cache_compact(void* pool, int64_t layers, int64_t n_pages, const hr_cache
                      const int32_t* lens, int64_t rows, int64_t max_pages, void* into, int64_t into_pages,
                      int32_t* new_table, int32_t* refs, int32_t* status, void* work, int64_t work_bytes, void* stream) {
     hr::CachePage pg;
-    int st = check_spec(spec, &pg);
+    const int st = check_spec(spec, &pg);
     if (st) return st;
-    if ((st = check_pages(n_pages, layers)) || (st = check_table(rows, max_pages, pg.page, "rows")) ||
-        (st = check_counted(rows, max_pages, "rows")))
-        return st;
-    if (into && (into_pages <= 0 || into_pages > kMaxCount))
-        return fail(HR_EINVAL, "into_pages = %lld must be in 1..2^30", (long long)into_pages);
-    if ((st = check_ptr(pool, "pool", 16)) || (into && (st = check_ptr(into, "into", 16))) ||
-        (st = check_ptr(refs, "refs", 4)) || (st = check_ptr(status, "status", 4)))
-        return st;
-    if (rows > 0 && ((st = check_ptr(table, "table", 4)) || (st = check_ptr(lens, "lens", 4)) ||
-                     (st = check_ptr(new_table, "new_table", 4))))
-        return st;
-    const int64_t need = hr::cache_compact_words(n_pages) * 4;
-    if ((st = check_ptr(work, "work", 16))) return st;
-    if (work_bytes < need) return fail(HR_EINVAL, "work_bytes = %lld: %lld are needed", (long long)work_bytes, (long long)need);
-    const Range r[] = {{"pool", pool, size_of(layers, n_pages, pg.page_bytes), true},
-                       {"into", into, into ? size_of(layers, into_pages, pg.page_bytes) : 0, true},
-                       {"new_table", new_table, rows * max_pages * 4, true},
-                       {"refs", refs, (into ? into_pages : n_pages) * 4, true},
-                       {"status", status, 16, true},
-                       {"work", work, need, true},
-                       {"table", table, rows * max_pages * 4, false},
-                       {"lens", lens, rows * 4, false}};
-    if ((st = check_overlap(r, 8))) return st;
-    hr::CacheCompactArgs a{};
-    a.pool = static_cast<uint8_t*>(pool);
-    a.into = static_cast<uint8_t*>(into);
-    a.table = table;
-    a.lens = lens;
-    a.new_table = new_table;
-    a.refs = refs;
-    a.status = status;
-    a.work = static_cast<int32_t*>(work);
-    a.layers = layers;
-    a.n_pages = n_pages;
-    a.into_pages = into ? into_pages : n_pages;
-    a.page_bytes = pg.page_bytes;
-    a.rows = static_cast<int32_t>(rows);
-    a.max_pages = static_cast<int32_t>(max_pages);
-    a.page = pg.page;
-    return launched(hr::launch_cache_compact(a, stream));
+    return hr::cache_compact(pool, layers, n_pages, pg, table, lens, rows, max_pages, into, into_pages, new_table, refs, status, work, work_bytes, stream);
 }
 
 }  // extern "C"
