@@ -55,7 +55,7 @@ struct LatentAttnArgs {
 // Which attention kernel a call takes: 16 rt wr query rows of a sequence to a
 // workgroup, in waves of 16 rt.
 struct LatentAttnKey {
-    int32_t d, ng;
+    int32_t d, ng, sf32;
     int32_t wide;              // float32 activations
     int32_t rt, wr;
 };

@@ -75,6 +75,7 @@ void attn_key(const hr::LatentPage& pg, int dtype, int64_t tokens, int32_t heads
     const int64_t rows = n * heads;
     k->d = pg.d;
     k->ng = pg.ng;
+    k->sf32 = pg.sf32;
     k->wide = dtype == HR_F32;
     k->rt = rows <= 32 || k->wide ? 1 : 2;
     k->wr = rows <= 16 ? 1 : 2;

@@ -8,24 +8,25 @@
 // bfloat16.  For the values the scales go into the probabilities, for each group
 // apart: P_g = exp(w - m) s_g, and O_g = P_g (k - z) is a matrix product over the
 // same integers.
-//   The softmax is taken in one pass.  Its reference m only keeps exponentials in
-// float32's range, so it moves when one passes 2^kFar.  P_g goes into the product
-// as float16 in a power of two of its row and group, which moves when a value would
-// pass 2^kTop: it follows the largest exp(w - m) s_g that the row has seen, so what
-// a row does not see has no part in it, and scales of any size keep their bits.
+//   The softmax is taken in one pass.  P_g goes into the product as float16, so its
+// reference m follows the largest exp(w - m) s_g that the row has seen: probabilities
+// are at most 2^kTop, 2^kSet when the reference is set, and what a row does not see
+// has no part in it.  Where scales are below 2^-92 or above 2^100 float32's own range
+// ends (the sum of exponentials is in the same units).
 //
 // Layout.  A workgroup takes M = 16 RT WR query rows (new tokens x heads) of a
-// sequence, and 64 keys a step.  Scores are formed transposed, S^T = C Q^T, by WR x
-// 4 waves: a wave takes 16 keys (A operand: packed codes made into float16 in its
-// registers, straight from memory) and 16 RT rows (B operand, in registers
-// throughout).  The operands go to LDS too, where the second product finds them:
-// O^T = C^T P^T, for which every wave takes all M rows and its share of the
-// dimensions, so that the sums are spread over the workgroup.  C^T comes out of LDS
-// by transposing reads (ds_read_b64_tr_b16), P^T by way of LDS from the waves that
-// made it, its 32 keys of a matrix step in the order 4 g + i, 16 + 4 g + i of the
-// registers of two score tiles.
-//   Elements of eight of a vector stand in the order 0 4 1 5 2 6 3 7 throughout:
-// that of the nibbles of a word under two masks.
+// sequence, and 32 keys a step, in waves of two kinds that work side by side, one step
+// apart, with one barrier a step:
+//   2 WR score waves form S^T = C Q^T (A operand: 16 keys out of LDS; B operand: 16 RT
+//   rows, in registers throughout) and put probabilities into LDS;
+//   4 value waves turn the packed codes of the step after into float16 operands in
+//   LDS, and add O^T += C^T P^T of the step before for all M rows, a quarter of the
+//   dimensions each.  C^T comes out of the same operands by transposing reads
+//   (ds_read_b64_tr_b16).  The codes are on their way from memory for kAhead steps.
+// A SIMD has a wave of each kind, so that one's matrix steps run while the other is at
+// its exponentials or codes.  P^T's 32 keys stand in the order 4 g + i, 16 + 4 g + i of
+// the registers of two score tiles.  Elements of eight of a vector stand in the order
+// 0 4 1 5 2 6 3 7 throughout: that of the nibbles of a word under two masks.
 //
 // Split.  latent_query rotates the queries, turns them into operands in the scratch
 // and numbers the work: a unit is a block of M rows of a sequence, an item 64 keys of
@@ -38,6 +39,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "cache_vectors.h"
 #include "latent.h"
@@ -54,10 +56,11 @@ typedef short short4v __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLow = -3.0e38f;      // reference of a row that has seen nothing
-constexpr float kFar = 0x1p20f;       // largest exponential before the reference moves
-constexpr float kTop = 0x1p15f;       // largest probability in its unit (float16 ends at 65504)
-constexpr int kSet = 8;               // log2 of the largest one when a unit is set
-constexpr int kUnit = 126;            // units are 2^-kUnit .. 2^kUnit
+constexpr float kTop = 0x1p15f;       // largest probability (float16 ends at 65504)
+constexpr int kSet = 8;               // log2 of the largest one when a reference is set
+constexpr int kLeastRef = -100;       // how far (log2) a reference may lie below the largest score
+constexpr float kMostExp = 0x1p110f;  // largest exponential
+constexpr int kAhead = 3;             // steps that keys are loaded ahead
 constexpr int kQTop = 14;             // a query's largest element is below 2^kQTop in float16
 
 __device__ __forceinline__ float4v mfma_f16(uint4v a, uint4v b, float4v c) {
@@ -88,25 +91,30 @@ __device__ __forceinline__ uint32_t to_bf16(float f) {
     if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
     return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
-// 2^e of an integer e in -126 .. 127
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+// floor(log2(v)) of v >= 0 that is a normal number (-127 of smaller ones, 128 of larger)
+__device__ __forceinline__ int exponent(float v) { return static_cast<int>((__float_as_uint(v) >> 23) & 255) - 127; }
 
-template <int D_, int NG_, bool WIDE_, int RT_, int WR_>
+// Matrix steps stay in order: left alone, the scheduler loads the operands of many of
+// them at once, and spills.
+#define HR_PHASE() __builtin_amdgcn_sched_barrier(0)
+
+template <int D_, int NG_, bool SF32_, bool WIDE_, int RT_, int WR_>
 struct Cfg {
     static constexpr int D = D_, NG = NG_, RT = RT_, WR = WR_;
-    static constexpr bool WIDE = WIDE_;
-    static constexpr int WK = 4, WAVES = WR * WK, THREADS = 64 * WAVES;
+    static constexpr bool SF32 = SF32_, WIDE = WIDE_;
+    static constexpr int WK = 2, SCORES = WR * WK, VALUES = 4, THREADS = 64 * (SCORES + VALUES);   // waves
     static constexpr int KEYS = 16 * WK;           // of a step
     static constexpr int TILES = RT * WR, M = 16 * TILES;
     static constexpr int T = WIDE ? 2 : 1;         // float16 terms of a query and a probability
     static constexpr int TR = WIDE ? 3 : 1;        // bfloat16 terms of a rotary query
-    static constexpr int KS = D / 32, KG = KS / NG, G = D / NG;
-    static constexpr int DW = D / WAVES, DT = DW / 16;   // dimensions of a wave in the second product
-    static constexpr int VS = 2 * D + 32;          // bytes of a key's operands in LDS
+    static constexpr int KS = D / 32, G = D / NG, KG = KS / NG;
+    static constexpr int DW = D / VALUES, DT = DW / 16;   // dimensions of a value wave
+    static constexpr int LK = 64 / (KEYS / VALUES);       // lanes that share a key's codes
+    static constexpr int CW = D / 8 / LK;          // words of codes of a lane
+    static constexpr int VS = 2 * (D + kRope) + 16;       // bytes of a key's operands in LDS
     static constexpr int PS = 2 * KEYS + 16;       // bytes of a row's probabilities
     static constexpr int QS = 2 * (T * D + TR * kRope);   // bytes of a row's query in the scratch
     static constexpr int RS = D + 4;               // floats of a row's sums
-    static constexpr int WGS = WR == 1 ? 2 : 1;    // workgroups of a CU
 };
 
 // A sequence of the call, clamped so that nothing leaves its buffer.
@@ -124,9 +132,10 @@ __device__ __forceinline__ Seq seq_at(const CacheSeqs& s, int logp, int b) {
     r.len = static_cast<int>(min(static_cast<int64_t>(max(s.lens[b], 0)), static_cast<int64_t>(s.max_pages) << logp));
     return r;
 }
-// items of a unit of a sequence, and its units
+// items of a unit of a sequence (kItem keys each), and its units
+constexpr int kItem = 64;
 template <class C>
-__device__ __forceinline__ int items_of(const Seq& s) { return static_cast<int>((static_cast<int64_t>(s.len) + C::KEYS - 1) / C::KEYS); }
+__device__ __forceinline__ int items_of(const Seq& s) { return static_cast<int>((static_cast<int64_t>(s.len) + kItem - 1) / kItem); }
 template <class C>
 __device__ __forceinline__ int units_of(const Seq& s, int heads) {
     return static_cast<int>((static_cast<int64_t>(s.n) * heads + C::M - 1) / C::M);
@@ -142,6 +151,33 @@ __device__ __forceinline__ int used_workers(int64_t total, int workers) {
     return static_cast<int>(n < workers ? (n > 1 ? n : 1) : workers);
 }
 
+// The run of items that a workgroup takes: neighbouring runs, which are of the same
+// sequences, on the same XCD (workgroups go to the XCDs in turn), so that row blocks of
+// the same keys find them in its L2.
+constexpr int kXcds = 8;
+__device__ __forceinline__ int worker_of(int block, int n) { return n % kXcds ? block : block % kXcds * (n / kXcds) + block / kXcds; }
+
+__device__ __forceinline__ float max_groups(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float sum_groups(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+// N floats (a multiple of 4) out of LDS
+template <int N>
+__device__ __forceinline__ void load_floats(const float* p, float* v) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const float4v x = *reinterpret_cast<const float4v*>(p + i);
+        v[i] = x.x;
+        v[i + 1] = x.y;
+        v[i + 2] = x.z;
+        v[i + 3] = x.w;
+    }
+}
+
 // 16 dimensions of four keys out of LDS: lane m of 16 gives the address of its four
 // dimensions 4 (m % 4) of key m / 4, and gets dimension m of the four keys.
 __device__ __forceinline__ uint2v transposed(const uint8_t* p) {
@@ -153,7 +189,7 @@ __device__ __forceinline__ uint2v transposed(const uint8_t* p) {
 template <class C>
 struct Work {
     int64_t* first;      // [rows + 1]: items before those of a sequence
-    float* factor;       // [query rows]: of a score's products with codes
+    float* factor;       // [query rows][4]: of a row's scores, and of its products with rotary keys before
     uint8_t* query;
     float* whole;        // [query rows][RS]: sums, the reference, and the sum of exponentials
     float* part;         // [workers][2][M][RS]
@@ -209,8 +245,14 @@ __global__ void __launch_bounds__(256) latent_query(const LatentAttnArgs a) {
 #pragma unroll
     for (int j = 1; j < 16; ++j) top = fmaxf(top, fabsf(x[j]));
     top = over_lanes<LPV>(top, [](float p, float q) { return fmaxf(p, q); });
+    // products with rotary keys are put in the same unit, which has to leave them in range
+    float rtop = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) rtop = fmaxf(rtop, fabsf(sizeof(In) == 2 ? bf2f(static_cast<uint32_t>(rp[i])) : static_cast<float>(rp[i])));
+    rtop = over_lanes<LPV>(rtop, [](float p, float q) { return fmaxf(p, q); });
+    const int most = min(100 - exponent(rtop), 110);
     int unit = 0;
-    if (top > 0.0f && top < __builtin_inff()) unit = min(max(kQTop - 1 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), -110), 110);
+    if (top > 0.0f && top < __builtin_inff()) unit = max(min(kQTop - 1 - exponent(top), most), -110);
     if (row >= total) return;
     uint8_t* to = work.query + row * C::QS;
 #pragma unroll
@@ -241,73 +283,54 @@ __global__ void __launch_bounds__(256) latent_query(const LatentAttnArgs a) {
             rope[i] = rp[i];
         }
     }
-    if (e == 0) work.factor[row] = __builtin_ldexpf(a.scale * kLog2e, -unit);
+    if (e == 0) {
+        work.factor[4 * row] = __builtin_ldexpf(a.scale * kLog2e, -unit);
+        work.factor[4 * row + 1] = __builtin_ldexpf(1.0f, unit);
+    }
 }
 
 // ---------------------------------------------------------------------------
 // the sums
 
-// What a wave holds of 16 keys before it works on them.
+// What a lane of a value wave holds of a key on its way: codes of CW / 4 runs of 32
+// elements with their groups' scales and zero points, and a part of the rotary key.
 template <class C>
 struct Raw {
-    uint4v codes[C::KS / 4];   // of key lane & 15: the lane group's quarter of every group
-    uint4v rope[2];
-    uint32_t scales[4 * C::NG];   // of keys 4 g .. 4 g + 3 (two to a word if bfloat16)
-    uint32_t zeros;            // of key lane & 15, a nibble for each group
+    uint4v codes[C::CW / 4], rope;
+    uint32_t scale[C::CW / 4], zero[C::CW / 4];
 };
 
 template <class C>
-__device__ __forceinline__ void load_keys(const LatentAttnArgs& a, int page, int t0, Raw<C>& w) {
-    constexpr int D = C::D, NG = C::NG;
-    const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
-    const uint8_t* base = a.pool + page * a.pg.page_bytes;
-    const int off = t0 & (a.pg.page - 1);
-    const uint8_t* codes = base + (off + m) * (D / 2) + g * (C::G / 8);
-#pragma unroll
-    for (int q = 0; q < NG; ++q)
-#pragma unroll
-        for (int i = 0; i < C::KG / 4; ++i) w.codes[q * (C::KG / 4) + i] = *reinterpret_cast<const uint4v*>(codes + q * (C::G / 2) + 16 * i);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) w.rope[i] = *reinterpret_cast<const uint4v*>(base + a.pg.rope + (off + m) * (2 * kRope) + 64 * i + 16 * g);
-    if (a.pg.sf32) {
-        const uint32_t* s = reinterpret_cast<const uint32_t*>(base + a.pg.scales) + (off + 4 * g) * NG;
-#pragma unroll
-        for (int i = 0; i < 4 * NG; ++i) w.scales[i] = s[i];
-    } else {
-        const uint32_t* s = reinterpret_cast<const uint32_t*>(base + a.pg.scales) + (off + 4 * g) * NG / 2;
-#pragma unroll
-        for (int i = 0; i < 2 * NG; ++i) w.scales[i] = s[i];
-    }
-    w.zeros = 0;
-    if (!a.pg.sym) {
-        const uint8_t* z = base + a.pg.zeros + (off + m) * NG / 2;
-        if constexpr (NG == 4) w.zeros = *reinterpret_cast<const uint16_t*>(z);
-        else if constexpr (NG == 2) w.zeros = *z;
-        else w.zeros = *z >> (4 * (m & 1));
-    }
-}
+struct Lds {
+    __attribute__((aligned(16))) uint8_t keys[3][C::KEYS * C::VS];
+    __attribute__((aligned(16))) uint8_t probs[2][C::T * C::NG * C::M * C::PS];
+    __attribute__((aligned(16))) float scales[3][C::KEYS * C::NG];
+    float top[C::WK * C::M], shift[C::M];
+    int there[3][C::WK];       // whether a step's 16 keys have a page
+    int moved[3];              // whether a reference moves after a step
+};
+
+// Integers read at an address that is the same in all lanes: through the scalar
+// cache, into scalar registers.
+typedef const int32_t __attribute__((address_space(4)))* ConstInts;
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, C::WGS * C::WAVES / 4) latent_sums(const LatentAttnArgs a) {
+__global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArgs a) {
     constexpr int D = C::D, NG = C::NG, RT = C::RT, T = C::T, M = C::M;
-    __shared__ __attribute__((aligned(16))) uint8_t values[C::KEYS * C::VS];
-    __shared__ __attribute__((aligned(16))) uint8_t probs[T * NG * M * C::PS];
-    __shared__ float top[C::WK * M];           // of a wave's keys, for each row
-    __shared__ float top_g[C::WK * M * NG];
-    __shared__ float shift[M * NG];            // what a row's sums are multiplied by
-    __shared__ int units[M * NG];              // log2 of a row's units
-    __shared__ int moved;
+    __shared__ Lds<C> lds;
     const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wk = wave % C::WK, wr = wave / C::WK;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const bool scoring = wave < C::SCORES;
+    const int wk = wave % C::WK, wr = wave / C::WK;      // of a score wave
+    const int vw = wave - C::SCORES;                     // of a value wave
     const Work<C> work(a);
     const LatentPage& pg = a.pg;
     const int64_t total = work.first[a.sq.rows];
     const int used = used_workers(total, gridDim.x);
-    if (static_cast<int>(blockIdx.x) >= used) return;
-    const int64_t end = begin_of(total, blockIdx.x + 1, used);
-    int64_t item = begin_of(total, blockIdx.x, used);
-    if (tid == 0) moved = 0;
-    const float f0 = a.scale * kLog2e;
+    const int worker = worker_of(blockIdx.x, gridDim.x);
+    if (worker >= used) return;
+    const int64_t end = begin_of(total, worker + 1, used);
+    int64_t item = begin_of(total, worker, used);
     while (item < end) {
         int lo = 0, hi = a.sq.rows - 1;        // the last sequence that begins at or before this item
         while (lo < hi) {
@@ -315,324 +338,354 @@ __global__ void __launch_bounds__(C::THREADS, C::WGS * C::WAVES / 4) latent_sums
             if (work.first[mid] <= item) lo = mid;
             else hi = mid - 1;
         }
+        lo = __builtin_amdgcn_readfirstlane(lo);
         const Seq s = seq_at(a.sq, pg.logp, lo);
         const int per = items_of<C>(s);
         const int64_t in_seq = item - work.first[lo];
-        const int rb = static_cast<int>(in_seq / per), k0 = static_cast<int>(in_seq % per);
-        const int k1 = static_cast<int>(min(static_cast<int64_t>(per), k0 + end - item));
+        const int rb = __builtin_amdgcn_readfirstlane(static_cast<int>(in_seq / per)), k0 = __builtin_amdgcn_readfirstlane(static_cast<int>(in_seq % per));
+        const int k1 = __builtin_amdgcn_readfirstlane(static_cast<int>(min(static_cast<int64_t>(per), k0 + end - item)));
         item += k1 - k0;
-        const int32_t* table = a.sq.table + static_cast<int64_t>(lo) * a.sq.max_pages;
-        const int rows = s.n * a.heads, r0 = rb * M, first = s.len - s.n;
-        const int64_t row_at = static_cast<int64_t>(s.start) * a.heads;
-
-        // the wave's rows as B operands
-        uint4v query[RT][T][C::KS], rope[RT][C::TR][2];
-        float factor[RT];
-        int pos[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const int r = min(r0 + (wr * RT + rt) * 16 + m, rows - 1);
-            const uint8_t* q = work.query + (row_at + r) * C::QS;
-#pragma unroll
-            for (int t = 0; t < T; ++t)
-#pragma unroll
-                for (int ks = 0; ks < C::KS; ++ks)
-                    query[rt][t][ks] = *reinterpret_cast<const uint4v*>(q + 2 * (t * D + (ks / C::KG) * C::G + g * (C::G / 4) + 8 * (ks % C::KG)));
-#pragma unroll
-            for (int t = 0; t < C::TR; ++t)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) rope[rt][t][i] = *reinterpret_cast<const uint4v*>(q + 2 * (T * D + t * kRope + 32 * i + 8 * g));
-            factor[rt] = work.factor[row_at + r];
-            pos[rt] = a.causal ? min(first + r / a.heads, s.len - 1) : s.len - 1;   // the last key that the row sees
-        }
+        const int len = __builtin_amdgcn_readfirstlane(s.len), rows = __builtin_amdgcn_readfirstlane(s.n) * a.heads;
+        const int r0 = rb * M, first = len - __builtin_amdgcn_readfirstlane(s.n);
+        const int64_t row_at = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(s.start)) * a.heads;
         const int last_row = min(r0 + M, rows) - 1;
-        const int limit = a.causal ? min(max(first + last_row / a.heads + 1, 0), s.len) : s.len;
-        // the first key that not all of the wave's rows see
-        const int all = a.causal ? min(first + min(r0 + wr * 16 * RT, rows - 1) / a.heads + 1, s.len) : s.len;
+        const int limit = a.causal ? min(max(first + last_row / a.heads + 1, 0), len) : len;   // no row sees keys past it
+        const int steps = (min(k1 * (kItem), limit) - k0 * kItem + C::KEYS - 1) / C::KEYS;     // (may be negative)
+        const bool whole = k0 == 0 && k1 == per;
+        float* out = whole ? work.whole + (row_at + r0) * C::RS
+                           : work.part + (static_cast<int64_t>(worker) * 2 + (k0 > 0 ? 0 : 1)) * M * C::RS;
+        const int key0 = k0 * kItem;
+        __syncthreads();                       // (the last segment's readers are done)
+        if (tid < 3) lds.moved[tid] = 0;
 
-        float4v acc[C::TILES][C::DT];
+        if (scoring) {
+            // the wave's rows as B operands
+            uint4v query[RT][T][C::KS], rope[RT][C::TR][2];
+            float factor[RT], rfactor[RT];
+            int pos[RT];
 #pragma unroll
-        for (int x = 0; x < C::TILES; ++x)
+            for (int rt = 0; rt < RT; ++rt) {
+                const int r = min(r0 + (wr * RT + rt) * 16 + m, rows - 1);
+                const uint8_t* q = work.query + (row_at + r) * C::QS;
 #pragma unroll
-            for (int d = 0; d < C::DT; ++d) acc[x][d] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-        float ref[RT], sum[RT];
-        int unit[RT][NG];                      // log2
+                for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            ref[rt] = kLow;
-            sum[rt] = 0.0f;
+                    for (int ks = 0; ks < C::KS; ++ks) query[rt][t][ks] = *reinterpret_cast<const uint4v*>(q + 2 * (t * D + 32 * ks + 8 * g));
 #pragma unroll
-            for (int q = 0; q < NG; ++q) unit[rt][q] = -kUnit;
-        }
-
-        const auto page_at = [&](int t0) {     // of the wave's keys from t0; -1: none are there
-            if (t0 >= limit) return -1;
-            const int p = table[t0 >> pg.logp];
-            return p >= 0 && p < a.sq.n_pages ? p : -1;
-        };
-        Raw<C> raw;
-        const int end_key = min(k1 * C::KEYS, limit);
-        int t0 = k0 * C::KEYS + 16 * wk;
-        int page = __builtin_amdgcn_readfirstlane(page_at(t0)), next = __builtin_amdgcn_readfirstlane(page_at(t0 + C::KEYS));
-        if (page >= 0) load_keys<C>(a, page, t0, raw);
-        __syncthreads();
-
-        for (; t0 - 16 * wk < end_key; t0 += C::KEYS) {
-            // scores, and the operands to LDS
-            float4v w[RT], wrope[RT];
-            float scale[4][NG];
-            const bool here = page >= 0;
-            if (here) {
-                const uint32_t f0c = 0x64006400u ^ (pg.sym ? 0x00080008u : 0u), f1c = 0x54005400u ^ (pg.sym ? 0x00800080u : 0u);
+                for (int t = 0; t < C::TR; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 2; ++i) rope[rt][t][i] = *reinterpret_cast<const uint4v*>(q + 2 * (T * D + t * kRope + 32 * i + 8 * g));
+                factor[rt] = work.factor[4 * (row_at + r)];
+                rfactor[rt] = work.factor[4 * (row_at + r) + 1];
+                pos[rt] = a.causal ? min(first + r / a.heads, len - 1) : len - 1;   // the last key that the row sees
+            }
+            // the first key that not all of the wave's rows see
+            const int all = a.causal ? min(first + min(r0 + wr * 16 * RT, rows - 1) / a.heads + 1, len) : len;
+            float ref[RT], sum[RT];
 #pragma unroll
-                    for (int q = 0; q < NG; ++q) {
-                        const int x = i * NG + q;
-                        scale[i][q] = pg.sf32 ? __uint_as_float(raw.scales[x])
-                                              : __uint_as_float((x & 1) ? raw.scales[x / 2] & 0xFFFF0000u : raw.scales[x / 2] << 16);
-                    }
+            for (int rt = 0; rt < RT; ++rt) {
+                ref[rt] = kLow;
+                sum[rt] = 0.0f;
+            }
+            __syncthreads();                   // (the first keys are there)
+            int b3 = 0;
+            for (int i = 0; i < steps; ++i) {
+                if (tid == 0) lds.moved[b3 == 2 ? 0 : b3 + 1] = 0;
+                const uint8_t* keys = lds.keys[b3] + (16 * wk + m) * C::VS + 16 * g;
+                float scale[4][NG];
+                load_floats<4 * NG>(lds.scales[b3] + (16 * wk + 4 * g) * NG, &scale[0][0]);
+                float4v w[RT];
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    wrope[rt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int rt = 0; rt < RT; ++rt) w[rt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint4v k = *reinterpret_cast<const uint4v*>(keys + 2 * D + 64 * x);
 #pragma unroll
                     for (int t = C::TR - 1; t >= 0; --t)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) wrope[rt] = mfma_bf16(raw.rope[i], rope[rt][t][i], wrope[rt]);
+                        for (int rt = 0; rt < RT; ++rt) w[rt] = mfma_bf16(k, rope[rt][t][x], w[rt]);
                 }
-                uint8_t* to = values + (16 * wk + m) * C::VS + g * (C::G / 4) * 2;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) w[rt][x] *= rfactor[rt];
 #pragma unroll
                 for (int q = 0; q < NG; ++q) {
-                    const uint32_t z = pg.sym ? 8u : (raw.zeros >> (4 * q)) & 15u;
-                    const uint32_t z0 = 0x64006400u + z * 0x00010001u, z1 = 0x54005400u + z * 0x00100010u;
                     float4v c[RT];
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) c[rt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int i = 0; i < C::KG; ++i) {
-                        const int ks = q * C::KG + i;
-                        uint32_t x = raw.codes[ks / 4][ks % 4];
-                        uint4v k;
-                        k.x = pk_sub((x & 0x000F000Fu) ^ f0c, z0);
-                        k.y = pk_sub((x & 0x00F000F0u) ^ f1c, z1);
-                        x >>= 8;
-                        k.z = pk_sub((x & 0x000F000Fu) ^ f0c, z0);
-                        k.w = pk_sub((x & 0x00F000F0u) ^ f1c, z1);
-                        // (waves of the same keys write half of the operands each)
-                        if (C::WR == 1 || ks * C::WR / C::KS == wr) *reinterpret_cast<uint4v*>(to + 2 * (q * C::G + 8 * i)) = k;
+                    for (int x = 0; x < C::KG; ++x) {
+                        const int ks = q * C::KG + x;
+                        if (ks % 4 == 0) HR_PHASE();
+                        const uint4v k = *reinterpret_cast<const uint4v*>(keys + 64 * ks);
 #pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) {
-                            if constexpr (C::WIDE) c[rt] = mfma_f16(k, query[rt][T - 1][ks], c[rt]);
-                            c[rt] = mfma_f16(k, query[rt][0][ks], c[rt]);
-                        }
+                        for (int t = T - 1; t >= 0; --t)
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) c[rt] = mfma_f16(k, query[rt][t][ks], c[rt]);
                     }
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) w[rt][i] = q ? __builtin_fmaf(c[rt][i], scale[i][q], w[rt][i]) : c[rt][i] * scale[i][0];
+                        for (int x = 0; x < 4; ++x) w[rt][x] = __builtin_fmaf(c[rt][x], scale[x][q], w[rt][x]);
                 }
+                HR_PHASE();
+                const int t0 = key0 + i * C::KEYS + 16 * wk, key = t0 + 4 * g;
+                const bool here = lds.there[b3][wk] != 0, full = here && t0 + 16 <= all;
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) w[rt][i] = __builtin_fmaf(w[rt][i], factor[rt], wrope[rt][i] * f0);
-            } else {
-                // keys that are not there: no probability, and finite operands
-                uint8_t* to = values + (16 * wk + m) * C::VS + g * (D / 4) * 2;
+                    for (int x = 0; x < 4; ++x) w[rt][x] *= factor[rt];
+                if (!full) {
 #pragma unroll
-                for (int ks = 0; ks < C::KS; ++ks)
-                    if (C::WR == 1 || ks * C::WR / C::KS == wr) *reinterpret_cast<uint4v*>(to + 16 * ks) = uint4v{0, 0, 0, 0};
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const int bound = here ? pos[rt] : -1;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int q = 0; q < NG; ++q) scale[i][q] = 0.0f;
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w[rt][i] = -__builtin_inff();
-            }
-            const int key = t0 + 4 * g;
-            const bool full = here && t0 + 16 <= all;
-            if (!full) {
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (key + i > pos[rt]) w[rt][i] = -__builtin_inff();
-            }
-            // the next keys
-            page = next;
-            next = __builtin_amdgcn_readfirstlane(page_at(t0 + 2 * C::KEYS));
-            if (page >= 0) load_keys<C>(a, page, t0 + C::KEYS, raw);
-
-            // probabilities in their units, to LDS
-            float more[RT];
-            bool far = false;
-            const auto put = [&]() {
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    float p[4];
-                    more[rt] = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        p[i] = __builtin_amdgcn_exp2f(w[rt][i] - ref[rt]);
-                        more[rt] += p[i];
-                        far = far || !(p[i] <= kFar);
-                    }
-#pragma unroll
-                    for (int q = 0; q < NG; ++q) {
-                        float x[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            x[i] = __builtin_ldexpf(p[i] * scale[i][q], -unit[rt][q]);
-                            // (an unseen key's scale may be anything)
-                            if (!full && key + i > pos[rt]) x[i] = 0.0f;
-                            far = far || !(x[i] <= kTop);
-                        }
-                        // keys 16 wk + 4 g + i stand at 8 g + 4 (wk & 1) + i of their 32
-                        uint8_t* to = probs + (q * M + (wr * RT + rt) * 16 + m) * C::PS + (wk / 2) * 64 + 16 * g + 8 * (wk & 1);
-                        if constexpr (C::WIDE) {
-                            uint2v hi, lost;
-                            uint32_t h, l;
-                            split_f16(x[0], x[1], h, l);
-                            hi.x = h;
-                            lost.x = l;
-                            split_f16(x[2], x[3], h, l);
-                            hi.y = h;
-                            lost.y = l;
-                            *reinterpret_cast<uint2v*>(to) = hi;
-                            *reinterpret_cast<uint2v*>(to + NG * M * C::PS) = lost;
-                        } else {
-                            *reinterpret_cast<uint2v*>(to) = uint2v{pack_f16(x[0], x[1]), pack_f16(x[2], x[3])};
-                        }
+                        for (int x = 0; x < 4; ++x) w[rt][x] = key + x > bound ? -__builtin_inff() : w[rt][x];
                     }
                 }
-            };
-            put();
-            if (__any(far) && lane == 0) moved = 1;
+                // an unseen key's scale may be anything, and its probability is 0: what is
+                // multiplied by it is finite (a key that is seen has a NaN score then)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int q = 0; q < NG; ++q) scale[x][q] = fminf(scale[x][q], 0x1.fffffep127f);
+                // probabilities, to LDS: keys 16 wk + 4 g + x stand at 8 g + 4 wk + x
+                uint8_t* to = lds.probs[i & 1] + (wr * 16 * RT + m) * C::PS + 16 * g + 8 * wk;
+                float more[RT];
+                const auto put = [&]() {
+                    float most = 0.0f, largest = 0.0f;
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        float p[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) p[x] = __builtin_amdgcn_exp2f(w[rt][x] - ref[rt]);
+                        more[rt] = (p[0] + p[1]) + (p[2] + p[3]);
+                        largest = fmaxf(fmaxf(largest, more[rt]), 0.0f);
+#pragma unroll
+                        for (int q = 0; q < NG; ++q) {
+                            float v[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) v[x] = p[x] * scale[x][q];
+                            most = fmaxf(fmaxf(most, v[0]), v[1]);
+                            most = fmaxf(fmaxf(most, v[2]), v[3]);
+                            uint8_t* p16 = to + (q * M + 16 * rt) * C::PS;
+                            if constexpr (C::WIDE) {
+                                uint2v hi, lost;
+                                uint32_t h, l;
+                                split_f16(v[0], v[1], h, l);
+                                hi.x = h;
+                                lost.x = l;
+                                split_f16(v[2], v[3], h, l);
+                                hi.y = h;
+                                lost.y = l;
+                                *reinterpret_cast<uint2v*>(p16) = hi;
+                                *reinterpret_cast<uint2v*>(p16 + NG * M * C::PS) = lost;
+                            } else {
+                                *reinterpret_cast<uint2v*>(p16) = uint2v{pack_f16(v[0], v[1]), pack_f16(v[2], v[3])};
+                            }
+                        }
+                    }
+                    return most > kTop || largest > kMostExp;
+                };
+                if (__any(put()) && lane == 0) lds.moved[b3] = 1;
+                __syncthreads();
+                if (lds.moved[b3]) {
+                    // references follow the largest of what the rows see
+                    float p[RT][4], base[RT];
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        float x = fmaxf(fmaxf(w[rt][0], w[rt][1]), fmaxf(w[rt][2], w[rt][3]));
+                        x = max_groups(x);
+                        if (g == 0) lds.top[wk * M + (wr * RT + rt) * 16 + m] = x;
+                    }
+                    __syncthreads();
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const int r = (wr * RT + rt) * 16 + m;
+                        base[rt] = ceilf(fmaxf(lds.top[r], lds.top[M + r]));   // (a whole number: factors are exact)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) p[rt][x] = __builtin_amdgcn_exp2f(w[rt][x] - base[rt]);
+                    }
+                    __syncthreads();
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        float y = 0.0f;
+#pragma unroll
+                        for (int q = 0; q < NG; ++q)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) y = fmaxf(y, p[rt][x] * scale[x][q]);
+                        y = max_groups(y);
+                        if (g == 0) lds.top[wk * M + (wr * RT + rt) * 16 + m] = y;
+                    }
+                    __syncthreads();
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const int r = (wr * RT + rt) * 16 + m;
+                        const float y = fmaxf(lds.top[r], lds.top[M + r]), was = ref[rt];
+                        if (base[rt] > kLow && base[rt] < __builtin_inff())
+                            ref[rt] = fmaxf(was, base[rt] + static_cast<float>(max(exponent(y) - kSet, kLeastRef)));
+                        const float f = __builtin_amdgcn_exp2f(was - ref[rt]);
+                        sum[rt] *= f;
+                        if (wk == 0 && g == 0) lds.shift[r] = f;
+                    }
+                    put();
+                    __syncthreads();
+                }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) sum[rt] += more[rt];
+                b3 = b3 == 2 ? 0 : b3 + 1;
+            }
+            __syncthreads();                   // (the value waves' last step)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const int r = (wr * RT + rt) * 16 + m;
+                const float l = sum_groups(sum[rt]);
+                if (g == 0) {
+                    lds.top[wk * M + r] = l;
+                    if (wk == 0 && r0 + r < rows) out[static_cast<int64_t>(r) * C::RS + D] = ref[rt];
+                }
+            }
             __syncthreads();
-            if (moved) {
-                // references and units follow the largest of what the rows see
+            if (tid < M && r0 + tid < rows) out[static_cast<int64_t>(tid) * C::RS + D + 1] = lds.top[tid] + lds.top[M + tid];
+        } else {
+            // keys of the wave: 8 vw + lane / LK, LK lanes to a key
+            const int kk = (C::KEYS / C::VALUES) * vw + lane / C::LK, part = lane % C::LK;
+            const ConstInts table = (ConstInts)(a.sq.table + static_cast<int64_t>(lo) * a.sq.max_pages);
+            const int slots = a.sq.max_pages - 1;
+            // the page of the 16 keys that the wave's are of in step i; absent past the
+            // sequence's end
+            const auto page_of = [&](int i) {
+                const int t = key0 + i * C::KEYS + (C::KEYS / C::VALUES) * vw / 16 * 16;
+                return i < steps && t < len ? table[min(t >> pg.logp, slots)] : -1;
+            };
+            // a lane's offsets from its wave's first key
+            const int ko = lane / C::LK, co = ko * (D / 2) + 16 * part, ro = ko * (2 * kRope) + 16 * part;
+            const auto group_of = [&](int x) { return (part + C::LK * x) * 32 / C::G; };
+            const auto load = [&](int page, int i, Raw<C>& w) {
+                const int t = key0 + i * C::KEYS + (C::KEYS / C::VALUES) * vw, off = t & (pg.page - 1);
+                // (an absent page has no bytes: its loads give zeros)
+                const bool here = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.sq.n_pages);
+                const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.pool + (here ? page : 0) * pg.page_bytes), 0,
+                                                                                   here ? static_cast<int>(pg.page_bytes) : 0, 0x00020000);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    float x = fmaxf(fmaxf(w[rt][0], w[rt][1]), fmaxf(w[rt][2], w[rt][3]));
-                    x = fmaxf(x, __shfl_xor(x, 16));
-                    x = fmaxf(x, __shfl_xor(x, 32));
-                    if (g == 0) top[wk * M + (wr * RT + rt) * 16 + m] = x;
+                for (int x = 0; x < C::CW / 4; ++x) {
+                    w.codes[x] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(r, co + 16 * C::LK * x, off * (D / 2), 0));
+                    const int at = ko * NG + group_of(x);
+                    if constexpr (C::SF32) w.scale[x] = __builtin_amdgcn_raw_buffer_load_b32(r, 4 * at, pg.scales + off * NG * 4, 0);
+                    else w.scale[x] = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, 2 * at, pg.scales + off * NG * 2, 0));
+                    // (symmetric: some byte, not looked at)
+                    w.zero[x] = static_cast<uint8_t>(__builtin_amdgcn_raw_buffer_load_b8(r, at / 2, pg.zeros + off * NG / 2, 0));
                 }
-                __syncthreads();
-                if (tid == 0) moved = 0;
-                int fall[RT];
+                w.rope = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(r, ro, pg.rope + off * (2 * kRope), 0));
+            };
+            // operands of a step
+            const uint32_t f0c = 0x64006400u ^ (pg.sym ? 0x00080008u : 0u), f1c = 0x54005400u ^ (pg.sym ? 0x00800080u : 0u);
+            const auto store = [&](const Raw<C>& w, int page, int b) {
+                uint8_t* to = lds.keys[b] + kk * C::VS;
+                if (lane == 0) lds.there[b][vw / 2] = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.sq.n_pages);   // (waves of the same 16 keys say the same)
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const int r = (wr * RT + rt) * 16 + m;
-                    const float x = fmaxf(fmaxf(top[r], top[M + r]), fmaxf(top[2 * M + r], top[3 * M + r]));
-                    const float was = ref[rt];
-                    // (a whole number, so that what follows from it is exact)
-                    if (x < __builtin_inff()) ref[rt] = fmaxf(was, ceilf(x));
-                    fall[rt] = static_cast<int>(fmaxf(was - ref[rt], -4000.0f));
-                    sum[rt] = __builtin_ldexpf(sum[rt], fall[rt]);
-                    float p[4];
+                for (int x = 0; x < C::CW / 4; ++x) {
+                    const int run = part + C::LK * x, at = ko * NG + group_of(x);
+                    const uint32_t z = pg.sym ? 8u : (w.zero[x] >> (4 * (at & 1))) & 15u;
+                    const uint32_t z0 = 0x64006400u + z * 0x00010001u, z1 = 0x54005400u + z * 0x00100010u;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(w[rt][i] - ref[rt]);
+                    for (int y = 0; y < 4; ++y) {
+                        uint32_t c = w.codes[x][y];
+                        uint4v k;
+                        k.x = pk_sub((c & 0x000F000Fu) ^ f0c, z0);
+                        k.y = pk_sub((c & 0x00F000F0u) ^ f1c, z1);
+                        c >>= 8;
+                        k.z = pk_sub((c & 0x000F000Fu) ^ f0c, z0);
+                        k.w = pk_sub((c & 0x00F000F0u) ^ f1c, z1);
+                        *reinterpret_cast<uint4v*>(to + 64 * run + 16 * y) = k;
+                    }
+                    if (run * 32 % C::G == 0) lds.scales[b][kk * NG + group_of(x)] = __uint_as_float(C::SF32 ? w.scale[x] : w.scale[x] << 16);
+                }
+                *reinterpret_cast<uint4v*>(to + 2 * D + 16 * part) = w.rope;
+            };
+            float4v acc[C::TILES][C::DT];
 #pragma unroll
-                    for (int q = 0; q < NG; ++q) {
-                        float y = 0.0f;
+            for (int x = 0; x < C::TILES; ++x)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (full || key + i <= pos[rt]) y = fmaxf(y, p[i] * scale[i][q]);
-                        y = fmaxf(y, __shfl_xor(y, 16));
-                        y = fmaxf(y, __shfl_xor(y, 32));
-                        if (g == 0) top_g[(wk * M + r) * NG + q] = y;
+                for (int d = 0; d < C::DT; ++d) acc[x][d] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+            const uint32_t grp = vw * C::DW / C::G;
+            // sums of the wave's dimensions over all rows, of the step in buffers b and p
+            const auto add = [&](int b, int p, bool moved) {
+                if (moved) {
+#pragma unroll
+                    for (int x = 0; x < C::TILES; ++x) {
+                        const float f = lds.shift[16 * x + m];
+#pragma unroll
+                        for (int d = 0; d < C::DT; ++d)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[x][d][i] *= f;
                     }
                 }
-                __syncthreads();
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const int r = (wr * RT + rt) * 16 + m;
-#pragma unroll
-                    for (int q = 0; q < NG; ++q) {
-                        float y = 0.0f;
-#pragma unroll
-                        for (int x = 0; x < C::WK; ++x) y = fmaxf(y, top_g[(x * M + r) * NG + q]);
-                        const int old = unit[rt][q] + fall[rt];
-                        const int now = max(old, (static_cast<int>(__float_as_uint(y) >> 23) & 255) - 127 - kSet);
-                        unit[rt][q] = min(max(now, -kUnit), kUnit);
-                        if (wk == 0 && g == 0) shift[r * NG + q] = __builtin_ldexpf(1.0f, max(old - unit[rt][q], -4000));
-                    }
-                }
-                put();
-                __syncthreads();
-#pragma unroll
-                for (int x = 0; x < C::TILES; ++x) {
-                    const float f = shift[(16 * x + m) * NG + wave * C::DW / C::G];
-#pragma unroll
-                    for (int d = 0; d < C::DT; ++d)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[x][d][i] *= f;
-                }
-            }
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) sum[rt] += more[rt];
-
-            // sums of the wave's dimensions over all rows
-            const uint8_t* pr = probs + (wave * C::DW / C::G * M + m) * C::PS + 16 * g;
-            const uint8_t* va = values + (4 * g + m / 4) * C::VS + (wave * C::DW + 4 * (m % 4)) * 2;
-#pragma unroll
-            for (int k = 0; k < C::KEYS / 32; ++k) {
-                uint4v p[T][C::TILES];
+                const uint8_t* pr = lds.probs[p] + (grp * M + m) * C::PS + 16 * g;
+                const uint8_t* va = lds.keys[b] + (4 * g + m / 4) * C::VS + (vw * C::DW + 4 * (m % 4)) * 2;
+                uint4v pb[T][C::TILES];
 #pragma unroll
                 for (int t = 0; t < T; ++t)
 #pragma unroll
-                    for (int x = 0; x < C::TILES; ++x) p[t][x] = *reinterpret_cast<const uint4v*>(pr + (t * NG * M + 16 * x) * C::PS + 64 * k);
+                    for (int x = 0; x < C::TILES; ++x) pb[t][x] = *reinterpret_cast<const uint4v*>(pr + (t * NG * M + 16 * x) * C::PS);
 #pragma unroll
                 for (int d = 0; d < C::DT; ++d) {
-                    const uint2v v0 = transposed(va + (32 * k) * C::VS + 32 * d), v1 = transposed(va + (32 * k + 16) * C::VS + 32 * d);
+                    const uint2v v0 = transposed(va + 32 * d), v1 = transposed(va + 16 * C::VS + 32 * d);
                     const uint4v v = {v0.x, v0.y, v1.x, v1.y};
 #pragma unroll
-                    for (int x = 0; x < C::TILES; ++x)
+                    for (int t = T - 1; t >= 0; --t)
 #pragma unroll
-                        for (int t = T - 1; t >= 0; --t) acc[x][d] = mfma_f16(v, p[t][x], acc[x][d]);
+                        for (int x = 0; x < C::TILES; ++x) acc[x][d] = mfma_f16(v, pb[t][x], acc[x][d]);
                 }
+            };
+            Raw<C> raw[kAhead];
+            int page[kAhead + 1];              // of the steps in raw, and of the one after
+#pragma unroll
+            for (int i = 0; i <= kAhead; ++i) page[i] = page_of(i);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) load(page[i], i, raw[i]);
+            // takes a step out of raw[0], and loads step i
+            const auto take = [&](int i, int b) {
+                store(raw[0], page[0], b);
+#pragma unroll
+                for (int x = 0; x + 1 < kAhead; ++x) raw[x] = raw[x + 1];
+#pragma unroll
+                for (int x = 0; x < kAhead; ++x) page[x] = page[x + 1];
+                load(page[kAhead - 1], i, raw[kAhead - 1]);
+                page[kAhead] = page_of(i + 1);
+            };
+            take(kAhead, 0);
+            __syncthreads();
+            int b3 = 0;                        // the buffer of the step that scores are formed of
+            bool moved = false;
+            for (int i = 0; i < steps; ++i) {
+                const int after = b3 == 2 ? 0 : b3 + 1, before = b3 == 0 ? 2 : b3 - 1;
+                take(i + 1 + kAhead, after);
+                if (i > 0) add(before, (i + 1) & 1, moved);
+                __syncthreads();
+                moved = lds.moved[b3] != 0;
+                if (moved) {
+                    __syncthreads();
+                    __syncthreads();
+                    __syncthreads();
+                    __syncthreads();
+                }
+                b3 = after;
+            }
+            if (steps > 0) add(b3 == 0 ? 2 : b3 - 1, (steps + 1) & 1, moved);
+            __syncthreads();
+            // the segment's sums
+#pragma unroll
+            for (int x = 0; x < C::TILES; ++x) {
+                const int r = 16 * x + m;
+                if (r0 + r < rows)
+#pragma unroll
+                    for (int d = 0; d < C::DT; ++d)
+                        *reinterpret_cast<float4v*>(out + static_cast<int64_t>(r) * C::RS + vw * C::DW + 16 * d + 4 * g) = acc[x][d];
             }
             __syncthreads();
         }
-
-        // the segment's sums: rows of the unit if it is whole, else one of the
-        // workgroup's two parts
-        const bool whole = k0 == 0 && k1 == per;
-        float* out = whole ? work.whole + (row_at + r0) * C::RS
-                           : work.part + (static_cast<int64_t>(blockIdx.x) * 2 + (k0 > 0 ? 0 : 1)) * M * C::RS;
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const int r = (wr * RT + rt) * 16 + m;
-            float l = sum[rt];
-            l += __shfl_xor(l, 16);
-            l += __shfl_xor(l, 32);
-            if (g == 0) {
-                top[wk * M + r] = l;
-                if (wk == 0) {
-#pragma unroll
-                    for (int q = 0; q < NG; ++q) units[r * NG + q] = unit[rt][q];
-                    if (r0 + r < rows) out[static_cast<int64_t>(r) * C::RS + D] = ref[rt];
-                }
-            }
-        }
-        __syncthreads();
-        if (tid < M && r0 + tid < rows)
-            out[static_cast<int64_t>(tid) * C::RS + D + 1] = (top[tid] + top[M + tid]) + (top[2 * M + tid] + top[3 * M + tid]);
-#pragma unroll
-        for (int x = 0; x < C::TILES; ++x) {
-            const int r = 16 * x + m, e = units[r * NG + wave * C::DW / C::G];
-            if (r0 + r < rows)
-#pragma unroll
-                for (int d = 0; d < C::DT; ++d) {
-                    float4v v = acc[x][d];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = __builtin_ldexpf(v[i], e);
-                    *reinterpret_cast<float4v*>(out + static_cast<int64_t>(r) * C::RS + wave * C::DW + 16 * d + 4 * g) = v;
-                }
-        }
-        __syncthreads();
     }
 }
 
@@ -757,7 +810,7 @@ int attn_workers(int* workers) {
         int cus;
         e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
         if (e != hipSuccess) return static_cast<int>(e);
-        n = C::WGS * cus;
+        n = cus;
         if (dev < kMaxDevices) known[dev].store(n, std::memory_order_relaxed);
     }
     *workers = n;
@@ -770,11 +823,16 @@ int attn_do(const LatentAttnArgs* a, int* workers, void* stream) {
     return attn_launch<C>(*a, static_cast<hipStream_t>(stream));
 }
 
-template <int D, int NG>
+template <int D, int NG, bool SF32>
 int pick_rows(const LatentAttnKey& k, const LatentAttnArgs* a, int* workers, void* stream) {
-    if (k.wide) return k.wr == 1 ? attn_do<Cfg<D, NG, true, 1, 1>>(a, workers, stream) : attn_do<Cfg<D, NG, true, 1, 2>>(a, workers, stream);
-    if (k.rt == 1) return k.wr == 1 ? attn_do<Cfg<D, NG, false, 1, 1>>(a, workers, stream) : attn_do<Cfg<D, NG, false, 1, 2>>(a, workers, stream);
-    return attn_do<Cfg<D, NG, false, 2, 2>>(a, workers, stream);
+    if (k.wide) return k.wr == 1 ? attn_do<Cfg<D, NG, SF32, true, 1, 1>>(a, workers, stream) : attn_do<Cfg<D, NG, SF32, true, 1, 2>>(a, workers, stream);
+    if (k.rt == 1) return k.wr == 1 ? attn_do<Cfg<D, NG, SF32, false, 1, 1>>(a, workers, stream) : attn_do<Cfg<D, NG, SF32, false, 1, 2>>(a, workers, stream);
+    return attn_do<Cfg<D, NG, SF32, false, 2, 2>>(a, workers, stream);
+}
+
+template <int D, int NG>
+int pick_scales(const LatentAttnKey& k, const LatentAttnArgs* a, int* workers, void* stream) {
+    return k.sf32 ? pick_rows<D, NG, true>(k, a, workers, stream) : pick_rows<D, NG, false>(k, a, workers, stream);
 }
 
 }  // namespace

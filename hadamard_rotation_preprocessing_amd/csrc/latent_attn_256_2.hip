@@ -3,6 +3,6 @@
 
 namespace hr {
 int latent_attn_256_2(const LatentAttnKey& k, const LatentAttnArgs* a, int* workers, void* stream) {
-    return pick_rows<256, 2>(k, a, workers, stream);
+    return pick_scales<256, 2>(k, a, workers, stream);
 }
 }  // namespace hr

@@ -3,6 +3,6 @@
 
 namespace hr {
 int latent_attn_512_2(const LatentAttnKey& k, const LatentAttnArgs* a, int* workers, void* stream) {
-    return pick_rows<512, 2>(k, a, workers, stream);
+    return pick_scales<512, 2>(k, a, workers, stream);
 }
 }  // namespace hr

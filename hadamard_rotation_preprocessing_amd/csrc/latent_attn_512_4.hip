@@ -3,6 +3,6 @@
 
 namespace hr {
 int latent_attn_512_4(const LatentAttnKey& k, const LatentAttnArgs* a, int* workers, void* stream) {
-    return pick_rows<512, 4>(k, a, workers, stream);
+    return pick_scales<512, 4>(k, a, workers, stream);
 }
 }  // namespace hr
