@@ -60,7 +60,8 @@ constexpr float kTop = 0x1p15f;       // largest probability (float16 ends at 65
 constexpr int kSet = 8;               // log2 of the largest one when a reference is set
 constexpr int kLeastRef = -100;       // how far (log2) a reference may lie below the largest score
 constexpr float kMostExp = 0x1p110f;  // largest exponential
-constexpr int kAhead = 3;             // steps that keys are loaded ahead
+constexpr int kBatch = 4;             // operands of scores loaded at once
+constexpr int kAhead = 3;             // steps that keys are loaded ahead (as many as there are buffers)
 constexpr int kQTop = 14;             // a query's largest element is below 2^kQTop in float16
 
 __device__ __forceinline__ float4v mfma_f16(uint4v a, uint4v b, float4v c) {
@@ -111,31 +112,46 @@ struct Cfg {
     static constexpr int DW = D / VALUES, DT = DW / 16;   // dimensions of a value wave
     static constexpr int LK = 64 / (KEYS / VALUES);       // lanes that share a key's codes
     static constexpr int CW = D / 8 / LK;          // words of codes of a lane
-    static constexpr int VS = 2 * (D + kRope) + 16;       // bytes of a key's operands in LDS
+    static constexpr int VS = 2 * (D + kRope) + 32;       // bytes of a key's operands in LDS (64 banks of 4: an eighth more than a multiple of all)
     static constexpr int PS = 2 * KEYS + 16;       // bytes of a row's probabilities
     static constexpr int QS = 2 * (T * D + TR * kRope);   // bytes of a row's query in the scratch
     static constexpr int RS = D + 4;               // floats of a row's sums
 };
 
-// A sequence of the call, clamped so that nothing leaves its buffer.
+// Integers read at an address that is the same in all lanes: through the scalar
+// cache, into scalar registers.
+typedef const int32_t __attribute__((address_space(4)))* ConstInts;
+typedef const int64_t __attribute__((address_space(4)))* ConstLongs;
+
+// A sequence of the call, clamped so that nothing leaves its buffer.  UNI: b is the same
+// in all lanes.
 struct Seq {
     int start, n, len;
 };
+template <bool UNI>
+__device__ __forceinline__ int int_at(const int32_t* p, int b) {
+    if constexpr (UNI) return ((ConstInts)(p))[b];
+    else return p[b];
+}
+template <bool UNI>
 __device__ __forceinline__ int cu_at(const CacheSeqs& s, int b) {
-    const int c = s.cu ? s.cu[b] : b * s.per;
+    const int c = s.cu ? int_at<UNI>(s.cu, b) : b * s.per;
     return min(max(c, 0), s.tokens);
 }
+template <bool UNI>
 __device__ __forceinline__ Seq seq_at(const CacheSeqs& s, int logp, int b) {
     Seq r;
-    r.start = cu_at(s, b);
-    r.n = max(cu_at(s, b + 1) - r.start, 0);
-    r.len = static_cast<int>(min(static_cast<int64_t>(max(s.lens[b], 0)), static_cast<int64_t>(s.max_pages) << logp));
+    r.start = cu_at<UNI>(s, b);
+    r.n = max(cu_at<UNI>(s, b + 1) - r.start, 0);
+    r.len = static_cast<int>(min(static_cast<int64_t>(max(int_at<UNI>(s.lens, b), 0)), static_cast<int64_t>(s.max_pages) << logp));
     return r;
 }
-// items of a unit of a sequence (kItem keys each), and its units
-constexpr int kItem = 64;
-template <class C>
-__device__ __forceinline__ int items_of(const Seq& s) { return static_cast<int>((static_cast<int64_t>(s.len) + kItem - 1) / kItem); }
+// items of a unit of a sequence, and its units.  An item is kItem keys; a unit that has
+// any counts kSetUp items more, before them, for what it costs beside its keys.
+constexpr int kItem = 64, kSetUp = 3;
+__device__ __forceinline__ int items_of(const Seq& s) {
+    return s.len > 0 ? static_cast<int>((static_cast<int64_t>(s.len) + kItem - 1) / kItem) + kSetUp : 0;
+}
 template <class C>
 __device__ __forceinline__ int units_of(const Seq& s, int heads) {
     return static_cast<int>((static_cast<int64_t>(s.n) * heads + C::M - 1) / C::M);
@@ -165,7 +181,7 @@ __device__ __forceinline__ float sum_groups(float v) {
     v += __shfl_xor(v, 16);
     return v + __shfl_xor(v, 32);
 }
-// N floats (a multiple of 4) out of LDS
+// N floats (a multiple of 4)
 template <int N>
 __device__ __forceinline__ void load_floats(const float* p, float* v) {
 #pragma unroll
@@ -178,6 +194,11 @@ __device__ __forceinline__ void load_floats(const float* p, float* v) {
     }
 }
 
+// In LDS a key's operands stand in runs of 64 bytes, four lanes' 16 bytes, whose order
+// within run r is g ^ swizzle(r): so that the lanes that write a key, a run each, reach
+// banks of their own.
+__device__ __forceinline__ constexpr int swizzle(int r) { return (r >> 1) & 3; }
+
 // 16 dimensions of four keys out of LDS: lane m of 16 gives the address of its four
 // dimensions 4 (m % 4) of key m / 4, and gets dimension m of the four keys.
 __device__ __forceinline__ uint2v transposed(const uint8_t* p) {
@@ -189,6 +210,7 @@ __device__ __forceinline__ uint2v transposed(const uint8_t* p) {
 template <class C>
 struct Work {
     int64_t* first;      // [rows + 1]: items before those of a sequence
+    int32_t* start;      // [workers]: the sequence that a workgroup's items begin in
     float* factor;       // [query rows][4]: of a row's scores, and of its products with rotary keys before
     uint8_t* query;
     float* whole;        // [query rows][RS]: sums, the reference, and the sum of exponentials
@@ -197,6 +219,8 @@ struct Work {
         const int64_t rows = static_cast<int64_t>(a.sq.tokens) * a.heads;
         first = reinterpret_cast<int64_t*>(a.work);
         uint8_t* p = a.work + latent_first_bytes(a.sq.rows);
+        start = reinterpret_cast<int32_t*>(p);
+        p += latent_start_bytes(a.workers);
         factor = reinterpret_cast<float*>(p);
         query = p + rows * 16;
         whole = reinterpret_cast<float*>(query + rows * C::QS);
@@ -212,27 +236,43 @@ __global__ void __launch_bounds__(256) latent_query(const LatentAttnArgs a) {
     constexpr int D = C::D, LPV = D / 16, R = kRope / LPV;
     const Work<C> work(a);
     if (blockIdx.x == 0) {     // the numbering of items
-        __shared__ int64_t sums[256];
+        __shared__ int64_t sums[4];
         int64_t before = 0;
         for (int r0 = 0; r0 < a.sq.rows; r0 += 256) {
+            const int r = r0 + threadIdx.x;
             int64_t v = 0;
-            if (r0 + static_cast<int>(threadIdx.x) < a.sq.rows) {
-                const Seq s = seq_at(a.sq, a.pg.logp, r0 + threadIdx.x);
-                v = static_cast<int64_t>(items_of<C>(s)) * units_of<C>(s, a.heads);
+            if (r < a.sq.rows) {
+                const Seq s = seq_at<false>(a.sq, a.pg.logp, r);
+                v = static_cast<int64_t>(items_of(s)) * units_of<C>(s, a.heads);
             }
-            sums[threadIdx.x] = v;
-            __syncthreads();
-            for (int x = 1; x < 256; x *= 2) {
-                const int64_t y = static_cast<int>(threadIdx.x) >= x ? sums[threadIdx.x - x] : 0;
-                __syncthreads();
-                sums[threadIdx.x] += y;
-                __syncthreads();
+            for (int x = 1; x < 64; x *= 2) {
+                const int64_t y = __shfl_up(v, x);
+                if ((threadIdx.x & 63) >= x) v += y;
             }
-            if (r0 + static_cast<int>(threadIdx.x) < a.sq.rows) work.first[r0 + threadIdx.x + 1] = before + sums[threadIdx.x];
-            before += sums[255];
             __syncthreads();
+            if ((threadIdx.x & 63) == 63) sums[threadIdx.x / 64] = v;
+            __syncthreads();
+            for (int x = 0; x < 4; ++x) {
+                if (x < static_cast<int>(threadIdx.x / 64)) v += sums[x];
+            }
+            if (r < a.sq.rows) work.first[r + 1] = before + v;
+            before += sums[0] + sums[1] + sums[2] + sums[3];
         }
         if (threadIdx.x == 0) work.first[0] = 0;
+        __threadfence_block();
+        __syncthreads();
+        // the sequence that each workgroup begins in
+        const int used = used_workers(before, a.workers);
+        for (int w = threadIdx.x; w < used; w += 256) {
+            const int64_t item = begin_of(before, w, used);
+            int lo = 0, hi = a.sq.rows - 1;    // the last sequence that begins at or before the item
+            while (lo < hi) {
+                const int mid = lo + (hi - lo + 1) / 2;
+                if (work.first[mid] <= item) lo = mid;
+                else hi = mid - 1;
+            }
+            work.start[w] = lo;
+        }
     }
     const int64_t row = (int64_t{blockIdx.x} * 256 + threadIdx.x) / LPV, total = static_cast<int64_t>(a.sq.tokens) * a.heads;
     const int lane = threadIdx.x & 63, e = lane % LPV;
@@ -310,10 +350,6 @@ struct Lds {
     int moved[3];              // whether a reference moves after a step
 };
 
-// Integers read at an address that is the same in all lanes: through the scalar
-// cache, into scalar registers.
-typedef const int32_t __attribute__((address_space(4)))* ConstInts;
-
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArgs a) {
     constexpr int D = C::D, NG = C::NG, RT = C::RT, T = C::T, M = C::M;
@@ -325,33 +361,30 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
     const int vw = wave - C::SCORES;                     // of a value wave
     const Work<C> work(a);
     const LatentPage& pg = a.pg;
-    const int64_t total = work.first[a.sq.rows];
+    const ConstLongs before = (ConstLongs)(work.first);
+    const int64_t total = before[a.sq.rows];
     const int used = used_workers(total, gridDim.x);
     const int worker = worker_of(blockIdx.x, gridDim.x);
     if (worker >= used) return;
     const int64_t end = begin_of(total, worker + 1, used);
     int64_t item = begin_of(total, worker, used);
+    int lo = ((ConstInts)(work.start))[worker];
     while (item < end) {
-        int lo = 0, hi = a.sq.rows - 1;        // the last sequence that begins at or before this item
-        while (lo < hi) {
-            const int mid = lo + (hi - lo + 1) / 2;
-            if (work.first[mid] <= item) lo = mid;
-            else hi = mid - 1;
-        }
-        lo = __builtin_amdgcn_readfirstlane(lo);
-        const Seq s = seq_at(a.sq, pg.logp, lo);
-        const int per = items_of<C>(s);
-        const int64_t in_seq = item - work.first[lo];
-        const int rb = __builtin_amdgcn_readfirstlane(static_cast<int>(in_seq / per)), k0 = __builtin_amdgcn_readfirstlane(static_cast<int>(in_seq % per));
-        const int k1 = __builtin_amdgcn_readfirstlane(static_cast<int>(min(static_cast<int64_t>(per), k0 + end - item)));
-        item += k1 - k0;
-        const int len = __builtin_amdgcn_readfirstlane(s.len), rows = __builtin_amdgcn_readfirstlane(s.n) * a.heads;
-        const int r0 = rb * M, first = len - __builtin_amdgcn_readfirstlane(s.n);
-        const int64_t row_at = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(s.start)) * a.heads;
+        while (before[lo + 1] <= item) ++lo;
+        const Seq s = seq_at<true>(a.sq, pg.logp, lo);
+        const int per = items_of(s);
+        const int64_t in_seq = item - before[lo];
+        const int rb = static_cast<int>(in_seq / per), i0 = static_cast<int>(in_seq % per);
+        const int i1 = static_cast<int>(min(static_cast<int64_t>(per), i0 + end - item));
+        item += i1 - i0;
+        if (i1 <= kSetUp) continue;            // none of the unit's keys
+        const int k0 = max(i0 - kSetUp, 0), k1 = i1 - kSetUp;
+        const int len = s.len, rows = s.n * a.heads, r0 = rb * M, first = len - s.n;
+        const int64_t row_at = static_cast<int64_t>(s.start) * a.heads;
         const int last_row = min(r0 + M, rows) - 1;
         const int limit = a.causal ? min(max(first + last_row / a.heads + 1, 0), len) : len;   // no row sees keys past it
         const int steps = (min(k1 * (kItem), limit) - k0 * kItem + C::KEYS - 1) / C::KEYS;     // (may be negative)
-        const bool whole = k0 == 0 && k1 == per;
+        const bool whole = k0 == 0 && i1 == per;
         float* out = whole ? work.whole + (row_at + r0) * C::RS
                            : work.part + (static_cast<int64_t>(worker) * 2 + (k0 > 0 ? 0 : 1)) * M * C::RS;
         const int key0 = k0 * kItem;
@@ -390,44 +423,53 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
             __syncthreads();                   // (the first keys are there)
             int b3 = 0;
             for (int i = 0; i < steps; ++i) {
-                if (tid == 0) lds.moved[b3 == 2 ? 0 : b3 + 1] = 0;
-                const uint8_t* keys = lds.keys[b3] + (16 * wk + m) * C::VS + 16 * g;
+                const uint8_t* keys = lds.keys[b3] + (16 * wk + m) * C::VS;
                 float scale[4][NG];
                 load_floats<4 * NG>(lds.scales[b3] + (16 * wk + 4 * g) * NG, &scale[0][0]);
-                float4v w[RT];
+                // operands: two of the rotary key, then the codes'; kBatch of them are on
+                // their way while as many are worked on
+                float4v w[RT], c[RT];
+                uint4v k[2][kBatch];
+                const auto operand = [&](int x) { return *reinterpret_cast<const uint4v*>(keys + (x < 2 ? 2 * D + 64 * x + 16 * g : 64 * (x - 2) + 16 * (g ^ swizzle(x - 2)))); };
+                constexpr int ALL = C::KS + 2;
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) w[rt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint4v k = *reinterpret_cast<const uint4v*>(keys + 2 * D + 64 * x);
+                for (int x = 0; x < kBatch; ++x) k[0][x] = operand(x);
 #pragma unroll
-                    for (int t = C::TR - 1; t >= 0; --t)
+                for (int x0 = 0; x0 < ALL; x0 += kBatch) {
+                    HR_PHASE();
 #pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) w[rt] = mfma_bf16(k, rope[rt][t][x], w[rt]);
-                }
+                    for (int x = x0 + kBatch; x < x0 + 2 * kBatch && x < ALL; ++x) k[x / kBatch % 2][x % kBatch] = operand(x);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
+                    for (int x = x0; x < x0 + kBatch && x < ALL; ++x) {
+                        const uint4v kx = k[x / kBatch % 2][x % kBatch];
+                        if (x < 2) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) w[rt][x] *= rfactor[rt];
+                            for (int t = C::TR - 1; t >= 0; --t)
 #pragma unroll
-                for (int q = 0; q < NG; ++q) {
-                    float4v c[RT];
+                                for (int rt = 0; rt < RT; ++rt) w[rt] = mfma_bf16(kx, rope[rt][t][x], w[rt]);
+                            if (x == 1)
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) c[rt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+                                for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                    for (int x = 0; x < C::KG; ++x) {
-                        const int ks = q * C::KG + x;
-                        if (ks % 4 == 0) HR_PHASE();
-                        const uint4v k = *reinterpret_cast<const uint4v*>(keys + 64 * ks);
+                                    for (int y = 0; y < 4; ++y) w[rt][y] *= rfactor[rt];
+                        } else {
+                            const int ks = x - 2, q = ks / C::KG;
+                            if (ks % C::KG == 0)
 #pragma unroll
-                        for (int t = T - 1; t >= 0; --t)
+                                for (int rt = 0; rt < RT; ++rt) c[rt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                            for (int rt = 0; rt < RT; ++rt) c[rt] = mfma_f16(k, query[rt][t][ks], c[rt]);
+                            for (int t = T - 1; t >= 0; --t)
+#pragma unroll
+                                for (int rt = 0; rt < RT; ++rt) c[rt] = mfma_f16(kx, query[rt][t][ks], c[rt]);
+                            if (ks % C::KG == C::KG - 1)
+#pragma unroll
+                                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y) w[rt][y] = __builtin_fmaf(c[rt][y], scale[y][q], w[rt][y]);
+                        }
                     }
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) w[rt][x] = __builtin_fmaf(c[rt][x], scale[x][q], w[rt][x]);
                 }
                 HR_PHASE();
                 const int t0 = key0 + i * C::KEYS + 16 * wk, key = t0 + 4 * g;
@@ -443,13 +485,13 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
 #pragma unroll
                         for (int x = 0; x < 4; ++x) w[rt][x] = key + x > bound ? -__builtin_inff() : w[rt][x];
                     }
+                    // an unseen key's scale may be anything, and its probability is 0: what is
+                    // multiplied by it is finite (a key that is seen has a NaN score then)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int q = 0; q < NG; ++q) scale[x][q] = fminf(scale[x][q], 0x1.fffffep127f);
                 }
-                // an unseen key's scale may be anything, and its probability is 0: what is
-                // multiplied by it is finite (a key that is seen has a NaN score then)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int q = 0; q < NG; ++q) scale[x][q] = fminf(scale[x][q], 0x1.fffffep127f);
                 // probabilities, to LDS: keys 16 wk + 4 g + x stand at 8 g + 4 wk + x
                 uint8_t* to = lds.probs[i & 1] + (wr * 16 * RT + m) * C::PS + 16 * g + 8 * wk;
                 float more[RT];
@@ -598,7 +640,7 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
                         c >>= 8;
                         k.z = pk_sub((c & 0x000F000Fu) ^ f0c, z0);
                         k.w = pk_sub((c & 0x00F000F0u) ^ f1c, z1);
-                        *reinterpret_cast<uint4v*>(to + 64 * run + 16 * y) = k;
+                        *reinterpret_cast<uint4v*>(to + 64 * run + 16 * (y ^ swizzle(part))) = k;
                     }
                     if (run * 32 % C::G == 0) lds.scales[b][kk * NG + group_of(x)] = __uint_as_float(C::SF32 ? w.scale[x] : w.scale[x] << 16);
                 }
@@ -623,7 +665,7 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
                     }
                 }
                 const uint8_t* pr = lds.probs[p] + (grp * M + m) * C::PS + 16 * g;
-                const uint8_t* va = lds.keys[b] + (4 * g + m / 4) * C::VS + (vw * C::DW + 4 * (m % 4)) * 2;
+                const uint8_t* va = lds.keys[b] + (4 * g + m / 4) * C::VS + vw * C::DW * 2 + m % 2 * 8;
                 uint4v pb[T][C::TILES];
 #pragma unroll
                 for (int t = 0; t < T; ++t)
@@ -631,7 +673,9 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
                     for (int x = 0; x < C::TILES; ++x) pb[t][x] = *reinterpret_cast<const uint4v*>(pr + (t * NG * M + 16 * x) * C::PS);
 #pragma unroll
                 for (int d = 0; d < C::DT; ++d) {
-                    const uint2v v0 = transposed(va + 32 * d), v1 = transposed(va + 16 * C::VS + 32 * d);
+                    // (dimensions 16 d + 4 (m % 4) of the wave's: half a 16-byte part of run d / 2)
+                    const int at = d / 2 * 64 + 16 * ((d % 2 * 2 + m % 4 / 2) ^ swizzle(vw * (C::DW / 32) + d / 2));
+                    const uint2v v0 = transposed(va + at), v1 = transposed(va + 16 * C::VS + at);
                     const uint4v v = {v0.x, v0.y, v1.x, v1.y};
 #pragma unroll
                     for (int t = T - 1; t >= 0; --t)
@@ -639,41 +683,47 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
                         for (int x = 0; x < C::TILES; ++x) acc[x][d] = mfma_f16(v, pb[t][x], acc[x][d]);
                 }
             };
+            // A step's codes have a place in raw that depends on its number alone, and the
+            // loop is unrolled: a load on its way cannot be moved to another register.
             Raw<C> raw[kAhead];
-            int page[kAhead + 1];              // of the steps in raw, and of the one after
+            int page[kAhead], next[kAhead];    // of the step in a place, and of the one after it
 #pragma unroll
-            for (int i = 0; i <= kAhead; ++i) page[i] = page_of(i);
+            for (int x = 0; x < kAhead; ++x) {
+                page[x] = page_of(x);
+                next[x] = page_of(x + kAhead);
+            }
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) load(page[i], i, raw[i]);
-            // takes a step out of raw[0], and loads step i
-            const auto take = [&](int i, int b) {
-                store(raw[0], page[0], b);
-#pragma unroll
-                for (int x = 0; x + 1 < kAhead; ++x) raw[x] = raw[x + 1];
-#pragma unroll
-                for (int x = 0; x < kAhead; ++x) page[x] = page[x + 1];
-                load(page[kAhead - 1], i, raw[kAhead - 1]);
-                page[kAhead] = page_of(i + 1);
+            for (int x = 0; x < kAhead; ++x) load(page[x], x, raw[x]);
+            // operands of step i, which is in place X, and the loads of the step after
+            const auto take = [&](auto X, int i) {
+                store(raw[X], page[X], X);
+                page[X] = next[X];
+                load(page[X], i + kAhead, raw[X]);
+                next[X] = page_of(i + 2 * kAhead);
             };
-            take(kAhead, 0);
+            take(std::integral_constant<int, 0>(), 0);
             __syncthreads();
-            int b3 = 0;                        // the buffer of the step that scores are formed of
             bool moved = false;
-            for (int i = 0; i < steps; ++i) {
-                const int after = b3 == 2 ? 0 : b3 + 1, before = b3 == 0 ? 2 : b3 - 1;
-                take(i + 1 + kAhead, after);
-                if (i > 0) add(before, (i + 1) & 1, moved);
+            // the interval in which the scores of step i are formed, in buffer B
+            const auto interval = [&](auto B, int i) {
+                if (vw == 0 && lane == 0) lds.moved[(B + 1) % 3] = 0;
+                take(std::integral_constant<int, (B + 1) % 3>(), i + 1);
+                if (i > 0) add((B + 2) % 3, (i + 1) & 1, moved);
                 __syncthreads();
-                moved = lds.moved[b3] != 0;
+                moved = lds.moved[B] != 0;
                 if (moved) {
                     __syncthreads();
                     __syncthreads();
                     __syncthreads();
                     __syncthreads();
                 }
-                b3 = after;
+            };
+            for (int i = 0; i < steps; i += 3) {
+                interval(std::integral_constant<int, 0>(), i);
+                if (i + 1 < steps) interval(std::integral_constant<int, 1>(), i + 1);
+                if (i + 2 < steps) interval(std::integral_constant<int, 2>(), i + 2);
             }
-            if (steps > 0) add(b3 == 0 ? 2 : b3 - 1, (steps + 1) & 1, moved);
+            if (steps > 0) add((steps - 1) % 3, (steps + 1) & 1, moved);
             __syncthreads();
             // the segment's sums
 #pragma unroll
@@ -692,97 +742,133 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
 // ---------------------------------------------------------------------------
 // the results
 
-// A workgroup takes one row: eight (or 16) groups of D / 16 lanes take its parts in
-// turn, and the first of them adds what they have, in their order.
+// What a group of D / 16 lanes adds up of a row's sums, 16 elements to a lane.
+struct Joined {
+    float v[16] = {}, ref = kLow, l = 0.0f;
+    __device__ __forceinline__ void add(const float (&x)[16], float xr, float xl) {
+        if (xl == 0.0f) return;
+        const float now = fmaxf(ref, xr), f0 = __builtin_amdgcn_exp2f(ref - now), f1 = __builtin_amdgcn_exp2f(xr - now);
+        l = l * f0 + xl * f1;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = v[i] * f0 + x[i] * f1;
+        ref = now;
+    }
+};
+
+// Where a row's sums are: `whole`, or in `parts` parts from workgroup w0 on.
+struct Where {
+    int parts, w0;
+    int64_t u0;                // the first item of the unit's keys
+    int in_unit;               // the row's place in its unit
+};
+template <class C, bool UNI>
+__device__ __forceinline__ Where where_of(const LatentAttnArgs& a, const Work<C>& work, int64_t total, int used, int64_t row) {
+    const int t = static_cast<int>(static_cast<uint32_t>(row) / a.heads);
+    int lo = 0, hi = a.sq.rows - 1;                // the last sequence that begins at or before this token
+    while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (cu_at<UNI>(a.sq, mid) <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    const Seq s = seq_at<UNI>(a.sq, a.pg.logp, lo);
+    Where w{0, 0, 0, 0};
+    const int per = items_of(s);
+    if (t < s.start || t >= s.start + s.n || per == 0) return w;   // (no workgroup had this row)
+    const int64_t r = row - static_cast<int64_t>(s.start) * a.heads;
+    w.in_unit = static_cast<int>(r % C::M);
+    w.u0 = (UNI ? ((ConstLongs)(work.first))[lo] : work.first[lo]) + r / C::M * per + kSetUp;
+    const int64_t last = w.u0 + per - kSetUp - 1;
+    w.w0 = static_cast<int>(((w.u0 + 1) * used - 1) / total);
+    w.parts = static_cast<int>(((last + 1) * used - 1) / total) - w.w0 + 1;
+    return w;
+}
+
 template <class C, class Out>
-__global__ void __launch_bounds__(256) latent_finish(const LatentAttnArgs a, int workers) {
+__device__ __forceinline__ void finish_row(const LatentAttnArgs& a, int64_t row, const Joined& j) {
+    constexpr int LPV = C::D / 16;
+    const int e = threadIdx.x % LPV, lane = threadIdx.x & 63;
+    const int t = static_cast<int>(static_cast<uint32_t>(row) / a.heads), h = static_cast<int>(static_cast<uint32_t>(row) % a.heads);
+    const float inverse = 1.0f / j.l;
+    // back to the elements' own order
+    float y[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i / 8 * 8 + (i % 2) * 4 + (i % 8) / 2] = j.l == 0.0f ? 0.0f : j.v[i] * inverse;
+    if (a.rotate) hadamard<C::D>(y, lane, a.norm);
+    Out* out = static_cast<Out*>(a.out) + t * a.o_st + h * a.o_sh + 16 * e;
+#pragma unroll
+    for (int i = 0; i < 16; i += 16 / sizeof(Out)) {
+        uint4v x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (sizeof(Out) == 2) x[k] = to_bf16(y[i + 2 * k]) | (to_bf16(y[i + 2 * k + 1]) << 16);
+            else x[k] = __float_as_uint(y[i + k]);
+        }
+        *reinterpret_cast<uint4v*>(out + i) = x;
+    }
+    if (a.lse && e == 0) a.lse[row] = j.l == 0.0f ? -__builtin_inff() : (j.ref + __builtin_amdgcn_logf(j.l)) * 0.6931471805599453f;
+}
+
+// Rows of few parts are joined by a group of D / 16 lanes each, the first workgroups'; a
+// row of many by a workgroup of its own, whose groups take its parts in turn and whose
+// first group adds what they have.  Either way a row's sums are added in one order, that
+// of its keys, or that of the groups and of its keys in them.
+constexpr int kFew = 8;
+template <class C, class Out>
+__global__ void __launch_bounds__(256) latent_finish(const LatentAttnArgs a) {
     constexpr int D = C::D, LPV = D / 16, GROUPS = 256 / LPV;
     __shared__ __attribute__((aligned(16))) float sums[GROUPS][D];
     __shared__ float refs[GROUPS], exps[GROUPS];
     const Work<C> work(a);
-    const int group = threadIdx.x / LPV, e = threadIdx.x % LPV, lane = threadIdx.x & 63;
-    const int64_t total = work.first[a.sq.rows];
-    const int used = used_workers(total, workers);
+    const int group = threadIdx.x / LPV, e = threadIdx.x % LPV;
+    const int64_t total = ((ConstLongs)(work.first))[a.sq.rows];
+    const int used = used_workers(total, a.workers);
     const int64_t rows = static_cast<int64_t>(a.sq.tokens) * a.heads;
+    const auto part = [&](const Where& w, int i) {
+        const int p = w.w0 + i, slot = begin_of(total, p, used) > w.u0 ? 0 : 1;
+        return work.part + ((static_cast<int64_t>(p) * 2 + slot) * C::M + w.in_unit) * C::RS;
+    };
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * GROUPS + group; row < rows; row += static_cast<int64_t>(gridDim.x) * GROUPS) {
+        const Where w = where_of<C, false>(a, work, total, used, row);
+        if (w.parts > kFew) continue;
+        Joined j;
+#pragma unroll 4
+        for (int i = 0; i < w.parts; ++i) {
+            const float* p = w.parts == 1 ? work.whole + row * C::RS : part(w, i);
+            float x[16];
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) load_floats<4>(p + 16 * e + k, x + k);
+            j.add(x, p[D], p[D + 1]);
+        }
+        finish_row<C, Out>(a, row, j);
+    }
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-        const int t = static_cast<int>(static_cast<uint32_t>(row) / a.heads), h = static_cast<int>(static_cast<uint32_t>(row) % a.heads);
-        int lo = 0, hi = a.sq.rows - 1;            // the last sequence that begins at or before this token
-        while (lo < hi) {
-            const int mid = lo + (hi - lo + 1) / 2;
-            if (cu_at(a.sq, mid) <= t) lo = mid;
-            else hi = mid - 1;
-        }
-        const Seq s = seq_at(a.sq, a.pg.logp, lo);
-        const int per = items_of<C>(s);
-        const int64_t r = row - static_cast<int64_t>(s.start) * a.heads;
-        const int64_t u0 = work.first[lo] + r / C::M * per, u1 = u0 + per;
-        const bool there = t >= s.start && t < s.start + s.n && per > 0;   // (else no workgroup had this row)
-        float v[16] = {}, ref = kLow, l = 0.0f;
-        const auto add = [&](const float* p) {
-            const float pl = p[D + 1];
-            if (!(pl == 0.0f)) {
-                const float pr = p[D], now = fmaxf(ref, pr);
-                const float f0 = __builtin_amdgcn_exp2f(ref - now), f1 = __builtin_amdgcn_exp2f(pr - now);
-                l = l * f0 + pl * f1;
+        const Where w = where_of<C, true>(a, work, total, used, row);
+        if (w.parts <= kFew) continue;             // (the same for the whole workgroup)
+        Joined j;
+        for (int i = group; i < w.parts; i += GROUPS) {
+            const float* p = part(w, i);
+            float x[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = v[i] * f0 + p[16 * e + i] * f1;
-                ref = now;
-            }
-        };
-        int groups = 1;
-        if (there) {
-            const int w0 = static_cast<int>(((u0 + 1) * used - 1) / total);
-            if (begin_of(total, w0 + 1, used) >= u1) {
-                if (group == 0) add(work.whole + row * C::RS);
-            } else {
-                groups = GROUPS;
-                for (int w = w0 + group; w < used && begin_of(total, w, used) < u1; w += GROUPS) {
-                    const int slot = begin_of(total, w, used) > u0 ? 0 : 1;
-                    add(work.part + ((static_cast<int64_t>(w) * 2 + slot) * C::M + r % C::M) * C::RS);
-                }
+            for (int k = 0; k < 16; k += 4) load_floats<4>(p + 16 * e + k, x + k);
+            j.add(x, p[D], p[D + 1]);
+        }
+        __syncthreads();
+        if (group > 0) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4v*>(&sums[group][16 * e + i]) = float4v{j.v[i], j.v[i + 1], j.v[i + 2], j.v[i + 3]};
+            if (e == 0) {
+                refs[group] = j.ref;
+                exps[group] = j.l;
             }
         }
-        if (groups > 1) {                          // (the same for the whole workgroup)
-            __syncthreads();
-            if (group > 0) {
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4v*>(&sums[group][16 * e + i]) = float4v{v[i], v[i + 1], v[i + 2], v[i + 3]};
-                if (e == 0) {
-                    refs[group] = ref;
-                    exps[group] = l;
-                }
-            }
-            __syncthreads();
-            if (group == 0)
-                for (int x = 1; x < GROUPS; ++x) {
-                    if (exps[x] == 0.0f) continue;
-                    const float now = fmaxf(ref, refs[x]);
-                    const float f0 = __builtin_amdgcn_exp2f(ref - now), f1 = __builtin_amdgcn_exp2f(refs[x] - now);
-                    l = l * f0 + exps[x] * f1;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = v[i] * f0 + sums[x][16 * e + i] * f1;
-                    ref = now;
-                }
-        }
+        __syncthreads();
         if (group > 0) continue;
-        const float inverse = l == 0.0f ? 0.0f : 1.0f / l;
-        // back to the elements' own order
-        float y[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i / 8 * 8 + (i % 2) * 4 + (i % 8) / 2] = l == 0.0f ? 0.0f : v[i] * inverse;
-        if (a.rotate) hadamard<D>(y, lane, a.norm);
-        Out* out = static_cast<Out*>(a.out) + t * a.o_st + h * a.o_sh + 16 * e;
-#pragma unroll
-        for (int i = 0; i < 16; i += 16 / sizeof(Out)) {
-            uint4v x;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (sizeof(Out) == 2) x[j] = to_bf16(y[i + 2 * j]) | (to_bf16(y[i + 2 * j + 1]) << 16);
-                else x[j] = __float_as_uint(y[i + j]);
-            }
-            *reinterpret_cast<uint4v*>(out + i) = x;
+        for (int x = 1; x < GROUPS; ++x) {
+            float v[16];
+            load_floats<16>(&sums[x][16 * e], v);
+            j.add(v, refs[x], exps[x]);
         }
-        if (a.lse && e == 0) a.lse[row] = l == 0.0f ? -__builtin_inff() : (ref + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+        finish_row<C, Out>(a, row, j);
     }
 }
 
@@ -793,8 +879,8 @@ int attn_launch(const LatentAttnArgs& a, hipStream_t s) {
     if constexpr (C::WIDE) hipLaunchKernelGGL((latent_query<C, float>), query, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((latent_query<C, uint16_t>), query, dim3(256), 0, s, a);
     hipLaunchKernelGGL((latent_sums<C>), dim3(a.workers), dim3(C::THREADS), 0, s, a);
-    if constexpr (C::WIDE) hipLaunchKernelGGL((latent_finish<C, float>), finish, dim3(256), 0, s, a, a.workers);
-    else hipLaunchKernelGGL((latent_finish<C, uint16_t>), finish, dim3(256), 0, s, a, a.workers);
+    if constexpr (C::WIDE) hipLaunchKernelGGL((latent_finish<C, float>), finish, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((latent_finish<C, uint16_t>), finish, dim3(256), 0, s, a);
     return static_cast<int>(hipGetLastError());
 }
 
