@@ -98,6 +98,8 @@ __device__ __forceinline__ int exponent(float v) { return static_cast<int>((__fl
 // Matrix steps stay in order: left alone, the scheduler loads the operands of many of
 // them at once, and spills.
 #define HR_PHASE() __builtin_amdgcn_sched_barrier(0)
+// The kernel's lambdas hold its registers: one that is called would keep them in memory.
+#define HR_INLINE __attribute__((always_inline))
 
 template <int D_, int NG_, bool SF32_, bool WIDE_, int RT_, int WR_>
 struct Cfg {
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
                 // their way while as many are worked on
                 float4v w[RT], c[RT];
                 uint4v k[2][kBatch];
-                const auto operand = [&](int x) { return *reinterpret_cast<const uint4v*>(keys + (x < 2 ? 2 * D + 64 * x + 16 * g : 64 * (x - 2) + 16 * (g ^ swizzle(x - 2)))); };
+                const auto operand = [&](int x) HR_INLINE { return *reinterpret_cast<const uint4v*>(keys + (x < 2 ? 2 * D + 64 * x + 16 * g : 64 * (x - 2) + 16 * (g ^ swizzle(x - 2)))); };
                 constexpr int ALL = C::KS + 2;
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) w[rt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
                 // probabilities, to LDS: keys 16 wk + 4 g + x stand at 8 g + 4 wk + x
                 uint8_t* to = lds.probs[i & 1] + (wr * 16 * RT + m) * C::PS + 16 * g + 8 * wk;
                 float more[RT];
-                const auto put = [&]() {
+                const auto put = [&]() HR_INLINE {
                     float most = 0.0f, largest = 0.0f;
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) {
@@ -597,14 +599,14 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
             const int slots = a.sq.max_pages - 1;
             // the page of the 16 keys that the wave's are of in step i; absent past the
             // sequence's end
-            const auto page_of = [&](int i) {
+            const auto page_of = [&](int i) HR_INLINE {
                 const int t = key0 + i * C::KEYS + (C::KEYS / C::VALUES) * vw / 16 * 16;
                 return i < steps && t < len ? table[min(t >> pg.logp, slots)] : -1;
             };
             // a lane's offsets from its wave's first key
             const int ko = lane / C::LK, co = ko * (D / 2) + 16 * part, ro = ko * (2 * kRope) + 16 * part;
-            const auto group_of = [&](int x) { return (part + C::LK * x) * 32 / C::G; };
-            const auto load = [&](int page, int i, Raw<C>& w) {
+            const auto group_of = [&](int x) HR_INLINE { return (part + C::LK * x) * 32 / C::G; };
+            const auto load = [&](int page, int i, Raw<C>& w) HR_INLINE {
                 const int t = key0 + i * C::KEYS + (C::KEYS / C::VALUES) * vw, off = t & (pg.page - 1);
                 // (an absent page has no bytes: its loads give zeros)
                 const bool here = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.sq.n_pages);
@@ -623,27 +625,26 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
             };
             // operands of a step
             const uint32_t f0c = 0x64006400u ^ (pg.sym ? 0x00080008u : 0u), f1c = 0x54005400u ^ (pg.sym ? 0x00800080u : 0u);
-            const auto store = [&](const Raw<C>& w, int page, int b) {
-                uint8_t* to = lds.keys[b] + kk * C::VS;
+            // operands of 8 of the lane's elements: word n of its codes
+            const auto store_word = [&](const Raw<C>& w, int n, uint8_t* to) HR_INLINE {
+                const int x = n / 4, y = n % 4, run = part + C::LK * x, at = ko * NG + group_of(x);
+                const uint32_t z = pg.sym ? 8u : (w.zero[x] >> (4 * (at & 1))) & 15u;
+                const uint32_t z0 = 0x64006400u + z * 0x00010001u, z1 = 0x54005400u + z * 0x00100010u;
+                uint32_t c = w.codes[x][y];
+                uint4v k;
+                k.x = pk_sub((c & 0x000F000Fu) ^ f0c, z0);
+                k.y = pk_sub((c & 0x00F000F0u) ^ f1c, z1);
+                c >>= 8;
+                k.z = pk_sub((c & 0x000F000Fu) ^ f0c, z0);
+                k.w = pk_sub((c & 0x00F000F0u) ^ f1c, z1);
+                *reinterpret_cast<uint4v*>(to + 64 * run + 16 * (y ^ swizzle(part))) = k;
+            };
+            // and what belongs to them
+            const auto store_rest = [&](const Raw<C>& w, int page, int b, uint8_t* to) HR_INLINE {
                 if (lane == 0) lds.there[b][vw / 2] = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.sq.n_pages);   // (waves of the same 16 keys say the same)
 #pragma unroll
-                for (int x = 0; x < C::CW / 4; ++x) {
-                    const int run = part + C::LK * x, at = ko * NG + group_of(x);
-                    const uint32_t z = pg.sym ? 8u : (w.zero[x] >> (4 * (at & 1))) & 15u;
-                    const uint32_t z0 = 0x64006400u + z * 0x00010001u, z1 = 0x54005400u + z * 0x00100010u;
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        uint32_t c = w.codes[x][y];
-                        uint4v k;
-                        k.x = pk_sub((c & 0x000F000Fu) ^ f0c, z0);
-                        k.y = pk_sub((c & 0x00F000F0u) ^ f1c, z1);
-                        c >>= 8;
-                        k.z = pk_sub((c & 0x000F000Fu) ^ f0c, z0);
-                        k.w = pk_sub((c & 0x00F000F0u) ^ f1c, z1);
-                        *reinterpret_cast<uint4v*>(to + 64 * run + 16 * (y ^ swizzle(part))) = k;
-                    }
-                    if (run * 32 % C::G == 0) lds.scales[b][kk * NG + group_of(x)] = __uint_as_float(C::SF32 ? w.scale[x] : w.scale[x] << 16);
-                }
+                for (int x = 0; x < C::CW / 4; ++x)
+                    if ((part + C::LK * x) * 32 % C::G == 0) lds.scales[b][kk * NG + group_of(x)] = __uint_as_float(C::SF32 ? w.scale[x] : w.scale[x] << 16);
                 *reinterpret_cast<uint4v*>(to + 2 * D + 16 * part) = w.rope;
             };
             float4v acc[C::TILES][C::DT];
@@ -652,8 +653,10 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
 #pragma unroll
                 for (int d = 0; d < C::DT; ++d) acc[x][d] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
             const uint32_t grp = vw * C::DW / C::G;
-            // sums of the wave's dimensions over all rows, of the step in buffers b and p
-            const auto add = [&](int b, int p, bool moved) {
+            // Sums of the wave's dimensions over all rows, of the step in buffers b and p;
+            // between its matrix steps, word by word, the operands of the codes in w go to
+            // buffer `into`: one keeps the matrix unit, the other vector unit and LDS busy.
+            const auto add = [&](int b, int p, bool moved, const Raw<C>& w, int into) HR_INLINE {
                 if (moved) {
 #pragma unroll
                     for (int x = 0; x < C::TILES; ++x) {
@@ -666,23 +669,32 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
                 }
                 const uint8_t* pr = lds.probs[p] + (grp * M + m) * C::PS + 16 * g;
                 const uint8_t* va = lds.keys[b] + (4 * g + m / 4) * C::VS + vw * C::DW * 2 + m % 2 * 8;
-                uint4v pb[T][C::TILES];
+                uint8_t* to = lds.keys[into] + kk * C::VS;
+                uint4v pb[T][C::TILES], v[2];
 #pragma unroll
                 for (int t = 0; t < T; ++t)
 #pragma unroll
                     for (int x = 0; x < C::TILES; ++x) pb[t][x] = *reinterpret_cast<const uint4v*>(pr + (t * NG * M + 16 * x) * C::PS);
-#pragma unroll
-                for (int d = 0; d < C::DT; ++d) {
+                const auto operand = [&](int d) HR_INLINE {
                     // (dimensions 16 d + 4 (m % 4) of the wave's: half a 16-byte part of run d / 2)
                     const int at = d / 2 * 64 + 16 * ((d % 2 * 2 + m % 4 / 2) ^ swizzle(vw * (C::DW / 32) + d / 2));
                     const uint2v v0 = transposed(va + at), v1 = transposed(va + 16 * C::VS + at);
-                    const uint4v v = {v0.x, v0.y, v1.x, v1.y};
+                    return uint4v{v0.x, v0.y, v1.x, v1.y};
+                };
+                v[0] = operand(0);
+#pragma unroll
+                for (int d = 0; d < C::DT; ++d) {
+                    if (d + 1 < C::DT) v[(d + 1) & 1] = operand(d + 1);
+                    HR_PHASE();
 #pragma unroll
                     for (int t = T - 1; t >= 0; --t)
 #pragma unroll
-                        for (int x = 0; x < C::TILES; ++x) acc[x][d] = mfma_f16(v, pb[t][x], acc[x][d]);
+                        for (int x = 0; x < C::TILES; ++x) acc[x][d] = mfma_f16(v[d & 1], pb[t][x], acc[x][d]);
+                    store_word(w, d, to);
+                    HR_PHASE();
                 }
             };
+            static_assert(C::CW == C::DT, "a word for each tile of dimensions");
             // A step's codes have a place in raw that depends on its number alone, and the
             // loop is unrolled: a load on its way cannot be moved to another register.
             Raw<C> raw[kAhead];
@@ -694,23 +706,30 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
             }
 #pragma unroll
             for (int x = 0; x < kAhead; ++x) load(page[x], x, raw[x]);
-            // operands of step i, which is in place X, and the loads of the step after
-            const auto take = [&](auto X, int i) {
-                store(raw[X], page[X], X);
+            // the loads of the step that takes place X after one that has been stored
+            const auto reload = [&](auto X, int i) HR_INLINE {
                 page[X] = next[X];
-                load(page[X], i + kAhead, raw[X]);
-                next[X] = page_of(i + 2 * kAhead);
+                load(page[X], i, raw[X]);
+                next[X] = page_of(i + kAhead);
             };
-            take(std::integral_constant<int, 0>(), 0);
+            const auto store = [&](auto X, int i) HR_INLINE {
+                uint8_t* to = lds.keys[X] + kk * C::VS;
+                store_rest(raw[X], page[X], X, to);
+#pragma unroll
+                for (int n = 0; n < C::CW; ++n) store_word(raw[X], n, to);
+                reload(X, i + kAhead);
+            };
+            typedef std::integral_constant<int, 0> P0;
+            typedef std::integral_constant<int, 1> P1;
+            typedef std::integral_constant<int, 2> P2;
+            store(P0(), 0);
             __syncthreads();
+            store(P1(), 1);
             bool moved = false;
-            // the interval in which the scores of step i are formed, in buffer B
-            const auto interval = [&](auto B, int i) {
-                if (vw == 0 && lane == 0) lds.moved[(B + 1) % 3] = 0;
-                take(std::integral_constant<int, (B + 1) % 3>(), i + 1);
-                if (i > 0) add((B + 2) % 3, (i + 1) & 1, moved);
+            // the end of the interval in which scores are formed in buffer b
+            const auto meet = [&](int b) HR_INLINE {
                 __syncthreads();
-                moved = lds.moved[B] != 0;
+                moved = lds.moved[b] != 0;
                 if (moved) {
                     __syncthreads();
                     __syncthreads();
@@ -718,12 +737,22 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
                     __syncthreads();
                 }
             };
-            for (int i = 0; i < steps; i += 3) {
-                interval(std::integral_constant<int, 0>(), i);
-                if (i + 1 < steps) interval(std::integral_constant<int, 1>(), i + 1);
-                if (i + 2 < steps) interval(std::integral_constant<int, 2>(), i + 2);
+            if (steps > 0) meet(0);
+            // an interval: the scores of step i are formed, in buffer B, the step before is
+            // added and the one after stored
+            const auto interval = [&](auto B, int i) HR_INLINE {
+                constexpr int next_b = (B + 1) % 3;
+                if (vw == 0 && lane == 0) lds.moved[next_b] = 0;
+                store_rest(raw[next_b], page[next_b], next_b, lds.keys[next_b] + kk * C::VS);
+                add((B + 2) % 3, (i + 1) & 1, moved, raw[next_b], next_b);
+                reload(std::integral_constant<int, next_b>(), i + 1 + kAhead);
+                if (i < steps) meet(B);
+            };
+            for (int i = 1; i <= steps; i += 3) {
+                interval(P1(), i);
+                if (i + 1 <= steps) interval(P2(), i + 1);
+                if (i + 2 <= steps) interval(P0(), i + 2);
             }
-            if (steps > 0) add((steps - 1) % 3, (steps + 1) & 1, moved);
             __syncthreads();
             // the segment's sums
 #pragma unroll
