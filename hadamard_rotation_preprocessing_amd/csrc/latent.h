@@ -87,7 +87,7 @@ int latent_attn_workers(const LatentAttnKey& k, int* workers);
 // numbering of the sequences' work, and where each workgroup begins; the queries as operands, with 16 bytes more for
 // each row; the sums of each row; and two partial sums for each workgroup.
 constexpr int64_t latent_first_bytes(int64_t seqs) { return ((seqs + 1) * 8 + 15) / 16 * 16; }
-constexpr int64_t latent_start_bytes(int workers) { return (int64_t{workers} * 4 + 15) / 16 * 16; }
+constexpr int64_t latent_start_bytes(int workers) { return (int64_t{workers} * 4 + 4 + 15) / 16 * 16; }
 constexpr int64_t latent_work_bytes(const LatentAttnKey& k, int64_t seqs, int64_t rows, int workers) {
     const int terms = k.wide ? 2 : 1, rope_terms = k.wide ? 3 : 1;
     return latent_first_bytes(seqs) + latent_start_bytes(workers) + rows * (16 + 2 * (terms * k.d + rope_terms * kRope) + 4 * (k.d + 4)) +

@@ -150,7 +150,7 @@ __device__ __forceinline__ Seq seq_at(const CacheSeqs& s, int logp, int b) {
 }
 // items of a unit of a sequence, and its units.  An item is kItem keys; a unit that has
 // any counts kSetUp items more, before them, for what it costs beside its keys.
-constexpr int kItem = 64, kSetUp = 3;
+constexpr int kItem = 64, kSetUp = 6;
 __device__ __forceinline__ int items_of(const Seq& s) {
     return s.len > 0 ? static_cast<int>((static_cast<int64_t>(s.len) + kItem - 1) / kItem) + kSetUp : 0;
 }
@@ -208,11 +208,13 @@ __device__ __forceinline__ uint2v transposed(const uint8_t* p) {
     return __builtin_bit_cast(uint2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(p)));
 }
 
+constexpr int kFew = 32;               // parts of a row that a lane group joins by itself
+
 // The scratch.
 template <class C>
 struct Work {
     int64_t* first;      // [rows + 1]: items before those of a sequence
-    int32_t* start;      // [workers]: the sequence that a workgroup's items begin in
+    int32_t* start;      // [workers + 1]: the sequence that a workgroup's items begin in; whether some rows have many parts
     float* factor;       // [query rows][4]: of a row's scores, and of its products with rotary keys before
     uint8_t* query;
     float* whole;        // [query rows][RS]: sums, the reference, and the sum of exponentials
@@ -238,14 +240,22 @@ __global__ void __launch_bounds__(256) latent_query(const LatentAttnArgs a) {
     constexpr int D = C::D, LPV = D / 16, R = kRope / LPV;
     const Work<C> work(a);
     if (blockIdx.x == 0) {     // the numbering of items
-        __shared__ int64_t sums[4];
+        __shared__ int64_t sums[4], firsts[257];     // (of the first 256 sequences)
+        __shared__ int longest;
+        if (threadIdx.x == 0) {
+            firsts[0] = work.first[0] = 0;
+            longest = 0;
+        }
         int64_t before = 0;
         for (int r0 = 0; r0 < a.sq.rows; r0 += 256) {
             const int r = r0 + threadIdx.x;
             int64_t v = 0;
+            int per = 0;
             if (r < a.sq.rows) {
                 const Seq s = seq_at<false>(a.sq, a.pg.logp, r);
-                v = static_cast<int64_t>(items_of(s)) * units_of<C>(s, a.heads);
+                per = items_of(s);
+                v = static_cast<int64_t>(per) * units_of<C>(s, a.heads);
+                if (v == 0) per = 0;
             }
             for (int x = 1; x < 64; x *= 2) {
                 const int64_t y = __shfl_up(v, x);
@@ -253,14 +263,15 @@ __global__ void __launch_bounds__(256) latent_query(const LatentAttnArgs a) {
             }
             __syncthreads();
             if ((threadIdx.x & 63) == 63) sums[threadIdx.x / 64] = v;
+            if (per > longest) atomicMax(&longest, per);
             __syncthreads();
             for (int x = 0; x < 4; ++x) {
                 if (x < static_cast<int>(threadIdx.x / 64)) v += sums[x];
             }
             if (r < a.sq.rows) work.first[r + 1] = before + v;
+            if (r0 == 0) firsts[threadIdx.x + 1] = v;
             before += sums[0] + sums[1] + sums[2] + sums[3];
         }
-        if (threadIdx.x == 0) work.first[0] = 0;
         __threadfence_block();
         __syncthreads();
         // the sequence that each workgroup begins in
@@ -270,11 +281,14 @@ __global__ void __launch_bounds__(256) latent_query(const LatentAttnArgs a) {
             int lo = 0, hi = a.sq.rows - 1;    // the last sequence that begins at or before the item
             while (lo < hi) {
                 const int mid = lo + (hi - lo + 1) / 2;
-                if (work.first[mid] <= item) lo = mid;
+                if ((mid <= 256 ? firsts[mid] : work.first[mid]) <= item) lo = mid;
                 else hi = mid - 1;
             }
             work.start[w] = lo;
         }
+        // whether a unit may have more than kFew parts: it touches that many runs of
+        // total / used items
+        if (threadIdx.x == 0) work.start[a.workers] = static_cast<int64_t>(longest) * used > static_cast<int64_t>(kFew - 2) * before;
     }
     const int64_t row = (int64_t{blockIdx.x} * 256 + threadIdx.x) / LPV, total = static_cast<int64_t>(a.sq.tokens) * a.heads;
     const int lane = threadIdx.x & 63, e = lane % LPV;
@@ -775,7 +789,7 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
 struct Joined {
     float v[16] = {}, ref = kLow, l = 0.0f;
     __device__ __forceinline__ void add(const float (&x)[16], float xr, float xl) {
-        if (xl == 0.0f) return;
+        // (a part that saw nothing has the reference kLow, and sums of 0)
         const float now = fmaxf(ref, xr), f0 = __builtin_amdgcn_exp2f(ref - now), f1 = __builtin_amdgcn_exp2f(xr - now);
         l = l * f0 + xl * f1;
 #pragma unroll
@@ -788,7 +802,7 @@ struct Joined {
 struct Where {
     int parts, w0;
     int64_t u0;                // the first item of the unit's keys
-    int in_unit;               // the row's place in its unit
+    int in_unit, left;         // the row's place in its unit, and the unit's rows
 };
 template <class C, bool UNI>
 __device__ __forceinline__ Where where_of(const LatentAttnArgs& a, const Work<C>& work, int64_t total, int used, int64_t row) {
@@ -800,11 +814,12 @@ __device__ __forceinline__ Where where_of(const LatentAttnArgs& a, const Work<C>
         else hi = mid - 1;
     }
     const Seq s = seq_at<UNI>(a.sq, a.pg.logp, lo);
-    Where w{0, 0, 0, 0};
+    Where w{0, 0, 0, 0, 0};
     const int per = items_of(s);
     if (t < s.start || t >= s.start + s.n || per == 0) return w;   // (no workgroup had this row)
     const int64_t r = row - static_cast<int64_t>(s.start) * a.heads;
     w.in_unit = static_cast<int>(r % C::M);
+    w.left = static_cast<int>(min(static_cast<int64_t>(C::M), static_cast<int64_t>(s.n) * a.heads - (r - w.in_unit)));
     w.u0 = (UNI ? ((ConstLongs)(work.first))[lo] : work.first[lo]) + r / C::M * per + kSetUp;
     const int64_t last = w.u0 + per - kSetUp - 1;
     w.w0 = static_cast<int>(((w.u0 + 1) * used - 1) / total);
@@ -841,7 +856,6 @@ __device__ __forceinline__ void finish_row(const LatentAttnArgs& a, int64_t row,
 // row of many by a workgroup of its own, whose groups take its parts in turn and whose
 // first group adds what they have.  Either way a row's sums are added in one order, that
 // of its keys, or that of the groups and of its keys in them.
-constexpr int kFew = 8;
 template <class C, class Out>
 __global__ void __launch_bounds__(256) latent_finish(const LatentAttnArgs a) {
     constexpr int D = C::D, LPV = D / 16, GROUPS = 256 / LPV;
@@ -856,20 +870,32 @@ __global__ void __launch_bounds__(256) latent_finish(const LatentAttnArgs a) {
         const int p = w.w0 + i, slot = begin_of(total, p, used) > w.u0 ? 0 : 1;
         return work.part + ((static_cast<int64_t>(p) * 2 + slot) * C::M + w.in_unit) * C::RS;
     };
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * GROUPS + group; row < rows; row += static_cast<int64_t>(gridDim.x) * GROUPS) {
-        const Where w = where_of<C, false>(a, work, total, used, row);
-        if (w.parts > kFew) continue;
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * GROUPS; row0 < rows; row0 += static_cast<int64_t>(gridDim.x) * GROUPS) {
+        const int64_t row = row0 + group;
+        // (most often the rows are of one unit, neighbours there)
+        Where w = where_of<C, true>(a, work, total, used, row0);
+        if (w.in_unit + group < w.left) w.in_unit += group;
+        else w = where_of<C, false>(a, work, total, used, min(row, rows - 1));
+        if (row >= rows || w.parts > kFew) continue;
         Joined j;
-#pragma unroll 4
-        for (int i = 0; i < w.parts; ++i) {
-            const float* p = w.parts == 1 ? work.whole + row * C::RS : part(w, i);
-            float x[16];
+        for (int i0 = 0; i0 < w.parts; i0 += 4) {
+            float x[4][16], xr[4], xl[4];
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) load_floats<4>(p + 16 * e + k, x + k);
-            j.add(x, p[D], p[D + 1]);
+            for (int i = 0; i < 4; ++i) {
+                const int n = min(i0 + i, w.parts - 1);
+                const float* p = w.parts == 1 ? work.whole + row * C::RS : part(w, n);
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) load_floats<4>(p + 16 * e + k, x[i] + k);
+                xr[i] = p[D];
+                xl[i] = p[D + 1];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i0 + i < w.parts) j.add(x[i], xr[i], xl[i]);
         }
         finish_row<C, Out>(a, row, j);
     }
+    if (!((ConstInts)(work.start))[a.workers]) return;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const Where w = where_of<C, true>(a, work, total, used, row);
         if (w.parts <= kFew) continue;             // (the same for the whole workgroup)
@@ -901,10 +927,16 @@ __global__ void __launch_bounds__(256) latent_finish(const LatentAttnArgs a) {
     }
 }
 
+// workgroups that join: for rows of few parts, and enough for rows of many
+inline int64_t finish_grid(int64_t rows, int groups) {
+    const int64_t few = (rows + groups - 1) / groups, many = rows < 1024 ? rows : 1024;
+    return few > (1 << 20) ? 1 << 20 : few > many ? few : many;
+}
+
 template <class C>
 int attn_launch(const LatentAttnArgs& a, hipStream_t s) {
     const int64_t rows = int64_t{a.sq.tokens} * a.heads, threads = rows * (C::D / 16);
-    const dim3 query(static_cast<uint32_t>((threads + 255) / 256)), finish(static_cast<uint32_t>(rows < (1 << 20) ? rows : 1 << 20));
+    const dim3 query(static_cast<uint32_t>((threads + 255) / 256)), finish(static_cast<uint32_t>(finish_grid(rows, 256 / (C::D / 16))));
     if constexpr (C::WIDE) hipLaunchKernelGGL((latent_query<C, float>), query, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((latent_query<C, uint16_t>), query, dim3(256), 0, s, a);
     hipLaunchKernelGGL((latent_sums<C>), dim3(a.workers), dim3(C::THREADS), 0, s, a);
