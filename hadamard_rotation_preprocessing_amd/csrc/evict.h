@@ -41,17 +41,20 @@ struct CacheWeightsArgs {
     int32_t hq, rep;           // query heads; query heads per kv head
     int32_t causal, window, rotate;
     int32_t workers;           // workgroups
+    int32_t few;               // row tiles of the kernel of few rows, or 0: that of many
 };
 
 // Launchers: 0 or a hipError_t.
 int launch_cache_weights(const CacheWeightsArgs& a, int bf16, void* stream);
 // workgroups that hr_cache_weights keeps in flight on the current device
-int cache_weights_workers(int* workers);
+int cache_weights_workers(int few, int* workers);
 int launch_cache_evict(const CacheEvictArgs& a, void* stream);
 
-// bytes of scratch: a row's factor and log-sum-exp, and its query as pairs of float16
-constexpr int64_t cache_weights_bytes(int64_t tokens, int32_t q_heads, int d) {
-    return (tokens * q_heads * 8 + 15) / 16 * 16 + tokens * q_heads * d * 4;
+// bytes of scratch: the numbering of the sequences' key blocks; a row's factor and
+// log-sum-exp, and its query as pairs of float16
+constexpr int64_t cache_weights_first(int64_t seqs) { return ((seqs + 1) * 8 + 15) / 16 * 16; }
+constexpr int64_t cache_weights_bytes(int64_t seqs, int64_t tokens, int32_t q_heads, int d) {
+    return cache_weights_first(seqs) + (tokens * q_heads * 8 + 15) / 16 * 16 + tokens * q_heads * d * 4;
 }
 // int32 words of scratch
 constexpr int64_t cache_evict_words(int64_t n_pages, int64_t rows) { return 3 * n_pages + rows + 16; }

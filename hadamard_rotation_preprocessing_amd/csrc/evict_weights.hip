@@ -20,6 +20,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cache_vectors.h"
 #include "evict.h"
 
@@ -33,6 +35,7 @@ typedef int int4v __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 32;     // rows of a stage
+constexpr int kItem = 64;     // keys of a block of weights_few: four tiles of 16, one of each on its way
 constexpr int kTop = 14;      // a row's largest query element is below 2^kTop in float16
 
 __device__ __forceinline__ float4v mfma(uint4v a, uint4v b, float4v c) {
@@ -71,8 +74,32 @@ struct RowScale {
 // Rows (t, i) of q, as [kv head][token][query head of it][hi, lo][D] float16.
 // Elements of eight stand in the order 0 4 1 5 2 6 3 7, that of the codes' operands.
 template <int D, class T>
-__global__ void __launch_bounds__(256) weights_query(const CacheWeightsArgs a, uint32_t* out, RowScale* rows) {
+__global__ void __launch_bounds__(256) weights_query(const CacheWeightsArgs a, uint32_t* out, RowScale* rows, int64_t* first_of) {
     constexpr int LPV = D / 16;
+    if (a.few && blockIdx.x == 0) {       // the numbering of weights_few's key blocks
+        __shared__ int64_t sums[4];
+        int64_t before = 0;
+        for (int r0 = 0; r0 < a.sq.rows; r0 += 256) {
+            const int r = r0 + threadIdx.x;
+            int64_t v = 0;
+            if (r < a.sq.rows && cu_at(a.sq, r + 1) > cu_at(a.sq, r)) {
+                const int64_t len = min(static_cast<int64_t>(max(a.sq.lens[r], 0)), static_cast<int64_t>(a.sq.max_pages) << a.pg.logp);
+                v = (len + kItem - 1) / kItem * a.pg.hkv;
+            }
+            for (int x = 1; x < 64; x *= 2) {
+                const int64_t y = __shfl_up(v, x);
+                if ((threadIdx.x & 63) >= x) v += y;
+            }
+            __syncthreads();
+            if ((threadIdx.x & 63) == 63) sums[threadIdx.x / 64] = v;
+            __syncthreads();
+            for (int x = 0; x < 4; ++x)
+                if (x < static_cast<int>(threadIdx.x / 64)) v += sums[x];
+            if (r < a.sq.rows) first_of[r + 1] = before + v;
+            before += sums[0] + sums[1] + sums[2] + sums[3];
+        }
+        if (threadIdx.x == 0) first_of[0] = 0;
+    }
     const int64_t v = (int64_t{blockIdx.x} * 256 + threadIdx.x) / LPV;
     const int64_t total = int64_t{a.sq.tokens} * a.hq;
     const int lane = threadIdx.x & 63, e = lane % LPV;
@@ -303,28 +330,257 @@ __global__ void __launch_bounds__(256) weights_add(const CacheWeightsArgs a, con
     }
 }
 
+// ---------------------------------------------------------------------------
+// few rows
+//
+// With up to 32 rows of a kv head (single tokens, drafts) the queries stay in
+// registers and the keys stream past them: every wave takes an equal, contiguous run
+// of all key blocks of all kv heads and sequences, numbered by weights_query, whatever
+// the lengths, and no wave waits for another.  The loads of the next kItem keys are on
+// their way throughout.
+
+typedef const int32_t __attribute__((address_space(4)))* ConstInts;
+
+// the last of first[0 .. n - 1], ascending, that is at most `item`, by the whole wave
+__device__ __forceinline__ int last_at_most(const int64_t* first, int n, int64_t item) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, end = n;
+    while (end - lo > 1) {
+        const int step = (end - lo + 63) / 64, at = lo + lane * step;
+        const int k = __popcll(__ballot(at < end && first[at < end ? at : lo] <= item));
+        lo += (k > 0 ? k - 1 : 0) * step;
+        end = min(lo + step, end);
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+template <int N>
+__device__ __forceinline__ void buffer_words(__amdgpu_buffer_rsrc_t r, int lane_at, int at, uint32_t* w) {
+    if constexpr (N == 1) {
+        w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, lane_at, at, 0);
+    } else if constexpr (N == 2) {
+        const uint2v x = __builtin_bit_cast(uint2v, __builtin_amdgcn_raw_buffer_load_b64(r, lane_at, at, 0));
+        w[0] = x.x;
+        w[1] = x.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4v x = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(r, lane_at + 4 * i, at, 0));
+            w[i] = x.x;
+            w[i + 1] = x.y;
+            w[i + 2] = x.z;
+            w[i + 3] = x.w;
+        }
+    }
+}
+
+// What a lane holds of a tile of 16 keys on its way: of key lane & 15 a quarter of each
+// group's codes, the scales and zero points, and the weight.
+template <int D, int NG>
+struct Tile {
+    uint32_t codes[D / 32], scales[NG], zeros, weight;
+};
+
+template <int D, int NG, int RT>
+__global__ void __launch_bounds__(256) weights_few(const CacheWeightsArgs a, const uint32_t* query, const RowScale* scales, const int64_t* first_of) {
+    constexpr int KG = D / 32 / NG, G = D / NG;
+    const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+    const CachePage& pg = a.pg;
+    const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6)), waves = gridDim.x * 4;
+    const int64_t total = ((const int64_t __attribute__((address_space(4)))*)(first_of))[a.sq.rows];
+    int64_t item = total * wave / waves;
+    const int64_t end = total * (wave + 1) / waves;
+    if (item >= end) return;
+    int b = last_at_most(first_of, a.sq.rows, item);
+    const int es = pg.sf32 ? 4 : 2;
+    const uint32_t flip0 = pg.sym ? 0x00080008u : 0u, flip1 = pg.sym ? 0x00800080u : 0u;
+    const uint32_t f0 = 0x64006400u ^ flip0, f1 = 0x54005400u ^ flip1;
+    while (item < end) {
+        const auto first_item = (const int64_t __attribute__((address_space(4)))*)(first_of);
+        while (first_item[b + 1] <= item) ++b;
+        const ConstInts cu = (ConstInts)(a.sq.cu), lens = (ConstInts)(a.sq.lens);
+        const int start = min(max(a.sq.cu ? cu[b] : b * a.sq.per, 0), a.sq.tokens);
+        const int n = max(min(max(a.sq.cu ? cu[b + 1] : (b + 1) * a.sq.per, 0), a.sq.tokens) - start, 0);
+        const int len = static_cast<int>(min(static_cast<int64_t>(max(lens[b], 0)), static_cast<int64_t>(a.sq.max_pages) << pg.logp));
+        const int blocks = static_cast<int>((static_cast<int64_t>(len) + kItem - 1) / kItem);
+        const int64_t in_row = item - first_item[b];
+        const int h = static_cast<int>(in_row / blocks), k0 = static_cast<int>(in_row % blocks);
+        const int k1 = static_cast<int>(min(static_cast<int64_t>(blocks), k0 + end - item));   // blocks k0 .. k1 - 1 of the head
+        item += k1 - k0;
+        const int first = len - n, rows = n * a.rep;
+        const ConstInts table = (ConstInts)(a.sq.table + static_cast<int64_t>(b) * a.sq.max_pages);
+        const int64_t at = (static_cast<int64_t>(h) * a.sq.tokens + start) * a.rep;   // the rows' place in `query`
+        float* out = a.weights + (static_cast<int64_t>(b) * pg.hkv + h) * a.width;
+        // (more rows than one pass takes: the passes after the first add to it)
+        for (int r0 = 0; r0 < rows; r0 += 16 * RT) {
+            uint4v qh[RT][D / 32], ql[RT][D / 32];
+            float factor[RT][4], lse[RT][4];
+            int from[RT][4], to[RT][4];            // the keys that a row sees
+            int all_from = 0, all_to = len;        // and those that all rows do
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const uint32_t* q = query + (at + min(r0 + 16 * rt + m, rows - 1)) * D;
+#pragma unroll
+                for (int x = 0; x < NG; ++x)
+#pragma unroll
+                    for (int i = 0; i < KG; ++i) {
+                        const int c = (x * G + g * (G / 4) + 8 * i) / 8;
+                        qh[rt][x * KG + i] = reinterpret_cast<const uint4v*>(q)[c];
+                        ql[rt][x * KG + i] = reinterpret_cast<const uint4v*>(q + D / 2)[c];
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = r0 + 16 * rt + 4 * g + i;
+                    const RowScale rs = scales[at + min(r, rows - 1)];
+                    const int pos = first + min(r, rows - 1) / a.rep;
+                    factor[rt][i] = rs.factor;
+                    lse[rt][i] = r < rows ? rs.lse : __builtin_inff();
+                    to[rt][i] = r < rows ? (a.causal ? min(pos + 1, len) : len) : 0;
+                    from[rt][i] = a.window ? max(pos - a.window + 1, 0) : 0;
+                }
+            }
+            if (a.causal) all_to = min(first + r0 / a.rep + 1, len);
+            if (a.window) all_from = max(first + (min(r0 + 16 * RT, rows) - 1) / a.rep - a.window + 1, 0);
+            const bool whole = r0 + 16 * RT <= rows;
+
+            Tile<D, NG> tile[4];
+            int page[4], next[4];                  // of the tile in a place, and of the one after it
+            const int upto = static_cast<int>(min(static_cast<int64_t>(k1) * kItem, static_cast<int64_t>(len)));   // the run's end
+            const auto page_of = [&](int t) __attribute__((always_inline)) { return t < upto ? table[t >> pg.logp] : -1; };
+            const auto load = [&](auto X, int t) __attribute__((always_inline)) {
+                const bool here = static_cast<uint32_t>(page[X]) < static_cast<uint64_t>(a.sq.n_pages);
+                const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+                    const_cast<uint8_t*>(a.pool + (here ? page[X] : 0) * pg.page_bytes + h * pg.head_bytes), 0, here ? static_cast<int>(pg.head_bytes) : 0, 0x00020000);
+                const int off = t & (pg.page - 1);
+                Tile<D, NG>& w = tile[X];
+                if constexpr (NG == 1) {
+                    buffer_words<D / 32>(r, m * (D / 2) + g * (D / 8), pg.kc + off * (D / 2), w.codes);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < NG; ++x) buffer_words<KG>(r, m * (D / 2) + g * (G / 8) + x * (G / 2), pg.kc + off * (D / 2), w.codes + x * KG);
+                }
+                if (pg.sf32) {
+                    buffer_words<NG>(r, 4 * m * NG, pg.ks + off * NG * 4, w.scales);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < NG; ++x)
+                        w.scales[x] = static_cast<uint32_t>(static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, 2 * (m * NG + x), pg.ks + off * NG * 2, 0))) << 16;
+                }
+                // (symmetric: some bytes, not looked at)
+                const int zl = m * NG / 2, zs = pg.kz + off * NG / 2;
+                if constexpr (NG <= 2) w.zeros = static_cast<uint8_t>(__builtin_amdgcn_raw_buffer_load_b8(r, zl, zs, 0));
+                else if constexpr (NG == 4) w.zeros = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, zl, zs, 0));
+                else w.zeros = __builtin_amdgcn_raw_buffer_load_b32(r, zl, zs, 0);
+                const int j = t + m;
+                w.weight = __float_as_uint(j < upto ? out[j] : 0.0f);
+            };
+            const auto work = [&](auto X, int t) __attribute__((always_inline)) {
+                const Tile<D, NG>& w = tile[X];
+                const bool here = static_cast<uint32_t>(page[X]) < static_cast<uint64_t>(a.sq.n_pages);
+                float sum = 0.0f;
+                if (here) {
+                    float4v s[RT];
+#pragma unroll
+                    for (int x = 0; x < NG; ++x) {
+                        const uint32_t z = pg.sym ? 8u : (w.zeros >> (4 * (NG == 1 ? m & 1 : x))) & 15u;
+                        const uint32_t z0 = 0x64006400u + z * 0x00010001u, z1 = 0x54005400u + z * 0x00100010u;
+                        float4v c[RT];
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) c[rt] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int i = 0; i < KG; ++i) {
+                            uint32_t v = w.codes[x * KG + i];
+                            uint4v k;
+                            k.x = pk_sub((v & 0x000F000Fu) ^ f0, z0);
+                            k.y = pk_sub((v & 0x00F000F0u) ^ f1, z1);
+                            v >>= 8;
+                            k.z = pk_sub((v & 0x000F000Fu) ^ f0, z0);
+                            k.w = pk_sub((v & 0x00F000F0u) ^ f1, z1);
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) {
+                                c[rt] = mfma(ql[rt][x * KG + i], k, c[rt]);
+                                c[rt] = mfma(qh[rt][x * KG + i], k, c[rt]);
+                            }
+                        }
+                        const float sc = __uint_as_float(w.scales[x]);
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) s[rt][i] = x ? __builtin_fmaf(c[rt][i], sc, s[rt][i]) : c[rt][i] * sc;
+                    }
+                    const bool full = whole && t >= all_from && t + 16 <= all_to;
+                    const int j = t + m;
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][i], factor[rt][i], -lse[rt][i]));
+                            if (!full) e = j >= from[rt][i] && j < to[rt][i] ? e : 0.0f;
+                            sum += e;
+                        }
+                    sum += __shfl_xor(sum, 16);
+                    sum += __shfl_xor(sum, 32);
+                }
+                const int j = t + m;
+                const float old = __uint_as_float(w.weight);
+                if (g == 0 && j < len) out[j] = (r0 > 0 ? old : j < first ? a.decay * old : 0.0f) + sum;
+            };
+            const int t0 = k0 * kItem;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                page[x] = page_of(t0 + 16 * x);
+                next[x] = page_of(t0 + 16 * x + kItem);
+            }
+            typedef std::integral_constant<int, 0> P0;
+            typedef std::integral_constant<int, 1> P1;
+            typedef std::integral_constant<int, 2> P2;
+            typedef std::integral_constant<int, 3> P3;
+            load(P0(), t0);
+            load(P1(), t0 + 16);
+            load(P2(), t0 + 32);
+            load(P3(), t0 + 48);
+            const auto turn = [&](auto X, int t) __attribute__((always_inline)) {
+                if (t < len) work(X, t);
+                page[X] = next[X];
+                load(X, t + kItem);
+                next[X] = page_of(t + 2 * kItem);
+            };
+            for (int k = k0; k < k1; ++k) {
+                const int t = k * kItem;
+                turn(P0(), t);
+                turn(P1(), t + 16);
+                turn(P2(), t + 32);
+                turn(P3(), t + 48);
+            }
+        }
+    }
+}
+
 template <int D, class T>
-void query_launch(const CacheWeightsArgs& a, uint32_t* out, RowScale* rows, hipStream_t s) {
+void query_launch(const CacheWeightsArgs& a, uint32_t* out, RowScale* rows, int64_t* first_of, hipStream_t s) {
     const int64_t threads = int64_t{a.sq.tokens} * a.hq * (D / 16);
-    hipLaunchKernelGGL((weights_query<D, T>), dim3(static_cast<uint32_t>((threads + 255) / 256)), dim3(256), 0, s, a, out, rows);
+    hipLaunchKernelGGL((weights_query<D, T>), dim3(static_cast<uint32_t>((threads + 255) / 256)), dim3(256), 0, s, a, out, rows, first_of);
 }
 
 template <int D, int NG>
 void add_launch(const CacheWeightsArgs& a, int bf16, hipStream_t s) {
-    RowScale* rows = reinterpret_cast<RowScale*>(a.work);
-    uint32_t* query = reinterpret_cast<uint32_t*>(a.work + (int64_t{a.sq.tokens} * a.hq * 8 + 15) / 16 * 16);
-    if (bf16) query_launch<D, uint16_t>(a, query, rows, s);
-    else query_launch<D, float>(a, query, rows, s);
-    hipLaunchKernelGGL((weights_add<D, NG>), dim3(a.workers), dim3(256), 0, s, a, query, rows);
+    int64_t* first_of = reinterpret_cast<int64_t*>(a.work);
+    RowScale* rows = reinterpret_cast<RowScale*>(a.work + cache_weights_first(a.sq.rows));
+    uint32_t* query = reinterpret_cast<uint32_t*>(a.work + cache_weights_first(a.sq.rows) + (int64_t{a.sq.tokens} * a.hq * 8 + 15) / 16 * 16);
+    if (bf16) query_launch<D, uint16_t>(a, query, rows, first_of, s);
+    else query_launch<D, float>(a, query, rows, first_of, s);
+    if (a.few == 0) hipLaunchKernelGGL((weights_add<D, NG>), dim3(a.workers), dim3(256), 0, s, a, query, rows);
+    else if (a.few == 1) hipLaunchKernelGGL((weights_few<D, NG, 1>), dim3(a.workers), dim3(256), 0, s, a, query, rows, first_of);
+    else hipLaunchKernelGGL((weights_few<D, NG, 2>), dim3(a.workers), dim3(256), 0, s, a, query, rows, first_of);
 }
 
 }  // namespace
 
-int cache_weights_workers(int* workers) {
+int cache_weights_workers(int few, int* workers) {
     int dev, cus;
     hipError_t e = hipGetDevice(&dev);
     if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-    if (e == hipSuccess) *workers = 4 * cus;
+    if (e == hipSuccess) *workers = (few == 2 ? 2 : 4) * cus;   // (as many as fit with heads of 128)
     return static_cast<int>(e);
 }
 
