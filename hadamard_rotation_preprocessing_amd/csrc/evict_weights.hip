@@ -158,8 +158,8 @@ template <int D, int NG>
 __global__ void __launch_bounds__(256) weights_add(const CacheWeightsArgs a, const uint32_t* query, const RowScale* scales) {
     using S = Shape<D>;
     constexpr int KT = S::KT, KG = D / 32 / NG;
-    __shared__ __attribute__((aligned(16))) uint8_t stage[kRows * S::STRIDE];
-    __shared__ __attribute__((aligned(16))) RowInfo info[kRows];
+    __shared__ __attribute__((aligned(16))) uint8_t stages_[2][kRows * S::STRIDE];
+    __shared__ __attribute__((aligned(16))) RowInfo infos[2][kRows];
     __shared__ int64_t first_of[257];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
     const CachePage& pg = a.pg;
@@ -242,27 +242,40 @@ __global__ void __launch_bounds__(256) weights_add(const CacheWeightsArgs a, con
                 if (a.window) p1 = min(p1, (static_cast<int64_t>(j0) + S::KEYS - 1 - first + a.window) * a.rep);
             }
             int stages = 0;
-            for (int64_t p = p0 / kRows * kRows; p < p1; p += kRows) {
-                __syncthreads();
-                constexpr int WORDS = kRows * D / 4;            // 16 bytes each
+            // the next rows are on their way while these are worked on
+            constexpr int LOADS = kRows * D / 4 / 256;          // of 16 bytes
+            uint4v ahead[LOADS];
+            RowScale rs{};
+            const auto load = [&](int64_t p) {
 #pragma unroll
-                for (int i = 0; i < WORDS / 256; ++i) {
+                for (int i = 0; i < LOADS; ++i) {
                     const int x = i * 256 + tid, r = x / (D / 4), c = x % (D / 4);
-                    const uint4v v = reinterpret_cast<const uint4v*>(query + (at + min(p + r, rows - 1)) * D)[c];
-                    *reinterpret_cast<uint4v*>(stage + r * S::STRIDE + c * 16) = v;
+                    ahead[i] = reinterpret_cast<const uint4v*>(query + (at + min(p + r, rows - 1)) * D)[c];
+                }
+                if (tid < kRows) rs = scales[at + min(p + tid, rows - 1)];
+            };
+            p0 = p0 / kRows * kRows;
+            if (p0 < p1) load(p0);
+            for (int64_t p = p0; p < p1; p += kRows) {
+                uint8_t* stage = stages_[stages & 1];
+                RowInfo* info = infos[stages & 1];
+#pragma unroll
+                for (int i = 0; i < LOADS; ++i) {
+                    const int x = i * 256 + tid, r = x / (D / 4), c = x % (D / 4);
+                    *reinterpret_cast<uint4v*>(stage + r * S::STRIDE + c * 16) = ahead[i];
                 }
                 if (tid < kRows) {
                     RowInfo ri;
-                    const int64_t r = min(p + tid, rows - 1);
-                    const RowScale rs = scales[at + r];
-                    const int pos = first + static_cast<int>(static_cast<uint32_t>(r) / a.rep);
+                    const int pos = first + static_cast<int>(static_cast<uint32_t>(min(p + tid, rows - 1)) / a.rep);
                     ri.factor = rs.factor;
                     ri.lse = rs.lse;
                     ri.lo = a.window ? max(pos - a.window + 1, 0) : 0;
                     ri.hi = p + tid < rows ? (a.causal ? min(pos + 1, len) : len) : 0;
                     info[tid] = ri;
                 }
+                // (two buffers: the last readers of this one are before the last barrier)
                 __syncthreads();
+                if (p + kRows < p1) load(p + kRows);
                 // whether every row of the stage is there and sees every key of the block
                 const int pos0 = first + static_cast<int>(static_cast<uint32_t>(p) / a.rep);
                 const int pos1 = first + static_cast<int>(static_cast<uint32_t>(min(p + kRows, rows) - 1) / a.rep);
@@ -316,6 +329,7 @@ __global__ void __launch_bounds__(256) weights_add(const CacheWeightsArgs a, con
                     }
                 }
             }
+            __syncthreads();                   // (the next block's rows)
             float* out = a.weights + (static_cast<int64_t>(b) * pg.hkv + h) * a.width;
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
@@ -392,7 +406,6 @@ __global__ void __launch_bounds__(256) weights_few(const CacheWeightsArgs a, con
     const int64_t end = total * (wave + 1) / waves;
     if (item >= end) return;
     int b = last_at_most(first_of, a.sq.rows, item);
-    const int es = pg.sf32 ? 4 : 2;
     const uint32_t flip0 = pg.sym ? 0x00080008u : 0u, flip1 = pg.sym ? 0x00800080u : 0u;
     const uint32_t f0 = 0x64006400u ^ flip0, f1 = 0x54005400u ^ flip1;
     while (item < end) {
