@@ -151,7 +151,7 @@ template <int D>
 struct Shape {
     static constexpr int KT = D == 256 ? 2 : 4;      // 16-key tiles of a wave
     static constexpr int KEYS = 4 * 16 * KT;         // of a block
-    static constexpr int STRIDE = 4 * D + 16;        // bytes of a row in LDS: hi, lo, and a shift of four banks
+    static constexpr int STRIDE = 4 * D + 32;        // bytes of a row in LDS: hi, lo, and a shift of eight banks
 };
 
 template <int D, int NG>
@@ -207,7 +207,13 @@ __global__ void __launch_bounds__(256) weights_add(const CacheWeightsArgs a, con
                 const int t0 = j0 + (wave * KT + kt) * 16;
                 const int page = t0 < len ? table[t0 >> pg.logp] : -1;
                 there[kt] = page >= 0 && page < a.sq.n_pages;
-                if (!there[kt]) continue;
+                if (!there[kt]) {              // (worked on all the same, and not added)
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) key[kt][i] = uint4v{0, 0, 0, 0};
+#pragma unroll
+                    for (int q = 0; q < NG; ++q) scale[kt][q] = 0.0f;
+                    continue;
+                }
                 const int off = (t0 & (pg.page - 1)) + m;
                 const uint8_t* base = a.pool + page * pg.page_bytes + h * pg.head_bytes;
                 const uint8_t* codes = base + pg.kc + off * (D / 2);
@@ -281,45 +287,48 @@ __global__ void __launch_bounds__(256) weights_add(const CacheWeightsArgs a, con
                 const int pos1 = first + static_cast<int>(static_cast<uint32_t>(min(p + kRows, rows) - 1) / a.rep);
                 const bool full = p + kRows <= rows && j0 + S::KEYS <= len && (!a.causal || j0 + S::KEYS - 1 <= pos0) &&
                                   (!a.window || j0 > pos1 - a.window);
+                const auto tiles = [&](auto FULL) __attribute__((always_inline)) {
 #pragma unroll
-                for (int rt = 0; rt < kRows / 16; ++rt) {
-                    uint4v qh[D / 32], ql[D / 32];
-                    const uint8_t* row = stage + (rt * 16 + m) * S::STRIDE;
+                    for (int rt = 0; rt < kRows / 16; ++rt) {
+                        uint4v qh[D / 32], ql[D / 32];
+                        const uint8_t* row = stage + (rt * 16 + m) * S::STRIDE;
 #pragma unroll
-                    for (int q = 0; q < NG; ++q)
-#pragma unroll
-                        for (int i = 0; i < KG; ++i) {
-                            const int c = 2 * (q * (D / NG) + g * (D / NG / 4) + 8 * i);
-                            qh[q * KG + i] = *reinterpret_cast<const uint4v*>(row + c);
-                            ql[q * KG + i] = *reinterpret_cast<const uint4v*>(row + 2 * D + c);
-                        }
-                    RowInfo ri[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) ri[i] = info[rt * 16 + 4 * g + i];
-#pragma unroll
-                    for (int kt = 0; kt < KT; ++kt) {
-                        if (!there[kt]) continue;
-                        float4v w = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int q = 0; q < NG; ++q) {
-                            float4v c = {0.0f, 0.0f, 0.0f, 0.0f};
+                        for (int q = 0; q < NG; ++q)
 #pragma unroll
                             for (int i = 0; i < KG; ++i) {
-                                c = mfma(ql[q * KG + i], key[kt][q * KG + i], c);
-                                c = mfma(qh[q * KG + i], key[kt][q * KG + i], c);
+                                const int c = 2 * (q * (D / NG) + g * (D / NG / 4) + 8 * i);
+                                qh[q * KG + i] = *reinterpret_cast<const uint4v*>(row + c);
+                                ql[q * KG + i] = *reinterpret_cast<const uint4v*>(row + 2 * D + c);
                             }
+                        RowInfo ri[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) w[i] = q ? __builtin_fmaf(c[i], scale[kt][q], w[i]) : c[i] * scale[kt][0];
-                        }
-                        const int j = j0 + (wave * KT + kt) * 16 + m;
+                        for (int i = 0; i < 4; ++i) ri[i] = info[rt * 16 + 4 * g + i];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float e = __builtin_amdgcn_exp2f(__builtin_fmaf(w[i], ri[i].factor, -ri[i].lse));
-                            if (!full) e = j >= ri[i].lo && j < ri[i].hi ? e : 0.0f;
-                            part[kt] += e;
+                        for (int kt = 0; kt < KT; ++kt) {
+                            float4v w = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                            for (int q = 0; q < NG; ++q) {
+                                float4v c = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                                for (int i = 0; i < KG; ++i) {
+                                    c = mfma(ql[q * KG + i], key[kt][q * KG + i], c);
+                                    c = mfma(qh[q * KG + i], key[kt][q * KG + i], c);
+                                }
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) w[i] = q ? __builtin_fmaf(c[i], scale[kt][q], w[i]) : c[i] * scale[kt][0];
+                            }
+                            const int j = j0 + (wave * KT + kt) * 16 + m;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float e = __builtin_amdgcn_exp2f(__builtin_fmaf(w[i], ri[i].factor, -ri[i].lse));
+                                if constexpr (!decltype(FULL)::value) e = j >= ri[i].lo && j < ri[i].hi ? e : 0.0f;
+                                part[kt] += e;
+                            }
                         }
                     }
-                }
+                };
+                if (full) tiles(std::true_type());
+                else tiles(std::false_type());
                 // sums of 16 stages apart, so that a long sum loses less
                 if (++stages % 16 == 0) {
 #pragma unroll
@@ -333,7 +342,7 @@ __global__ void __launch_bounds__(256) weights_add(const CacheWeightsArgs a, con
             float* out = a.weights + (static_cast<int64_t>(b) * pg.hkv + h) * a.width;
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
-                float v = sum[kt] + part[kt];
+                float v = there[kt] ? sum[kt] + part[kt] : 0.0f;
                 v += __shfl_xor(v, 16);
                 v += __shfl_xor(v, 32);
                 const int j = j0 + (wave * KT + kt) * 16 + m;
