@@ -303,26 +303,36 @@ __global__ void __launch_bounds__(256) weights_add(const CacheWeightsArgs a, con
                         RowInfo ri[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) ri[i] = info[rt * 16 + 4 * g + i];
+// (two tiles at a time: no matrix instruction waits for the one before it)
 #pragma unroll
-                        for (int kt = 0; kt < KT; ++kt) {
-                            float4v w = {0.0f, 0.0f, 0.0f, 0.0f};
+                        for (int kt = 0; kt < KT; kt += 2) {
+                            float4v w[2];
 #pragma unroll
                             for (int q = 0; q < NG; ++q) {
-                                float4v c = {0.0f, 0.0f, 0.0f, 0.0f};
+                                float4v c[2];
+                                c[0] = c[1] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                                 for (int i = 0; i < KG; ++i) {
-                                    c = mfma(ql[q * KG + i], key[kt][q * KG + i], c);
-                                    c = mfma(qh[q * KG + i], key[kt][q * KG + i], c);
+#pragma unroll
+                                    for (int x = 0; x < 2; ++x) c[x] = mfma(ql[q * KG + i], key[kt + x][q * KG + i], c[x]);
+#pragma unroll
+                                    for (int x = 0; x < 2; ++x) c[x] = mfma(qh[q * KG + i], key[kt + x][q * KG + i], c[x]);
                                 }
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) w[i] = q ? __builtin_fmaf(c[i], scale[kt][q], w[i]) : c[i] * scale[kt][0];
-                            }
-                            const int j = j0 + (wave * KT + kt) * 16 + m;
+                                for (int x = 0; x < 2; ++x)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                float e = __builtin_amdgcn_exp2f(__builtin_fmaf(w[i], ri[i].factor, -ri[i].lse));
-                                if constexpr (!decltype(FULL)::value) e = j >= ri[i].lo && j < ri[i].hi ? e : 0.0f;
-                                part[kt] += e;
+                                    for (int i = 0; i < 4; ++i)
+                                        w[x][i] = q ? __builtin_fmaf(c[x][i], scale[kt + x][q], w[x][i]) : c[x][i] * scale[kt + x][0];
+                            }
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const int j = j0 + (wave * KT + kt + x) * 16 + m;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    float e = __builtin_amdgcn_exp2f(__builtin_fmaf(w[x][i], ri[i].factor, -ri[i].lse));
+                                    if constexpr (!decltype(FULL)::value) e = j >= ri[i].lo && j < ri[i].hi ? e : 0.0f;
+                                    part[kt + x] += e;
+                                }
                             }
                         }
                     }
