@@ -169,6 +169,14 @@ int check_seqs(const hr_cache_seqs* s, const hr::CachePage& pg, int64_t n_pages,
     return HR_OK;
 }
 
+// For kernels that look some tiles past a sequence's end: positions there are still ints.
+int check_reach(const hr_cache_seqs* s, int page) {
+    constexpr int64_t most = (int64_t{1} << 31) - (1 << 16);
+    if (s->max_pages * page > most)
+        return fail(HR_EUNSUPPORTED, "max_pages = %lld hold more than 2^31 - 2^16 positions", (long long)s->max_pages);
+    return HR_OK;
+}
+
 int check_tokens(int dtype, int64_t tokens) {
     if (dtype != HR_F32 && dtype != HR_BF16) return fail(HR_EINVAL, "dtype %d is not HR_F32 or HR_BF16", dtype);
     if (tokens < 0 || tokens > kMaxCount) return fail(HR_EINVAL, "tokens = %lld must be in 0..2^30", (long long)tokens);

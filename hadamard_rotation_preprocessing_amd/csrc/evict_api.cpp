@@ -20,7 +20,10 @@ int check_width(int64_t width, int64_t max_pages, int page) {
 
 // Row tiles of the kernel of few rows for a call, by the rows (new tokens x query heads
 // of a kv head) that a sequence has by the caller's bound, or without one in the mean; 0
-// for the kernel of many rows.
+// for the kernel of many rows.  Queries in registers and keys streaming past take 34 us
+// for 4 rows where the keys of a block in registers and rows through LDS take 90 us
+// (24 sequences of up to 32768, 8 heads of 128); more rows than two tiles need several
+// passes over the keys there, and one here.
 int few_tiles(int64_t tokens, int rep, int64_t seqs, int64_t max_q) {
     const int64_t n = max_q > 0 ? (max_q < tokens ? max_q : tokens) : (tokens + seqs - 1) / seqs;
     return n * rep <= 16 ? 1 : n * rep <= 32 ? 2 : 0;
@@ -50,7 +53,7 @@ int hr_cache_weights(const void* q, int64_t q_stride_token, int64_t q_stride_hea
     int st = check_spec(spec, &a.pg);
     if (st) return st;
     if ((st = check_attention_sizes(dtype, tokens, q_heads, a.pg, max_q)) || (st = check_seqs(seqs, a.pg, n_pages, tokens, &a.sq)) ||
-        (st = check_mask(scale, causal, window)))
+        (st = check_reach(seqs, a.pg.page)) || (st = check_mask(scale, causal, window)))
         return st;
     if (!(decay >= 0.0f) || !std::isfinite(decay)) return fail(HR_EINVAL, "decay must be finite and not negative");
     if ((st = check_width(width, seqs->max_pages, a.pg.page))) return st;

@@ -216,7 +216,8 @@ int hr_latent_attention(const void* q, int64_t q_stride_token, int64_t q_stride_
     int st = check_latent(spec, &a.pg);
     if (st) return st;
     if ((st = check_tokens(dtype, tokens)) || (st = check_heads(tokens, heads, max_q)) ||
-        (st = check_seqs(seqs, like(a.pg), n_pages, tokens, &a.sq)) || (st = check_scale(scale, false)))
+        (st = check_seqs(seqs, like(a.pg), n_pages, tokens, &a.sq)) || (st = check_reach(seqs, a.pg.page)) ||
+        (st = check_scale(scale, false)))
         return st;
     if (tokens == 0) return ok();
     int64_t qb, rb, ob;

@@ -38,6 +38,7 @@ extern "C" {
  *   weights  device float32, read and written.
  *   max_q    an upper bound of one row's new tokens, or 0 if not known.
  *   work     device scratch of hr_cache_weights_work bytes, 16-byte aligned.
+ * max_pages * page_size: at most 2^31 - 2^16 (else HR_EUNSUPPORTED).
  * Sums are taken in a fixed order: the result does not depend on scheduling.
  */
 int hr_cache_weights(const void* q, int64_t q_stride_token, int64_t q_stride_head,

@@ -91,7 +91,8 @@ int hr_latent_read(const void* pool, int64_t n_pages, const hr_latent_spec* spec
  *            latent_dim elements a row; q_rope the same with rope_dim; rows
  *            16-byte aligned, `dtype` HR_F32 or HR_BF16.
  *   scale    positive and finite.
- *   lse, max_q, work  as in hr_cache_attention.
+ *   lse, max_q, work  as in hr_cache_attention; max_pages * page_size at most 2^31 -
+ *            2^16 (else HR_EUNSUPPORTED).
  * Positions of absent pages are not seen; what a token does not see has no
  * influence, whatever its bytes are.  A token that sees nothing gets zeros (and a
  * log-sum-exp of -inf).  Scales are the append's: positive and finite, or NaN.
