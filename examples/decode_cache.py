@@ -9,6 +9,7 @@ of a row is drawn from the last layer's output.
 
     python examples/decode_cache.py                      # 4 rows, 256 tokens of prompt, 64 steps
     python examples/decode_cache.py --rows 32 --prompt 4000 --steps 32 --layers 8
+    python examples/decode_cache.py --prompt 4000 --budget 1024   # rows cut to their 1024 heaviest positions
 
 It prints the error of the first layer's attention against exact attention over
 the unquantized keys and values, and the time of a step.
@@ -26,7 +27,8 @@ import hadamard_rotation_preprocessing_amd as hr  # noqa: E402
 class Decoder:
     """Attention layers whose keys and values live in one pool of pages."""
 
-    def __init__(self, layers, rows, positions, q_heads, kv_heads, head_dim, vocab=256, page=64, device="cuda", seed=0):
+    def __init__(self, layers, rows, positions, q_heads, kv_heads, head_dim, vocab=256, page=64, device="cuda", seed=0,
+                 budget=0):
         g = torch.Generator(device=device).manual_seed(seed)
         width = q_heads * head_dim
         self.q_heads, self.kv_heads, self.head_dim, self.page = q_heads, kv_heads, head_dim, page
@@ -43,12 +45,25 @@ class Decoder:
         self.head = weight(width, vocab)
         self.table = torch.full((rows, self.width), -1, dtype=torch.int32, device=device)
         self.lens = torch.zeros(rows, dtype=torch.int32, device=device)
+        # with a budget: the attention weight that each position has got so far
+        self.budget = budget
+        self.weights = torch.zeros((layers, rows, kv_heads, self.width * page), device=device) if budget else None
 
     def schedule(self, parents, grow):
         """Row i continues row parents[i] (-1: a new one), grown by grow[i]."""
         step = hr.cache_update(self.pool, self.spec, self.table, self.lens, parents, grow)
         self.table, self.lens = step["table"], step["lens"]
+        if self.budget:
+            self.weights = self.weights[:, parents.clamp(min=0).long()]     # (a new row's are written before they are read)
         return step["status"]
+
+    def evict(self):
+        """Cuts the rows to the budget: 4 first positions, the newest eighth, and the
+        heaviest of the others; layer by layer and head by head."""
+        r = hr.cache_evict(self.pool, self.spec, self.table, self.lens, self.weights, self.budget, min(4, self.budget // 8),
+                           self.budget // 8)
+        self.table, self.lens = r["table"], r["lens"]
+        return r["status"]
 
     def forward(self, tokens, new):
         """tokens int64 [rows * new], row by row; returns logits of each row's last token."""
@@ -60,7 +75,10 @@ class Decoder:
             qkv = (y @ wi).view(-1, hq + 2 * hk, d)
             q, k, v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]     # read in place, as slices
             hr.cache_append(self.pool[i], self.spec, k, v, self.table, self.lens)
-            o = hr.cache_attention(q, self.pool[i], self.spec, self.table, self.lens, max_q=new)
+            o = hr.cache_attention(q, self.pool[i], self.spec, self.table, self.lens, max_q=new, lse=bool(self.budget))
+            if self.budget:
+                o, lse = o
+                hr.cache_weights(q, self.pool[i], self.spec, self.table, self.lens, lse, self.weights[i], max_q=new)
             if i == 0:
                 self.first = (q, k, v, o)
             x = x + o.reshape(x.shape) @ wo
@@ -91,9 +109,10 @@ def main(argv=None):
     p.add_argument("--q-heads", type=int, default=32)
     p.add_argument("--kv-heads", type=int, default=8)
     p.add_argument("--head-dim", type=int, default=128)
+    p.add_argument("--budget", type=int, default=0, help="positions that a row keeps (0: all)")
     a = p.parse_args(argv)
     dev = "cuda"
-    m = Decoder(a.layers, a.rows, a.prompt + a.steps, a.q_heads, a.kv_heads, a.head_dim, device=dev)
+    m = Decoder(a.layers, a.rows, a.prompt + a.steps, a.q_heads, a.kv_heads, a.head_dim, device=dev, budget=a.budget)
     g = torch.Generator(device=dev).manual_seed(1)
     fresh = torch.full((a.rows,), -1, dtype=torch.int32, device=dev)
     m.schedule(fresh, torch.full_like(fresh, a.prompt))
@@ -114,6 +133,8 @@ def main(argv=None):
         parents = same.clone()
         if step % 8 == 7:
             parents[-1] = 0
+        if a.budget and step % 8 == 0:
+            m.evict()
         status = m.schedule(parents, one)
         p = torch.softmax(logits[parents.long()].float(), -1)
         token = torch.multinomial(p, 1, generator=g)[:, 0]
