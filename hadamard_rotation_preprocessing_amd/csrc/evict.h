@@ -50,11 +50,15 @@ int launch_cache_weights(const CacheWeightsArgs& a, int bf16, void* stream);
 int cache_weights_workers(int few, int* workers);
 int launch_cache_evict(const CacheEvictArgs& a, void* stream);
 
-// bytes of scratch: the numbering of the sequences' key blocks; a row's factor and
-// log-sum-exp, and its query as pairs of float16
+// bytes of scratch: the numbering of the sequences' work; a row's factor and
+// log-sum-exp, and its query as pairs of float16; and in the kernel of many rows two
+// partial sums of a block of up to 256 keys for each workgroup, of which there are at
+// most kWeightsParts
+constexpr int kWeightsParts = 512;
 constexpr int64_t cache_weights_first(int64_t seqs) { return ((seqs + 1) * 8 + 15) / 16 * 16; }
-constexpr int64_t cache_weights_bytes(int64_t seqs, int64_t tokens, int32_t q_heads, int d) {
-    return cache_weights_first(seqs) + (tokens * q_heads * 8 + 15) / 16 * 16 + tokens * q_heads * d * 4;
+constexpr int64_t cache_weights_bytes(int64_t seqs, int64_t tokens, int32_t q_heads, int d, int few) {
+    return cache_weights_first(seqs) + (tokens * q_heads * 8 + 15) / 16 * 16 + tokens * q_heads * d * 4 +
+           (few == 0 ? int64_t{kWeightsParts} * 2 * 256 * 4 : 0);
 }
 // int32 words of scratch
 constexpr int64_t cache_evict_words(int64_t n_pages, int64_t rows) { return 3 * n_pages + rows + 16; }

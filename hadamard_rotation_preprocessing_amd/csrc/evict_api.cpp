@@ -25,7 +25,7 @@ int check_width(int64_t width, int64_t max_pages, int page) {
 // (24 sequences of up to 32768, 8 heads of 128); more rows than two tiles need several
 // passes over the keys there, and one here.
 int few_tiles(int64_t tokens, int rep, int64_t seqs, int64_t max_q) {
-    const int64_t n = max_q > 0 ? (max_q < tokens ? max_q : tokens) : (tokens + seqs - 1) / seqs;
+    const int64_t n = max_q > 0 ? (max_q < tokens ? max_q : tokens) : seqs > 0 ? (tokens + seqs - 1) / seqs : tokens;
     return n * rep <= 16 ? 1 : n * rep <= 32 ? 2 : 0;
 }
 
@@ -41,7 +41,7 @@ int hr_cache_weights_work(int dtype, int64_t tokens, int32_t q_heads, const hr_c
     if (!bytes) return fail(HR_EINVAL, "bytes is NULL");
     if ((st = check_attention_sizes(dtype, tokens, q_heads, pg, max_q))) return st;
     if (rows < 0 || rows > kMaxCount) return fail(HR_EINVAL, "rows = %lld must be in 0..2^30", (long long)rows);
-    *bytes = tokens == 0 ? 0 : hr::cache_weights_bytes(rows, tokens, q_heads, pg.d);
+    *bytes = tokens == 0 ? 0 : hr::cache_weights_bytes(rows, tokens, q_heads, pg.d, few_tiles(tokens, q_heads / pg.hkv, rows, max_q));
     return ok();
 }
 
@@ -62,7 +62,8 @@ int hr_cache_weights(const void* q, int64_t q_stride_token, int64_t q_stride_hea
     if ((st = check_rows(q, "q", q_stride_token, q_stride_head, tokens, q_heads, a.pg.d, dtype, &qb)) ||
         (st = check_ptr(pool, "pool", 16)) || (st = check_ptr(lse, "lse", 4)) || (st = check_ptr(weights, "weights", 4)))
         return st;
-    const int64_t need = hr::cache_weights_bytes(seqs->rows, tokens, q_heads, a.pg.d);
+    a.few = few_tiles(tokens, q_heads / a.pg.hkv, seqs->rows, max_q);
+    const int64_t need = hr::cache_weights_bytes(seqs->rows, tokens, q_heads, a.pg.d, a.few);
     if ((st = check_ptr(work, "work", 16))) return st;
     if (work_bytes < need) return fail(HR_EINVAL, "work_bytes = %lld: %lld are needed", (long long)work_bytes, (long long)need);
     const Range r[] = {{"weights", weights, size_of(size_of(seqs->rows, a.pg.hkv), width, 4), true},
@@ -75,7 +76,6 @@ int hr_cache_weights(const void* q, int64_t q_stride_token, int64_t q_stride_hea
                        {"cu_q", seqs->cu_q, (seqs->rows + 1) * 4, false}};
     if ((st = check_overlap(r, 8))) return st;
     int workers;
-    a.few = few_tiles(tokens, q_heads / a.pg.hkv, seqs->rows, max_q);
     const int e = hr::cache_weights_workers(a.few, &workers);
     if (e != 0) return fail(HR_EDEVICE, "device query failed: %s", hipGetErrorString(static_cast<hipError_t>(e)));
     a.q = q;

@@ -12,11 +12,25 @@
 //
 // Layout.  weights_query rotates the queries once and leaves them in the scratch
 // in the order of a lane's operand, kv head by kv head, with each row's scale and
-// log-sum-exp.  A workgroup of weights_add takes the keys of a block of one kv head
-// of one sequence, 16 KT of them to a wave, as operands in registers, and passes
-// over all rows that see some of them, kRows at a time through LDS, shared by its
-// four waves.  Blocks are numbered over all sequences and kv heads, and workgroups
-// take them in turn.  Nothing is joined afterwards.
+// log-sum-exp.
+//
+// Many rows (chunks of prompts): a workgroup of weights_add takes the keys of a block
+// of one kv head of one sequence, 16 KT of them to a wave, as operands in registers,
+// and passes over the rows that see some of them, kRows at a time through LDS, shared
+// by its four waves; two buffers, and the next rows on their way.  Blocks are numbered
+// over all sequences and kv heads; where they do not go into the workgroups evenly,
+// their rows are numbered, a workgroup takes an equal run of those, and weights_join
+// adds up the blocks that were cut.  Two chunks of 2048 tokens against 8192 positions,
+// 32 heads over 8 of 128: weights_query 24 us, weights_add 566 us, 860 TFLOP/s with the
+// two products counted.  The matrix instructions are 47% of its cycles, and the vector
+// ones (of 112 cycles for a tile 64 are exponentials) and the reads
+// of rows from LDS nearly all of the rest; the clock falls to 1.7 GHz under them.
+// Tried: one tile of keys at a time 586 us, a branch for each absent tile 681 us, no
+// rows on their way 702 us.
+//
+// Few rows (steps): weights_few, below.  24 sequences of up to 32768, one token each:
+// 34 us for 74 MB, 2.2 TB/s; what bounds it is the way of a wave's small loads (64 bytes
+// of a key's codes, its scale, zero point and weight), of which four tiles' are under way.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -36,6 +50,8 @@ typedef int int4v __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 32;     // rows of a stage
 constexpr int kItem = 64;     // keys of a block of weights_few: four tiles of 16, one of each on its way
+constexpr int kSetUp = 2;     // stages that the keys' way into registers and the sums' way out cost
+constexpr int kLeast = 4;     // of work to a workgroup: with less there are fewer workgroups
 constexpr int kTop = 14;      // a row's largest query element is below 2^kTop in float16
 
 __device__ __forceinline__ float4v mfma(uint4v a, uint4v b, float4v c) {
@@ -61,6 +77,55 @@ __device__ __forceinline__ int cu_at(const CacheSeqs& s, int b) {
     return min(max(c, 0), s.tokens);
 }
 
+template <int D>
+struct Shape {
+    static constexpr int KT = D == 256 ? 2 : 4;      // 16-key tiles of a wave
+    static constexpr int KEYS = 4 * 16 * KT;         // of a block
+    static constexpr int STRIDE = 4 * D + 32;        // bytes of a row in LDS: hi, lo, and a shift of eight banks
+};
+
+// A sequence: its tokens from `start`, its positions, and the position of its first
+// new token (which may lie before 0).
+struct Seq {
+    int start, n, len, first;
+};
+__device__ __forceinline__ Seq seq_of(const CacheWeightsArgs& a, int b) {
+    Seq s;
+    s.start = cu_at(a.sq, b);
+    s.n = max(cu_at(a.sq, b + 1) - s.start, 0);
+    s.len = static_cast<int>(min(static_cast<int64_t>(max(a.sq.lens[b], 0)), static_cast<int64_t>(a.sq.max_pages) << a.pg.logp));
+    s.first = s.len - s.n;
+    return s;
+}
+
+// The rows of a kv head that see some key of [j0, j0 + keys): from p0, a multiple of
+// kRows, to p1; their stages.
+__device__ __forceinline__ int stages_of(const CacheWeightsArgs& a, const Seq& s, int64_t j0, int keys, int64_t& p0, int64_t& p1) {
+    p0 = 0;
+    p1 = static_cast<int64_t>(s.n) * a.rep;
+    if (a.causal) {
+        p0 = max(j0 - s.first, int64_t{0}) * a.rep;
+        if (a.window) p1 = min(p1, (j0 + keys - 1 - s.first + a.window) * a.rep);
+    }
+    p0 = p0 / kRows * kRows;
+    return p1 > p0 ? static_cast<int>((p1 - p0 + kRows - 1) / kRows) : 0;
+}
+
+typedef const int32_t __attribute__((address_space(4)))* ConstInts;
+
+// the last of first[0 .. n - 1], ascending, that is at most `item`, by the whole wave
+__device__ __forceinline__ int last_at_most(const int64_t* first, int n, int64_t item) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, end = n;
+    while (end - lo > 1) {
+        const int step = (end - lo + 63) / 64, at = lo + lane * step;
+        const int k = __popcll(__ballot(at < end && first[at < end ? at : lo] <= item));
+        lo += (k > 0 ? k - 1 : 0) * step;
+        end = min(lo + step, end);
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
 // ---------------------------------------------------------------------------
 // the queries
 
@@ -76,15 +141,63 @@ struct RowScale {
 template <int D, class T>
 __global__ void __launch_bounds__(256) weights_query(const CacheWeightsArgs a, uint32_t* out, RowScale* rows, int64_t* first_of) {
     constexpr int LPV = D / 16;
-    if (a.few && blockIdx.x == 0) {       // the numbering of weights_few's key blocks
-        __shared__ int64_t sums[4];
+    if (blockIdx.x == 0) {       // the numbering of the work
+        __shared__ int64_t sums[4], counts[256];
+        constexpr int KEYS = Shape<D>::KEYS;
+        // stages of a sequence's head, by the whole wave, and the most of one of its blocks
+        const auto stages = [&](const Seq& s, int& most) {
+            int64_t mine = 0, p0, p1;
+            if (s.n > 0)
+                for (int64_t j0 = static_cast<int64_t>(threadIdx.x & 63) * KEYS; j0 < s.len; j0 += 64 * KEYS) {
+                    const int w = kSetUp + stages_of(a, s, j0, KEYS, p0, p1);
+                    mine += w;
+                    most = max(most, w);
+                }
+#pragma unroll
+            for (int x = 1; x < 64; x *= 2) mine += __shfl_xor(mine, x);
+            return mine;
+        };
+        bool whole = true;
+        if (!a.few) {
+            int64_t work = 0, blocks = 0;
+            int most = 0;
+            for (int i = threadIdx.x / 64; i < a.sq.rows; i += 4) {
+                const Seq s = seq_of(a, i);
+                work += stages(s, most) * a.pg.hkv;
+                if (s.n > 0) blocks += (static_cast<int64_t>(s.len) + KEYS - 1) / KEYS * a.pg.hkv;
+            }
+#pragma unroll
+            for (int x = 1; x < 64; x *= 2) most = max(most, __shfl_xor(most, x));
+            if ((threadIdx.x & 63) == 0) {
+                counts[threadIdx.x / 64] = work;
+                counts[4 + threadIdx.x / 64] = blocks;
+                counts[8 + threadIdx.x / 64] = most;
+            }
+            __syncthreads();
+            work = counts[0] + counts[1] + counts[2] + counts[3];
+            blocks = counts[4] + counts[5] + counts[6] + counts[7];
+            const int64_t heaviest = max(max(counts[8], counts[9]), max(counts[10], counts[11]));
+            whole = 4 * heaviest * ((blocks + a.workers - 1) / a.workers) * a.workers <= 5 * work;
+            __syncthreads();
+        }
         int64_t before = 0;
         for (int r0 = 0; r0 < a.sq.rows; r0 += 256) {
             const int r = r0 + threadIdx.x;
             int64_t v = 0;
-            if (r < a.sq.rows && cu_at(a.sq, r + 1) > cu_at(a.sq, r)) {
-                const int64_t len = min(static_cast<int64_t>(max(a.sq.lens[r], 0)), static_cast<int64_t>(a.sq.max_pages) << a.pg.logp);
-                v = (len + kItem - 1) / kItem * a.pg.hkv;
+            if (whole) {                      // in blocks of keys
+                if (r < a.sq.rows) {
+                    const Seq s = seq_of(a, r);
+                    const int keys = a.few ? kItem : KEYS;
+                    if (s.n > 0) v = (static_cast<int64_t>(s.len) + keys - 1) / keys * a.pg.hkv;
+                }
+            } else {                          // in stages, a wave for a sequence
+                int most = 0;
+                for (int i = threadIdx.x / 64; i < 256 && r0 + i < a.sq.rows; i += 4) {
+                    const int64_t n = stages(seq_of(a, r0 + i), most);
+                    if ((threadIdx.x & 63) == 0) counts[i] = n * a.pg.hkv;
+                }
+                __syncthreads();
+                if (r < a.sq.rows) v = counts[threadIdx.x];
             }
             for (int x = 1; x < 64; x *= 2) {
                 const int64_t y = __shfl_up(v, x);
@@ -98,7 +211,7 @@ __global__ void __launch_bounds__(256) weights_query(const CacheWeightsArgs a, u
             if (r < a.sq.rows) first_of[r + 1] = before + v;
             before += sums[0] + sums[1] + sums[2] + sums[3];
         }
-        if (threadIdx.x == 0) first_of[0] = 0;
+        if (threadIdx.x == 0) first_of[0] = whole && !a.few ? -1 : 0;     // (and how it is numbered)
     }
     const int64_t v = (int64_t{blockIdx.x} * 256 + threadIdx.x) / LPV;
     const int64_t total = int64_t{a.sq.tokens} * a.hq;
@@ -147,220 +260,283 @@ struct RowInfo {
     int lo, hi;
 };
 
-template <int D>
-struct Shape {
-    static constexpr int KT = D == 256 ? 2 : 4;      // 16-key tiles of a wave
-    static constexpr int KEYS = 4 * 16 * KT;         // of a block
-    static constexpr int STRIDE = 4 * D + 32;        // bytes of a row in LDS: hi, lo, and a shift of eight banks
+// a value that all lanes have, as the compiler cannot see
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uni(int64_t v) {
+    return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(uni(static_cast<int>(v >> 32)))) << 32 |
+                                static_cast<uint32_t>(uni(static_cast<int>(v))));
+}
+
+// The work of all sequences and kv heads, in stages: a block of keys has kSetUp and
+// those of its rows.  Workgroup `worker` takes [begin, end) of it.  Where whole blocks
+// go into the workgroups evenly (the longest takes at most 5/4 of the mean) the work
+// is numbered in blocks, one each, and first_of[0] is -1: workgroups then keep step
+// and share the queries in their caches (two chunks of 2048 tokens against 8192: 566 us,
+// 603 in stages, evenly); where not, a few blocks with many rows are the work of all (two
+// chunks of 269 tokens against 447, 7 heads of one kv head: 93 us whole, 31 in stages).
+struct Range {
+    int64_t begin, end;
 };
+__device__ __forceinline__ Range range_of(const CacheWeightsArgs& a, int64_t total, bool whole, int worker) {
+    const int64_t n = min(max(whole ? total : total / kLeast, int64_t{1}), static_cast<int64_t>(a.workers));
+    if (worker >= n) return {total, total};
+    return {total * worker / n, total * (worker + 1) / n};
+}
+
+// The block that `item` belongs to: its sequence, kv head, first key and work, and what
+// of its work lies before item.  All lanes of a wave ask for the same.
+struct Block {
+    Seq s;
+    int b, h, work;
+    int64_t j0, at;
+};
+template <int KEYS>
+__device__ __forceinline__ Block block_of(const CacheWeightsArgs& a, const int64_t* first_of, bool whole, int64_t item) {
+    Block k;
+    k.b = last_at_most(first_of, a.sq.rows, item);
+    k.s = seq_of(a, k.b);
+    const int64_t before = max(first_of[k.b], int64_t{0}), heads = (first_of[k.b + 1] - before) / a.pg.hkv;   // work of a head
+    k.h = static_cast<int>((item - before) / heads);
+    k.at = (item - before) % heads;
+    k.work = 1;
+    if (whole) {
+        k.j0 = k.at * KEYS;
+        k.at = 0;
+        return k;
+    }
+    const int lane = threadIdx.x & 63;
+    for (k.j0 = 0;; k.j0 += 64 * KEYS) {
+        int64_t p0, p1;
+        const int64_t j0 = k.j0 + static_cast<int64_t>(lane) * KEYS;
+        const int mine = j0 < k.s.len ? kSetUp + stages_of(a, k.s, j0, KEYS, p0, p1) : 0;
+        int64_t upto = mine;
+#pragma unroll
+        for (int x = 1; x < 64; x *= 2) {
+            const int64_t y = __shfl_up(upto, x);
+            if (lane >= x) upto += y;
+        }
+        const uint64_t past = __ballot(upto > k.at);
+        if (past) {
+            const int l = __ffsll(static_cast<unsigned long long>(past)) - 1;
+            k.work = __shfl(mine, l);
+            k.at -= __shfl(upto, l) - k.work;
+            k.j0 += static_cast<int64_t>(l) * KEYS;
+            return k;
+        }
+        k.at -= __shfl(upto, 63);
+        if (k.j0 + 64 * KEYS >= k.s.len) return k;     // (never: the numbering has the item)
+    }
+}
 
 template <int D, int NG>
-__global__ void __launch_bounds__(256) weights_add(const CacheWeightsArgs a, const uint32_t* query, const RowScale* scales) {
+__global__ void __launch_bounds__(256) weights_add(const CacheWeightsArgs a, const uint32_t* query, const RowScale* scales, const int64_t* first_of, float* parts) {
     using S = Shape<D>;
     constexpr int KT = S::KT, KG = D / 32 / NG;
     __shared__ __attribute__((aligned(16))) uint8_t stages_[2][kRows * S::STRIDE];
     __shared__ __attribute__((aligned(16))) RowInfo infos[2][kRows];
-    __shared__ int64_t first_of[257];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
     const CachePage& pg = a.pg;
-    int64_t mine = blockIdx.x;             // this workgroup's next block among those of rows r0 and on
-    for (int r0 = 0; r0 < a.sq.rows; r0 += 256) {
-        // the blocks of 256 rows, numbered
-        int64_t n_blocks = 0;
-        if (r0 + tid < a.sq.rows && cu_at(a.sq, r0 + tid + 1) > cu_at(a.sq, r0 + tid)) {
-            const int64_t len = min(static_cast<int64_t>(max(a.sq.lens[r0 + tid], 0)), static_cast<int64_t>(a.sq.max_pages) << pg.logp);
-            n_blocks = (len + S::KEYS - 1) / S::KEYS * pg.hkv;
-        }
-        __syncthreads();
-        first_of[tid + 1] = n_blocks;
-        if (tid == 0) first_of[0] = 0;
-        __syncthreads();
-        for (int x = 1; x < 256; x *= 2) {
-            const int64_t y = tid + 1 > x ? first_of[tid + 1 - x] : 0;
-            __syncthreads();
-            first_of[tid + 1] += y;
-            __syncthreads();
-        }
-        const int64_t total = first_of[256];
-        for (; mine < total; mine += gridDim.x) {
-            int lo = 0, hi = 255;          // the last row whose blocks begin at or before this one
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) / 2;
-                if (first_of[mid] <= mine) lo = mid;
-                else hi = mid - 1;
-            }
-            const int b = r0 + lo;
-            const int start = cu_at(a.sq, b), n = cu_at(a.sq, b + 1) - start;
-            const int len = static_cast<int>(min(static_cast<int64_t>(max(a.sq.lens[b], 0)), static_cast<int64_t>(a.sq.max_pages) << pg.logp));
-            const int blocks = static_cast<int>((static_cast<int64_t>(len) + S::KEYS - 1) / S::KEYS);
-            const int64_t in_row = mine - first_of[lo];
-            const int h = static_cast<int>(in_row / blocks), j0 = static_cast<int>(in_row % blocks) * S::KEYS;
-            const int first = len - n;     // position of the first new token (may lie before 0)
-            const int32_t* table = a.sq.table + static_cast<int64_t>(b) * a.sq.max_pages;
+    // neighbouring work, which reads the same queries, on the same die
+    const int worker = a.workers % 8 ? blockIdx.x : blockIdx.x % 8 * (a.workers / 8) + blockIdx.x / 8;
+    const bool by_block = uni(first_of[0]) < 0;
+    const Range range = range_of(a, uni(first_of[a.sq.rows]), by_block, worker);
+    for (int64_t item = range.begin; item < range.end;) {
+        Block k = block_of<S::KEYS>(a, first_of, by_block, item);
+        k.s = {uni(k.s.start), uni(k.s.n), uni(k.s.len), uni(k.s.first)};
+        k.work = uni(k.work);
+        const int b = uni(k.b), h = uni(k.h), j0 = uni(static_cast<int>(k.j0)), n = k.s.n, len = k.s.len, first = k.s.first, start = k.s.start;
+        const int u0 = uni(static_cast<int>(k.at)), u1 = static_cast<int>(min(static_cast<int64_t>(k.work), u0 + range.end - item));
+        item += max(u1 - u0, 1);
+        const int32_t* table = a.sq.table + static_cast<int64_t>(b) * a.sq.max_pages;
 
-            // the wave's keys: B operands of c - z, and their scales
-            uint4v key[KT][D / 32];
-            float scale[KT][NG];
-            bool there[KT];
+        // the wave's keys: B operands of c - z, and their scales
+        uint4v key[KT][D / 32];
+        float scale[KT][NG];
+        bool there[KT];
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                const int t0 = j0 + (wave * KT + kt) * 16;
-                const int page = t0 < len ? table[t0 >> pg.logp] : -1;
-                there[kt] = page >= 0 && page < a.sq.n_pages;
-                if (!there[kt]) {              // (worked on all the same, and not added)
+        for (int kt = 0; kt < KT; ++kt) {
+            const int t0 = j0 + (wave * KT + kt) * 16;
+            const int page = t0 < len ? table[t0 >> pg.logp] : -1;
+            there[kt] = page >= 0 && page < a.sq.n_pages;
+            if (!there[kt]) {              // (worked on all the same, and not added)
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i) key[kt][i] = uint4v{0, 0, 0, 0};
+                for (int i = 0; i < D / 32; ++i) key[kt][i] = uint4v{0, 0, 0, 0};
 #pragma unroll
-                    for (int q = 0; q < NG; ++q) scale[kt][q] = 0.0f;
-                    continue;
-                }
-                const int off = (t0 & (pg.page - 1)) + m;
-                const uint8_t* base = a.pool + page * pg.page_bytes + h * pg.head_bytes;
-                const uint8_t* codes = base + pg.kc + off * (D / 2);
+                for (int q = 0; q < NG; ++q) scale[kt][q] = 0.0f;
+                continue;
+            }
+            const int off = (t0 & (pg.page - 1)) + m;
+            const uint8_t* base = a.pool + page * pg.page_bytes + h * pg.head_bytes;
+            const uint8_t* codes = base + pg.kc + off * (D / 2);
 #pragma unroll
-                for (int q = 0; q < NG; ++q) {
-                    const int at = off * NG + q;
-                    scale[kt][q] = pg.sf32 ? reinterpret_cast<const float*>(base + pg.ks)[at]
-                                           : bf2f(reinterpret_cast<const uint16_t*>(base + pg.ks)[at]);
-                    const uint32_t z = pg.sym ? 8u : (base[pg.kz + at / 2] >> (4 * (at & 1))) & 15u;
-                    // ORed with 1024 (at bit 4: 64) a code c is the float16 1024 + c (64 + c)
-                    const uint32_t f0 = 0x64006400u ^ (pg.sym ? 0x00080008u : 0u), f1 = 0x54005400u ^ (pg.sym ? 0x00800080u : 0u);
-                    const uint32_t z0 = 0x64006400u + z * 0x00010001u, z1 = 0x54005400u + z * 0x00100010u;
+            for (int q = 0; q < NG; ++q) {
+                const int at = off * NG + q;
+                scale[kt][q] = pg.sf32 ? reinterpret_cast<const float*>(base + pg.ks)[at]
+                                       : bf2f(reinterpret_cast<const uint16_t*>(base + pg.ks)[at]);
+                const uint32_t z = pg.sym ? 8u : (base[pg.kz + at / 2] >> (4 * (at & 1))) & 15u;
+                // ORed with 1024 (at bit 4: 64) a code c is the float16 1024 + c (64 + c)
+                const uint32_t f0 = 0x64006400u ^ (pg.sym ? 0x00080008u : 0u), f1 = 0x54005400u ^ (pg.sym ? 0x00800080u : 0u);
+                const uint32_t z0 = 0x64006400u + z * 0x00010001u, z1 = 0x54005400u + z * 0x00100010u;
 #pragma unroll
-                    for (int i = 0; i < KG; ++i) {
-                        uint32_t w = reinterpret_cast<const uint32_t*>(codes)[q * (D / NG / 8) + g * KG + i];
-                        uint4v k;
-                        k.x = pk_sub((w & 0x000F000Fu) ^ f0, z0);
-                        k.y = pk_sub((w & 0x00F000F0u) ^ f1, z1);
-                        w >>= 8;
-                        k.z = pk_sub((w & 0x000F000Fu) ^ f0, z0);
-                        k.w = pk_sub((w & 0x00F000F0u) ^ f1, z1);
-                        key[kt][q * KG + i] = k;
-                    }
+                for (int i = 0; i < KG; ++i) {
+                    uint32_t w = reinterpret_cast<const uint32_t*>(codes)[q * (D / NG / 8) + g * KG + i];
+                    uint4v k;
+                    k.x = pk_sub((w & 0x000F000Fu) ^ f0, z0);
+                    k.y = pk_sub((w & 0x00F000F0u) ^ f1, z1);
+                    w >>= 8;
+                    k.z = pk_sub((w & 0x000F000Fu) ^ f0, z0);
+                    k.w = pk_sub((w & 0x00F000F0u) ^ f1, z1);
+                    key[kt][q * KG + i] = k;
                 }
             }
-            float sum[KT] = {}, part[KT] = {};
-            const int64_t rows = static_cast<int64_t>(n) * a.rep;
-            const int64_t at = (static_cast<int64_t>(h) * a.sq.tokens + start) * a.rep;   // the rows' place in `query`
-            int64_t p0 = 0, p1 = rows;     // rows that see some key of the block
-            if (a.causal) {
-                p0 = max(static_cast<int64_t>(j0) - first, int64_t{0}) * a.rep;
-                if (a.window) p1 = min(p1, (static_cast<int64_t>(j0) + S::KEYS - 1 - first + a.window) * a.rep);
+        }
+        float sum[KT] = {}, sums[KT] = {};
+        const int64_t rows = static_cast<int64_t>(n) * a.rep;
+        const int64_t at = (static_cast<int64_t>(h) * a.sq.tokens + start) * a.rep;   // the rows' place in `query`
+        int64_t p0, p1;                // the rows that see some key of the block; of them, this workgroup's
+        stages_of(a, k.s, j0, S::KEYS, p0, p1);
+        if (!by_block) {
+            p1 = min(p1, p0 + static_cast<int64_t>(max(u1 - kSetUp, 0)) * kRows);
+            p0 += static_cast<int64_t>(max(u0 - kSetUp, 0)) * kRows;
+        }
+        int stages = 0;
+        // the next rows are on their way while these are worked on
+        constexpr int LOADS = kRows * D / 4 / 256;          // of 16 bytes
+        uint4v ahead[LOADS];
+        RowScale rs{};
+        const auto load = [&](int64_t p) {
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                const int x = i * 256 + tid, r = x / (D / 4), c = x % (D / 4);
+                ahead[i] = reinterpret_cast<const uint4v*>(query + (at + min(p + r, rows - 1)) * D)[c];
             }
-            int stages = 0;
-            // the next rows are on their way while these are worked on
-            constexpr int LOADS = kRows * D / 4 / 256;          // of 16 bytes
-            uint4v ahead[LOADS];
-            RowScale rs{};
-            const auto load = [&](int64_t p) {
+            if (tid < kRows) rs = scales[at + min(p + tid, rows - 1)];
+        };
+        if (p0 < p1) load(p0);
+        for (int64_t p = p0; p < p1; p += kRows) {
+            uint8_t* stage = stages_[stages & 1];
+            RowInfo* info = infos[stages & 1];
 #pragma unroll
-                for (int i = 0; i < LOADS; ++i) {
-                    const int x = i * 256 + tid, r = x / (D / 4), c = x % (D / 4);
-                    ahead[i] = reinterpret_cast<const uint4v*>(query + (at + min(p + r, rows - 1)) * D)[c];
-                }
-                if (tid < kRows) rs = scales[at + min(p + tid, rows - 1)];
-            };
-            p0 = p0 / kRows * kRows;
-            if (p0 < p1) load(p0);
-            for (int64_t p = p0; p < p1; p += kRows) {
-                uint8_t* stage = stages_[stages & 1];
-                RowInfo* info = infos[stages & 1];
+            for (int i = 0; i < LOADS; ++i) {
+                const int x = i * 256 + tid, r = x / (D / 4), c = x % (D / 4);
+                *reinterpret_cast<uint4v*>(stage + r * S::STRIDE + c * 16) = ahead[i];
+            }
+            if (tid < kRows) {
+                RowInfo ri;
+                const int pos = first + static_cast<int>(static_cast<uint32_t>(min(p + tid, rows - 1)) / a.rep);
+                ri.factor = rs.factor;
+                ri.lse = rs.lse;
+                ri.lo = a.window ? max(pos - a.window + 1, 0) : 0;
+                ri.hi = p + tid < rows ? (a.causal ? min(pos + 1, len) : len) : 0;
+                info[tid] = ri;
+            }
+            // (two buffers: the last readers of this one are before the last barrier)
+            __syncthreads();
+            if (p + kRows < p1) load(p + kRows);
+            // whether every row of the stage is there and sees every key of the block
+            const int pos0 = first + static_cast<int>(static_cast<uint32_t>(p) / a.rep);
+            const int pos1 = first + static_cast<int>(static_cast<uint32_t>(min(p + kRows, rows) - 1) / a.rep);
+            const bool full = p + kRows <= rows && j0 + S::KEYS <= len && (!a.causal || j0 + S::KEYS - 1 <= pos0) &&
+                              (!a.window || j0 > pos1 - a.window);
+            const auto tiles = [&](auto FULL) __attribute__((always_inline)) {
 #pragma unroll
-                for (int i = 0; i < LOADS; ++i) {
-                    const int x = i * 256 + tid, r = x / (D / 4), c = x % (D / 4);
-                    *reinterpret_cast<uint4v*>(stage + r * S::STRIDE + c * 16) = ahead[i];
-                }
-                if (tid < kRows) {
-                    RowInfo ri;
-                    const int pos = first + static_cast<int>(static_cast<uint32_t>(min(p + tid, rows - 1)) / a.rep);
-                    ri.factor = rs.factor;
-                    ri.lse = rs.lse;
-                    ri.lo = a.window ? max(pos - a.window + 1, 0) : 0;
-                    ri.hi = p + tid < rows ? (a.causal ? min(pos + 1, len) : len) : 0;
-                    info[tid] = ri;
-                }
-                // (two buffers: the last readers of this one are before the last barrier)
-                __syncthreads();
-                if (p + kRows < p1) load(p + kRows);
-                // whether every row of the stage is there and sees every key of the block
-                const int pos0 = first + static_cast<int>(static_cast<uint32_t>(p) / a.rep);
-                const int pos1 = first + static_cast<int>(static_cast<uint32_t>(min(p + kRows, rows) - 1) / a.rep);
-                const bool full = p + kRows <= rows && j0 + S::KEYS <= len && (!a.causal || j0 + S::KEYS - 1 <= pos0) &&
-                                  (!a.window || j0 > pos1 - a.window);
-                const auto tiles = [&](auto FULL) __attribute__((always_inline)) {
+                for (int rt = 0; rt < kRows / 16; ++rt) {
+                    uint4v qh[D / 32], ql[D / 32];
+                    const uint8_t* row = stage + (rt * 16 + m) * S::STRIDE;
 #pragma unroll
-                    for (int rt = 0; rt < kRows / 16; ++rt) {
-                        uint4v qh[D / 32], ql[D / 32];
-                        const uint8_t* row = stage + (rt * 16 + m) * S::STRIDE;
+                    for (int q = 0; q < NG; ++q)
 #pragma unroll
-                        for (int q = 0; q < NG; ++q)
+                        for (int i = 0; i < KG; ++i) {
+                            const int c = 2 * (q * (D / NG) + g * (D / NG / 4) + 8 * i);
+                            qh[q * KG + i] = *reinterpret_cast<const uint4v*>(row + c);
+                            ql[q * KG + i] = *reinterpret_cast<const uint4v*>(row + 2 * D + c);
+                        }
+                    RowInfo ri[4];
 #pragma unroll
-                            for (int i = 0; i < KG; ++i) {
-                                const int c = 2 * (q * (D / NG) + g * (D / NG / 4) + 8 * i);
-                                qh[q * KG + i] = *reinterpret_cast<const uint4v*>(row + c);
-                                ql[q * KG + i] = *reinterpret_cast<const uint4v*>(row + 2 * D + c);
-                            }
-                        RowInfo ri[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) ri[i] = info[rt * 16 + 4 * g + i];
+                    for (int i = 0; i < 4; ++i) ri[i] = info[rt * 16 + 4 * g + i];
 // (two tiles at a time: no matrix instruction waits for the one before it)
 #pragma unroll
-                        for (int kt = 0; kt < KT; kt += 2) {
-                            float4v w[2];
+                    for (int kt = 0; kt < KT; kt += 2) {
+                        float4v w[2];
 #pragma unroll
-                            for (int q = 0; q < NG; ++q) {
-                                float4v c[2];
-                                c[0] = c[1] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+                        for (int q = 0; q < NG; ++q) {
+                            float4v c[2];
+                            c[0] = c[1] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                                for (int i = 0; i < KG; ++i) {
+                            for (int i = 0; i < KG; ++i) {
 #pragma unroll
-                                    for (int x = 0; x < 2; ++x) c[x] = mfma(ql[q * KG + i], key[kt + x][q * KG + i], c[x]);
+                                for (int x = 0; x < 2; ++x) c[x] = mfma(ql[q * KG + i], key[kt + x][q * KG + i], c[x]);
 #pragma unroll
-                                    for (int x = 0; x < 2; ++x) c[x] = mfma(qh[q * KG + i], key[kt + x][q * KG + i], c[x]);
-                                }
-#pragma unroll
-                                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i)
-                                        w[x][i] = q ? __builtin_fmaf(c[x][i], scale[kt + x][q], w[x][i]) : c[x][i] * scale[kt + x][0];
+                                for (int x = 0; x < 2; ++x) c[x] = mfma(qh[q * KG + i], key[kt + x][q * KG + i], c[x]);
                             }
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const int j = j0 + (wave * KT + kt + x) * 16 + m;
+                            for (int x = 0; x < 2; ++x)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    float e = __builtin_amdgcn_exp2f(__builtin_fmaf(w[x][i], ri[i].factor, -ri[i].lse));
-                                    if constexpr (!decltype(FULL)::value) e = j >= ri[i].lo && j < ri[i].hi ? e : 0.0f;
-                                    part[kt + x] += e;
-                                }
+                                for (int i = 0; i < 4; ++i)
+                                    w[x][i] = q ? __builtin_fmaf(c[x][i], scale[kt + x][q], w[x][i]) : c[x][i] * scale[kt + x][0];
+                        }
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int j = j0 + (wave * KT + kt + x) * 16 + m;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float e = __builtin_amdgcn_exp2f(__builtin_fmaf(w[x][i], ri[i].factor, -ri[i].lse));
+                                if constexpr (!decltype(FULL)::value) e = j >= ri[i].lo && j < ri[i].hi ? e : 0.0f;
+                                sums[kt + x] += e;
                             }
                         }
                     }
-                };
-                if (full) tiles(std::true_type());
-                else tiles(std::false_type());
-                // sums of 16 stages apart, so that a long sum loses less
-                if (++stages % 16 == 0) {
+                }
+            };
+            if (full) tiles(std::true_type());
+            else tiles(std::false_type());
+            // sums of 16 stages apart, so that a long sum loses less
+            if (++stages % 16 == 0) {
 #pragma unroll
-                    for (int kt = 0; kt < KT; ++kt) {
-                        sum[kt] += part[kt];
-                        part[kt] = 0.0f;
-                    }
+                for (int kt = 0; kt < KT; ++kt) {
+                    sum[kt] += sums[kt];
+                    sums[kt] = 0.0f;
                 }
             }
-            __syncthreads();                   // (the next block's rows)
-            float* out = a.weights + (static_cast<int64_t>(b) * pg.hkv + h) * a.width;
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                float v = there[kt] ? sum[kt] + part[kt] : 0.0f;
-                v += __shfl_xor(v, 16);
-                v += __shfl_xor(v, 32);
-                const int j = j0 + (wave * KT + kt) * 16 + m;
-                if (g == 0 && j < len) out[j] = (j < first ? a.decay * out[j] : 0.0f) + v;
-            }
         }
-        mine -= total;
+        __syncthreads();                   // (the next block's rows)
+        const bool whole = u0 == 0 && u1 == k.work;
+        float* out = a.weights + (static_cast<int64_t>(b) * pg.hkv + h) * a.width;
+        float* part = parts + (static_cast<int64_t>(worker) * 2 + (u0 == 0)) * S::KEYS;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            float v = there[kt] ? sum[kt] + sums[kt] : 0.0f;
+            v += __shfl_xor(v, 16);
+            v += __shfl_xor(v, 32);
+            const int j = j0 + (wave * KT + kt) * 16 + m;
+            if (g == 0 && !whole) part[(wave * KT + kt) * 16 + m] = v;
+            if (g == 0 && whole && j < len) out[j] = (j < first ? a.decay * out[j] : 0.0f) + v;
+        }
     }
+}
+
+// Sums of a block that several workgroups took: parts[w][1] of the one that began it,
+// parts[w][0] of those after it, in their order.
+template <int D>
+__global__ void __launch_bounds__(Shape<D>::KEYS) weights_join(const CacheWeightsArgs a, const int64_t* first_of, const float* parts) {
+    constexpr int KEYS = Shape<D>::KEYS;
+    if (first_of[0] < 0) return;           // (whole blocks)
+    const int64_t total = first_of[a.sq.rows];
+    const int worker = blockIdx.x;
+    const Range mine = range_of(a, total, false, worker);
+    if (mine.begin == mine.end || mine.end == total) return;
+    const Block k = block_of<KEYS>(a, first_of, false, mine.end);
+    if (k.at == 0 || mine.end - k.at < mine.begin) return;     // no block is cut here, or it began before
+    const int64_t end = mine.end - k.at + k.work;
+    const int t = threadIdx.x;
+    float sum = parts[(static_cast<int64_t>(worker) * 2 + 1) * KEYS + t];
+    for (int w = worker + 1;; ++w) {
+        sum += parts[static_cast<int64_t>(w) * 2 * KEYS + t];
+        if (range_of(a, total, false, w).end >= end) break;
+    }
+    const int64_t j = k.j0 + t;
+    float* out = a.weights + (static_cast<int64_t>(k.b) * a.pg.hkv + k.h) * a.width;
+    if (j < k.s.len) out[j] = (j < k.s.first ? a.decay * out[j] : 0.0f) + sum;
 }
 
 // ---------------------------------------------------------------------------
@@ -371,21 +547,6 @@ __global__ void __launch_bounds__(256) weights_add(const CacheWeightsArgs a, con
 // of all key blocks of all kv heads and sequences, numbered by weights_query, whatever
 // the lengths, and no wave waits for another.  The loads of the next kItem keys are on
 // their way throughout.
-
-typedef const int32_t __attribute__((address_space(4)))* ConstInts;
-
-// the last of first[0 .. n - 1], ascending, that is at most `item`, by the whole wave
-__device__ __forceinline__ int last_at_most(const int64_t* first, int n, int64_t item) {
-    const int lane = threadIdx.x & 63;
-    int lo = 0, end = n;
-    while (end - lo > 1) {
-        const int step = (end - lo + 63) / 64, at = lo + lane * step;
-        const int k = __popcll(__ballot(at < end && first[at < end ? at : lo] <= item));
-        lo += (k > 0 ? k - 1 : 0) * step;
-        end = min(lo + step, end);
-    }
-    return __builtin_amdgcn_readfirstlane(lo);
-}
 
 template <int N>
 __device__ __forceinline__ void buffer_words(__amdgpu_buffer_rsrc_t r, int lane_at, int at, uint32_t* w) {
@@ -601,8 +762,11 @@ void add_launch(const CacheWeightsArgs& a, int bf16, hipStream_t s) {
     uint32_t* query = reinterpret_cast<uint32_t*>(a.work + cache_weights_first(a.sq.rows) + (int64_t{a.sq.tokens} * a.hq * 8 + 15) / 16 * 16);
     if (bf16) query_launch<D, uint16_t>(a, query, rows, first_of, s);
     else query_launch<D, float>(a, query, rows, first_of, s);
-    if (a.few == 0) hipLaunchKernelGGL((weights_add<D, NG>), dim3(a.workers), dim3(256), 0, s, a, query, rows);
-    else if (a.few == 1) hipLaunchKernelGGL((weights_few<D, NG, 1>), dim3(a.workers), dim3(256), 0, s, a, query, rows, first_of);
+    if (a.few == 0) {
+        float* parts = reinterpret_cast<float*>(query + int64_t{a.sq.tokens} * a.hq * D);
+        hipLaunchKernelGGL((weights_add<D, NG>), dim3(a.workers), dim3(256), 0, s, a, query, rows, first_of, parts);
+        hipLaunchKernelGGL((weights_join<D>), dim3(a.workers), dim3(Shape<D>::KEYS), 0, s, a, first_of, parts);
+    } else if (a.few == 1) hipLaunchKernelGGL((weights_few<D, NG, 1>), dim3(a.workers), dim3(256), 0, s, a, query, rows, first_of);
     else hipLaunchKernelGGL((weights_few<D, NG, 2>), dim3(a.workers), dim3(256), 0, s, a, query, rows, first_of);
 }
 
@@ -612,7 +776,8 @@ int cache_weights_workers(int few, int* workers) {
     int dev, cus;
     hipError_t e = hipGetDevice(&dev);
     if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-    if (e == hipSuccess) *workers = (few == 2 ? 2 : 4) * cus;   // (as many as fit with heads of 128)
+    // (as many as fit with heads of 128)
+    if (e == hipSuccess) *workers = few == 0 ? (2 * cus < kWeightsParts ? 2 * cus : kWeightsParts) : (few == 2 ? 2 : 4) * cus;
     return static_cast<int>(e);
 }
 

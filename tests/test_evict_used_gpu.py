@@ -175,3 +175,20 @@ def test_decode_example_with_a_budget(rows, prompt, steps, budget, capsys):
     assert logits.shape == (rows, 256) and torch.isfinite(logits).all()
     left = budget + (steps - 1) % 8 + 1
     assert "lengths %s" % ([left] * rows) in capsys.readouterr().out
+
+
+@pytest.mark.parametrize("d,group,page", [(64, 64, 16), (128, 32, 64), (256, 128, 32), (256, 32, 16)])
+@pytest.mark.parametrize("kw", [dict(), dict(window=50), dict(causal=False)], ids=["causal", "window", "full"])
+def test_weights_of_few_blocks_with_many_rows(d, group, page, kw):
+    """Blocks whose rows are shared out among workgroups: some with a whole block, some
+    with a part, sequences without tokens and with more tokens than positions, and
+    blocks that no row sees."""
+    seqs = [(500, 700), (0, 40), (130, 900), (300, 280), (1, 1)]
+    run_weights(O.CacheDef(2, d, page, group, False, "bf16"), seqs, 4, seed=d, absent=[(2, 3, -1)], **kw)
+
+
+def test_weights_of_blocks_that_stay_whole():
+    """As many blocks as workgroups take without a cut, of one length and of two."""
+    c = O.CacheDef(1, 64, 16, 64, False, "bf16")
+    run_weights(c, [(12, 60)] * 1000, 4, seed=1)
+    run_weights(c, [(12, 60), (0, 5), (14, 300)] * 170, 4, seed=2)
