@@ -24,7 +24,7 @@
 // 32 heads over 8 of 128: weights_query 24 us, weights_add 566 us, 860 TFLOP/s with the
 // two products counted.  The matrix instructions are 47% of its cycles, and the vector
 // ones (of 112 cycles for a tile 64 are exponentials) and the reads
-// of rows from LDS nearly all of the rest; the clock falls to 1.7 GHz under them.
+// of rows from LDS nearly all of the rest, at some 1.7 GHz (busy cycles over time).
 // Tried: one tile of keys at a time 586 us, a branch for each absent tile 681 us, no
 // rows on their way 702 us.
 //

@@ -33,6 +33,16 @@
 // it, and every workgroup takes an equal, contiguous run of all items.  A row's sums
 // are left in the scratch, for units that are cut in parts, and latent_finish joins
 // the parts in key order, divides, rotates back and rounds.
+//
+// Measured.  32 sequences of up to 32768, one token, 128 heads, latents of 512 in four
+// groups: latent_query 7 us, latent_sums 144 us (470 TFLOP/s, 1.55 us a step of 32 keys
+// and 64 rows), latent_finish 16 us.  The value waves bound it: LDS gives 64 bytes a
+// cycle to wide reads and takes 43 of wide writes, and their operands' writes and
+// transposing reads fill most of a step, with stores between the matrix steps.  Tried:
+// waves of one kind, each with scores and values, 517 us for the whole call where this
+// form takes 165; sixteen waves with half the registers 2.44 us a step; codes turned
+// into operands in registers by every wave, without LDS, 1.99 us a step.
+// One sequence of 331, 16 heads: 4.0, 13.2 and 4.5 us, of which most is latency.
 #pragma once
 
 #include <hip/hip_runtime.h>

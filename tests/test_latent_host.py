@@ -167,7 +167,7 @@ def test_attention_refusals(kw, status, text):
     refused(attention(**kw), status, text)
 
 
-def prompt(q=Q, st=16 * 192, sh=192, k=KP, kt=4096, kh=256, v=VP, vt=4096, vh=256, rope=X1, rt=64, dt=L.HR_BF16, tokens=200,
+def prompt(q=Q, st=16 * 200, sh=200, k=KP, kt=4096, kh=256, v=VP, vt=4096, vh=256, rope=X1, rt=64, dt=L.HR_BF16, tokens=200,
            positions=300, heads=16, nope=128, cu_q=CU, cu_k=LENS, rows=4, scale=0.0, causal=1, out=OUT, ost=2048, osh=128, lse=None):
     return A._latent_lib().hr_latent_prompt_attention(q, st, sh, k, kt, kh, v, vt, vh, rope, rt, dt, tokens, positions, heads, nope, cu_q,
                                                       cu_k, rows, scale, causal, out, ost, osh, lse, None)
