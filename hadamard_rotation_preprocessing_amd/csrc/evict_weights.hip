@@ -144,30 +144,36 @@ __global__ void __launch_bounds__(256) weights_query(const CacheWeightsArgs a, u
     if (blockIdx.x == 0) {       // the numbering of the work
         __shared__ int64_t sums[4], counts[256];
         constexpr int KEYS = Shape<D>::KEYS;
-        // stages of a sequence's head, by the whole wave, and the most of one of its blocks
+        // `lanes` threads to a sequence, as many as there are for each
+        int lanes = 64;
+        while (lanes > 1 && 256 / lanes < a.sq.rows) lanes /= 2;
+        const int at_once = 256 / lanes, part = threadIdx.x % lanes;
+        // a thread's part of the stages of a sequence's head, and the most of one block
         const auto stages = [&](const Seq& s, int& most) {
             int64_t mine = 0, p0, p1;
             if (s.n > 0)
-                for (int64_t j0 = static_cast<int64_t>(threadIdx.x & 63) * KEYS; j0 < s.len; j0 += 64 * KEYS) {
+                for (int64_t j0 = static_cast<int64_t>(part) * KEYS; j0 < s.len; j0 += lanes * KEYS) {
                     const int w = kSetUp + stages_of(a, s, j0, KEYS, p0, p1);
                     mine += w;
                     most = max(most, w);
                 }
-#pragma unroll
-            for (int x = 1; x < 64; x *= 2) mine += __shfl_xor(mine, x);
             return mine;
         };
         bool whole = true;
         if (!a.few) {
             int64_t work = 0, blocks = 0;
             int most = 0;
-            for (int i = threadIdx.x / 64; i < a.sq.rows; i += 4) {
+            for (int i = threadIdx.x / lanes; i < a.sq.rows; i += at_once) {
                 const Seq s = seq_of(a, i);
                 work += stages(s, most) * a.pg.hkv;
-                if (s.n > 0) blocks += (static_cast<int64_t>(s.len) + KEYS - 1) / KEYS * a.pg.hkv;
+                if (s.n > 0 && part == 0) blocks += (static_cast<int64_t>(s.len) + KEYS - 1) / KEYS * a.pg.hkv;
             }
 #pragma unroll
-            for (int x = 1; x < 64; x *= 2) most = max(most, __shfl_xor(most, x));
+            for (int x = 1; x < 64; x *= 2) {
+                work += __shfl_xor(work, x);
+                blocks += __shfl_xor(blocks, x);
+                most = max(most, __shfl_xor(most, x));
+            }
             if ((threadIdx.x & 63) == 0) {
                 counts[threadIdx.x / 64] = work;
                 counts[4 + threadIdx.x / 64] = blocks;
@@ -190,11 +196,12 @@ __global__ void __launch_bounds__(256) weights_query(const CacheWeightsArgs a, u
                     const int keys = a.few ? kItem : KEYS;
                     if (s.n > 0) v = (static_cast<int64_t>(s.len) + keys - 1) / keys * a.pg.hkv;
                 }
-            } else {                          // in stages, a wave for a sequence
+            } else {                          // in stages
                 int most = 0;
-                for (int i = threadIdx.x / 64; i < 256 && r0 + i < a.sq.rows; i += 4) {
-                    const int64_t n = stages(seq_of(a, r0 + i), most);
-                    if ((threadIdx.x & 63) == 0) counts[i] = n * a.pg.hkv;
+                for (int i = threadIdx.x / lanes; i < 256 && r0 + i < a.sq.rows; i += at_once) {
+                    int64_t n = stages(seq_of(a, r0 + i), most);
+                    for (int x = 1; x < lanes; x *= 2) n += __shfl_xor(n, x);
+                    if (part == 0) counts[i] = n * a.pg.hkv;
                 }
                 __syncthreads();
                 if (r < a.sq.rows) v = counts[threadIdx.x];
