@@ -1,5 +1,5 @@
 // Argument structs shared by the eviction's host layer (evict_api.cpp) and its
-// kernels (evict_weights_*.hip, evict_pages.hip).  Plain data only.
+// kernels (evict_weights.hip, evict_pages.hip).  Plain data only.
 #pragma once
 
 #include <stddef.h>
