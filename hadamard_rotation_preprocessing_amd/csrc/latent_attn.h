@@ -511,12 +511,13 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
 #pragma unroll
                         for (int x = 0; x < 4; ++x) w[rt][x] = key + x > bound ? -__builtin_inff() : w[rt][x];
                     }
-                    // an unseen key's scale may be anything, and its probability is 0: what is
-                    // multiplied by it is finite (a key that is seen has a NaN score then)
+                    // an unseen key's scale may be any bits, NaN and infinities of both signs among
+                    // them, and its probability is 0: what is multiplied by it is finite (a key
+                    // that is seen has a NaN score then)
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
 #pragma unroll
-                        for (int q = 0; q < NG; ++q) scale[x][q] = fminf(scale[x][q], 0x1.fffffep127f);
+                        for (int q = 0; q < NG; ++q) scale[x][q] = fmaxf(fminf(scale[x][q], 0x1.fffffep127f), -0x1.fffffep127f);
                 }
                 // probabilities, to LDS: keys 16 wk + 4 g + x stand at 8 g + 4 wk + x
                 uint8_t* to = lds.probs[i & 1] + (wr * 16 * RT + m) * C::PS + 16 * g + 8 * wk;

@@ -1,0 +1,71 @@
+"""Bytes, numbers and tokens at the edge of what the eviction and the latent cache
+take, on the GPU against their definitions in float64 (oracle/).  Tolerances are
+those of test_latent_gpu.py and test_evict_gpu.py."""
+import numpy as np
+import pytest
+import torch
+
+import hadamard_rotation_preprocessing_amd as hr
+from oracle import latent as OL
+from test_latent_gpu import gpu, ints, run_attention
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu_ready():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible: the gpu-marked tests need an MI355X")
+    hr.lib()
+
+
+# the upper halves of a NaN, both infinities, the largest numbers of both signs, -1, both zeros and a subnormal number
+ODD = np.array([0x7FC0, 0x7F80, 0xFF80, 0xFF7F, 0x7F7F, 0xBF80, 0x0000, 0x8000, 0x8001], dtype=np.uint16)
+
+
+def odd_bytes(n, rng, wide):
+    """n scales (float32 where wide, else bfloat16) of any bits, extremes most often, as bytes."""
+    v = np.where(rng.random(n) < 0.7, rng.choice(ODD, n), rng.integers(0, 1 << 16, n).astype(np.uint16)).astype(np.uint16)
+    return ((v.astype(np.uint32) << 16) if wide else v).view(np.uint8)
+
+
+def unseen_slots(c, table, lens, n_pages):
+    """(page, slot) of positions past each length and of pages that nobody holds."""
+    held = {int(table[b, j]) for b, n in enumerate(lens) for j in range(-(-n // c.page))}
+    out = [(p, s) for p in range(n_pages) if p not in held for s in range(c.page)]
+    return out + [(int(table[b, n // c.page]), s) for b, n in enumerate(lens) if n % c.page for s in range(n % c.page, c.page)]
+
+
+# ---------------------------------------------------------------------------
+# bytes that nobody sees
+
+@pytest.mark.parametrize("d,group,sym,sdt", [(512, 128, False, "bf16"), (512, 512, True, "f32"), (512, 256, False, "bf16"),
+                                             (256, 128, False, "f32"), (256, 256, True, "bf16")])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("heads", [4, 20, 48], ids=["h4", "h20", "h48"])
+def test_latents_that_nobody_sees_may_be_any_bytes(d, group, sym, sdt, dtype, heads):
+    c = OL.LatentDef(d, 32, group, sym, sdt)
+    seqs = [(1, 1), (1, 77), (2, 130), (3, 17)]
+
+    def odd(pool, table):
+        rng = np.random.default_rng(heads)
+        for p, s in unseen_slots(c, table, [n for _, n in seqs], len(pool)):
+            OL.section(pool[p], c, "scales").reshape(c.page, -1)[s] = odd_bytes(c.ng, rng, sdt == "f32")
+            OL.section(pool[p], c, "rope").reshape(c.page, -1)[s] = odd_bytes(c.rope, rng, False)
+    run_attention(c, seqs, heads, dtype, prepare=odd, poisoned=False, seed=d + group + heads)
+
+
+def test_a_later_latent_of_minus_infinity_leaves_the_tokens_before_it():
+    """Of tokens in one workgroup's rows only those that see the key may be other than without it."""
+    c = OL.LatentDef(512, 16, 128, False, "bf16")
+    spec = hr.LatentSpec(512, 64, 16, hr.QSpec("int", 4, 128, False, "bf16"))
+    pool = OL.random_pool(c, 3, 1)
+    g = torch.Generator().manual_seed(1)
+    q, qr = (torch.randn((6, 3, n), generator=g).to(BF).to(DEV) for n in (512, 64))
+    table = ints([[2, 0, 1]])
+    want = hr.latent_attention(q, qr, gpu(pool), spec, table, ints([40]), 0.07)
+    OL.section(pool[1], c, "scales").reshape(16, -1)[5] = np.full(4, 0xFF80, dtype=np.uint16).view(np.uint8)   # position 37
+    got = hr.latent_attention(q, qr, gpu(pool), spec, table, ints([40]), 0.07)
+    assert torch.isfinite(want.float()).all() and torch.equal(got[:3], want[:3])      # tokens 34, 35, 36
