@@ -135,6 +135,9 @@ __device__ __forceinline__ int last_at_most(const int64_t* first, int n, int64_t
 struct RowScale {
     float factor, lse;
 };
+// Whether a row's log-sum-exp is -inf (as inf here): it is left out by selection, as
+// its scores may be NaN.
+__device__ __forceinline__ bool adds_nothing(const RowScale& r) { return r.lse == __builtin_inff(); }
 
 // Rows (t, i) of q, as [kv head][token][query head of it][hi, lo][D] float16.
 // Elements of eight stand in the order 0 4 1 5 2 6 3 7, that of the codes' operands.
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(256) weights_add(const CacheWeightsArgs a, con
                 const int x = i * 256 + tid, r = x / (D / 4), c = x % (D / 4);
                 ahead[i] = reinterpret_cast<const uint4v*>(query + (at + min(p + r, rows - 1)) * D)[c];
             }
-            if (tid < kRows) rs = scales[at + min(p + tid, rows - 1)];
+            rs = scales[at + min(p + lane % kRows, rows - 1)];   // (every wave asks about them, below)
         };
         if (p0 < p1) load(p0);
         for (int64_t p = p0; p < p1; p += kRows) {
@@ -434,16 +437,17 @@ __global__ void __launch_bounds__(256) weights_add(const CacheWeightsArgs a, con
                 ri.factor = rs.factor;
                 ri.lse = rs.lse;
                 ri.lo = a.window ? max(pos - a.window + 1, 0) : 0;
-                ri.hi = p + tid < rows ? (a.causal ? min(pos + 1, len) : len) : 0;
+                ri.hi = p + tid < rows && !adds_nothing(rs) ? (a.causal ? min(pos + 1, len) : len) : 0;
                 info[tid] = ri;
             }
+            const bool some_out = __any(adds_nothing(rs));
             // (two buffers: the last readers of this one are before the last barrier)
             __syncthreads();
             if (p + kRows < p1) load(p + kRows);
-            // whether every row of the stage is there and sees every key of the block
+            // whether every row of the stage is there, adds something and sees every key of the block
             const int pos0 = first + static_cast<int>(static_cast<uint32_t>(p) / a.rep);
             const int pos1 = first + static_cast<int>(static_cast<uint32_t>(min(p + kRows, rows) - 1) / a.rep);
-            const bool full = p + kRows <= rows && j0 + S::KEYS <= len && (!a.causal || j0 + S::KEYS - 1 <= pos0) &&
+            const bool full = !some_out && p + kRows <= rows && j0 + S::KEYS <= len && (!a.causal || j0 + S::KEYS - 1 <= pos0) &&
                               (!a.window || j0 > pos1 - a.window);
             const auto tiles = [&](auto FULL) __attribute__((always_inline)) {
 #pragma unroll
@@ -617,6 +621,7 @@ __global__ void __launch_bounds__(256) weights_few(const CacheWeightsArgs a, con
             float factor[RT][4], lse[RT][4];
             int from[RT][4], to[RT][4];            // the keys that a row sees
             int all_from = 0, all_to = len;        // and those that all rows do
+            bool some_out = false;                 // whether one of the lane's rows adds nothing
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 const uint32_t* q = query + (at + min(r0 + 16 * rt + m, rows - 1)) * D;
@@ -635,13 +640,14 @@ __global__ void __launch_bounds__(256) weights_few(const CacheWeightsArgs a, con
                     const int pos = first + min(r, rows - 1) / a.rep;
                     factor[rt][i] = rs.factor;
                     lse[rt][i] = r < rows ? rs.lse : __builtin_inff();
-                    to[rt][i] = r < rows ? (a.causal ? min(pos + 1, len) : len) : 0;
+                    to[rt][i] = r < rows && !adds_nothing(rs) ? (a.causal ? min(pos + 1, len) : len) : 0;
+                    some_out = some_out || adds_nothing(rs);
                     from[rt][i] = a.window ? max(pos - a.window + 1, 0) : 0;
                 }
             }
             if (a.causal) all_to = min(first + r0 / a.rep + 1, len);
             if (a.window) all_from = max(first + (min(r0 + 16 * RT, rows) - 1) / a.rep - a.window + 1, 0);
-            const bool whole = r0 + 16 * RT <= rows;
+            const bool whole = r0 + 16 * RT <= rows && !__any(some_out);
 
             Tile<D, NG> tile[4];
             int page[4], next[4];                  // of the tile in a place, and of the one after it

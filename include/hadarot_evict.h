@@ -30,7 +30,8 @@ extern "C" {
  *                        h that see j of exp(scale q'(t, i) . k_j - lse(t, i))
  * for j < lens[b], with n(b) the row's new tokens: a position that is new starts
  * at 0 whatever was there.  Positions past lens, and all of a row without new
- * tokens, are left as they are.  A token whose lse is -inf adds nothing.
+ * tokens, are left as they are.  A token whose lse is -inf adds nothing, whatever
+ * its query is (a padded one's may be NaN).
  *   q        as in hr_cache_attention; queries carry 22 bits here for both
  *            types, so that the weights have float32's precision.
  *   lse      device float32 [tokens, q_heads].

@@ -6,7 +6,12 @@ import pytest
 import torch
 
 import hadamard_rotation_preprocessing_amd as hr
+from oracle import cache as OC
+from oracle import evict as OE
 from oracle import latent as OL
+from test_cache_gpu import make_q, make_table
+from test_cache_gpu import spec_of as cache_spec
+from test_evict_gpu import check_weights
 from test_latent_gpu import gpu, ints, run_attention
 
 pytestmark = pytest.mark.gpu
@@ -69,3 +74,36 @@ def test_a_later_latent_of_minus_infinity_leaves_the_tokens_before_it():
     OL.section(pool[1], c, "scales").reshape(16, -1)[5] = np.full(4, 0xFF80, dtype=np.uint16).view(np.uint8)   # position 37
     got = hr.latent_attention(q, qr, gpu(pool), spec, table, ints([40]), 0.07)
     assert torch.isfinite(want.float()).all() and torch.equal(got[:3], want[:3])      # tokens 34, 35, 36
+
+
+# ---------------------------------------------------------------------------
+# tokens that are masked out
+
+@pytest.mark.parametrize("d,group", [(64, 64), (128, 32), (256, 256)])
+@pytest.mark.parametrize("new,hq,max_q", [(1, 4, 1), (5, 8, 5), (6, 8, 1), (70, 8, 70)], ids=["step", "draft", "more-than-bound", "chunk"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_tokens_without_a_log_sum_exp_add_nothing(d, group, new, hq, max_q, dtype):
+    """A padded batch: tokens whose lse is -inf add nothing, whatever their queries
+    are and though they see keys, and the rows beside them keep their weights."""
+    c = OC.CacheDef(2, d, 16, group, False, "bf16")
+    lens = [250, 97, 150]
+    table, n_pages = make_table(c, lens, d)
+    pool = OC.random_pool(c, n_pages, d)
+    cu = np.arange(4, dtype=np.int32) * new
+    q = make_q(3 * new, hq, d, dtype, d)
+    _, lse, _ = OC.attention(q.double().numpy(), pool, c, table, lens, cu)
+    lse = lse.astype(np.float32)
+    lse[:new, 1] = -np.inf                    # one head of the first sequence's tokens, some tokens of the second, all of the third
+    lse[new: 2 * new][::3] = -np.inf
+    lse[2 * new:] = -np.inf
+    fine = q.clone()
+    out = torch.from_numpy(lse == -np.inf)
+    fine[out] = 0.0
+    old = np.random.default_rng(1).random((3, 2, table.shape[1] * 16)).astype(np.float32)
+    ref, need = OE.weights(fine.double().numpy(), pool, c, table, lens, cu, lse, old, decay=0.5)
+    odd = torch.tensor([float("nan"), float("inf"), -float("inf"), 3.0])
+    q[out] = odd[torch.arange(int(out.sum()) * d) % 4].view(-1, d).to(dtype)
+    for x in (q, fine):
+        w = gpu(old)
+        hr.cache_weights(x.to(DEV), gpu(pool), cache_spec(c), gpu(table), ints(lens), gpu(lse), w, cu_q=gpu(cu), max_q=max_q, decay=0.5)
+        check_weights(w, ref, need, c, new * hq // 2)
