@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(256) weights_query(const CacheWeightsArgs a, u
     for (int j = 1; j < 16; ++j) top = fmaxf(top, fabsf(x[j]));
     top = over_lanes<LPV>(top, [](float p, float q) { return fmaxf(p, q); });
     int unit = 0;
-    if (top > 0.0f && top < __builtin_inff()) unit = min(max(kTop - 1 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), -110), 110);
+    if (top > 0.0f && top < __builtin_inff()) unit = min(kTop - 1 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), 110);   // (from -114)
     const int64_t r = (int64_t{h} * a.sq.tokens + t) * a.rep + i % a.rep;
     if (v >= total) return;
     uint32_t* to = out + r * D;       // hi: D / 2 words, then lo

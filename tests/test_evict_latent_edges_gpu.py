@@ -107,3 +107,34 @@ def test_tokens_without_a_log_sum_exp_add_nothing(d, group, new, hq, max_q, dtyp
         w = gpu(old)
         hr.cache_weights(x.to(DEV), gpu(pool), cache_spec(c), gpu(table), ints(lens), gpu(lse), w, cu_q=gpu(cu), max_q=max_q, decay=0.5)
         check_weights(w, ref, need, c, new * hq // 2)
+
+
+# ---------------------------------------------------------------------------
+# queries near the end of float32
+
+def small_keys(pool, c, heads=None):
+    """Scales 2^-80 as large."""
+    for p in range(len(pool)):
+        for s in [OL.section(pool[p], c, "scales")] if heads is None else [OC.section(pool[p], c, h, "k_scales") for h in range(heads)]:
+            s.view("<f4")[:] *= np.float32(2.0 ** -80)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 40], ids=["few", "many"])
+@pytest.mark.parametrize("d,group", [(64, 64), (128, 32), (256, 128)])
+def test_weights_of_the_largest_queries(dtype, new, d, group):
+    c = OC.CacheDef(2, d, 16, group, False, "f32")
+    lens, cu = [130, 77], np.array([0, new, 2 * new], dtype=np.int32)
+    table, n_pages = make_table(c, lens, d)
+    pool = OC.random_pool(c, n_pages, d)
+    small_keys(pool, c, 2)
+    q = make_q(2 * new, 8, d, dtype, d, std=2.0 ** 125)
+    q[:, :, 0] = 1.875 * 2.0 ** 127           # (every row's largest element)
+    scale = 2.0 ** -52
+    _, lse, _ = OC.attention(q.double().numpy(), pool, c, table, lens, cu, scale, rotate=False)
+    lse = lse.astype(np.float32)
+    old = np.zeros((2, 2, table.shape[1] * 16), dtype=np.float32)
+    ref, need = OE.weights(q.double().numpy(), pool, c, table, lens, cu, lse, old, scale, rotate=False)
+    w = gpu(old)
+    hr.cache_weights(q.to(DEV), gpu(pool), cache_spec(c), gpu(table), ints(lens), gpu(lse), w, cu_q=gpu(cu), max_q=new, scale=scale, rotate=False)
+    check_weights(w, ref, need, c, new * 4)
