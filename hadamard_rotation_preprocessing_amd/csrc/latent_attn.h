@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(256) latent_query(const LatentAttnArgs a) {
     rtop = over_lanes<LPV>(rtop, [](float p, float q) { return fmaxf(p, q); });
     const int most = min(100 - exponent(rtop), 110);
     int unit = 0;
-    if (top > 0.0f && top < __builtin_inff()) unit = max(min(kQTop - 1 - exponent(top), most), -110);
+    if (top > 0.0f && top < __builtin_inff()) unit = min(kQTop - 1 - exponent(top), most);   // (from -114)
     if (row >= total) return;
     uint8_t* to = work.query + row * C::QS;
 #pragma unroll

@@ -120,6 +120,15 @@ def small_keys(pool, c, heads=None):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("d,group,heads", [(512, 128, 20), (256, 256, 4), (512, 512, 48)])
+def test_latent_attention_of_the_largest_queries(dtype, d, group, heads):
+    """Elements of 2^126 and more over small latents: scores of ordinary size."""
+    c = OL.LatentDef(d, 16, group, False, "f32")
+    run_attention(c, [(2, 100), (1, 37)], heads, dtype, rotate=False, std=2.0 ** 125, scale=2.0 ** -51, seed=d,
+                  prepare=lambda pool, table: small_keys(pool, c))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("new", [1, 40], ids=["few", "many"])
 @pytest.mark.parametrize("d,group", [(64, 64), (128, 32), (256, 128)])
 def test_weights_of_the_largest_queries(dtype, new, d, group):
