@@ -11,7 +11,7 @@ from oracle import evict as OE
 from oracle import latent as OL
 from test_cache_gpu import make_q, make_table
 from test_cache_gpu import spec_of as cache_spec
-from test_evict_gpu import check_weights
+from test_evict_gpu import check_weights, run_evict, run_weights
 from test_latent_gpu import gpu, ints, run_attention
 
 pytestmark = pytest.mark.gpu
@@ -107,6 +107,73 @@ def test_tokens_without_a_log_sum_exp_add_nothing(d, group, new, hq, max_q, dtyp
         w = gpu(old)
         hr.cache_weights(x.to(DEV), gpu(pool), cache_spec(c), gpu(table), ints(lens), gpu(lse), w, cu_q=gpu(cu), max_q=max_q, decay=0.5)
         check_weights(w, ref, need, c, new * hq // 2)
+
+
+@pytest.mark.parametrize("d,group,sym,sdt", [(64, 64, False, "bf16"), (128, 32, True, "f32"), (128, 64, False, "f32"), (256, 256, True, "bf16")])
+@pytest.mark.parametrize("new,max_q", [(1, 1), (3, 3), (40, 40)], ids=["step", "draft", "chunk"])
+@pytest.mark.parametrize("window", [0, 29])
+def test_weights_of_keys_that_nobody_sees_may_be_any_bytes(d, group, sym, sdt, new, max_q, window):
+    """Scales past each length and in pages that nobody holds, and in positions that a
+    window has left (whose weights only decay)."""
+    c = OC.CacheDef(2, d, 16, group, sym, sdt)
+    lens, cu = [205, 77], np.array([0, new, 2 * new], dtype=np.int32)
+    table, n_pages = make_table(c, lens, d)
+    pool = OC.random_pool(c, n_pages, d)
+    rng = np.random.default_rng(d + new)
+    slots = unseen_slots(c, table, lens, n_pages)
+    if window:
+        slots += [(int(table[b, j // 16]), j % 16) for b, n in enumerate(lens) for j in range(max(n - new - window + 1, 0))]
+    for p, s in slots:
+        for h in range(2):
+            OC.section(pool[p], c, h, "k_scales").reshape(16, -1)[s] = odd_bytes(c.ng, rng, sdt == "f32")
+    q = make_q(2 * new, 6, d, BF, d)
+    _, lse, _ = OC.attention(q.double().numpy(), pool, c, table, lens, cu, window=window)
+    lse = lse.astype(np.float32)
+    old = rng.random((2, 2, table.shape[1] * 16)).astype(np.float32)
+    ref, need = OE.weights(q.double().numpy(), pool, c, table, lens, cu, lse, old, window=window, decay=0.9)
+    assert np.isfinite(ref).all()
+    w = gpu(old)
+    hr.cache_weights(q.to(DEV), gpu(pool), cache_spec(c), gpu(table), ints(lens), gpu(lse), w, cu_q=gpu(cu), max_q=max_q, window=window, decay=0.9)
+    check_weights(w, ref, need, c, new * 3)
+
+
+# ---------------------------------------------------------------------------
+# many sequences, of which few have much work
+
+@pytest.mark.parametrize("seqs", [[(1, 20)] * 300 + [(700, 900)] + [(0, 5)] * 40, [(700, 900)] + [(1, 20 + i % 60) for i in range(400)],
+                                  [(i % 2, 40) for i in range(255)] + [(600, 700), (500, 500)] + [(2, 300)] * 300],
+                         ids=["in-the-second-256", "first", "around-256"])
+def test_weights_shared_out_among_many_sequences(seqs):
+    """A prompt's chunk among hundreds of single tokens: rows are numbered over more
+    sequences than a workgroup takes at once.  (Not in whole blocks: 4 times the
+    heaviest, of 24 stages of 32 rows at least, is above 5 times the mean.)"""
+    blocks = [2 + -(-4 * n // 32) for n, length in seqs if n for _ in range(-(-length // 256))]
+    assert 4 * max(blocks) * 512 * -(-len(blocks) // 512) > 5 * sum(blocks)
+    run_weights(OC.CacheDef(1, 64, 16, 64, False, "bf16"), seqs, 4, max_q=700, seed=len(seqs))
+
+
+# ---------------------------------------------------------------------------
+# pages that are absent, or held twice by the same row
+
+def test_evict_leaves_the_row_with_the_absent_page_and_cuts_the_other():
+    c = OC.CacheDef(2, 64, 16, 64, False, "bf16")
+    got = run_evict(c, [100, 100], 41, absent=[(0, 5, -1), (1, 6, 1 << 20)])
+    assert got["lens"].tolist() == [100, 100] and got["status"][2].item() == 0
+    got = run_evict(c, [100, 100], 41, absent=[(0, 5, -1)])
+    assert got["lens"].tolist() == [100, 41] and got["status"][2].item() == 1
+    got = run_evict(c, [100, 100], 41, absent=[(1, 0, 1 << 20)], layers=2)
+    assert got["lens"].tolist() == [41, 100] and got["status"][2].item() == 1
+
+
+def test_evict_of_a_page_that_a_row_holds_twice():
+    """Each of its places that stays gets a page of its own, and reads what was there."""
+    c = OC.CacheDef(2, 64, 16, 64, False, "bf16")
+    table, _ = make_table(c, [100, 90], 0)
+    twice = [(0, 1, int(table[0, 0])), (1, 5, int(table[1, 2]))]     # both places stay, and one of two
+    got = run_evict(c, [100, 90], 41, 2, 4, layers=2, absent=twice, spare=6)
+    assert got["lens"].tolist() == [41, 41] and got["status"][1].item() == 0
+    got = run_evict(c, [100, 90], 41, 2, 4, absent=twice, spare=0)    # (the pages that left the table are free)
+    assert got["lens"].tolist()[0] == 41
 
 
 # ---------------------------------------------------------------------------
