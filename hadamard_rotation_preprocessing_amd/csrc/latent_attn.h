@@ -511,13 +511,13 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
 #pragma unroll
                         for (int x = 0; x < 4; ++x) w[rt][x] = key + x > bound ? -__builtin_inff() : w[rt][x];
                     }
-                    // an unseen key's scale may be any bits, NaN and infinities of both signs among
-                    // them, and its probability is 0: what is multiplied by it is finite (a key
-                    // that is seen has a NaN score then)
+                    // an unseen key's scale may be any bits (infinities are NaN here), and its
+                    // probability is 0: what is multiplied by it is finite (a key that is seen
+                    // has a NaN score then)
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
 #pragma unroll
-                        for (int q = 0; q < NG; ++q) scale[x][q] = fmaxf(fminf(scale[x][q], 0x1.fffffep127f), -0x1.fffffep127f);
+                        for (int q = 0; q < NG; ++q) scale[x][q] = fminf(scale[x][q], 0x1.fffffep127f);
                 }
                 // probabilities, to LDS: keys 16 wk + 4 g + x stand at 8 g + 4 wk + x
                 uint8_t* to = lds.probs[i & 1] + (wr * 16 * RT + m) * C::PS + 16 * g + 8 * wk;
@@ -669,7 +669,11 @@ __global__ void __launch_bounds__(C::THREADS, 2) latent_sums(const LatentAttnArg
                 if (lane == 0) lds.there[b][vw / 2] = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.sq.n_pages);   // (waves of the same 16 keys say the same)
 #pragma unroll
                 for (int x = 0; x < C::CW / 4; ++x)
-                    if ((part + C::LK * x) * 32 % C::G == 0) lds.scales[b][kk * NG + group_of(x)] = __uint_as_float(C::SF32 ? w.scale[x] : w.scale[x] << 16);
+                    if ((part + C::LK * x) * 32 % C::G == 0) {
+                        // (the scale of an infinite latent is infinite, and its codes say nothing: NaN)
+                        const float s = __uint_as_float(C::SF32 ? w.scale[x] : w.scale[x] << 16);
+                        lds.scales[b][kk * NG + group_of(x)] = fabsf(s) == __builtin_inff() ? __builtin_nanf("") : s;
+                    }
                 *reinterpret_cast<uint4v*>(to + 2 * D + 16 * part) = w.rope;
             };
             float4v acc[C::TILES][C::DT];

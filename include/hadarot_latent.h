@@ -95,7 +95,8 @@ int hr_latent_read(const void* pool, int64_t n_pages, const hr_latent_spec* spec
  *            2^16 (else HR_EUNSUPPORTED).
  * Positions of absent pages are not seen; what a token does not see has no
  * influence, whatever its bytes are.  A token that sees nothing gets zeros (and a
- * log-sum-exp of -inf).  Scales are the append's: positive and finite, or NaN.
+ * log-sum-exp of -inf).  Scales are the append's: positive, or NaN; an infinite one,
+ * of an infinite latent, counts as NaN, which the tokens that see it get.
  * Products use float16 operands with float32 sums for HR_BF16: codes are exact,
  * queries and probabilities carry 11 bits (a pair of float16, 22 bits, for
  * HR_F32), and the products with rotary keys are exact.  The result does not

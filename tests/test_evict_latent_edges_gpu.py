@@ -76,6 +76,32 @@ def test_a_later_latent_of_minus_infinity_leaves_the_tokens_before_it():
     assert torch.isfinite(want.float()).all() and torch.equal(got[:3], want[:3])      # tokens 34, 35, 36
 
 
+@pytest.mark.parametrize("sym,sdt", [(False, "bf16"), (True, "bf16"), (True, "f32")])
+@pytest.mark.parametrize("rotate", [True, False])
+@pytest.mark.parametrize("heads,dtype", [(1, BF), (5, BF), (40, BF), (4, F32), (20, F32)])
+def test_an_infinite_latent_gives_nan_to_the_tokens_that_see_it(sym, sdt, rotate, heads, dtype):
+    """Its scale is infinite and its codes are anything: no score may come out as a number
+    that drops the position.  In a step that not all tokens see whole, and in one that they do."""
+    spec = hr.LatentSpec(512, 64, 16, hr.QSpec("int", 4, 128, sym, sdt))
+    g = torch.Generator().manual_seed(heads)
+    table, lens = ints([[2, 0, 1, 3, 5, 4]]), ints([90])
+
+    def draw(*shape):
+        return torch.randn(shape, generator=g).to(dtype).to(DEV)
+    c, rope, q, qr = draw(90, 512), draw(90, 64), draw(14, heads, 512), draw(14, heads, 64)
+    for at, sees in ((80, 4), (10, 0)):           # the tokens are at 76 to 89
+        for bad in (float("inf"), -float("inf")):
+            out = []
+            for x in (0.0, bad):
+                pool = hr.cache_pool(spec, 6)
+                v = c.clone()
+                v[at, 7] = x
+                hr.latent_append(pool, spec, v, rope, table, lens, rotate=rotate)
+                out.append(hr.latent_attention(q, qr, pool, spec, table, lens, 0.07, rotate=rotate))
+            assert torch.isfinite(out[0].float()).all() and torch.equal(out[0][:sees], out[1][:sees])
+            assert torch.isnan(out[1][sees:]).all()
+
+
 # ---------------------------------------------------------------------------
 # tokens that are masked out
 
