@@ -10,7 +10,6 @@ namespace hr {
 namespace {
 
 typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
-typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------------------
 // the plan
@@ -156,12 +155,13 @@ __global__ void __launch_bounds__(kScan) evict_plan(const CacheEvictArgs a, int3
 // never past its source, and the sources of the next kMove lie past all of these,
 // so that loads of one step need not wait for the stores of the one before.
 //
-// Measured: 32 rows of up to 16384 cut to 4096, 4 layers of 8 heads of 128: evict_plan 18
-// us, evict_move 165 to 176 us for 334 MB of traffic, 2.0 TB/s.  Positions that stay are
-// scattered, so that a read is 64 bytes of a key's or value's codes, and a step's loads
-// take 12 us (512 positions of each of 320 workgroups) however they are issued.  Four rows
-// of 1100 cut to 1024, 2 layers: 6 and 16 us, of which the selection is 5 and each of two
-// steps 5.  Tried: weights held in registers through the passes, the first histogram in
+// Measured: 32 rows of up to 16384 cut to 4096, 4 layers of 8 heads of 128: evict_plan 19
+// us, evict_move 165 to 176 us, which read 289 MB and write 173 MB by counters, 2.7 TB/s
+// (of 374 MB that the moves and the selection need): positions that stay are scattered,
+// so that a read is 64 bytes of a key's or value's codes.  Waves wait 80% of their time: a
+// step's loads take 12 us (512 positions of each of 320 workgroups) however they are
+// issued.  Four rows of 1100 cut to 1024, 2 layers: 6 and 16 us, of which the selection is 5
+// and each of two steps 5.  The selection needs nothing of the plan, and waits for it.  Tried: weights held in registers through the passes, the first histogram in
 // copies, eight parts a thread, two workgroups of half the threads a compute unit, the
 // rows over budget first, non-temporal loads: 165 to 173 us, and 18 to 20 for the few rows.
 

@@ -21,16 +21,20 @@
 // over all sequences and kv heads; where they do not go into the workgroups evenly,
 // their rows are numbered, a workgroup takes an equal run of those, and weights_join
 // adds up the blocks that were cut.  Two chunks of 2048 tokens against 8192 positions,
-// 32 heads over 8 of 128: weights_query 24 us, weights_add 566 us, 860 TFLOP/s with the
-// two products counted.  The matrix instructions are 47% of its cycles, and the vector
-// ones (of 112 cycles for a tile 64 are exponentials) and the reads
-// of rows from LDS nearly all of the rest, at some 1.7 GHz (busy cycles over time).
-// Tried: one tile of keys at a time 586 us, a branch for each absent tile 681 us, no
-// rows on their way 702 us.
+// 32 heads over 8 of 128: the whole call 503 to 513 us, of which weights_query is 22 and
+// weights_join 5 (480 GFLOP with the two products counted, 950 TFLOP/s).  By counters
+// the matrix instructions are 42% of weights_add's cycles, the vector ones 48% (of 112
+// cycles for a tile 64 are exponentials), LDS is active for 32% of them and 10% are
+// conflicts; waves wait a fifth of their time.  Steps to this form, whole calls, each
+// beside the one before: no rows on their way 702 us; with them, and a branch for each absent tile, 681;
+// one tile of keys at a time 586, two 581; neighbouring work on one die 566.
 //
 // Few rows (steps): weights_few, below.  24 sequences of up to 32768, one token each:
-// 34 us for 74 MB, 2.2 TB/s; what bounds it is the way of a wave's small loads (64 bytes
-// of a key's codes, its scale, zero point and weight), of which four tiles' are under way.
+// 34 us for 74 MB, 2.2 TB/s.  Waves wait 60% of their time, and vector instructions are
+// 47% of the cycles: for 64 keys a wave has 16 loads (codes, and a scale, a zero point
+// and a weight of 2, 1 and 4 bytes for each of 16 keys, the same in four lane groups) and
+// 4 stores under way.  A window saves nothing here: tiles that no row sees are loaded and
+// multiplied too (24 of 32768, all of it or a window of 4096: 155 us both).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -50,8 +54,14 @@ typedef int int4v __attribute__((ext_vector_type(4)));
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kRows = 32;     // rows of a stage
 constexpr int kItem = 64;     // keys of a block of weights_few: four tiles of 16, one of each on its way
-constexpr int kSetUp = 2;     // stages that the keys' way into registers and the sums' way out cost
-constexpr int kLeast = 4;     // of work to a workgroup: with less there are fewer workgroups
+// Stages that the keys' way into registers and the sums' way out cost.  (With 1 or 4 for
+// 2 one chunk of 64 tokens behind 3936, 32 heads over 8, takes 29 or 27 us for 27, three
+// of 777 tokens of up to 900, 8 over 2 of 64, 34 or 33 for 32.)
+constexpr int kSetUp = 2;
+// Of work to a workgroup: with less there are fewer workgroups.  (With 1 the latter take
+// 34 us for 32, and four chunks of 100 tokens behind 900, 8 heads over 2, 24 for 31;
+// with 16 50 and 44.)
+constexpr int kLeast = 4;
 constexpr int kTop = 14;      // a row's largest query element is below 2^kTop in float16
 
 __device__ __forceinline__ float4v mfma(uint4v a, uint4v b, float4v c) {
@@ -281,8 +291,8 @@ __device__ __forceinline__ int64_t uni(int64_t v) {
 // those of its rows.  Workgroup `worker` takes [begin, end) of it.  Where whole blocks
 // go into the workgroups evenly (the longest takes at most 5/4 of the mean) the work
 // is numbered in blocks, one each, and first_of[0] is -1: workgroups then keep step
-// and share the queries in their caches (two chunks of 2048 tokens against 8192: 566 us,
-// 603 in stages, evenly); where not, a few blocks with many rows are the work of all (two
+// and share the queries in their caches (two chunks of 2048 tokens against 8192: 518 us,
+// 537 in stages, evenly); where not, a few blocks with many rows are the work of all (two
 // chunks of 269 tokens against 447, 7 heads of one kv head: 93 us whole, 31 in stages).
 struct Range {
     int64_t begin, end;
@@ -789,7 +799,12 @@ int cache_weights_workers(int few, int* workers) {
     int dev, cus;
     hipError_t e = hipGetDevice(&dev);
     if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-    // (as many as fit with heads of 128)
+    // With few rows, four to a compute unit with one tile of rows and two with two: what
+    // fits at once with heads of 64 and 128 in one or two groups (24 sequences of up to 32768
+    // and single tokens, 128: 38 us, with three 42; of 8000 and 8 new tokens 72, with one
+    // 118).  Kernels of more registers run a second round: single tokens with heads of 128
+    // in groups of 32 take 68 us where three take 59, of 256 65 where three take 54, and of
+    // 256 in groups of 64 or 32 80 and 118 where two take 78 and 115.
     if (e == hipSuccess) *workers = few == 0 ? (2 * cus < kWeightsParts ? 2 * cus : kWeightsParts) : (few == 2 ? 2 : 4) * cus;
     return static_cast<int>(e);
 }

@@ -8,7 +8,8 @@
 // bfloat16.  For the values the scales go into the probabilities, for each group
 // apart: P_g = exp(w - m) s_g, and O_g = P_g (k - z) is a matrix product over the
 // same integers.
-//   The softmax is taken in one pass.  P_g goes into the product as float16, so its
+//   The softmax is taken in one pass.  P_g goes into the product as float16, one for
+// bfloat16 activations (11 bits, of which the result keeps 8) and a pair for float32, so its
 // reference m follows the largest exp(w - m) s_g that the row has seen: probabilities
 // are at most 2^kTop, 2^kSet when the reference is set, and what a row does not see
 // has no part in it.  Where scales are below 2^-92 or above 2^100 float32's own range
@@ -35,14 +36,19 @@
 // the parts in key order, divides, rotates back and rounds.
 //
 // Measured.  32 sequences of up to 32768, one token, 128 heads, latents of 512 in four
-// groups: latent_query 7 us, latent_sums 144 us (470 TFLOP/s, 1.55 us a step of 32 keys
-// and 64 rows), latent_finish 16 us.  The value waves bound it: LDS gives 64 bytes a
-// cycle to wide reads and takes 43 of wide writes, and their operands' writes and
-// transposing reads fill most of a step, with stores between the matrix steps.  Tried:
-// waves of one kind, each with scores and values, 517 us for the whole call where this
-// form takes 165; sixteen waves with half the registers 2.44 us a step; codes turned
-// into operands in registers by every wave, without LDS, 1.99 us a step.
-// One sequence of 331, 16 heads: 4.0, 13.2 and 4.5 us, of which most is latency.
+// groups: latent_query 7 us, latent_sums 145 us (465 TFLOP/s, 1.55 us a step of 32 keys
+// and 64 rows), latent_finish 15 us; the call 164 us.  By counters the matrix units are
+// busy 20% of the cycles, the vector units 30%, LDS 24% (and 4% with conflicts), and waves
+// wait 54% of their time: two waves a SIMD, of two kinds that meet at a barrier each step,
+// and chains of LDS writes, transposing reads and matrix steps in each.  Registers allow
+// no third: this kernel takes all 256 and spills 45 (all those of 64 rows and latents of
+// 512 spill 32 to 46, the float32 ones 7 to 27; those of latents of 256 none).  128 heads
+// are two units of 64 rows, which load and unpack every code twice.  Tried: waves of one
+// kind, each with scores and values, 517 us for the whole call where this form takes 165;
+// sixteen waves with half the registers 2.44 us a step; codes turned into operands in
+// registers by every wave, without LDS, 1.99 us a step.
+// One sequence of 331, 16 heads: 4.0, 13.2 and 4.5 us, of which most is latency: three
+// workgroups take part, one of them with items of set-up alone.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -105,8 +111,9 @@ __device__ __forceinline__ uint32_t to_bf16(float f) {
 // floor(log2(v)) of v >= 0 that is a normal number (-127 of smaller ones, 128 of larger)
 __device__ __forceinline__ int exponent(float v) { return static_cast<int>((__float_as_uint(v) >> 23) & 255) - 127; }
 
-// Matrix steps stay in order: left alone, the scheduler loads the operands of many of
-// them at once, and spills.
+// Matrix steps stay in order, with the loads of the operands of kBatch of them ahead.
+// (Measured with 512 in four groups: without these barriers to the scheduler the kernels
+// spill as many registers, or up to 6 fewer, and a server's step takes 163 us for 165.)
 #define HR_PHASE() __builtin_amdgcn_sched_barrier(0)
 // The kernel's lambdas hold its registers: one that is called would keep them in memory.
 #define HR_INLINE __attribute__((always_inline))
@@ -159,7 +166,10 @@ __device__ __forceinline__ Seq seq_at(const CacheSeqs& s, int logp, int b) {
     return r;
 }
 // items of a unit of a sequence, and its units.  An item is kItem keys; a unit that has
-// any counts kSetUp items more, before them, for what it costs beside its keys.
+// any counts kSetUp items more, before them, for what it costs beside its keys.  (32
+// sequences of up to 32768 and 128 heads take 162 us with 6, 219 with 0, 168 with 3 and
+// 165 with 12; 8 sequences of 2000, 40 new tokens, 32 heads 127, 129, 126 and 137; one
+// sequence the same with all of them.)
 constexpr int kItem = 64, kSetUp = 6;
 __device__ __forceinline__ int items_of(const Seq& s) {
     return s.len > 0 ? static_cast<int>((static_cast<int64_t>(s.len) + kItem - 1) / kItem) + kSetUp : 0;
@@ -172,7 +182,8 @@ __device__ __forceinline__ int units_of(const Seq& s, int heads) {
 __device__ __forceinline__ int64_t begin_of(int64_t total, int w, int n) { return total * w / n; }
 
 // How many workgroups take part: not so many that joining their parts costs more
-// than it saves.
+// than it saves.  (16 heads, one sequence of 331, 1000, 4096 and 32768: 24, 26, 30 and 37
+// us with 4; 21, 24, 25 and 42 with 1; 22, 23, 31 and 42 with 2; 27, 31, 34 and 40 with 8.)
 constexpr int kLeast = 4;              // items of a workgroup
 __device__ __forceinline__ int used_workers(int64_t total, int workers) {
     const int64_t n = (total + kLeast - 1) / kLeast;

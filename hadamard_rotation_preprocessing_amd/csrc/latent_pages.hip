@@ -4,9 +4,12 @@
 // Both are one pass over the data: D / 16 lanes share a latent, 16 consecutive
 // elements each, as in cache_vectors.h, and the same lanes take the rotary key.
 // The floor is the bytes; what comes next is the instruction stream of the
-// transform and the codes.  Measured: 32768 latents of 512 appended in 16.8 us (50 MB,
-// 3.0 TB/s), single tokens of 64 sequences in 9 us a call, 4.8 us of it in the kernel;
-// 24 sequences of up to 32768 read in 55 us (192 MB, 3.5 TB/s), 76 us a call.
+// transform and the codes, which by counters takes the vector units nearly all of their
+// cycles.  Measured: 32768 latents of 512 appended in 16.8 us (50 MB, 3.0 TB/s), single
+// tokens of 64 sequences in 9 us a call, 4.9 us of it in the kernel; 24 sequences of up to
+// 32768 read in 55 us (192 MB, 3.5 TB/s), 76 us a call where inputs and outputs change from
+// call to call.  Over two sets of inputs in turn the append takes 18.6 us, and 12.6 without
+// the rotation; the read 52 us into the same buffers, and 41 without it (4.7 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

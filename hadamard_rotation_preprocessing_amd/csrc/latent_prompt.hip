@@ -13,14 +13,20 @@
 // S^T = K Q^T (A operand: keys, B operand: queries, in registers throughout), so that
 // a lane holds four keys of one row, and two tiles of 16 keys are as they stand the B
 // operand of O^T = V^T P^T, with V^T out of LDS by transposing reads: probabilities
-// never leave the registers.  Everything is bfloat16 with float32 sums.
+// never leave the registers.  Operands are bfloat16 and sums float32: a probability is
+// rounded to 8 bits, since the values may lie anywhere in bfloat16's range, which float16
+// has not, and both operands of a product are of one type; the sum that divides them is
+// of the unrounded ones.  A chunk errs by 2.3e-3 of its norm, where the result's own
+// rounding makes 1.7e-3.
 //
 // Measured: a chunk of 2048 tokens behind 6144 positions, 32 heads of 128 + 64 (301
-// GFLOP), in 332 us, 907 TFLOP/s, three quarters of what a large bfloat16 product
-// reaches here; three ragged prompts of up to 777, 16 heads, in 34 us, of which the
-// longest one's last rows take most.  Exponentials and the reads of keys and values from
-// LDS stand beside the matrix steps of two waves a SIMD; registers leave no room for a
-// third with 32 rows a wave, and with 16 each the reads are twice as many.
+// GFLOP), in 329 us, 915 TFLOP/s, three quarters of what a large bfloat16 product
+// reaches here; three ragged prompts of up to 777, 16 heads, in 34 us: 160 workgroups, one
+// wave a SIMD, and the longest prompt's last rows with 13 steps of 2.6 us in a row.
+// Exponentials and the reads of keys and values from LDS stand beside the matrix steps of
+// two waves a SIMD (of the chunk's cycles 38% are matrix instructions, 42% vector ones, and
+// LDS is active for 40%, 11% of them conflicts); registers leave no room for a third with
+// 32 rows a wave, and with 16 each the reads are twice as many.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

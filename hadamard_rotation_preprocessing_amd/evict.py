@@ -61,7 +61,8 @@ def cache_weights(q: torch.Tensor, pool: torch.Tensor, spec: CacheSpec, table: t
     max_pages * page_size) the attention weight that each position gets from the
     new tokens q [tokens, q_heads, head_dim], whose log-sum-exp cache_attention
     gave with the same arguments; earlier positions' weights are multiplied by
-    ``decay`` first, new positions start at 0.  Returns ``weights``.  ``work``:
+    ``decay`` first, new positions start at 0.  A token whose lse is -inf adds
+    nothing, whatever its query is.  Returns ``weights``.  ``work``:
     scratch of hr_cache_weights_work bytes (allocated if not given)."""
     r, dev, l = K._resolved(spec), pool.device, _evict_lib()
     _, n = K._pages(pool, r, False)

@@ -99,7 +99,11 @@ int hr_latent_read(const void* pool, int64_t n_pages, const hr_latent_spec* spec
  * of an infinite latent, counts as NaN, which the tokens that see it get.
  * Products use float16 operands with float32 sums for HR_BF16: codes are exact,
  * queries and probabilities carry 11 bits (a pair of float16, 22 bits, for
- * HR_F32), and the products with rotary keys are exact.  The result does not
+ * HR_F32), and the products with rotary keys are exact.  An element of a query has
+ * 11 of them down to 2^-27 of the row's largest, or to 2^-114 of its rotary query's
+ * largest, and a probability times its latent's scale down to 2^-22 of the row's
+ * largest; 22 down to 2^-15, 2^-102 and 2^-10.  Scales below 2^-92 or above 2^100 cost
+ * more.  The result does not
  * depend on scheduling: partial sums over a long sequence are joined in a fixed
  * order.
  */
