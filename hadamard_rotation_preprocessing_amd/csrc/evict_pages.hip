@@ -161,9 +161,10 @@ __global__ void __launch_bounds__(kScan) evict_plan(const CacheEvictArgs a, int3
 // so that a read is 64 bytes of a key's or value's codes.  Waves wait 80% of their time: a
 // step's loads take 12 us (512 positions of each of 320 workgroups) however they are
 // issued.  Four rows of 1100 cut to 1024, 2 layers: 6 and 16 us, of which the selection is 5
-// and each of two steps 5.  The selection needs nothing of the plan, and waits for it.  Tried: weights held in registers through the passes, the first histogram in
-// copies, eight parts a thread, two workgroups of half the threads a compute unit, the
-// rows over budget first, non-temporal loads: 165 to 173 us, and 18 to 20 for the few rows.
+// and each of two steps 5.  The selection needs nothing of the plan, and waits for it.
+// Tried: weights held in registers through the passes, the first histogram in copies,
+// eight parts a thread, two workgroups of half the threads a compute unit, the rows over
+// budget first, non-temporal loads: 165 to 173 us, and 18 to 20 for the few rows.
 
 constexpr int kThreads = 1024;
 constexpr int kPer = 4;                     // positions of a thread in a chunk

@@ -25,9 +25,10 @@
 // weights_join 5 (480 GFLOP with the two products counted, 950 TFLOP/s).  By counters
 // the matrix instructions are 42% of weights_add's cycles, the vector ones 48% (of 112
 // cycles for a tile 64 are exponentials), LDS is active for 32% of them and 10% are
-// conflicts; waves wait a fifth of their time.  Steps to this form, whole calls, each
-// beside the one before: no rows on their way 702 us; with them, and a branch for each absent tile, 681;
-// one tile of keys at a time 586, two 581; neighbouring work on one die 566.
+// conflicts; waves wait a fifth of their time.  Steps to this form, each beside the one
+// before (on a day when the last took 566 us): no rows on their way 702 us; with them, and
+// a branch for each absent tile, 681; one tile of keys at a time 586, two 581;
+// neighbouring work on one die 566.
 //
 // Few rows (steps): weights_few, below.  24 sequences of up to 32768, one token each:
 // 34 us for 74 MB, 2.2 TB/s.  Waves wait 60% of their time, and vector instructions are

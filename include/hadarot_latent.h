@@ -103,9 +103,8 @@ int hr_latent_read(const void* pool, int64_t n_pages, const hr_latent_spec* spec
  * 11 of them down to 2^-27 of the row's largest, or to 2^-114 of its rotary query's
  * largest, and a probability times its latent's scale down to 2^-22 of the row's
  * largest; 22 down to 2^-15, 2^-102 and 2^-10.  Scales below 2^-92 or above 2^100 cost
- * more.  The result does not
- * depend on scheduling: partial sums over a long sequence are joined in a fixed
- * order.
+ * more.  The result does not depend on scheduling: partial sums over a long sequence
+ * are joined in a fixed order.
  */
 int hr_latent_attention(const void* q, int64_t q_stride_token, int64_t q_stride_head,
                         const void* q_rope, int64_t q_rope_stride_token, int64_t q_rope_stride_head,
